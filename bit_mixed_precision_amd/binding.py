@@ -38,6 +38,8 @@ TQ_OK, TQ_ERR_NULL, TQ_ERR_SHAPE, TQ_ERR_VALUE, TQ_ERR_ALIGN, TQ_ERR_DEVICE, TQ_
     0, -1, -2, -3, -4, -5, -6
 TQ_SRC_TERNARY_I8, TQ_SRC_LATENT_F32 = 0, 1
 TQ_PATH_AUTO, TQ_PATH_SKINNY, TQ_PATH_TILED, TQ_PATH_SIMPLE = 0, 1, 2, 3
+TQ_F16, TQ_BF16, TQ_F32 = 0, 1, 2
+TQ_ROPE_NONE, TQ_ROPE_LINEAR, TQ_ROPE_BASE, TQ_ROPE_PARTS = 0, 1, 2, 3
 
 _P, _I64, _I, _D = C.c_void_p, C.c_int64, C.c_int, C.c_double
 
@@ -73,6 +75,22 @@ SIGNATURES = {
     "tq_pack_tq2_dev": (_I, [_P, _I64, _I64, C.c_double, _P, _P, _P, _P, _P, _I64, _P]),
     "tq_pack_tq1_dev": (_I, [_P, _I64, _I64, C.c_double, _I64, _P, _P, _P, _P, _P, _I64, _P]),
     "tq_pack_tq2_dev_noalloc": (_I, [_P, _I64, _I64, C.c_double, _P, _P, _P, _P, _P]),
+    "tq_rope_table": (_I, [_I64, _I64, _D, _I, _D, _D, _D, _D, _D, _P]),
+    "tq_rope": (_I, [_I, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64,
+                     _I, _I, _P]),
+    "tq_rope_append": (_I, [_I, _P, _I64, _P, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _P, _I64,
+                            _I64, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I, _P]),
+    "tq_paged_attention": (_I, [_I, _P, _I64, _I64, _P, _P, _I64, _I64, _I64, _I64, _I64, _P,
+                                _I64, _P, _I64, _I64, _I64, _I64, _D, _I64, _P, _P, _P, _I64,
+                                _P]),
+    "tq_paged_attention_workspace": (_I64, [_I64, _I64, _I64, _I64, _I64, _I64]),
+    "tq_pages_fork": (_I, [_P, _I64, _I64, _I64, _P, _P, _I64, _P, _I64, _I64, _I64, _P, _P, _P,
+                           _P, _P, _I64, _P]),
+    "tq_pages_grow": (_I, [_P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _P]),
+    "tq_pages_compact": (_I, [_P, _I64, _I64, _I64, _P, _P, _I64, _I64, _I64, _P, _P, _P, _I64,
+                              _P]),
+    "tq_pages_copy": (_I, [_P, _I64, _I64, _I64, _P, _P, _I64, _P]),
+    "tq_pages_workspace": (_I64, [_I64, _I64]),
 }
 for _name, (_res, _args) in SIGNATURES.items():
     _fn = getattr(lib, _name)
@@ -190,7 +208,8 @@ def tq_unpack_tq1(qs: np.ndarray, K: int) -> np.ndarray:
 
 # ------------------------------------------------------------------ device
 
-_DTYPES = {"f16": "float16", "f32": "float32", "u8": "uint8", "i32": "int32"}
+_DTYPES = {"f16": "float16", "bf16": "bfloat16", "f32": "float32", "u8": "uint8",
+           "i32": "int32"}
 
 
 def _need(t, name, dtype, shape=None, where=""):
@@ -524,6 +543,318 @@ def tq_kernel_name(fmt: int, M: int, N: int, K: int, path: int = TQ_PATH_AUTO) -
     buf = C.create_string_buffer(128)
     _check(lib.tq_kernel_name(fmt, M, N, K, path, buf, 128), "tq_kernel_name")
     return buf.value.decode()
+
+
+# ------------------------------------------------------------------ decode
+
+def _kind(t, name, where, f32=False):
+    """tq_dtype of a float tensor whose last dimension is contiguous."""
+    import torch
+    if not torch.is_tensor(t):
+        raise TQError(TQ_ERR_VALUE, f"{where}: {name} must be a torch tensor")
+    if t.dtype is torch.float16:
+        return TQ_F16
+    if t.dtype is torch.bfloat16:
+        return TQ_BF16
+    if f32 and t.dtype is torch.float32:
+        return TQ_F32
+    raise TQError(TQ_ERR_VALUE, f"{where}: {name} has dtype {t.dtype}")
+
+
+def _heads(t, name, where, like=None):
+    """Shape of a [..][heads][D] tensor: three dimensions, numbers of a head adjacent."""
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise TQError(TQ_ERR_SHAPE, f"{where}: {name} must be [tokens][heads][D] with adjacent "
+                                    f"numbers, not {tuple(t.shape)} at strides {t.stride()}")
+    if like is not None and t.dtype != like.dtype:
+        raise TQError(TQ_ERR_VALUE, f"{where}: {name} is {t.dtype}, expected {like.dtype}")
+    return t.shape
+
+
+def _cache(k_pages, v_pages, like, D, where):
+    """(n_pages, page_size, Hkv, page, row and head stride) of the two halves of a
+    paged cache [pages][slots][Hkv][D], any order in memory, numbers adjacent."""
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if _kind(t, name, where) is not None and t.dtype != like.dtype:
+            raise TQError(TQ_ERR_VALUE, f"{where}: {name} is {t.dtype}, expected {like.dtype}")
+        if t.dim() != 4 or t.shape[3] != D or (D > 1 and t.stride(3) != 1):
+            raise TQError(TQ_ERR_SHAPE, f"{where}: {name} must be [pages][slots][heads][{D}] with "
+                                        f"adjacent numbers, not {tuple(t.shape)}")
+    if k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride():
+        raise TQError(TQ_ERR_SHAPE, f"{where}: k_pages and v_pages differ in shape or strides")
+    return (*k_pages.shape[:3], *k_pages.stride()[:3])
+
+
+def _table(table, where):
+    """(n_pos, rot) of a cosine / sine table [n_pos][rot / 2][2]."""
+    import torch
+    if not torch.is_tensor(table) or table.dim() != 3 or table.shape[2] != 2:
+        raise TQError(TQ_ERR_SHAPE, f"{where}: table must be [positions][rot / 2][2]")
+    _need(table, "table", "f32", None, where)
+    return table.shape[0], 2 * table.shape[1]
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor whose memory belongs to the stream that the call runs on: the
+    allocator hands a freed block out again in the order of its own stream, so
+    memory of the current stream must not be written on another one."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _int32(t, name, shape, where):
+    return _need(t, name, "i32", shape, where)
+
+
+def tq_rope_table(n_pos: int, rot: int, theta: float = 5e5, scaling: int = TQ_ROPE_NONE,
+                  factor: float = 1.0, trained: float = 4096.0, fast: float = 32.0,
+                  slow: float = 1.0, gain: float = 1.0) -> np.ndarray:
+    """Cosines and sines float32 [n_pos][rot / 2][2] (numpy) for tq_rope."""
+    table = np.empty((max(n_pos, 0), max(rot // 2, 0), 2), dtype=np.float32)
+    _check(lib.tq_rope_table(n_pos, rot, theta, scaling, factor, trained, fast, slow, gain,
+                             _ptr(table)), "tq_rope_table")
+    return table
+
+
+def tq_rope(X, table, positions, interleaved: bool = False, inverse: bool = False, Y=None,
+            stream=None):
+    """Rotary positions: X [T][H][D] (fp16, bfloat16 or float32; a view with any
+    strides, numbers of a head adjacent) turned by table[positions] over the first
+    rot numbers of each head; inverse turns back, which is the gradient.  Y may be
+    X; a new contiguous tensor when None."""
+    where = "tq_rope"
+    kind = _kind(X, "X", where, f32=True)
+    T, H, D = _heads(X, "X", where)
+    n_pos, rot = _table(table, where)
+    _int32(positions, "positions", (T,), where)
+    if Y is not None:
+        _kind(Y, "Y", where, f32=True)
+        if _heads(Y, "Y", where, X) != X.shape:
+            raise TQError(TQ_ERR_SHAPE, f"{where}: Y has shape {tuple(Y.shape)}, "
+                                        f"expected {tuple(X.shape)}")
+    _on_gpu(where, ("X", X), ("table", table), ("positions", positions), ("Y", Y))
+    if Y is None:
+        Y = _empty((T, H, D), X.dtype, X.device, stream)
+    with _device_of(X):
+        _check(lib.tq_rope(kind, X.data_ptr(), X.stride(0), X.stride(1), Y.data_ptr(), Y.stride(0),
+                           Y.stride(1), table.data_ptr(), n_pos, rot, positions.data_ptr(), T, H,
+                           D, interleaved, inverse, _stream(stream, X.device)), where)
+    return Y
+
+
+def tq_rope_append(QKV, table, positions, page_table, k_pages, v_pages, interleaved: bool = False,
+                   seqs=None, Q=None, stream=None):
+    """Rotate the query and key heads of QKV [T][Hq + 2 Hkv][D], write the keys and
+    values of token t into slot positions[t] of row seqs[t] (t when None) of the
+    paged cache, and return the queries [T][Hq][D].  k_pages, v_pages:
+    [pages][slots][Hkv][D], any strides, numbers of a head adjacent."""
+    where = "tq_rope_append"
+    kind = _kind(QKV, "QKV", where)
+    T, H, D = _heads(QKV, "QKV", where)
+    if H > 1 and QKV.stride(1) != D:
+        raise TQError(TQ_ERR_SHAPE, f"{where}: the heads of QKV must be adjacent")
+    n_pos, rot = _table(table, where)
+    _int32(positions, "positions", (T,), where)
+    n_seqs, width = _rank2(page_table, "page_table", where)
+    _int32(page_table, "page_table", None, where)
+    if seqs is not None:
+        _int32(seqs, "seqs", (T,), where)
+    P, size, Hkv, page_stride, row_stride, head_stride = _cache(k_pages, v_pages, QKV, D, where)
+    Hq = H - 2 * Hkv
+    if Hq < 1:
+        raise TQError(TQ_ERR_SHAPE, f"{where}: {H} heads in QKV, {Hkv} in the cache")
+    if Q is not None:
+        _need(Q, "Q", "f16" if kind == TQ_F16 else "bf16", (T, Hq, D), where)
+    _on_gpu(where, ("QKV", QKV), ("table", table), ("positions", positions),
+            ("page_table", page_table), ("seqs", seqs), ("k_pages", k_pages),
+            ("v_pages", v_pages), ("Q", Q))
+    if Q is None:
+        Q = _empty((T, Hq, D), QKV.dtype, QKV.device, stream)
+    with _device_of(QKV):
+        _check(lib.tq_rope_append(kind, QKV.data_ptr(), QKV.stride(0), table.data_ptr(), n_pos,
+                                  rot, positions.data_ptr(), _ptr(seqs), page_table.data_ptr(),
+                                  n_seqs, width, k_pages.data_ptr(), v_pages.data_ptr(), P, size,
+                                  page_stride, row_stride, head_stride, Q.data_ptr(), T, Hq, Hkv,
+                                  D, interleaved, _stream(stream, QKV.device)), where)
+    return Q
+
+
+def tq_paged_attention_workspace(B: int, Hq: int, Hkv: int, D: int, page_size: int,
+                                 width: int) -> int:
+    """Workspace bytes of tq_paged_attention on the current GPU."""
+    n = int(lib.tq_paged_attention_workspace(B, Hq, Hkv, D, page_size, width))
+    _check(min(n, 0), "tq_paged_attention_workspace")
+    return n
+
+
+def tq_paged_attention(Q, k_pages, v_pages, page_table, lens, scale: float | None = None,
+                       window: int = 0, out=None, return_lse: bool = False, workspace=None,
+                       stream=None):
+    """Attention of one new token per sequence: Q [B][Hq][D] over the last `window`
+    (0: all) of lens[b] tokens in the paged cache k_pages, v_pages
+    [pages][slots][Hkv][D] named by page_table [B][width].  Returns out [B][Hq][D],
+    and lse float32 [B][Hq] with return_lse.  scale: 1 / sqrt(D) when None."""
+    import torch
+    where = "tq_paged_attention"
+    kind = _kind(Q, "Q", where)
+    B, Hq, D = _heads(Q, "Q", where)
+    P, size, Hkv, page_stride, row_stride, head_stride = _cache(k_pages, v_pages, Q, D, where)
+    rows, width = _rank2(page_table, "page_table", where)
+    _int32(page_table, "page_table", (B, width), where)
+    _int32(lens, "lens", (B,), where)
+    if out is not None:
+        _need(out, "out", "f16" if kind == TQ_F16 else "bf16", (B, Hq, D), where)
+    if workspace is not None:
+        _need(workspace, "workspace", "u8", None, where)
+    _on_gpu(where, ("Q", Q), ("k_pages", k_pages), ("v_pages", v_pages),
+            ("page_table", page_table), ("lens", lens), ("out", out), ("workspace", workspace))
+    with _device_of(Q):
+        n = lib.tq_paged_attention_workspace(B, Hq, Hkv, D, size, width)
+        _check(min(n, 0), where)
+        if workspace is None and n > 0:
+            workspace = _empty((n,), torch.uint8, Q.device, stream)
+        if out is None:
+            out = _empty((B, Hq, D), Q.dtype, Q.device, stream)
+        lse = _empty((B, Hq), torch.float32, Q.device, stream) if return_lse else None
+        _check(lib.tq_paged_attention(
+            kind, Q.data_ptr(), Q.stride(0), Q.stride(1), k_pages.data_ptr(), v_pages.data_ptr(),
+            P, size, page_stride, row_stride, head_stride, page_table.data_ptr(), width,
+            lens.data_ptr(), B, Hq, Hkv, D, D ** -0.5 if scale is None else scale, window,
+            out.data_ptr(), _ptr(lse), _ptr(workspace),
+            0 if workspace is None else workspace.numel(), _stream(stream, Q.device)), where)
+    return (out, lse) if return_lse else out
+
+
+def _pool(pool, where):
+    """(planes, n_pages, bytes of a page) of a contiguous pool [planes][pages]..."""
+    import torch
+    if not torch.is_tensor(pool) or pool.dim() < 3 or not pool.is_contiguous():
+        raise TQError(TQ_ERR_SHAPE, f"{where}: pool must be a contiguous [planes][pages][...] tensor")
+    planes, pages = pool.shape[:2]
+    size = pool.element_size()
+    for n in pool.shape[2:]:
+        size *= n
+    return planes, pages, size
+
+
+def _state(page_table, lens, where):
+    rows, width = _rank2(page_table, "page_table", where)
+    _int32(page_table, "page_table", None, where)
+    _int32(lens, "lens", (rows,), where)
+    return rows, width
+
+
+def _pages_workspace(rows, n_pages, workspace, device, stream, where):
+    import torch
+    n = lib.tq_pages_workspace(rows, n_pages)
+    _check(min(n, 0), where)
+    return _empty((n,), torch.uint8, device, stream) if workspace is None else workspace
+
+
+def tq_pages_workspace(rows: int, n_pages: int) -> int:
+    """Workspace bytes of tq_pages_fork, tq_pages_grow and tq_pages_compact."""
+    n = int(lib.tq_pages_workspace(rows, n_pages))
+    _check(min(n, 0), "tq_pages_workspace")
+    return n
+
+
+def tq_pages_fork(pool, page_table, lens, parent, page_size: int, workspace=None, stream=None):
+    """Continue row parent[r] as row r (an empty sequence where parent[r] names no
+    row): pages are shared, a partly filled last page is copied for all but the
+    first row that continues it.  pool [planes][pages][...], page_table [rows][width],
+    lens [rows], parent [new rows].  Returns (page_table, lens, refs, short): the new
+    state, how often each page is held, and the rows that found no free page."""
+    import torch
+    where = "tq_pages_fork"
+    planes, P, size = _pool(pool, where)
+    rows_in, width = _state(page_table, lens, where)
+    if not torch.is_tensor(parent) or parent.dim() != 1:
+        raise TQError(TQ_ERR_SHAPE, f"{where}: parent must be a 1-D tensor")
+    rows = parent.shape[0]
+    _int32(parent, "parent", None, where)
+    if workspace is not None:
+        _need(workspace, "workspace", "u8", None, where)
+    _on_gpu(where, ("pool", pool), ("page_table", page_table), ("lens", lens), ("parent", parent),
+            ("workspace", workspace))
+    with _device_of(pool):
+        dev = pool.device
+        ws = _pages_workspace(rows, P, workspace, dev, stream, where)
+        table_out = _empty((rows, width), torch.int32, dev, stream)
+        lens_out = _empty((rows,), torch.int32, dev, stream)
+        refs = _empty((P,), torch.int32, dev, stream)
+        short = _empty((1,), torch.int32, dev, stream)
+        _check(lib.tq_pages_fork(pool.data_ptr(), planes, P, size, page_table.data_ptr(),
+                                 lens.data_ptr(), rows_in, parent.data_ptr(), rows, width,
+                                 page_size, table_out.data_ptr(), lens_out.data_ptr(),
+                                 refs.data_ptr(), short.data_ptr(), ws.data_ptr(), ws.numel(),
+                                 _stream(stream, dev)), where)
+    return table_out, lens_out, refs, short
+
+
+def tq_pages_grow(page_table, lens, add, n_pages: int, page_size: int, workspace=None,
+                  stream=None):
+    """Room for add[r] more tokens in row r, from the pages that no row holds.
+    Returns (page_table, lens, short): the new state and how many rows were refused."""
+    import torch
+    where = "tq_pages_grow"
+    rows, width = _state(page_table, lens, where)
+    _int32(add, "add", (rows,), where)
+    if workspace is not None:
+        _need(workspace, "workspace", "u8", None, where)
+    _on_gpu(where, ("page_table", page_table), ("lens", lens), ("add", add),
+            ("workspace", workspace))
+    with _device_of(page_table):
+        dev = page_table.device
+        ws = _pages_workspace(rows, n_pages, workspace, dev, stream, where)
+        table_out = _empty((rows, width), torch.int32, dev, stream)
+        lens_out = _empty((rows,), torch.int32, dev, stream)
+        short = _empty((1,), torch.int32, dev, stream)
+        _check(lib.tq_pages_grow(page_table.data_ptr(), lens.data_ptr(), add.data_ptr(), rows,
+                                 width, page_size, n_pages, table_out.data_ptr(),
+                                 lens_out.data_ptr(), short.data_ptr(), ws.data_ptr(), ws.numel(),
+                                 _stream(stream, dev)), where)
+    return table_out, lens_out, short
+
+
+def tq_pages_compact(pool, page_table, lens, page_size: int, workspace=None, stream=None):
+    """Move the pages in use to the low end of the pool.  Returns (page_table, used):
+    the new table and the number of pages in use (int32 [1]), all below it."""
+    import torch
+    where = "tq_pages_compact"
+    planes, P, size = _pool(pool, where)
+    rows, width = _state(page_table, lens, where)
+    if workspace is not None:
+        _need(workspace, "workspace", "u8", None, where)
+    _on_gpu(where, ("pool", pool), ("page_table", page_table), ("lens", lens),
+            ("workspace", workspace))
+    with _device_of(pool):
+        dev = pool.device
+        ws = _pages_workspace(rows, P, workspace, dev, stream, where)
+        table_out = _empty((rows, width), torch.int32, dev, stream)
+        used = _empty((1,), torch.int32, dev, stream)
+        _check(lib.tq_pages_compact(pool.data_ptr(), planes, P, size, page_table.data_ptr(),
+                                    lens.data_ptr(), rows, width, page_size, table_out.data_ptr(),
+                                    used.data_ptr(), ws.data_ptr(), ws.numel(),
+                                    _stream(stream, dev)), where)
+    return table_out, used
+
+
+def tq_pages_copy(pool, src, dst, stream=None):
+    """Copy page src[i] over page dst[i] in every plane of pool [planes][pages][...]."""
+    import torch
+    where = "tq_pages_copy"
+    planes, P, size = _pool(pool, where)
+    if not torch.is_tensor(src) or src.dim() != 1:
+        raise TQError(TQ_ERR_SHAPE, f"{where}: src must be a 1-D tensor")
+    _int32(src, "src", None, where)
+    _int32(dst, "dst", src.shape, where)
+    _on_gpu(where, ("pool", pool), ("src", src), ("dst", dst))
+    with _device_of(pool):
+        _check(lib.tq_pages_copy(pool.data_ptr(), planes, P, size, src.data_ptr(), dst.data_ptr(),
+                                 src.shape[0], _stream(stream, pool.device)), where)
 
 
 def raw_call(name: str, *args) -> int:

@@ -1,0 +1,430 @@
+// The pages of a key-value cache: forking, growing, compacting, copying.
+//
+// The page tables and lengths are the state.  Which pages are free follows from
+// them: a bitmap with one bit per page is filled from the held table entries
+// (bit-wise or and integer counts only, so the order of the atomics does not
+// show), one workgroup ranks its free (or used) bits by popcounts and a prefix
+// sum, and the data moves in a last launch that reads the list of pairs and
+// their number from device memory: no call waits for the host.
+//
+// Bound: the copied pages, read and written once per plane.
+
+#include "tq.h"
+#include "tq_common.h"
+#include "tq_decode.h"
+#include "tq_kernels.h"
+
+namespace tq {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kPagesThreads = 256;
+constexpr int kScanThreads = 1024;
+
+struct PagesParams {
+  unsigned char* pool;
+  int64_t planes, page_bytes;
+  int32_t n_pages, page_size, rows_in, rows, width;
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* parent;
+  const int32_t* add;
+  int32_t* table_out;
+  int32_t* lens_out;
+  int32_t* refs;
+  int32_t* result;
+  // workspace
+  uint32_t* bits;   // ceil(n_pages / 32)
+  int32_t* need;    // [rows] pages wanted by a row
+  int32_t* last;    // [rows] fork: the page a row copies
+  int32_t* src;     // [n_pages]
+  int32_t* dst;     // [n_pages]: also the list of free pages
+  int32_t* map;     // [n_pages] compact: where a page goes
+  int32_t* pairs;   // [1] number of (src, dst)
+};
+
+__device__ __forceinline__ bool names_page(const PagesParams& p, int32_t id) {
+  return (uint32_t)id < (uint32_t)p.n_pages;
+}
+// Tokens and table entries of an input row.
+__device__ __forceinline__ int tokens_of(const PagesParams& p, int row) {
+  const int64_t cap = (int64_t)p.width * p.page_size;
+  const int n = p.lens[row];
+  return n < 0 ? 0 : n < cap ? n : (int)cap;
+}
+__device__ __forceinline__ int entries(const PagesParams& p, int tokens) {
+  return (int)(((int64_t)tokens + p.page_size - 1) / p.page_size);
+}
+
+__global__ __launch_bounds__(kPagesThreads) void pages_clear_kernel(PagesParams p) {
+  const int words = (p.n_pages + 31) / 32;
+  for (int i = blockIdx.x * kPagesThreads + threadIdx.x; i < p.n_pages;
+       i += gridDim.x * kPagesThreads) {
+    if (i < words) p.bits[i] = 0;
+    if (p.refs) p.refs[i] = 0;
+  }
+}
+
+enum { kFork = 0, kGrow = 1, kCompact = 2 };
+
+// One workgroup per output row: copies the row, marks the pages it holds and
+// says how many pages it wants.
+template <int OP>
+__global__ __launch_bounds__(kPagesThreads) void pages_rows_kernel(PagesParams p) {
+  const int r = blockIdx.x;
+  int from = r;
+  if constexpr (OP == kFork) {
+    from = p.parent[r];
+    if ((uint32_t)from >= (uint32_t)p.rows_in) from = -1;
+  }
+  const int tokens = from < 0 ? 0 : tokens_of(p, from);
+  const int n = entries(p, tokens);
+  const int32_t* row = p.table + (int64_t)(from < 0 ? 0 : from) * p.width;
+  int32_t* out = p.table_out + (int64_t)r * p.width;
+  int copied = -1;  // entry that this row does not share
+  if constexpr (OP == kFork) {
+    __shared__ int sLater;
+    if (threadIdx.x == 0) sLater = 0;
+    __syncthreads();
+    if (from >= 0 && tokens % p.page_size != 0) {
+      int later = 0;
+      for (int i = threadIdx.x; i < r; i += kPagesThreads) later |= p.parent[i] == from;
+      if (later) sLater = 1;  // every writer writes 1
+    }
+    __syncthreads();
+    if (sLater && names_page(p, row[n - 1])) copied = n - 1;
+    if (threadIdx.x == 0) {
+      p.need[r] = copied >= 0;
+      p.last[r] = copied >= 0 ? row[copied] : -1;
+      p.lens_out[r] = tokens;
+    }
+  }
+  if constexpr (OP == kGrow) {
+    if (threadIdx.x == 0) {
+      const int64_t want = (int64_t)tokens + (p.add[r] > 0 ? p.add[r] : 0);
+      const int64_t cap = (int64_t)p.width * p.page_size;
+      p.need[r] = want > cap ? -1 : entries(p, (int)want) - n;
+    }
+  }
+  for (int i = threadIdx.x; i < p.width; i += kPagesThreads) {
+    int32_t id = -1;
+    if (i < n) {
+      id = row[i];
+      if (i != copied && names_page(p, id)) {
+        atomicOr(&p.bits[id >> 5], 1u << (id & 31));
+        if (p.refs) atomicAdd(&p.refs[id], 1);
+      }
+    }
+    if constexpr (OP != kCompact) out[i] = id;
+  }
+}
+
+// Exclusive prefix sum over the workgroup and its total.
+__device__ __forceinline__ int scan_block(int v, int* red, int& total) {
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
+  int inc = v;
+#pragma unroll
+  for (int off = 1; off < kWave; off <<= 1) {
+    const int o = __shfl_up(inc, off, kWave);
+    if (lane >= off) inc += o;
+  }
+  __syncthreads();  // red of the previous call has been read
+  if (lane == 63) red[w] = inc;
+  __syncthreads();
+  int before = inc - v;
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < kScanThreads / kWave; ++i) {
+    if (i < w) before += red[i];
+    total += red[i];
+  }
+  return before;
+}
+
+__device__ __forceinline__ uint32_t valid_bits(const PagesParams& p, int word) {
+  const int left = p.n_pages - word * 32;
+  return left >= 32 ? 0xffffffffu : (1u << left) - 1;
+}
+
+// One workgroup: ranks the free pages, in ascending order, into dst[0 .. limit)
+// and returns how many there are in all.
+__device__ __forceinline__ int list_free(const PagesParams& p, int limit, int* red) {
+  const int words = (p.n_pages + 31) / 32;
+  const int per = (words + kScanThreads - 1) / kScanThreads;
+  const int w0 = threadIdx.x * per, w1 = w0 + per < words ? w0 + per : words;
+  int mine = 0;
+  for (int w = w0; w < w1; ++w) mine += __popc(~p.bits[w] & valid_bits(p, w));
+  int total;
+  int rank = scan_block(mine, red, total);
+  for (int w = w0; w < w1 && rank < limit; ++w) {
+    uint32_t f = ~p.bits[w] & valid_bits(p, w);
+    while (f && rank < limit) {
+      p.dst[rank++] = w * 32 + __ffs(f) - 1;
+      f &= f - 1;
+    }
+  }
+  __syncthreads();  // dst is complete for this workgroup
+  return total;
+}
+
+__global__ __launch_bounds__(kScanThreads) void pages_fork_assign_kernel(PagesParams p) {
+  __shared__ int red[kScanThreads / kWave];
+  const int t = threadIdx.x;
+  int wanted = 0;
+  for (int r0 = 0; r0 < p.rows; r0 += kScanThreads) {
+    int total;
+    (void)scan_block(r0 + t < p.rows ? p.need[r0 + t] : 0, red, total);
+    wanted += total;
+  }
+  const int free_pages = list_free(p, wanted, red);
+  int base = 0, kept = 0;
+  for (int r0 = 0; r0 < p.rows; r0 += kScanThreads) {
+    const int r = r0 + t;
+    const int need = r < p.rows ? p.need[r] : 0;
+    int total;
+    const int rank = base + scan_block(need, red, total);
+    base += total;
+    if (need) {
+      const int tokens = p.lens_out[r];
+      int32_t* out = p.table_out + (int64_t)r * p.width + entries(p, tokens) - 1;
+      if (rank < free_pages) {
+        const int32_t id = p.dst[rank];
+        p.src[rank] = p.last[r];
+        *out = id;
+        if (p.refs) p.refs[id] = 1;
+      } else {
+        *out = -1;
+        p.lens_out[r] = tokens / p.page_size * p.page_size;
+      }
+    }
+  }
+  kept = wanted < free_pages ? wanted : free_pages;
+  if (t == 0) {
+    *p.pairs = kept;
+    *p.result = wanted - kept;
+  }
+}
+
+__global__ __launch_bounds__(kScanThreads) void pages_grow_assign_kernel(PagesParams p) {
+  __shared__ int red[kScanThreads / kWave];
+  const int t = threadIdx.x, lane = t & 63;
+  const int free_pages = list_free(p, p.n_pages, red);
+  int64_t base = 0;  // pages wanted by the rows before this round
+  int refused = 0;
+  for (int r0 = 0; r0 < p.rows; r0 += kScanThreads) {
+    const int r = r0 + t;
+    const int want = r < p.rows ? p.need[r] : 0;
+    // more pages than there are count as one more, so that sums stay small
+    const int need = want < 0 ? 0 : want <= p.n_pages ? want : p.n_pages + 1;
+    // rows are ranked one wave at a time: 64 (n_pages + 1) fits in 32 bits
+    int64_t rank = base;
+    for (int w = 0; w < kScanThreads / kWave; ++w) {
+      int total;
+      const int before = scan_block((t >> 6) == w ? need : 0, red, total);
+      if ((t >> 6) == w) rank = base + before;
+      base += total;
+    }
+    const bool ok = r < p.rows && want >= 0 && (need == 0 || rank + need <= free_pages);
+    if (r < p.rows) {
+      const int tokens = tokens_of(p, r);
+      p.lens_out[r] = ok ? tokens + (p.add[r] > 0 ? p.add[r] : 0) : tokens;
+      refused += !ok;
+    }
+    // the wave writes its rows' new pages together
+    for (int k = 0; k < kWave; ++k) {
+      const int cnt = __shfl(ok ? need : 0, k, kWave);
+      if (cnt == 0) continue;
+      const int from = __shfl((int)rank, k, kWave);
+      const int row = r0 + (t & ~63) + k;
+      int32_t* out = p.table_out + (int64_t)row * p.width + entries(p, tokens_of(p, row));
+      for (int i = lane; i < cnt; i += kWave) out[i] = p.dst[from + i];
+    }
+  }
+  int total;
+  (void)scan_block(refused, red, total);
+  if (t == 0) *p.result = total;
+}
+
+__global__ __launch_bounds__(kScanThreads) void pages_compact_assign_kernel(PagesParams p) {
+  __shared__ int red[kScanThreads / kWave];
+  const int words = (p.n_pages + 31) / 32;
+  const int per = (words + kScanThreads - 1) / kScanThreads;
+  const int w0 = threadIdx.x * per, w1 = w0 + per < words ? w0 + per : words;
+  int mine = 0, used;
+  for (int w = w0; w < w1; ++w) mine += __popc(p.bits[w]);
+  (void)scan_block(mine, red, used);
+  // bits at or above `used`, and free bits below it
+  auto above = [&](int w) {
+    const int left = used - w * 32;
+    return left <= 0 ? p.bits[w] : left >= 32 ? 0u : p.bits[w] & ~((1u << left) - 1);
+  };
+  auto below = [&](int w) {
+    const int left = used - w * 32;
+    return left <= 0 ? 0u : left >= 32 ? ~p.bits[w] : ~p.bits[w] & ((1u << left) - 1);
+  };
+  int na = 0, nb = 0, moves, holes;
+  for (int w = w0; w < w1; ++w) {
+    na += __popc(above(w));
+    nb += __popc(below(w));
+  }
+  int ra = scan_block(na, red, moves);
+  int rb = scan_block(nb, red, holes);  // holes == moves
+  for (int w = w0; w < w1; ++w) {
+    for (uint32_t f = above(w); f; f &= f - 1) p.src[ra++] = w * 32 + __ffs(f) - 1;
+    for (uint32_t f = below(w); f; f &= f - 1) p.dst[rb++] = w * 32 + __ffs(f) - 1;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < moves; i += kScanThreads) p.map[p.src[i]] = p.dst[i];
+  if (threadIdx.x == 0) {
+    *p.pairs = moves;
+    *p.result = used;
+  }
+}
+
+// Rewrites the table after compaction: one workgroup per row.
+__global__ __launch_bounds__(kPagesThreads) void pages_retable_kernel(PagesParams p) {
+  const int r = blockIdx.x;
+  const int n = entries(p, tokens_of(p, r));
+  const int32_t* row = p.table + (int64_t)r * p.width;
+  int32_t* out = p.table_out + (int64_t)r * p.width;
+  const int used = *p.result;
+  for (int i = threadIdx.x; i < p.width; i += kPagesThreads) {
+    int32_t id = i < n ? row[i] : -1;
+    if (i < n && names_page(p, id) && id >= used) id = p.map[id];
+    out[i] = id;
+  }
+}
+
+constexpr int kCopyBytes = kPagesThreads * 16 * 4;  // bytes of one workgroup's step
+
+// pairs x planes x pieces of a page, taken in turn by a fixed grid.
+__global__ __launch_bounds__(kPagesThreads) void pages_copy_kernel(
+    unsigned char* pool, int64_t planes, int32_t n_pages, int64_t page_bytes, const int32_t* src,
+    const int32_t* dst, const int32_t* count, int64_t n) {
+  const int64_t pieces = (page_bytes + kCopyBytes - 1) / kCopyBytes;
+  const int64_t total = (count ? (int64_t)*count : n) * planes * pieces;
+  for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
+    const int64_t piece = i % pieces, rest = i / pieces;
+    const int64_t plane = rest % planes, pair = rest / planes;
+    const int32_t s = src[pair], d = dst[pair];
+    if ((uint32_t)s >= (uint32_t)n_pages || (uint32_t)d >= (uint32_t)n_pages) continue;
+    const unsigned char* from = pool + (plane * n_pages + s) * page_bytes;
+    unsigned char* to = pool + (plane * n_pages + d) * page_bytes;
+    const int64_t at = piece * kCopyBytes + threadIdx.x * 16;
+    u32x4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (at + k * kPagesThreads * 16 < page_bytes)
+        v[k] = *reinterpret_cast<const u32x4*>(from + at + k * kPagesThreads * 16);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (at + k * kPagesThreads * 16 < page_bytes)
+        *reinterpret_cast<u32x4*>(to + at + k * kPagesThreads * 16) = v[k];
+  }
+}
+
+int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
+
+PagesParams params(const PagesArgs& a) {
+  PagesParams p{};
+  p.pool = a.pool;
+  p.planes = a.planes;
+  p.page_bytes = a.page_bytes;
+  p.n_pages = (int32_t)a.n_pages;
+  p.page_size = (int32_t)a.page_size;
+  p.rows_in = (int32_t)a.rows_in;
+  p.rows = (int32_t)a.rows;
+  p.width = (int32_t)a.width;
+  p.table = a.table;
+  p.lens = a.lens;
+  p.parent = a.parent;
+  p.add = a.add;
+  p.table_out = a.table_out;
+  p.lens_out = a.lens_out;
+  p.refs = a.refs;
+  p.result = a.result;
+  unsigned char* w = static_cast<unsigned char*>(a.workspace);
+  auto take = [&](int64_t count) {
+    unsigned char* q = w;
+    w += up16(4 * count);
+    return q;
+  };
+  p.bits = reinterpret_cast<uint32_t*>(take((a.n_pages + 31) / 32));
+  p.need = reinterpret_cast<int32_t*>(take(a.rows));
+  p.last = reinterpret_cast<int32_t*>(take(a.rows));
+  p.src = reinterpret_cast<int32_t*>(take(a.n_pages));
+  p.dst = reinterpret_cast<int32_t*>(take(a.n_pages));
+  p.map = reinterpret_cast<int32_t*>(take(a.n_pages));
+  p.pairs = reinterpret_cast<int32_t*>(take(1));
+  return p;
+}
+
+void clear(const PagesParams& p, hipStream_t s) {
+  const int64_t blocks = (p.n_pages + kPagesThreads - 1) / kPagesThreads;
+  hipLaunchKernelGGL(pages_clear_kernel, dim3((uint32_t)(blocks < 1024 ? blocks : 1024)),
+                     dim3(kPagesThreads), 0, s, p);
+}
+
+// `most`: an upper bound on the pairs.
+hipError_t copy(unsigned char* pool, int64_t planes, int64_t n_pages, int64_t page_bytes,
+                const int32_t* src, const int32_t* dst, const int32_t* count, int64_t most,
+                hipStream_t s) {
+  const int64_t pieces = (page_bytes + kCopyBytes - 1) / kCopyBytes;
+  const int64_t grid = 8 * device_cus();
+  if (most == 0 || planes == 0) return hipSuccess;
+  const int64_t items = most > grid ? grid : most * planes * pieces;  // no overflow: see limits
+  hipLaunchKernelGGL(pages_copy_kernel, dim3((uint32_t)(items < grid ? items : grid)),
+                     dim3(kPagesThreads), 0, s, pool, planes, (int32_t)n_pages, page_bytes, src, dst,
+                     count, most);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t pages_workspace_bytes(int64_t rows, int64_t n_pages) {
+  return up16(4 * ((n_pages + 31) / 32)) + 2 * up16(4 * rows) + 3 * up16(4 * n_pages) + 16;
+}
+
+hipError_t launch_pages_fork(const PagesArgs& a, hipStream_t s) {
+  const PagesParams p = params(a);
+  clear(p, s);
+  if (p.rows > 0)
+    hipLaunchKernelGGL(pages_rows_kernel<kFork>, dim3(p.rows), dim3(kPagesThreads), 0, s, p);
+  hipLaunchKernelGGL(pages_fork_assign_kernel, dim3(1), dim3(kScanThreads), 0, s, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return copy(p.pool, p.planes, p.n_pages, p.page_bytes, p.src, p.dst, p.pairs,
+              a.rows < a.n_pages ? a.rows : a.n_pages, s);
+}
+
+hipError_t launch_pages_grow(const PagesArgs& a, hipStream_t s) {
+  const PagesParams p = params(a);
+  clear(p, s);
+  if (p.rows > 0)
+    hipLaunchKernelGGL(pages_rows_kernel<kGrow>, dim3(p.rows), dim3(kPagesThreads), 0, s, p);
+  hipLaunchKernelGGL(pages_grow_assign_kernel, dim3(1), dim3(kScanThreads), 0, s, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_pages_compact(const PagesArgs& a, hipStream_t s) {
+  const PagesParams p = params(a);
+  clear(p, s);
+  if (p.rows > 0)
+    hipLaunchKernelGGL(pages_rows_kernel<kCompact>, dim3(p.rows), dim3(kPagesThreads), 0, s, p);
+  hipLaunchKernelGGL(pages_compact_assign_kernel, dim3(1), dim3(kScanThreads), 0, s, p);
+  if (p.rows > 0)
+    hipLaunchKernelGGL(pages_retable_kernel, dim3(p.rows), dim3(kPagesThreads), 0, s, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return copy(p.pool, p.planes, p.n_pages, p.page_bytes, p.src, p.dst, p.pairs,
+              a.n_pages / 2 + 1, s);
+}
+
+hipError_t launch_pages_copy(unsigned char* pool, int64_t planes, int64_t n_pages,
+                             int64_t page_bytes, const int32_t* src, const int32_t* dst, int64_t n,
+                             hipStream_t s) {
+  return copy(pool, planes, n_pages, page_bytes, src, dst, nullptr, n, s);
+}
+
+}  // namespace tq

@@ -344,6 +344,181 @@ int tq_gemm_tq1_tile(const void* X, const void* qs, int64_t ldq, const void* sca
                      int64_t M, int64_t N, int64_t K, int mt, int nr, int ng, int kg,
                      void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Between the products of a decoder layer: rotary positions, attention of one
+ * new token over a paged key-value cache, and the pages of that cache.  The
+ * architecture section of the project page names rotary positions (base 5e5)
+ * and LLaMA-style attention; the operators are the standard ones, stated below.
+ *
+ * Types: fp16, bfloat16 and, for tq_rope, fp32 (tq_dtype).  Strides are in
+ * elements.  Device entry points enqueue on `stream` and return; they never
+ * allocate, synchronize or use memory that is not an argument, and can be
+ * captured in a HIP graph.
+ *
+ * A paged cache.  Keys and values live in pages of page_size tokens; number
+ * d of head h of slot i of page p is at
+ *   pages[p * page_stride + i * row_stride + h * head_stride + d].
+ * A page table int32 [rows][width] names, for every sequence, the pages of its
+ * tokens in order: token t is in slot t % page_size of page
+ * table[row][t / page_size].  A sequence of len tokens holds the first
+ * ceil(len / page_size) entries of its row; entries past them are not read.
+ * ------------------------------------------------------------------------- */
+
+typedef enum { TQ_F16 = 0, TQ_BF16 = 1, TQ_F32 = 2 } tq_dtype;
+
+/* How the rotation frequencies f_i = theta^(-2 i / rot), i < rot / 2, are
+ * changed for contexts `factor` times longer than the trained one. */
+typedef enum {
+  TQ_ROPE_NONE = 0,   /* not at all                                             */
+  TQ_ROPE_LINEAR = 1, /* f_i / factor: positions interpolated                   */
+  TQ_ROPE_BASE = 2,   /* theta * factor^(rot / (rot - 2)): the base raised      */
+  TQ_ROPE_PARTS = 3   /* f_i k_i + f_i / factor (1 - k_i), k_i = (r_i - slow) / */
+                      /* (fast - slow) clipped to [0, 1], r_i = trained f_i /   */
+                      /* (2 pi) the turns pair i makes in the trained context   */
+} tq_rope_scaling;
+
+/* Host function: the table [n_pos][rot / 2][2] of (cos, sin) of p f_i for
+ * positions p < n_pos, both times `gain`, computed in fp64 and rounded once to
+ * fp32.  factor is ignored for TQ_ROPE_NONE; trained, fast and slow are used by
+ * TQ_ROPE_PARTS only.  Errors: TQ_ERR_NULL; TQ_ERR_SHAPE (n_pos outside
+ * [0, 2^30], rot odd or outside [2, 2^16], rot = 2 with TQ_ROPE_BASE);
+ * TQ_ERR_VALUE (unknown scaling; theta, factor, gain, trained not finite and
+ * positive; fast <= slow). */
+int tq_rope_table(int64_t n_pos, int64_t rot, double theta, int scaling, double factor,
+                  double trained, double fast, double slow, double gain, float* table);
+
+/* Rotary positions.  The first rot numbers of every head of X [T][H][D] are
+ * rot / 2 pairs -- (x_i, x_{i + rot/2}), or (x_{2i}, x_{2i+1}) with interleaved
+ * -- and pair i of token t is turned by the angle that row pos[t] of `table`
+ * holds:
+ *   y_a = x_a cos - x_b sin,   y_b = x_b cos + x_a sin;
+ * numbers rot .. D - 1 are copied.  inverse = 1 turns back by the same angles:
+ * with the same table this is the gradient dX of dY (the rotation's transpose,
+ * table gain included).  Computed in fp32, rounded once to X's type.
+ * X and Y: device pointers, number d of head h of token t at
+ * x_tok t + x_head h + d; heads and tokens may lie in any order and X may
+ * repeat (stride 0), but no two elements of Y may share an address
+ * (TQ_ERR_SHAPE).  Y = X with equal strides is allowed, any other overlap not.
+ * pos int32 [T], device; a token whose position is outside [0, n_pos) comes
+ * out as zeros.  table: fp32 [n_pos][rot / 2][2], device, 8-byte aligned (NULL
+ * when n_pos = 0).
+ * T = 0 or H = 0 is a no-op.  D <= 2^16, rot even, 2 <= rot <= D, H <= 2^16,
+ * T <= 2^30.  Errors: TQ_ERR_NULL, TQ_ERR_SHAPE, TQ_ERR_ALIGN (X or Y not
+ * aligned to an element), TQ_ERR_VALUE (dtype, interleaved, inverse). */
+int tq_rope(int dtype, const void* X, int64_t x_tok, int64_t x_head, void* Y, int64_t y_tok,
+            int64_t y_head, const float* table, int64_t n_pos, int64_t rot, const int32_t* pos,
+            int64_t T, int64_t H, int64_t D, int interleaved, int inverse, void* stream);
+
+/* The decode step's use of tq_rope in one launch: QKV holds, for each of T
+ * tokens, Hq query, Hkv key and Hkv value heads of D numbers (the row of a
+ * fused q/k/v product), token t at QKV + qkv_tok t.  Turned queries are written
+ * to Q [T][Hq][D]; turned keys and the values go to the slot of position pos[t]
+ * in the paged cache (as above), in the row seqs[t] of the page table, or row t
+ * when seqs is NULL.  fp16 or bfloat16.
+ * A token whose position is outside [0, n_pos) gets zeros in Q, and nothing of
+ * it is written to the cache; nor is it where the row is outside
+ * [0, n_seqs), the position is past the table's width, or the page is outside
+ * [0, n_pages).  Two tokens of one call must not name the same slot.
+ * Errors as tq_rope's, and TQ_ERR_SHAPE for page geometry (page_size < 1,
+ * negative strides, width * page_size > 2^30). */
+int tq_rope_append(int dtype, const void* QKV, int64_t qkv_tok, const float* table, int64_t n_pos,
+                   int64_t rot, const int32_t* pos, const int32_t* seqs, const int32_t* page_table,
+                   int64_t n_seqs, int64_t width, void* k_pages, void* v_pages, int64_t n_pages,
+                   int64_t page_size, int64_t page_stride, int64_t row_stride,
+                   int64_t head_stride, void* Q, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                   int interleaved, void* stream);
+
+/* Attention of one new token per sequence over the paged cache:
+ *   out[b][h] = sum_t w_t v[t][h / G],  w = softmax_t(scale q[b][h] . k[t][h / G])
+ * over the tokens t in [max(0, len - window), len) of sequence b (window = 0:
+ * all), G = Hq / Hkv.  Q: number d of head h of sequence b at q_tok b +
+ * q_head h + d; Out [B][Hq][D]; lse fp32 [B][Hq] or NULL: ln of the sum of the
+ * exponentials, for joining with other parts of the same softmax.  lens int32
+ * [B]: negative counts as 0, and at most width * page_size tokens are read.
+ * A sequence with no token gives zeros and lse = -inf.  A page outside
+ * [0, n_pages) counts as absent: its tokens are left out.  What the cache holds
+ * in other slots, NaN included, has no influence.
+ * fp16 or bfloat16 in and out, fp32 scores, weights and sums.  The same bits on
+ * every run.
+ * D a multiple of 8, 8 <= D <= 256; Hq a multiple of Hkv, Hq <= 2^12; B <=
+ * 2^20; width * page_size <= 2^30; strides multiples of 8, row_stride <= 2^24;
+ * pointers 16-byte aligned.  workspace: tq_paged_attention_workspace(...)
+ * bytes, 16-byte aligned, contents irrelevant; calls that overlap on one
+ * workspace race.
+ * Errors: TQ_ERR_NULL, TQ_ERR_SHAPE (a workspace that is too small included),
+ * TQ_ERR_ALIGN, TQ_ERR_VALUE (dtype, scale not finite, window < 0),
+ * TQ_ERR_DEVICE.  B = 0 is a no-op. */
+int tq_paged_attention(int dtype, const void* Q, int64_t q_tok, int64_t q_head,
+                       const void* k_pages, const void* v_pages, int64_t n_pages,
+                       int64_t page_size, int64_t page_stride, int64_t row_stride,
+                       int64_t head_stride, const int32_t* page_table, int64_t width,
+                       const int32_t* lens, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                       double scale, int64_t window, void* Out, float* lse, void* workspace,
+                       int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of tq_paged_attention for tables of `width` pages;
+ * TQ_ERR_SHAPE for shapes it refuses. */
+int64_t tq_paged_attention_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                                     int64_t page_size, int64_t width);
+
+/* The pages of a cache.  The page table and the lengths are the whole state: a
+ * page is free when no row holds it, and a page held by several rows is shared.
+ * The functions read one state and write another, so a step can be repeated and
+ * captured; outputs must not overlap inputs.  Tables are int32 [rows][width],
+ * lengths int32 [rows] (negative counts as 0; at most width * page_size tokens
+ * are looked at).  Output rows are written whole, -1 past the held entries.
+ * The pool holds `planes` planes (the keys and the values of every layer, say)
+ * of n_pages pages of page_bytes contiguous bytes each; a page's copy is made
+ * in every plane.  page_bytes a multiple of 16, pool 16-byte aligned.
+ * Entries outside [0, n_pages) name no page: they are kept and never followed.
+ * workspace: tq_pages_workspace(rows, n_pages) bytes, 16-byte aligned.
+ * Limits: rows <= 2^16, width * page_size <= 2^30, n_pages <= 2^24, planes <=
+ * 2^16, page_bytes <= 2^30.  Free pages are taken in ascending order for rows
+ * in ascending order, so results do not depend on timing. */
+
+/* Forking: row r of the output continues input row parent[r] (no row, an empty
+ * sequence, when parent[r] is outside [0, rows_in)).  Pages are shared, except
+ * the last one where it is partly filled: the first row that continues a parent
+ * keeps it, every further row gets a free page and a copy.  Input rows that no
+ * output row continues release their pages, also for these copies.
+ * refs int32 [n_pages] or NULL: how many output entries hold each page.
+ * short_out int32 [1]: rows for which no free page was left; such a row is cut
+ * to its full pages.  This is also how sequences are freed (parent = -1). */
+int tq_pages_fork(void* pool, int64_t planes, int64_t n_pages, int64_t page_bytes,
+                  const int32_t* table, const int32_t* lens, int64_t rows_in,
+                  const int32_t* parent, int64_t rows, int64_t width, int64_t page_size,
+                  int32_t* table_out, int32_t* lens_out, int32_t* refs, int32_t* short_out,
+                  void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Growing: row r gets add[r] more tokens (negative counts as 0), with free
+ * pages for those that its last page cannot hold; nothing is copied.  Where the
+ * table's width does not suffice, or the row and those before it need more pages
+ * together than are free, the row keeps its length and pages, and short_out
+ * int32 [1] counts such rows. */
+int tq_pages_grow(const int32_t* table, const int32_t* lens, const int32_t* add, int64_t rows,
+                  int64_t width, int64_t page_size, int64_t n_pages, int32_t* table_out,
+                  int32_t* lens_out, int32_t* short_out, void* workspace,
+                  int64_t workspace_bytes, void* stream);
+
+/* Compacting: with n pages in use, the i-th used page at or above n (in
+ * ascending order) moves to the i-th free page below n and the tables follow,
+ * so that pages 0 .. n - 1 are used and the rest of the pool can be given back.
+ * used_out int32 [1]: n.  Lengths do not change. */
+int tq_pages_compact(void* pool, int64_t planes, int64_t n_pages, int64_t page_bytes,
+                     const int32_t* table, const int32_t* lens, int64_t rows, int64_t width,
+                     int64_t page_size, int32_t* table_out, int32_t* used_out, void* workspace,
+                     int64_t workspace_bytes, void* stream);
+
+/* Copying: page src[i] over page dst[i] in every plane, i < n; pairs with
+ * either outside [0, n_pages) are left out.  src, dst int32 [n], device.  A
+ * page must not be a destination twice, nor both a source and a destination. */
+int tq_pages_copy(void* pool, int64_t planes, int64_t n_pages, int64_t page_bytes,
+                  const int32_t* src, const int32_t* dst, int64_t n, void* stream);
+
+/* Workspace bytes of fork, grow and compact; TQ_ERR_SHAPE for sizes that they
+ * refuse. */
+int64_t tq_pages_workspace(int64_t rows, int64_t n_pages);
+
 #ifdef __cplusplus
 }
 #endif

@@ -25,3 +25,11 @@ from .tq_oracle import (  # noqa: F401
     gemm_bwd_x_ref,
     ste_grad_w_ref,
 )
+from .decode_oracle import (  # noqa: F401,E402
+    rope_frequencies_ref,
+    rope_ref,
+    paged_attention_ref,
+    pages_fork_ref,
+    pages_grow_ref,
+    pages_compact_ref,
+)
