@@ -39,6 +39,8 @@
 // and join through LDS; a (sequence, head) that spans workgroups leaves partial
 // sums in the workspace for the joining kernel.
 
+#include <atomic>
+
 #include "tq.h"
 #include "tq_common.h"
 #include "tq_decode.h"
@@ -73,12 +75,18 @@ struct AttnParams {
   const int32_t* lens;
   unsigned char* Out;
   float* lse;
-  float* partial;  // [2 * workgroups][kHeads * D + 2 * kHeads]
+  float* partial;  // [workgroups][2][slot_floats]
+  int2* owner;     // [workgroups]: the row it began and left unfinished (or -1), its last workgroup
   FastDiv page;
   int32_t n_pages, width, B, Hq, Hkv, D, G, qtiles, window;
   int32_t direct;  // one workgroup per (sequence, head): nothing is split
   float scale;
 };
+
+// Floats of one partial sum: heads x D numbers, maxima, sums.
+__host__ __device__ __forceinline__ int64_t slot_floats(int heads, int D) {
+  return heads * D + (2 * heads + 3) / 4 * 4;
+}
 
 template <bool BF>
 __device__ __forceinline__ float4v mma(u32x4 a, u32x4 b, float4v c) {
@@ -149,61 +157,82 @@ __device__ __forceinline__ float sum_over_groups(float v) {
   return v + __shfl_xor(v, 32, kWave);
 }
 
-// Tokens [lo, hi) of sequence b, clamped to what its table row can name.
+// A value that every lane holds, as the scalar it is.
+__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Reads of what no kernel of a call writes, through the scalar cache where the
+// index is uniform.
+typedef const __attribute__((address_space(4))) int32_t* const_i32;
+__device__ __forceinline__ int32_t read_const(const int32_t* p, int64_t i) {
+  return ((const_i32)(uint64_t)p)[i];
+}
+
+// Tokens [lo, hi) of sequence b, clamped to what its table row can name, and
+// the tiles [t0, t1) that hold them.
 struct Range {
-  int lo, hi;
+  int lo, hi, t0, t1;
 };
 __device__ __forceinline__ Range range_of(const AttnParams& p, int b) {
-  const int64_t cap = (int64_t)p.width * p.page.d;
-  int n = p.lens[b];
-  n = n < 0 ? 0 : n;
-  const int hi = n < cap ? n : (int)cap;
-  const int lo = p.window > 0 && n > p.window ? n - p.window : 0;
-  return {lo < hi ? lo : hi, hi};
-}
-__device__ __forceinline__ int tiles_of(Range r) {
-  return r.hi > r.lo ? (r.hi + kTileTokens - 1) / kTileTokens - r.lo / kTileTokens : 0;
+  const int cap = p.width * (int)p.page.d;
+  const int len = read_const(p.lens, b);
+  const int n = len < 0 ? 0 : len;
+  const int hi = n < cap ? n : cap;
+  const int from = p.window > 0 && n > p.window ? n - p.window : 0;
+  const int lo = from < hi ? from : hi;
+  const int t0 = lo / kTileTokens;
+  return {lo, hi, t0, lo < hi ? (hi + kTileTokens - 1) / kTileTokens : t0};
 }
 
-// How the flattened tiles are cut: `total` tiles over `parts` workgroups, part
-// w taking [w total / parts, (w + 1) total / parts).  A part has at least four
-// tiles, one for each wave.
+// The flattened list of `units` tiles (sequence, then head, then tile) cut into
+// `parts` runs of q or, the first r of them, q + 1 tiles: one for each wave.
 struct Cut {
-  int64_t total;
-  int64_t parts;
-  __device__ __forceinline__ int64_t start(int64_t w) const { return w * total / parts; }
-};
-__device__ __forceinline__ Cut cut_of(int64_t total, int64_t grid) {
-  const int64_t most = (total + kAttnWaves - 1) / kAttnWaves;
-  return {total, most < grid ? most : grid};
-}
-
-// Sum of tiles over all sequences and over those before this thread's; thread
-// i looks after the sequences [i * per, (i + 1) * per).
-__device__ __forceinline__ int64_t scan_tiles(const AttnParams& p, int per, int64_t* red,
-                                              int64_t& total) {
-  const int t = threadIdx.x;
-  int64_t mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int b = t * per + i;
-    if (b < p.B) mine += tiles_of(range_of(p, b));
+  uint32_t units, parts, q, r;
+  __device__ __forceinline__ Cut(uint32_t n, uint32_t most) {
+    units = n;
+    parts = n < most ? n : most;
+    q = parts ? n / parts : 0;
+    r = n - parts * q;
   }
-  int64_t inc = mine;
+  __device__ __forceinline__ uint32_t start(uint32_t i) const { return i * q + (i < r ? i : r); }
+  __device__ __forceinline__ uint32_t part_of(uint32_t unit) const {
+    const uint32_t wide = r * (q + 1);
+    return unit < wide ? unit / (q + 1) : r + (unit - wide) / q;
+  }
+};
+
+// Every wave by itself: the number of tiles of all sequences, and those before
+// this lane's; lane i looks after the sequences [i * per, (i + 1) * per).
+__device__ __forceinline__ uint32_t scan_tiles(const AttnParams& p, int lane, int per,
+                                               uint32_t& mine, uint32_t& total) {
+  mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int b = lane * per + i;
+    if (b < p.B) {
+      const Range r = range_of(p, b);
+      mine += r.t1 - r.t0;
+    }
+  }
+  uint32_t inc = mine;
 #pragma unroll
   for (int off = 1; off < kWave; off <<= 1) {
-    const int64_t o = __shfl_up(inc, off, kWave);
-    if ((t & 63) >= off) inc += o;
+    const uint32_t o = __shfl_up(inc, off, kWave);
+    inc += lane >= off ? o : 0;
   }
-  if ((t & 63) == 63) red[t >> 6] = inc;
-  __syncthreads();
-  int64_t before = inc - mine;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kAttnWaves; ++w) {
-    if (w < (t >> 6)) before += red[w];
-    total += red[w];
-  }
-  return before;
+  total = uni((int)__shfl(inc, 63, kWave));
+  return inc - mine;
+}
+
+// A tile of the flattened list: head h (key-value head and group of 16 query
+// heads) of sequence b, and the tile's place in its row.
+struct Cursor {
+  int b, h, tile;
+  Range r;
+};
+
+// ln of the sum of exponentials, from the base-2 maximum and the scaled sum.
+template <bool BF>
+__device__ __forceinline__ float lse_of(float m, float sum) {
+  return (m + __builtin_amdgcn_logf(sum) - (BF ? 0.f : 14.f)) / kLog2e;
 }
 
 // Divides by the sum and writes numbers d .. d + 7 of one head, and its lse.
@@ -217,272 +246,264 @@ __device__ __forceinline__ void finish(const AttnParams& p, int b, int head, int
     u[e] = to16<BF>(v[2 * e] * inv) | ((uint32_t)to16<BF>(v[2 * e + 1] * inv) << 16);
   const int64_t at = (int64_t)b * p.Hq + head;
   *reinterpret_cast<u32x4*>(p.Out + (at * p.D + d) * 2) = u;
-  if (p.lse && d == 0) p.lse[at] = (m + __builtin_amdgcn_logf(sum) - (BF ? 0.f : 14.f)) / kLog2e;
+  if (p.lse && d == 0) p.lse[at] = lse_of<BF>(m, sum);
 }
 
 // DV: 64, 128 or 256, the head dimension rounded up (D <= DV, D % 8 == 0).
 // UNI: the page size is a multiple of 16, so a half tile lies in one page and
 // its base address is uniform.
 template <bool BF, int DV, bool UNI>
-struct Tile {
-  static constexpr int kSteps = DV / 32;              // MFMA steps of a score
-  static constexpr int kOps = DV / 16;                // V operands (numbers per lane)
-  static constexpr int kVecs = DV == 256 ? 2 : 1;     // 16-byte (8-byte) pieces per token and lane
-  static constexpr int kLane = DV == 64 ? 4 : 8;      // consecutive numbers per piece
-};
-
-template <bool BF, int DV, bool UNI>
 __global__ __launch_bounds__(kAttnThreads, DV == 256 ? 2 : 3) void paged_attention_kernel(
     AttnParams p) {
-  using TT = Tile<BF, DV, UNI>;
-  constexpr int KS = TT::kSteps, NE = TT::kOps, NV = TT::kVecs, LN = TT::kLane;
-  constexpr int PW = LN * 16;   // numbers of one piece: the joining buffer's width
-  constexpr int kRow = PW + 4;  // floats per head, 4 of padding
-  __shared__ __attribute__((aligned(16))) float sO[kAttnWaves * kHeads * kRow];
-  __shared__ float sM[kAttnWaves * kHeads], sL[kAttnWaves * kHeads];
-  __shared__ int64_t sRed[kAttnWaves];
-  __shared__ int64_t sStart;
-  __shared__ int sSeq;
+  constexpr int KS = DV / 32;             // MFMA steps of a score
+  constexpr int NE = DV / 16;             // V operands (numbers per lane)
+  constexpr int NV = DV == 256 ? 2 : 1;   // pieces of a head: LN numbers per lane each
+  constexpr int LN = DV == 64 ? 4 : 8;
+  constexpr int PW = LN * 16;             // numbers of a piece
+  // partial sums of this workgroup's waves: [wave][first, last][heads][D + 4]
+  extern __shared__ __attribute__((aligned(16))) float sO[];
+  __shared__ float sM[2 * kAttnWaves][kHeads], sL[2 * kAttnWaves][kHeads];
+  __shared__ int sRow[2 * kAttnWaves], sEnds[2 * kAttnWaves], sLast[2 * kAttnWaves];
 
   const int tid = threadIdx.x;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = uni(tid >> 6);
   const int lane = tid & 63, li = lane & 15, g = lane >> 4;
   const int H = p.Hkv * p.qtiles;
+  const int slot_heads = p.G < kHeads ? p.G : kHeads;
+  const int row_floats = p.D + 4;
 
-  // rows without tokens: zeros and -inf, spread over the workgroups
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    const Range r = range_of(p, b);
-    if (r.hi > r.lo) continue;
-    uint16_t* o = reinterpret_cast<uint16_t*>(p.Out) + (int64_t)b * p.Hq * p.D;
-    for (int i = tid; i < p.Hq * p.D; i += kAttnThreads) o[i] = 0;
-    if (p.lse)
-      for (int i = tid; i < p.Hq; i += kAttnThreads) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
-  }
-
-  // this workgroup's share [at, end) of the flattened tiles and where it begins
-  int64_t at, end;
-  int b;
-  uint32_t row_units;  // tiles x heads of sequence b
-  uint32_t in_row;     // offset of `at` inside sequence b
+  // this wave's run of tiles
+  uint32_t left, run_end = 0;  // run_end: the unit after the run
+  Cursor cur;
+  Cut cut(0, 1);
   if (p.direct) {
-    b = blockIdx.x / H;
-    const int n = tiles_of(range_of(p, b));
-    at = 0;
-    end = n;
-    in_row = (uint32_t)(blockIdx.x % H) * n;
-    row_units = (uint32_t)n * H;
+    cur.b = blockIdx.x / H;
+    cur.h = blockIdx.x % H;
+    cur.r = range_of(p, cur.b);
+    const int n = cur.r.t1 - cur.r.t0;
+    cur.tile = cur.r.t0 + n * wave / kAttnWaves;
+    left = cur.r.t0 + n * (wave + 1) / kAttnWaves - cur.tile;
   } else {
-    const int per = (p.B + kAttnThreads - 1) / kAttnThreads;
-    int64_t total;
-    int64_t before = scan_tiles(p, per, sRed, total);
-    const Cut c = cut_of(total * H, gridDim.x);
-    if ((int64_t)blockIdx.x >= c.parts) return;
-    at = c.start(blockIdx.x);
-    end = c.start((int64_t)blockIdx.x + 1);
-    // the thread whose sequences hold unit `at` names the sequence
-    for (int i = 0; i < per; ++i) {
-      const int q = tid * per + i;
-      if (q >= p.B) break;
-      const int64_t n = tiles_of(range_of(p, q));
-      if (before * H <= at && at < (before + n) * H) {
-        sSeq = q;
-        sStart = before * H;
+    const int per = (p.B + kWave - 1) / kWave;
+    uint32_t mine, total;
+    const uint32_t before = scan_tiles(p, lane, per, mine, total);
+    cut = Cut(total * H, gridDim.x * kAttnWaves);
+    const uint32_t part = blockIdx.x * kAttnWaves + wave;
+    left = 0;
+    if (part < cut.parts) {
+      const uint32_t at = cut.start(part);
+      run_end = cut.start(part + 1);
+      left = run_end - at;
+      const uint64_t has = __ballot(before * H <= at && at < (before + mine) * H);
+      const int src = __builtin_ctzll(has);
+      uint32_t in_row = at - (uint32_t)__builtin_amdgcn_readlane((int)before, src) * H;
+      cur.b = src * per;
+      cur.r = range_of(p, cur.b);
+      uint32_t n;
+      while (in_row >= (n = (uint32_t)(cur.r.t1 - cur.r.t0)) * H) {
+        in_row -= n * H;
+        cur.r = range_of(p, ++cur.b);
       }
-      before += n;
+      cur.h = in_row / n;
+      cur.tile = cur.r.t0 + in_row % n;
     }
-    __syncthreads();
-    b = __builtin_amdgcn_readfirstlane(sSeq);
-    in_row = __builtin_amdgcn_readfirstlane((int)(at - sStart));
-    row_units = (uint32_t)tiles_of(range_of(p, b)) * H;
   }
-  const int64_t first_unit = at;
+  if (lane < 2) sRow[2 * wave + lane] = -1;
 
-  while (at < end) {
-    if (in_row >= row_units) {  // next sequence that has tiles
-      in_row = 0;
-      do {
-        ++b;
-        row_units = (uint32_t)tiles_of(range_of(p, b)) * H;
-      } while (row_units == 0);
+  auto advance = [&](Cursor& c) {  // only where another tile follows
+    if (++c.tile < c.r.t1) return;
+    if (++c.h == H) {
+      c.h = 0;
+      do c.r = range_of(p, ++c.b);
+      while (c.r.t1 == c.r.t0);
     }
-    const Range rg = range_of(p, b);
-    const int n = tiles_of(rg);
-    const int h = (int)(in_row / (uint32_t)n);
-    const int t_first = (int)(in_row % (uint32_t)n);
-    const int64_t left = end - at;
-    const int t_last = (int)(t_first + left < n ? t_first + left : n);  // past the last tile
-    const int hk = h / p.qtiles, qt = h % p.qtiles;
-    const int heads = p.G - qt * kHeads < kHeads ? p.G - qt * kHeads : kHeads;
-    const int hq0 = hk * p.G + qt * kHeads;
+    c.tile = c.r.t0;
+  };
 
-    // Q as the B operand: lane li holds head hq0 + li
-    u32x4 q[KS];
-    {
-      const unsigned char* qp = p.Q + b * p.q_tok + (int64_t)(hq0 + li) * p.q_head;
+  u32x4 kreg[2][KS];
+  u32x4 vreg[8][NV];  // DV == 64 uses the first two dwords of each
+  const uint32_t rs = (uint32_t)p.row_stride;
+  // byte offsets of this lane's pieces in a half tile, out of range past the head's end
+  const uint32_t koff = li * rs + g * 16;
+  uint32_t voff[4];
 #pragma unroll
-      for (int c = 0; c < KS; ++c) {
-        q[c] = u32x4{0, 0, 0, 0};
-        if (li < heads && c * 32 + g * 8 < p.D)
-          q[c] = *reinterpret_cast<const u32x4*>(qp + (c * 32 + g * 8) * 2);
+  for (int j = 0; j < 4; ++j) voff[j] = li * LN < p.D ? (g * 4 + j) * rs + li * (LN * 2) : kOut;
+  const bool kpart = g * 8 < p.D % 32;  // the step that holds the head's end
+
+  // where a tile's tokens lie
+  struct Place {
+    int id[2];         // UNI: the pages of its halves, -1 if absent
+    int64_t off;       // else: byte offset of token lane % 32, -1 if masked
+  };
+  auto place_of = [&](const Cursor& c) {
+    Place w;
+    const int64_t row = (int64_t)c.b * p.width;
+    const int t = c.tile * kTileTokens;
+    if constexpr (UNI) {
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        const int ta = t + 16 * a;
+        const int id = read_const(p.table, row + (int)div_page(p.page, ta < c.r.hi ? ta : t));
+        w.id[a] = (uint32_t)id < (uint32_t)p.n_pages ? id : -1;
+      }
+      w.off = 0;
+    } else {
+      const int tl = t + (lane & 31);
+      const bool in = (uint32_t)(tl - c.r.lo) < (uint32_t)(c.r.hi - c.r.lo);
+      const uint32_t pg = div_page(p.page, in ? tl : c.r.lo);
+      const int id = p.table[row + pg];
+      const bool ok = in & ((uint32_t)id < (uint32_t)p.n_pages);
+      w.off = ok ? id * p.page_stride + (int64_t)(tl - (int)(pg * p.page.d)) * p.row_stride : -1;
+      w.id[0] = w.id[1] = 0;
+    }
+    return w;
+  };
+  // tokens of half a that are present: [lo, lo + span) of the sequence
+  auto span_of = [&](const Cursor& c, const Place& w, int a) {
+    return !UNI || w.id[a] >= 0 ? (uint32_t)(c.r.hi - c.r.lo) : 0u;
+  };
+  auto base_of = [&](const unsigned char* pool, const Cursor& c, const Place& w, int a) {
+    const int ta = c.tile * kTileTokens + 16 * a;
+    const int slot = ta - (int)(div_page(p.page, ta) * p.page.d);
+    const int id = w.id[a] < 0 ? 0 : w.id[a];
+    return rsrc_at(pool + (c.h / p.qtiles) * p.head_stride + id * p.page_stride +
+                   slot * p.row_stride);
+  };
+  auto shfl64 = [&](int64_t v, int src) {
+    const int lo = __shfl((int)v, src, kWave), hi = __shfl((int)(v >> 32), src, kWave);
+    return ((int64_t)hi << 32) | (uint32_t)lo;
+  };
+  auto load_k = [&](const Cursor& c, const Place& w) {
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      if constexpr (UNI) {
+        const auto r = base_of(p.K, c, w, a);
+        const int t = c.tile * kTileTokens + 16 * a + li;
+        const uint32_t off = (uint32_t)(t - c.r.lo) < span_of(c, w, a) ? koff : kOut;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          const bool in = i * 32 + 32 <= p.D || (i * 32 < p.D && kpart);
+          kreg[a][i] = load16(r, in ? off + i * 64 : kOut);
+        }
+      } else {
+        const int64_t o = shfl64(w.off, 16 * a + li);
+        const unsigned char* k = p.K + (c.h / p.qtiles) * p.head_stride + o;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          kreg[a][i] = u32x4{0, 0, 0, 0};
+          if (o >= 0 && i * 32 + g * 8 < p.D)
+            kreg[a][i] = *reinterpret_cast<const u32x4*>(k + i * 64 + g * 16);
+        }
       }
     }
+  };
+  auto load_v = [&](const Cursor& c, const Place& w) {
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      if constexpr (UNI) {
+        const auto r = base_of(p.V, c, w, a);
+        const int t = c.tile * kTileTokens + 16 * a + g * 4;
+        const uint32_t span = span_of(c, w, a);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t off = (uint32_t)(t + j - c.r.lo) < span ? voff[j] : kOut;
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            const uint32_t o = i == 0 || i * PW + li * LN < p.D ? off + i * PW * 2 : kOut;
+            if constexpr (LN == 8) {
+              vreg[4 * a + j][i] = load16(r, o);
+            } else {
+              const u32x2 x = load8(r, o);
+              vreg[4 * a + j][i] = u32x4{x[0], x[1], 0, 0};
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int64_t o = shfl64(w.off, 16 * a + g * 4 + j);
+          const unsigned char* v = p.V + (c.h / p.qtiles) * p.head_stride + o + li * (LN * 2);
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            vreg[4 * a + j][i] = u32x4{0, 0, 0, 0};
+            if (o >= 0 && i * PW + li * LN < p.D) {
+              if constexpr (LN == 8) {
+                vreg[4 * a + j][i] = *reinterpret_cast<const u32x4*>(v + i * PW * 2);
+              } else {
+                const u32x2 x = *reinterpret_cast<const u32x2*>(v);
+                vreg[4 * a + j][i] = u32x4{x[0], x[1], 0, 0};
+              }
+            }
+          }
+        }
+      }
+    }
+  };
 
-    float4v acc[NE];
+  u32x4 q[KS];
+  float4v acc[NE];
+  float m = -INFINITY, l = 0.f;
+  int heads = 0, hq0 = 0;
+  auto open_row = [&](const Cursor& c) {
+    const int hk = c.h / p.qtiles, qt = c.h - hk * p.qtiles;
+    heads = p.G - qt * kHeads < kHeads ? p.G - qt * kHeads : kHeads;
+    hq0 = hk * p.G + qt * kHeads;
+    // Q as the B operand: lane li holds head hq0 + li
+    const unsigned char* qp = p.Q + c.b * p.q_tok + (int64_t)(hq0 + li) * p.q_head;
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      q[i] = u32x4{0, 0, 0, 0};
+      if (li < heads && i * 32 + g * 8 < p.D)
+        q[i] = *reinterpret_cast<const u32x4*>(qp + (i * 32 + g * 8) * 2);
+    }
 #pragma unroll
     for (int e = 0; e < NE; ++e) acc[e] = float4v{0, 0, 0, 0};
-    float m = -INFINITY, l = 0.f;
+    m = -INFINITY;
+    l = 0.f;
+  };
 
-    const unsigned char* kh = p.K + hk * p.head_stride;
-    const unsigned char* vh = p.V + hk * p.head_stride;
-    const int32_t* row = p.table + (int64_t)b * p.width;
-    const int tile0 = rg.lo / kTileTokens;
-    const uint32_t rs = (uint32_t)p.row_stride;
-
-    u32x4 kreg[2][KS];
-    u32x4 vreg[8][NV];  // DV == 64 uses the first two dwords of each
-
-    // page of the half tile at token t, or -1
-    auto page_of = [&](int t) -> int {
-      if (t >= rg.hi) return -1;
-      const int id = row[div_page(p.page, (uint32_t)t)];
-      return (uint32_t)id < (uint32_t)p.n_pages ? id : -1;
-    };
-    auto in_range = [&](int t) { return t >= rg.lo && t < rg.hi; };
-
-    // byte offset of token t (per lane; pages that end inside a half tile), -1 if masked
-    auto token_at = [&](int t) -> int64_t {
-      if (!in_range(t)) return -1;
-      const uint32_t pg = div_page(p.page, (uint32_t)t);
-      const int id = row[pg];
-      if ((uint32_t)id >= (uint32_t)p.n_pages) return -1;
-      return id * p.page_stride + (int64_t)(t - (int)(pg * p.page.d)) * p.row_stride;
-    };
-
-    int id_next[2];  // pages of the tile whose loads come next (UNI)
-    auto fetch_ids = [&](int tile) {
-      if constexpr (UNI) {
-        const int t0 = (tile0 + tile) * kTileTokens;
-        id_next[0] = __builtin_amdgcn_readfirstlane(page_of(t0));
-        id_next[1] = __builtin_amdgcn_readfirstlane(page_of(t0 + 16));
-      }
-    };
-    int id_k[2], id_v[2];
-    auto load_k = [&](int tile) {
-      const int t0 = (tile0 + tile) * kTileTokens;
-#pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        const int t = t0 + 16 * a + li;
-        if constexpr (UNI) {
-          const int id = id_next[a];
-          id_k[a] = id;
-          const int ta = t0 + 16 * a;
-          const int in_page = ta - (int)(div_page(p.page, (uint32_t)ta) * p.page.d);
-          const auto r = rsrc_at(kh + (id < 0 ? 0 : id) * p.page_stride + in_page * p.row_stride);
-          const bool ok = id >= 0 && in_range(t);
-          const uint32_t off = ok ? li * rs + g * 16 : kOut;
-#pragma unroll
-          for (int c = 0; c < KS; ++c)
-            kreg[a][c] = load16(r, c * 32 + g * 8 < p.D ? off + c * 64 : kOut);
-        } else {
-          const int64_t o = token_at(t);
-#pragma unroll
-          for (int c = 0; c < KS; ++c) {
-            kreg[a][c] = u32x4{0, 0, 0, 0};
-            if (o >= 0 && c * 32 + g * 8 < p.D)
-              kreg[a][c] = *reinterpret_cast<const u32x4*>(kh + o + c * 64 + g * 16);
-          }
-        }
-      }
-    };
-    auto load_v = [&](int tile) {
-      const int t0 = (tile0 + tile) * kTileTokens;
-#pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        if constexpr (UNI) {
-          const int id = id_v[a];
-          const int ta = t0 + 16 * a;
-          const int in_page = ta - (int)(div_page(p.page, (uint32_t)ta) * p.page.d);
-          const auto r = rsrc_at(vh + (id < 0 ? 0 : id) * p.page_stride + in_page * p.row_stride);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const bool ok = id >= 0 && in_range(ta + g * 4 + j);
-            const uint32_t off = ok ? (g * 4 + j) * rs + li * (LN * 2) : kOut;
-#pragma unroll
-            for (int c = 0; c < NV; ++c) {
-              const uint32_t o = c * 128 + li * LN < p.D ? off + c * 256 : kOut;
-              if constexpr (LN == 8) {
-                vreg[4 * a + j][c] = load16(r, o);
-              } else {
-                const u32x2 x = load8(r, o);
-                vreg[4 * a + j][c] = u32x4{x[0], x[1], 0, 0};
-              }
-            }
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int64_t o = token_at(t0 + 16 * a + g * 4 + j);
-#pragma unroll
-            for (int c = 0; c < NV; ++c) {
-              vreg[4 * a + j][c] = u32x4{0, 0, 0, 0};
-              if (o >= 0 && c * 128 + li * LN < p.D) {
-                const unsigned char* src = vh + o + c * 256 + li * (LN * 2);
-                if constexpr (LN == 8) {
-                  vreg[4 * a + j][c] = *reinterpret_cast<const u32x4*>(src);
-                } else {
-                  const u32x2 x = *reinterpret_cast<const u32x2*>(src);
-                  vreg[4 * a + j][c] = u32x4{x[0], x[1], 0, 0};
-                }
-              }
-            }
-          }
-        }
-      }
-    };
-
-    int tile = t_first + wave;
-    if (tile < t_last) {
-      fetch_ids(tile);
-      load_k(tile);
-      id_v[0] = id_k[0];
-      id_v[1] = id_k[1];
-      load_v(tile);
-      if (tile + kAttnWaves < t_last) fetch_ids(tile + kAttnWaves);
+  if (left > 0) {
+    Place w_cur, w_next;
+    Cursor next = cur;
+    int first_tile = cur.tile;
+    bool first_row = true;
+    w_cur = place_of(cur);
+    load_k(cur, w_cur);
+    load_v(cur, w_cur);
+    if (left > 1) {
+      advance(next);
+      w_next = place_of(next);
     }
-    for (; tile < t_last; tile += kAttnWaves) {
-      const bool more = tile + kAttnWaves < t_last;
-      const int t0 = (tile0 + tile) * kTileTokens;
+    open_row(cur);
+    while (true) {
+      const bool more = left > 1;
       float4v s[2];
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
         s[a] = float4v{0, 0, 0, 0};
 #pragma unroll
-        for (int c = 0; c < KS; ++c) s[a] = mma<BF>(kreg[a][c], q[c], s[a]);
+        for (int i = 0; i < KS; ++i) s[a] = mma<BF>(kreg[a][i], q[i], s[a]);
       }
-      // masked tokens, by the page that the loads used
-      bool page_ok[2] = {true, true};
-      if constexpr (UNI) {
-        page_ok[0] = id_k[0] >= 0;
-        page_ok[1] = id_k[1] >= 0;
-      }
-      if (more) load_k(tile + kAttnWaves);
+      if (more) load_k(next, w_next);
 
       float x[8];
       float mt = -INFINITY;
 #pragma unroll
-      for (int a = 0; a < 2; ++a)
+      for (int a = 0; a < 2; ++a) {
+        const int t = cur.tile * kTileTokens + 16 * a + g * 4;
+        const uint32_t span = span_of(cur, w_cur, a);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int t = t0 + 16 * a + g * 4 + j;
           bool ok;
           if constexpr (UNI)
-            ok = page_ok[a] && in_range(t);
+            ok = (uint32_t)(t + j - cur.r.lo) < span;
           else
-            ok = token_at(t) >= 0;
+            ok = __shfl((int)(w_cur.off >> 32), 16 * a + g * 4 + j, kWave) >= 0;
           const float v = ok ? s[a][j] * p.scale : -INFINITY;
           x[4 * a + j] = v;
           mt = fmaxf(mt, v);
         }
+      }
       mt = max_over_groups(mt);
       if (!__all(mt <= m)) {
         const float mn = fmaxf(m, mt);
@@ -520,125 +541,199 @@ __global__ __launch_bounds__(kAttnThreads, DV == 256 ? 2 : 3) void paged_attenti
         acc[e] = mma<BF>(a, hi, acc[e]);
         acc[e] = mma<BF>(a, lo, acc[e]);
       }
-      if (more) {
-        id_v[0] = id_k[0];
-        id_v[1] = id_k[1];
-        load_v(tile + kAttnWaves);
-        if (tile + 2 * kAttnWaves < t_last) fetch_ids(tile + 2 * kAttnWaves);
-      }
-    }
-    l = sum_over_groups(l);
+      if (more) load_v(next, w_next);
+      --left;
 
-    // join the waves, one piece of the head at a time: sO[wave][head][number]
-    const bool whole = t_first == 0 && t_last == n;
-    const int64_t slot = 2 * (int64_t)blockIdx.x + (at == first_unit ? 0 : 1);
-    float* part = p.partial + slot * (kHeads * (p.D + 2));
+      const bool row_ends = cur.tile + 1 == cur.r.t1;
+      if (!more || row_ends) {
+        // the row, or this wave's part of it, is done
+        const bool begins = first_tile == cur.r.t0;
+        const float lsum = sum_over_groups(l);
+        if (begins && row_ends) {
+          if (li < heads) {
 #pragma unroll
-    for (int c = 0; c < NV; ++c) {
-      __syncthreads();  // the previous readers are done
-      if (li < heads) {
-        float* o = sO + (wave * kHeads + li) * kRow;
+            for (int c = 0; c < NV; ++c)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+              for (int r = 0; r < 4; r += 8 / LN) {
+                const int d = c * PW + (g * 4 + r) * LN;
+                float o[8];
 #pragma unroll
-          for (int e = 0; e < LN; e += 4)
-            *reinterpret_cast<float4v*>(o + (g * 4 + r) * LN + e) =
-                float4v{acc[c * 8 + e][r], acc[c * 8 + e + 1][r], acc[c * 8 + e + 2][r],
-                        acc[c * 8 + e + 3][r]};
-        if (g == 0) {
-          sM[wave * kHeads + li] = m;
-          sL[wave * kHeads + li] = l;
-        }
-      }
-      __syncthreads();
-      const int units = (p.D - c * PW < PW ? p.D - c * PW : PW) / 8;  // 8 numbers each
-      for (int i = tid; i < heads * units; i += kAttnThreads) {
-        const int hd = i / units, dl = (i % units) * 8, d = c * PW + dl;
-        float mm = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kAttnWaves; ++w) mm = fmaxf(mm, sM[w * kHeads + hd]);
-        const float base = mm == -INFINITY ? 0.f : mm;
-        float sum = 0.f, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-        for (int w = 0; w < kAttnWaves; ++w) {
-          const float f = __builtin_amdgcn_exp2f(sM[w * kHeads + hd] - base);
-          sum += f * sL[w * kHeads + hd];
-          const float* o = sO + (w * kHeads + hd) * kRow + dl;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += f * o[e];
-        }
-        if (whole) {
-          finish<BF>(p, b, hq0 + hd, d, mm, sum, v);
+                for (int e = 0; e < 8; ++e) o[e] = acc[c * 8 + e % LN][r + e / LN];
+                if (d < p.D) finish<BF>(p, cur.b, hq0 + li, d, m, lsum, o);
+              }
+          }
         } else {
-          float* o = part + hd * p.D + d;
-          *reinterpret_cast<float4v*>(o) = float4v{v[0], v[1], v[2], v[3]};
-          *reinterpret_cast<float4v*>(o + 4) = float4v{v[4], v[5], v[6], v[7]};
-          if (d == 0) {
-            part[kHeads * p.D + hd] = mm;
-            part[kHeads * p.D + kHeads + hd] = sum;
+          const int slot = 2 * wave + (first_row ? 0 : 1);
+          if (li < heads) {
+            float* o = sO + (slot * slot_heads + li) * row_floats;
+#pragma unroll
+            for (int c = 0; c < NV; ++c)
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int e = 0; e < LN; e += 4) {
+                  const int d = c * PW + (g * 4 + r) * LN + e;
+                  if (d < p.D)
+                    *reinterpret_cast<float4v*>(o + d) =
+                        float4v{acc[c * 8 + e][r], acc[c * 8 + e + 1][r], acc[c * 8 + e + 2][r],
+                                acc[c * 8 + e + 3][r]};
+                }
+            if (g == 0) {
+              sM[slot][li] = m;
+              sL[slot][li] = lsum;
+            }
+          }
+          if (lane == 0) {
+            sRow[slot] = cur.b * H + cur.h;
+            sEnds[slot] = (begins ? 1 : 0) | (row_ends ? 2 : 0);
+            sLast[slot] = (int)(run_end - left) - 1 + (cur.r.t1 - cur.tile - 1);  // unit of the row's last tile
           }
         }
+        first_row = false;
+      }
+      if (!more) break;
+      cur = next;
+      w_cur = w_next;
+      if (row_ends) {
+        first_tile = cur.tile;
+        open_row(cur);
+      }
+      if (left > 1) {
+        advance(next);
+        w_next = place_of(next);
       }
     }
-    at += t_last - t_first;
-    in_row += t_last - t_first;
+  }
+
+  // Runs of slots of one row are joined: into the output where the row begins
+  // and ends in this workgroup, else into the workspace (its first slot for a row
+  // that began before, the second for one that goes on).
+  __syncthreads();
+  int owned = -1, last = 0;
+  for (int i = 0; i < 2 * kAttnWaves;) {
+    const int row = uni(sRow[i]);
+    if (row < 0) {
+      ++i;
+      continue;
+    }
+    int end = i + 1, ends = uni(sEnds[i]);
+    const bool begins = ends & 1;
+    for (int k = i + 1; k < 2 * kAttnWaves; ++k) {
+      const int other = uni(sRow[k]);
+      if (other < 0) continue;
+      if (other != row) break;
+      end = k + 1;
+      ends = uni(sEnds[k]);
+    }
+    const bool whole = begins && (ends & 2);
+    const int b = row / H, h = row - b * H;
+    const int hk = h / p.qtiles, qt = h - hk * p.qtiles;
+    const int nh = p.G - qt * kHeads < kHeads ? p.G - qt * kHeads : kHeads;
+    float* part = p.partial + (2 * (int64_t)blockIdx.x + (begins ? 1 : 0)) * slot_floats(slot_heads, p.D);
+    const int units = p.D / 8;
+    for (int j = tid; j < nh * units; j += kAttnThreads) {
+      const int hd = j / units, d = (j - hd * units) * 8;
+      float mm = -INFINITY;
+      for (int k = i; k < end; ++k)
+        if (sRow[k] == row) mm = fmaxf(mm, sM[k][hd]);
+      const float base = mm == -INFINITY ? 0.f : mm;
+      float sum = 0.f, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      for (int k = i; k < end; ++k) {
+        if (sRow[k] != row) continue;
+        const float f = __builtin_amdgcn_exp2f(sM[k][hd] - base);
+        sum += f * sL[k][hd];
+        const float* o = sO + (k * slot_heads + hd) * row_floats + d;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += f * o[e];
+      }
+      if (whole) {
+        finish<BF>(p, b, hk * p.G + qt * kHeads + hd, d, mm, sum, v);
+      } else {
+        float* o = part + hd * p.D + d;
+        *reinterpret_cast<float4v*>(o) = float4v{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<float4v*>(o + 4) = float4v{v[4], v[5], v[6], v[7]};
+        if (d == 0) {
+          part[slot_heads * p.D + hd] = mm;
+          part[slot_heads * p.D + slot_heads + hd] = sum;
+        }
+      }
+    }
+    if (begins && !whole) {  // goes on in the following workgroups
+      owned = row;
+      last = (int)(cut.part_of((uint32_t)sLast[i]) / kAttnWaves);
+    }
+    i = end;
+  }
+  if (!p.direct && tid == 0) p.owner[blockIdx.x] = make_int2(owned, last);
+
+  // sequences without tokens: zeros and -inf, spread over the workgroups
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    const Range r = range_of(p, b);
+    if (r.hi > r.lo) continue;
+    uint16_t* o = reinterpret_cast<uint16_t*>(p.Out) + (int64_t)b * p.Hq * p.D;
+    for (int i = tid; i < p.Hq * p.D; i += kAttnThreads) o[i] = 0;
+    if (p.lse)
+      for (int i = tid; i < p.Hq; i += kAttnThreads) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
   }
 }
 
-// Joins the partial sums of every (sequence, head) that spans workgroups of the
-// first kernel (grid `parts_grid`); one workgroup per (sequence, head).
+// Joins the partial sums of the rows that span workgroups of the first kernel:
+// one wave per query head of the row that workgroup blockIdx.x began and left
+// unfinished, D / 4 lanes on each part and as many parts at once as that allows.
 template <bool BF>
-__global__ __launch_bounds__(kAttnThreads) void paged_attention_join_kernel(AttnParams p,
-                                                                            int parts_grid) {
-  __shared__ int64_t sRed[kAttnWaves];
-  __shared__ int64_t sBefore;
-  const int tid = threadIdx.x;
+__global__ __launch_bounds__(kAttnThreads) void paged_attention_join_kernel(AttnParams p) {
+  const int2 own = p.owner[blockIdx.x];
+  if (own.x < 0) return;
+  const int lane = threadIdx.x & 63;
+  const int hd = uni(blockIdx.y * kAttnWaves + (threadIdx.x >> 6));
   const int H = p.Hkv * p.qtiles;
-  const int b = blockIdx.x / H, h = blockIdx.x % H;
-  const int n = tiles_of(range_of(p, b));
-  if (n == 0) return;
-  const int per = (p.B + kAttnThreads - 1) / kAttnThreads;
-  int64_t total;
-  int64_t before = scan_tiles(p, per, sRed, total);
-  for (int i = 0; i < per; ++i) {
-    const int q = tid * per + i;
-    if (q >= p.B) break;
-    if (q == b) sBefore = before;
-    before += tiles_of(range_of(p, q));
-  }
-  __syncthreads();
-  const Cut c = cut_of(total * H, parts_grid);
-  const int64_t u0 = sBefore * H + (int64_t)h * n, u1 = u0 + n;
-  // the first part that reaches past u0, and the one that reaches u1
-  int64_t w0 = u0 * c.parts / c.total;
-  while (c.start(w0 + 1) <= u0) ++w0;
-  while (c.start(w0) > u0) --w0;
-  if (c.start(w0 + 1) >= u1) return;  // one part had it all
-  const int hk = h / p.qtiles, qt = h % p.qtiles;
-  const int heads = p.G - qt * kHeads < kHeads ? p.G - qt * kHeads : kHeads;
-  const int hq0 = hk * p.G + qt * kHeads;
-  const int64_t size = kHeads * (p.D + 2);
-  const int per_head = p.D / 8;
-  for (int i = tid; i < heads * per_head; i += kAttnThreads) {
-    const int hd = i / per_head, d = (i % per_head) * 8;
-    float m = -INFINITY, sum = 0.f, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int64_t w = w0; c.start(w) < u1; ++w) {
-      // a part's first fragment is in its even slot, its last one in the odd
-      const int64_t slot = 2 * w + (c.start(w) >= u0 ? 0 : 1);
-      const float* part = p.partial + slot * size;
-      const float pm = part[kHeads * p.D + hd], pl = part[kHeads * p.D + kHeads + hd];
-      const float mn = fmaxf(m, pm);
-      const float base = mn == -INFINITY ? 0.f : mn;
-      const float fa = __builtin_amdgcn_exp2f(m - base), fb = __builtin_amdgcn_exp2f(pm - base);
-      m = mn;
-      sum = sum * fa + pl * fb;
-      const float* o = part + hd * p.D + d;
+  const int b = own.x / H, h = own.x - b * H;
+  const int hk = h / p.qtiles, qt = h - hk * p.qtiles;
+  if (hd >= kHeads || qt * kHeads + hd >= p.G) return;
+  const int slot_heads = p.G < kHeads ? p.G : kHeads;
+  const int64_t size = slot_floats(slot_heads, p.D);
+  const int n = own.y - (int)blockIdx.x + 1;
+  // part 0 is this workgroup's second slot, the others the first slots that follow
+  auto part = [&](int k) {
+    return p.partial + (2 * ((int64_t)blockIdx.x + k) + (k == 0 ? 1 : 0)) * size;
+  };
+  const int at_m = slot_heads * p.D + hd, at_l = at_m + slot_heads;
+  float m = -INFINITY;
+  for (int k = lane; k < n; k += kWave) m = fmaxf(m, part(k)[at_m]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = v[e] * fa + o[e] * fb;
+  for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, kWave));
+  const float base = m == -INFINITY ? 0.f : m;
+  float sum = 0.f;
+  for (int k = lane; k < n; k += kWave)
+    sum += __builtin_amdgcn_exp2f(part(k)[at_m] - base) * part(k)[at_l];
+  sum = wave_sum(sum);
+  const int L = p.D / 4, conc = kWave / L;
+  const int sub = lane / L, col = lane - sub * L;
+  float4v v = {0, 0, 0, 0};
+  if (sub < conc) {
+#pragma unroll 4
+    for (int k = sub; k < n; k += conc) {
+      const float* o = part(k);
+      const float f = __builtin_amdgcn_exp2f(o[at_m] - base);
+      v += f * *reinterpret_cast<const float4v*>(o + hd * p.D + col * 4);
     }
-    finish<BF>(p, b, hq0 + hd, d, m, sum, v);
+  }
+  float4v t = v;
+  for (int i = 1; i < conc; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t[e] += __shfl(v[e], (col + i * L) & 63, kWave);
+  if (sub == 0) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t head = (int64_t)b * p.Hq + hk * p.G + qt * kHeads + hd;
+    u32x2 u;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      u[e] = to16<BF>(t[2 * e] * inv) | ((uint32_t)to16<BF>(t[2 * e + 1] * inv) << 16);
+    *reinterpret_cast<u32x2*>(p.Out + (head * p.D + col * 4) * 2) = u;
+    if (p.lse && col == 0) p.lse[head] = lse_of<BF>(m, sum);
   }
 }
+
 
 FastDiv fast_div(int64_t d) {
   uint32_t s = 0;
@@ -647,49 +742,69 @@ FastDiv fast_div(int64_t d) {
   return {(uint32_t)d, (uint32_t)m, 30 + s};
 }
 
-int waves_grid(int64_t D) { return device_cus() * (D > 128 ? 2 : 3); }
+int64_t lds_bytes(int heads, int64_t D) { return 2 * kAttnWaves * heads * (D + 4) * 4; }
 
-// Workgroups of the first kernel, and whether each (sequence, head) has its own.
-// With at most four tiles in a row every wave has one and a join would only
-// cost its launch.
-int64_t attn_grid(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity, bool* direct) {
+struct Grid {
+  int64_t blocks, partials;  // workgroups; partial sums they may leave
+  bool direct;
+};
+
+// Workgroups of the first kernel: as many as the GPU holds at once, or one for
+// each (sequence, head) where a table names at most four tiles a row: every wave
+// has one tile then and a join would only cost its launch.
+Grid attn_grid(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity) {
   const int64_t G = Hq / Hkv, H = Hkv * ((G + kHeads - 1) / kHeads);
+  const int heads = (int)(G < kHeads ? G : kHeads);
+  if (capacity <= kAttnWaves * kTileTokens) return {B * H, 0, true};
   const int64_t tiles = capacity / kTileTokens + 2;  // a window may begin inside a tile
-  *direct = capacity <= kAttnWaves * kTileTokens;
-  if (*direct) return B * H;
   const int64_t most = (B * H * tiles + kAttnWaves - 1) / kAttnWaves;
-  const int64_t grid = waves_grid(D);
-  return most < grid ? most : grid;
+  const int64_t by_lds = 155 * 1024 / (lds_bytes(heads, D) + 2048), by_regs = D > 128 ? 2 : 3;
+  const int64_t grid = device_cus() * (by_lds < by_regs ? by_lds : by_regs);
+  const int64_t blocks = most < grid ? most : grid;
+  return {blocks, 2 * blocks, false};
 }
 
-template <bool BF, int DV>
-hipError_t launch_dv(const AttnParams& p, int grid, hipStream_t s) {
-  if (p.page.d % 16 == 0)
-    hipLaunchKernelGGL((paged_attention_kernel<BF, DV, true>), dim3(grid), dim3(kAttnThreads), 0, s,
-                       p);
-  else
-    hipLaunchKernelGGL((paged_attention_kernel<BF, DV, false>), dim3(grid), dim3(kAttnThreads), 0,
-                       s, p);
+template <bool BF, int DV, bool UNI>
+hipError_t launch_kernel(const AttnParams& p, int64_t grid, hipStream_t s) {
+  const auto fn = paged_attention_kernel<BF, DV, UNI>;
+  const int lds = (int)lds_bytes(p.G < kHeads ? p.G : kHeads, p.D);
+  if (lds > 48 * 1024) {  // above what every kernel may use
+    static std::atomic<uint64_t> done{0};
+    const hipError_t e = lds_limit_once(reinterpret_cast<const void*>(fn),
+                                        (int)lds_bytes(kHeads, DV), done);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(fn, dim3((uint32_t)grid), dim3(kAttnThreads), lds, s, p);
   return hipGetLastError();
 }
 
+template <bool BF, int DV>
+hipError_t launch_dv(const AttnParams& p, int64_t grid, hipStream_t s) {
+  return p.page.d % 16 == 0 ? launch_kernel<BF, DV, true>(p, grid, s)
+                            : launch_kernel<BF, DV, false>(p, grid, s);
+}
+
 template <bool BF>
-hipError_t launch_t(const AttnParams& p, int grid, hipStream_t s) {
-  hipError_t e = p.D <= 64    ? launch_dv<BF, 64>(p, grid, s)
-                 : p.D <= 128 ? launch_dv<BF, 128>(p, grid, s)
-                              : launch_dv<BF, 256>(p, grid, s);
+hipError_t launch_t(const AttnParams& p, int64_t grid, hipStream_t s) {
+  const hipError_t e = p.D <= 64    ? launch_dv<BF, 64>(p, grid, s)
+                       : p.D <= 128 ? launch_dv<BF, 128>(p, grid, s)
+                                    : launch_dv<BF, 256>(p, grid, s);
   if (e != hipSuccess || p.direct) return e;
-  hipLaunchKernelGGL((paged_attention_join_kernel<BF>), dim3(p.B * p.Hkv * p.qtiles),
-                     dim3(kAttnThreads), 0, s, p, grid);
+  const int heads = p.G < kHeads ? p.G : kHeads;
+  hipLaunchKernelGGL((paged_attention_join_kernel<BF>),
+                     dim3((uint32_t)grid, (heads + kAttnWaves - 1) / kAttnWaves),
+                     dim3(kAttnThreads), 0, s, p);
   return hipGetLastError();
 }
 
 }  // namespace
 
 int64_t attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity) {
-  bool direct;
-  const int64_t grid = attn_grid(B, Hq, Hkv, D, capacity, &direct);
-  return direct ? 0 : 2 * grid * kHeads * (D + 2) * (int64_t)sizeof(float);
+  const Grid g = attn_grid(B, Hq, Hkv, D, capacity);
+  const int64_t G = Hq / Hkv;
+  if (g.direct) return 0;
+  return g.partials * slot_floats((int)(G < kHeads ? G : kHeads), (int)D) * (int64_t)sizeof(float) +
+         g.blocks * (int64_t)sizeof(int2);
 }
 
 hipError_t launch_paged_attention(int dtype, const AttnArgs& a, hipStream_t stream) {
@@ -718,11 +833,12 @@ hipError_t launch_paged_attention(int dtype, const AttnArgs& a, hipStream_t stre
   p.qtiles = (p.G + kHeads - 1) / kHeads;
   p.window = (int32_t)a.window;
   p.scale = a.scale_log2;
-  bool direct;
-  const int64_t grid = attn_grid(a.B, a.Hq, a.Hkv, a.D, a.width * a.page_size, &direct);
-  p.direct = direct;
-  return dtype == TQ_BF16 ? launch_t<true>(p, (int)grid, stream)
-                          : launch_t<false>(p, (int)grid, stream);
+  const Grid g = attn_grid(a.B, a.Hq, a.Hkv, a.D, a.width * a.page_size);
+  p.direct = g.direct;
+  p.owner = reinterpret_cast<int2*>(
+      p.partial + g.partials * slot_floats(p.G < kHeads ? p.G : kHeads, p.D));
+  return dtype == TQ_BF16 ? launch_t<true>(p, g.blocks, stream)
+                          : launch_t<false>(p, g.blocks, stream);
 }
 
 }  // namespace tq

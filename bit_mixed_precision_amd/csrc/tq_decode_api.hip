@@ -79,9 +79,9 @@ int attn_shapes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size
       D > 256 || D % 8 || page_size < 1 || width < 1 || page_size > kMaxTokens ||
       width > kMaxTokens || width * page_size > kMaxTokens)
     return TQ_ERR_SHAPE;
-  // the kernels count a sequence's tiles (32 tokens) times its heads in 32 bits,
-  // and use one join workgroup per (sequence, head)
-  if ((width * page_size / 32 + 2) * Hq > INT32_MAX || B * Hq > INT32_MAX) return TQ_ERR_SHAPE;
+  // the kernels count all tiles (32 tokens of one key-value head) in 32 bits
+  const int64_t rows = B * Hkv * ((Hq / Hkv + 15) / 16);
+  if (rows > INT32_MAX || rows * (width * page_size / 32 + 2) > INT32_MAX) return TQ_ERR_SHAPE;
   return TQ_OK;
 }
 

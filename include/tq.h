@@ -441,7 +441,8 @@ int tq_rope_append(int dtype, const void* QKV, int64_t qkv_tok, const float* tab
  * fp16 or bfloat16 in and out, fp32 scores, weights and sums.  The same bits on
  * every run.
  * D a multiple of 8, 8 <= D <= 256; Hq a multiple of Hkv, Hq <= 2^12; B <=
- * 2^20; width * page_size <= 2^30; strides multiples of 8, row_stride <= 2^24;
+ * 2^20; width * page_size <= 2^30; B * Hkv * ceil(Hq / Hkv / 16) * (width *
+ * page_size / 32 + 2) < 2^31; strides multiples of 8, row_stride <= 2^24;
  * pointers 16-byte aligned.  workspace: tq_paged_attention_workspace(...)
  * bytes, 16-byte aligned, contents irrelevant; calls that overlap on one
  * workspace race.
