@@ -212,6 +212,9 @@ _DTYPES = {"f16": "float16", "bf16": "bfloat16", "f32": "float32", "u8": "uint8"
            "i32": "int32"}
 
 
+_DT = {k: getattr(_torch, v) for k, v in _DTYPES.items()} if _torch is not None else {}
+
+
 def _need(t, name, dtype, shape=None, where=""):
     """Check one device-tensor argument before its pointer reaches the C ABI,
     which receives bare pointers and cannot check sizes itself: a buffer that
@@ -221,7 +224,7 @@ def _need(t, name, dtype, shape=None, where=""):
     import torch
     if not torch.is_tensor(t):
         raise TQError(TQ_ERR_VALUE, f"{where}: {name} must be a torch tensor")
-    if t.dtype != getattr(torch, _DTYPES[dtype]):
+    if t.dtype != _DT[dtype]:
         raise TQError(TQ_ERR_VALUE, f"{where}: {name} must be {_DTYPES[dtype]}, not {t.dtype}")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise TQError(TQ_ERR_SHAPE, f"{where}: {name} has shape {tuple(t.shape)}, "
@@ -546,67 +549,109 @@ def tq_kernel_name(fmt: int, M: int, N: int, K: int, path: int = TQ_PATH_AUTO) -
 
 
 # ------------------------------------------------------------------ decode
+#
+# These calls are a few microseconds of GPU work in a decode step, so the checks
+# look at every attribute once and leave the wording of a refusal to slow helpers.
+
+if _torch is not None:
+    _KIND = {_torch.float16: TQ_F16, _torch.bfloat16: TQ_BF16, _torch.float32: TQ_F32}
+    _I32T = _torch.int32
+
 
 def _kind(t, name, where, f32=False):
-    """tq_dtype of a float tensor whose last dimension is contiguous."""
-    import torch
-    if not torch.is_tensor(t):
+    """tq_dtype of a float tensor."""
+    if not isinstance(t, _torch.Tensor):
         raise TQError(TQ_ERR_VALUE, f"{where}: {name} must be a torch tensor")
-    if t.dtype is torch.float16:
-        return TQ_F16
-    if t.dtype is torch.bfloat16:
-        return TQ_BF16
-    if f32 and t.dtype is torch.float32:
-        return TQ_F32
-    raise TQError(TQ_ERR_VALUE, f"{where}: {name} has dtype {t.dtype}")
+    k = _KIND.get(t.dtype)
+    if k is None or (k == TQ_F32 and not f32):
+        raise TQError(TQ_ERR_VALUE, f"{where}: {name} has dtype {t.dtype}")
+    return k
 
 
-def _heads(t, name, where, like=None):
-    """Shape of a [..][heads][D] tensor: three dimensions, numbers of a head adjacent."""
+def _heads(t, name, where):
+    """Shape of a [tokens][heads][D] tensor, the numbers of a head adjacent."""
     if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
         raise TQError(TQ_ERR_SHAPE, f"{where}: {name} must be [tokens][heads][D] with adjacent "
                                     f"numbers, not {tuple(t.shape)} at strides {t.stride()}")
-    if like is not None and t.dtype != like.dtype:
-        raise TQError(TQ_ERR_VALUE, f"{where}: {name} is {t.dtype}, expected {like.dtype}")
     return t.shape
+
+
+def _same(t, name, like, shape, where, strided=False):
+    """An output of the type and shape of another tensor's."""
+    if not isinstance(t, _torch.Tensor) or t.dtype != like.dtype:
+        raise TQError(TQ_ERR_VALUE, f"{where}: {name} must be a tensor of {like.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise TQError(TQ_ERR_SHAPE, f"{where}: {name} has shape {tuple(t.shape)}, "
+                                    f"expected {tuple(shape)}")
+    if strided:
+        _heads(t, name, where)
+    elif not t.is_contiguous():
+        raise TQError(TQ_ERR_SHAPE, f"{where}: {name} must be contiguous (row-major)")
+
+
+def _int32(t, name, shape, where):
+    """An int32 tensor of the given shape, contiguous."""
+    if not (isinstance(t, _torch.Tensor) and t.dtype is _I32T and t.shape == shape
+            and t.is_contiguous()):
+        _need(t, name, "i32", shape, where)
 
 
 def _cache(k_pages, v_pages, like, D, where):
     """(n_pages, page_size, Hkv, page, row and head stride) of the two halves of a
     paged cache [pages][slots][Hkv][D], any order in memory, numbers adjacent."""
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if _kind(t, name, where) is not None and t.dtype != like.dtype:
-            raise TQError(TQ_ERR_VALUE, f"{where}: {name} is {t.dtype}, expected {like.dtype}")
-        if t.dim() != 4 or t.shape[3] != D or (D > 1 and t.stride(3) != 1):
-            raise TQError(TQ_ERR_SHAPE, f"{where}: {name} must be [pages][slots][heads][{D}] with "
-                                        f"adjacent numbers, not {tuple(t.shape)}")
-    if k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride():
-        raise TQError(TQ_ERR_SHAPE, f"{where}: k_pages and v_pages differ in shape or strides")
-    return (*k_pages.shape[:3], *k_pages.stride()[:3])
+    ks, kst = k_pages.shape, k_pages.stride()
+    if not (k_pages.dtype is v_pages.dtype is like.dtype and len(ks) == 4 and ks[3] == D
+            and kst[3] == 1 and v_pages.shape == ks and v_pages.stride() == kst):
+        for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+            if t.dtype != like.dtype:
+                raise TQError(TQ_ERR_VALUE, f"{where}: {name} is {t.dtype}, expected {like.dtype}")
+            if t.dim() != 4 or t.shape[3] != D or (D > 1 and t.stride(3) != 1):
+                raise TQError(TQ_ERR_SHAPE, f"{where}: {name} must be [pages][slots][heads][{D}] "
+                                            f"with adjacent numbers, not {tuple(t.shape)}")
+        if v_pages.shape != ks or v_pages.stride() != kst:
+            raise TQError(TQ_ERR_SHAPE, f"{where}: k_pages and v_pages differ in shape or strides")
+    return ks[0], ks[1], ks[2], kst[0], kst[1], kst[2]
 
 
 def _table(table, where):
     """(n_pos, rot) of a cosine / sine table [n_pos][rot / 2][2]."""
-    import torch
-    if not torch.is_tensor(table) or table.dim() != 3 or table.shape[2] != 2:
+    if not isinstance(table, _torch.Tensor) or table.dim() != 3 or table.shape[2] != 2:
         raise TQError(TQ_ERR_SHAPE, f"{where}: table must be [positions][rot / 2][2]")
-    _need(table, "table", "f32", None, where)
+    if table.dtype is not _torch.float32 or not table.is_contiguous():
+        _need(table, "table", "f32", None, where)
     return table.shape[0], 2 * table.shape[1]
 
 
-def _empty(shape, dtype, device, stream):
-    """A new tensor whose memory belongs to the stream that the call runs on: the
-    allocator hands a freed block out again in the order of its own stream, so
-    memory of the current stream must not be written on another one."""
-    import torch
+def _empty(like, shape, dtype, stream):
+    """A new tensor on like's GPU whose memory belongs to the stream that the call
+    runs on: the allocator hands a freed block out again in the order of its own
+    stream, so memory of the current stream must not be written on another one."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device)):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
+    with _torch.cuda.stream(_torch.cuda.ExternalStream(stream, like.device)):
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _int32(t, name, shape, where):
-    return _need(t, name, "i32", shape, where)
+def _pieces(like, sizes, stream):
+    """int32 vectors of the given sizes from one allocation."""
+    return _empty(like, (sum(sizes),), _I32T, stream).split_with_sizes(sizes)
+
+
+def _launch(where, dev, fn, *args):
+    """Call a C entry point with GPU `dev` current and raise for its status."""
+    if _torch.cuda.current_device() != dev:
+        with _torch.cuda.device(dev):
+            st = fn(*args)
+    else:
+        st = fn(*args)
+    if st:
+        raise TQError(st, where)
+
+
+def _raw_stream(stream, dev):
+    if stream is not None:
+        return stream
+    return _torch._C._cuda_getCurrentRawStream(dev)
 
 
 def tq_rope_table(n_pos: int, rot: int, theta: float = 5e5, scaling: int = TQ_ROPE_NONE,
@@ -631,17 +676,17 @@ def tq_rope(X, table, positions, interleaved: bool = False, inverse: bool = Fals
     n_pos, rot = _table(table, where)
     _int32(positions, "positions", (T,), where)
     if Y is not None:
-        _kind(Y, "Y", where, f32=True)
-        if _heads(Y, "Y", where, X) != X.shape:
-            raise TQError(TQ_ERR_SHAPE, f"{where}: Y has shape {tuple(Y.shape)}, "
-                                        f"expected {tuple(X.shape)}")
-    _on_gpu(where, ("X", X), ("table", table), ("positions", positions), ("Y", Y))
+        _same(Y, "Y", X, (T, H, D), where, strided=True)
+    dev = X.get_device()
+    if dev < 0 or table.get_device() != dev or positions.get_device() != dev or (
+            Y is not None and Y.get_device() != dev):
+        _on_gpu(where, ("X", X), ("table", table), ("positions", positions), ("Y", Y))
     if Y is None:
-        Y = _empty((T, H, D), X.dtype, X.device, stream)
-    with _device_of(X):
-        _check(lib.tq_rope(kind, X.data_ptr(), X.stride(0), X.stride(1), Y.data_ptr(), Y.stride(0),
-                           Y.stride(1), table.data_ptr(), n_pos, rot, positions.data_ptr(), T, H,
-                           D, interleaved, inverse, _stream(stream, X.device)), where)
+        Y = _empty(X, (T, H, D), X.dtype, stream)
+    xs, ys = X.stride(), Y.stride()
+    _launch(where, dev, lib.tq_rope, kind, X.data_ptr(), xs[0], xs[1], Y.data_ptr(), ys[0], ys[1],
+            table.data_ptr(), n_pos, rot, positions.data_ptr(), T, H, D, interleaved, inverse,
+            _raw_stream(stream, dev))
     return Y
 
 
@@ -654,12 +699,13 @@ def tq_rope_append(QKV, table, positions, page_table, k_pages, v_pages, interlea
     where = "tq_rope_append"
     kind = _kind(QKV, "QKV", where)
     T, H, D = _heads(QKV, "QKV", where)
-    if H > 1 and QKV.stride(1) != D:
+    xs = QKV.stride()
+    if H > 1 and xs[1] != D:
         raise TQError(TQ_ERR_SHAPE, f"{where}: the heads of QKV must be adjacent")
     n_pos, rot = _table(table, where)
     _int32(positions, "positions", (T,), where)
     n_seqs, width = _rank2(page_table, "page_table", where)
-    _int32(page_table, "page_table", None, where)
+    _int32(page_table, "page_table", (n_seqs, width), where)
     if seqs is not None:
         _int32(seqs, "seqs", (T,), where)
     P, size, Hkv, page_stride, row_stride, head_stride = _cache(k_pages, v_pages, QKV, D, where)
@@ -667,18 +713,22 @@ def tq_rope_append(QKV, table, positions, page_table, k_pages, v_pages, interlea
     if Hq < 1:
         raise TQError(TQ_ERR_SHAPE, f"{where}: {H} heads in QKV, {Hkv} in the cache")
     if Q is not None:
-        _need(Q, "Q", "f16" if kind == TQ_F16 else "bf16", (T, Hq, D), where)
-    _on_gpu(where, ("QKV", QKV), ("table", table), ("positions", positions),
-            ("page_table", page_table), ("seqs", seqs), ("k_pages", k_pages),
-            ("v_pages", v_pages), ("Q", Q))
+        _same(Q, "Q", QKV, (T, Hq, D), where)
+    dev = QKV.get_device()
+    if dev < 0 or not (table.get_device() == positions.get_device() == page_table.get_device()
+                       == k_pages.get_device() == v_pages.get_device() == dev) or (
+            seqs is not None and seqs.get_device() != dev) or (
+            Q is not None and Q.get_device() != dev):
+        _on_gpu(where, ("QKV", QKV), ("table", table), ("positions", positions),
+                ("page_table", page_table), ("seqs", seqs), ("k_pages", k_pages),
+                ("v_pages", v_pages), ("Q", Q))
     if Q is None:
-        Q = _empty((T, Hq, D), QKV.dtype, QKV.device, stream)
-    with _device_of(QKV):
-        _check(lib.tq_rope_append(kind, QKV.data_ptr(), QKV.stride(0), table.data_ptr(), n_pos,
-                                  rot, positions.data_ptr(), _ptr(seqs), page_table.data_ptr(),
-                                  n_seqs, width, k_pages.data_ptr(), v_pages.data_ptr(), P, size,
-                                  page_stride, row_stride, head_stride, Q.data_ptr(), T, Hq, Hkv,
-                                  D, interleaved, _stream(stream, QKV.device)), where)
+        Q = _empty(QKV, (T, Hq, D), QKV.dtype, stream)
+    _launch(where, dev, lib.tq_rope_append, kind, QKV.data_ptr(), xs[0], table.data_ptr(), n_pos,
+            rot, positions.data_ptr(), None if seqs is None else seqs.data_ptr(),
+            page_table.data_ptr(), n_seqs, width, k_pages.data_ptr(), v_pages.data_ptr(), P, size,
+            page_stride, row_stride, head_stride, Q.data_ptr(), T, Hq, Hkv, D, interleaved,
+            _raw_stream(stream, dev))
     return Q
 
 
@@ -697,61 +747,60 @@ def tq_paged_attention(Q, k_pages, v_pages, page_table, lens, scale: float | Non
     (0: all) of lens[b] tokens in the paged cache k_pages, v_pages
     [pages][slots][Hkv][D] named by page_table [B][width].  Returns out [B][Hq][D],
     and lse float32 [B][Hq] with return_lse.  scale: 1 / sqrt(D) when None."""
-    import torch
     where = "tq_paged_attention"
     kind = _kind(Q, "Q", where)
     B, Hq, D = _heads(Q, "Q", where)
     P, size, Hkv, page_stride, row_stride, head_stride = _cache(k_pages, v_pages, Q, D, where)
-    rows, width = _rank2(page_table, "page_table", where)
+    width = _rank2(page_table, "page_table", where)[1]
     _int32(page_table, "page_table", (B, width), where)
     _int32(lens, "lens", (B,), where)
     if out is not None:
-        _need(out, "out", "f16" if kind == TQ_F16 else "bf16", (B, Hq, D), where)
+        _same(out, "out", Q, (B, Hq, D), where)
     if workspace is not None:
         _need(workspace, "workspace", "u8", None, where)
-    _on_gpu(where, ("Q", Q), ("k_pages", k_pages), ("v_pages", v_pages),
-            ("page_table", page_table), ("lens", lens), ("out", out), ("workspace", workspace))
-    with _device_of(Q):
+    dev = Q.get_device()
+    if dev < 0 or not (k_pages.get_device() == v_pages.get_device() == page_table.get_device()
+                       == lens.get_device() == dev) or (
+            out is not None and out.get_device() != dev) or (
+            workspace is not None and workspace.get_device() != dev):
+        _on_gpu(where, ("Q", Q), ("k_pages", k_pages), ("v_pages", v_pages),
+                ("page_table", page_table), ("lens", lens), ("out", out),
+                ("workspace", workspace))
+    if workspace is None:
         n = lib.tq_paged_attention_workspace(B, Hq, Hkv, D, size, width)
-        _check(min(n, 0), where)
-        if workspace is None and n > 0:
-            workspace = _empty((n,), torch.uint8, Q.device, stream)
-        if out is None:
-            out = _empty((B, Hq, D), Q.dtype, Q.device, stream)
-        lse = _empty((B, Hq), torch.float32, Q.device, stream) if return_lse else None
-        _check(lib.tq_paged_attention(
-            kind, Q.data_ptr(), Q.stride(0), Q.stride(1), k_pages.data_ptr(), v_pages.data_ptr(),
-            P, size, page_stride, row_stride, head_stride, page_table.data_ptr(), width,
-            lens.data_ptr(), B, Hq, Hkv, D, D ** -0.5 if scale is None else scale, window,
-            out.data_ptr(), _ptr(lse), _ptr(workspace),
-            0 if workspace is None else workspace.numel(), _stream(stream, Q.device)), where)
+        if n:
+            _check(min(n, 0), where)
+            workspace = _empty(Q, (n,), _torch.uint8, stream)
+    else:
+        n = workspace.numel()
+    if out is None:
+        out = _empty(Q, (B, Hq, D), Q.dtype, stream)
+    lse = _empty(Q, (B, Hq), _torch.float32, stream) if return_lse else None
+    qs = Q.stride()
+    _launch(where, dev, lib.tq_paged_attention, kind, Q.data_ptr(), qs[0], qs[1],
+            k_pages.data_ptr(), v_pages.data_ptr(), P, size, page_stride, row_stride, head_stride,
+            page_table.data_ptr(), width, lens.data_ptr(), B, Hq, Hkv, D,
+            D ** -0.5 if scale is None else scale, window, out.data_ptr(),
+            None if lse is None else lse.data_ptr(),
+            None if workspace is None else workspace.data_ptr(), n, _raw_stream(stream, dev))
     return (out, lse) if return_lse else out
 
 
 def _pool(pool, where):
     """(planes, n_pages, bytes of a page) of a contiguous pool [planes][pages]..."""
-    import torch
-    if not torch.is_tensor(pool) or pool.dim() < 3 or not pool.is_contiguous():
+    if not isinstance(pool, _torch.Tensor) or pool.dim() < 3 or not pool.is_contiguous():
         raise TQError(TQ_ERR_SHAPE, f"{where}: pool must be a contiguous [planes][pages][...] tensor")
-    planes, pages = pool.shape[:2]
     size = pool.element_size()
     for n in pool.shape[2:]:
         size *= n
-    return planes, pages, size
+    return pool.shape[0], pool.shape[1], size
 
 
 def _state(page_table, lens, where):
     rows, width = _rank2(page_table, "page_table", where)
-    _int32(page_table, "page_table", None, where)
+    _int32(page_table, "page_table", (rows, width), where)
     _int32(lens, "lens", (rows,), where)
     return rows, width
-
-
-def _pages_workspace(rows, n_pages, workspace, device, stream, where):
-    import torch
-    n = lib.tq_pages_workspace(rows, n_pages)
-    _check(min(n, 0), where)
-    return _empty((n,), torch.uint8, device, stream) if workspace is None else workspace
 
 
 def tq_pages_workspace(rows: int, n_pages: int) -> int:
@@ -761,100 +810,79 @@ def tq_pages_workspace(rows: int, n_pages: int) -> int:
     return n
 
 
-def tq_pages_fork(pool, page_table, lens, parent, page_size: int, workspace=None, stream=None):
+def tq_pages_fork(pool, page_table, lens, parent, page_size: int, stream=None):
     """Continue row parent[r] as row r (an empty sequence where parent[r] names no
     row): pages are shared, a partly filled last page is copied for all but the
     first row that continues it.  pool [planes][pages][...], page_table [rows][width],
     lens [rows], parent [new rows].  Returns (page_table, lens, refs, short): the new
     state, how often each page is held, and the rows that found no free page."""
-    import torch
     where = "tq_pages_fork"
     planes, P, size = _pool(pool, where)
     rows_in, width = _state(page_table, lens, where)
-    if not torch.is_tensor(parent) or parent.dim() != 1:
+    if not isinstance(parent, _torch.Tensor) or parent.dim() != 1:
         raise TQError(TQ_ERR_SHAPE, f"{where}: parent must be a 1-D tensor")
     rows = parent.shape[0]
-    _int32(parent, "parent", None, where)
-    if workspace is not None:
-        _need(workspace, "workspace", "u8", None, where)
-    _on_gpu(where, ("pool", pool), ("page_table", page_table), ("lens", lens), ("parent", parent),
-            ("workspace", workspace))
-    with _device_of(pool):
-        dev = pool.device
-        ws = _pages_workspace(rows, P, workspace, dev, stream, where)
-        table_out = _empty((rows, width), torch.int32, dev, stream)
-        lens_out = _empty((rows,), torch.int32, dev, stream)
-        refs = _empty((P,), torch.int32, dev, stream)
-        short = _empty((1,), torch.int32, dev, stream)
-        _check(lib.tq_pages_fork(pool.data_ptr(), planes, P, size, page_table.data_ptr(),
-                                 lens.data_ptr(), rows_in, parent.data_ptr(), rows, width,
-                                 page_size, table_out.data_ptr(), lens_out.data_ptr(),
-                                 refs.data_ptr(), short.data_ptr(), ws.data_ptr(), ws.numel(),
-                                 _stream(stream, dev)), where)
-    return table_out, lens_out, refs, short
+    _int32(parent, "parent", (rows,), where)
+    dev = pool.get_device()
+    if dev < 0 or not (page_table.get_device() == lens.get_device() == parent.get_device() == dev):
+        _on_gpu(where, ("pool", pool), ("page_table", page_table), ("lens", lens),
+                ("parent", parent))
+    n = tq_pages_workspace(rows, P)
+    ws, table_out, lens_out, refs, short = _pieces(lens, (n // 4, rows * width, rows, P, 1), stream)
+    _launch(where, dev, lib.tq_pages_fork, pool.data_ptr(), planes, P, size, page_table.data_ptr(),
+            lens.data_ptr(), rows_in, parent.data_ptr(), rows, width, page_size,
+            table_out.data_ptr(), lens_out.data_ptr(), refs.data_ptr(), short.data_ptr(),
+            ws.data_ptr(), n, _raw_stream(stream, dev))
+    return table_out.view(rows, width), lens_out, refs, short
 
 
-def tq_pages_grow(page_table, lens, add, n_pages: int, page_size: int, workspace=None,
-                  stream=None):
+def tq_pages_grow(page_table, lens, add, n_pages: int, page_size: int, stream=None):
     """Room for add[r] more tokens in row r, from the pages that no row holds.
     Returns (page_table, lens, short): the new state and how many rows were refused."""
-    import torch
     where = "tq_pages_grow"
     rows, width = _state(page_table, lens, where)
     _int32(add, "add", (rows,), where)
-    if workspace is not None:
-        _need(workspace, "workspace", "u8", None, where)
-    _on_gpu(where, ("page_table", page_table), ("lens", lens), ("add", add),
-            ("workspace", workspace))
-    with _device_of(page_table):
-        dev = page_table.device
-        ws = _pages_workspace(rows, n_pages, workspace, dev, stream, where)
-        table_out = _empty((rows, width), torch.int32, dev, stream)
-        lens_out = _empty((rows,), torch.int32, dev, stream)
-        short = _empty((1,), torch.int32, dev, stream)
-        _check(lib.tq_pages_grow(page_table.data_ptr(), lens.data_ptr(), add.data_ptr(), rows,
-                                 width, page_size, n_pages, table_out.data_ptr(),
-                                 lens_out.data_ptr(), short.data_ptr(), ws.data_ptr(), ws.numel(),
-                                 _stream(stream, dev)), where)
-    return table_out, lens_out, short
+    dev = page_table.get_device()
+    if dev < 0 or not (lens.get_device() == add.get_device() == dev):
+        _on_gpu(where, ("page_table", page_table), ("lens", lens), ("add", add))
+    n = tq_pages_workspace(rows, n_pages)
+    ws, table_out, lens_out, short = _pieces(lens, (n // 4, rows * width, rows, 1), stream)
+    _launch(where, dev, lib.tq_pages_grow, page_table.data_ptr(), lens.data_ptr(), add.data_ptr(),
+            rows, width, page_size, n_pages, table_out.data_ptr(), lens_out.data_ptr(),
+            short.data_ptr(), ws.data_ptr(), n, _raw_stream(stream, dev))
+    return table_out.view(rows, width), lens_out, short
 
 
-def tq_pages_compact(pool, page_table, lens, page_size: int, workspace=None, stream=None):
+def tq_pages_compact(pool, page_table, lens, page_size: int, stream=None):
     """Move the pages in use to the low end of the pool.  Returns (page_table, used):
     the new table and the number of pages in use (int32 [1]), all below it."""
-    import torch
     where = "tq_pages_compact"
     planes, P, size = _pool(pool, where)
     rows, width = _state(page_table, lens, where)
-    if workspace is not None:
-        _need(workspace, "workspace", "u8", None, where)
-    _on_gpu(where, ("pool", pool), ("page_table", page_table), ("lens", lens),
-            ("workspace", workspace))
-    with _device_of(pool):
-        dev = pool.device
-        ws = _pages_workspace(rows, P, workspace, dev, stream, where)
-        table_out = _empty((rows, width), torch.int32, dev, stream)
-        used = _empty((1,), torch.int32, dev, stream)
-        _check(lib.tq_pages_compact(pool.data_ptr(), planes, P, size, page_table.data_ptr(),
-                                    lens.data_ptr(), rows, width, page_size, table_out.data_ptr(),
-                                    used.data_ptr(), ws.data_ptr(), ws.numel(),
-                                    _stream(stream, dev)), where)
-    return table_out, used
+    dev = pool.get_device()
+    if dev < 0 or not (page_table.get_device() == lens.get_device() == dev):
+        _on_gpu(where, ("pool", pool), ("page_table", page_table), ("lens", lens))
+    n = tq_pages_workspace(rows, P)
+    ws, table_out, used = _pieces(lens, (n // 4, rows * width, 1), stream)
+    _launch(where, dev, lib.tq_pages_compact, pool.data_ptr(), planes, P, size,
+            page_table.data_ptr(), lens.data_ptr(), rows, width, page_size, table_out.data_ptr(),
+            used.data_ptr(), ws.data_ptr(), n, _raw_stream(stream, dev))
+    return table_out.view(rows, width), used
 
 
 def tq_pages_copy(pool, src, dst, stream=None):
     """Copy page src[i] over page dst[i] in every plane of pool [planes][pages][...]."""
-    import torch
     where = "tq_pages_copy"
     planes, P, size = _pool(pool, where)
-    if not torch.is_tensor(src) or src.dim() != 1:
+    if not isinstance(src, _torch.Tensor) or src.dim() != 1:
         raise TQError(TQ_ERR_SHAPE, f"{where}: src must be a 1-D tensor")
-    _int32(src, "src", None, where)
+    _int32(src, "src", src.shape, where)
     _int32(dst, "dst", src.shape, where)
-    _on_gpu(where, ("pool", pool), ("src", src), ("dst", dst))
-    with _device_of(pool):
-        _check(lib.tq_pages_copy(pool.data_ptr(), planes, P, size, src.data_ptr(), dst.data_ptr(),
-                                 src.shape[0], _stream(stream, pool.device)), where)
+    dev = pool.get_device()
+    if dev < 0 or not (src.get_device() == dst.get_device() == dev):
+        _on_gpu(where, ("pool", pool), ("src", src), ("dst", dst))
+    _launch(where, dev, lib.tq_pages_copy, pool.data_ptr(), planes, P, size, src.data_ptr(),
+            dst.data_ptr(), src.shape[0], _raw_stream(stream, dev))
 
 
 def raw_call(name: str, *args) -> int:

@@ -141,10 +141,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_at(const unsigned char* p
 }
 
 __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 2));
 }
 __device__ __forceinline__ u32x2 load8(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 2));
 }
 
 // Largest of the four lanes (li, g = 0..3) that hold one head.
@@ -711,7 +711,7 @@ __global__ __launch_bounds__(kAttnThreads) void paged_attention_join_kernel(Attn
   const int sub = lane / L, col = lane - sub * L;
   float4v v = {0, 0, 0, 0};
   if (sub < conc) {
-#pragma unroll 4
+#pragma unroll 8
     for (int k = sub; k < n; k += conc) {
       const float* o = part(k);
       const float f = __builtin_amdgcn_exp2f(o[at_m] - base);

@@ -57,6 +57,13 @@ __device__ __forceinline__ int entries(const PagesParams& p, int tokens) {
   return (int)(((int64_t)tokens + p.page_size - 1) / p.page_size);
 }
 
+// Pages that growing row r asks for; -1 if its row of the table is too short.
+__device__ __forceinline__ int wanted_pages(const PagesParams& p, int r, int tokens) {
+  const int64_t want = (int64_t)tokens + (p.add[r] > 0 ? p.add[r] : 0);
+  const int64_t cap = (int64_t)p.width * p.page_size;
+  return want > cap ? -1 : entries(p, (int)want) - entries(p, tokens);
+}
+
 __global__ __launch_bounds__(kPagesThreads) void pages_clear_kernel(PagesParams p) {
   const int words = (p.n_pages + 31) / 32;
   for (int i = blockIdx.x * kPagesThreads + threadIdx.x; i < p.n_pages;
@@ -101,11 +108,7 @@ __global__ __launch_bounds__(kPagesThreads) void pages_rows_kernel(PagesParams p
     }
   }
   if constexpr (OP == kGrow) {
-    if (threadIdx.x == 0) {
-      const int64_t want = (int64_t)tokens + (p.add[r] > 0 ? p.add[r] : 0);
-      const int64_t cap = (int64_t)p.width * p.page_size;
-      p.need[r] = want > cap ? -1 : entries(p, (int)want) - n;
-    }
+    if (threadIdx.x == 0) p.need[r] = wanted_pages(p, r, tokens);
   }
   for (int i = threadIdx.x; i < p.width; i += kPagesThreads) {
     int32_t id = -1;
@@ -168,8 +171,7 @@ __device__ __forceinline__ int list_free(const PagesParams& p, int limit, int* r
   return total;
 }
 
-__global__ __launch_bounds__(kScanThreads) void pages_fork_assign_kernel(PagesParams p) {
-  __shared__ int red[kScanThreads / kWave];
+__device__ __forceinline__ void fork_assign(const PagesParams& p, int* red) {
   const int t = threadIdx.x;
   int wanted = 0;
   for (int r0 = 0; r0 < p.rows; r0 += kScanThreads) {
@@ -206,8 +208,7 @@ __global__ __launch_bounds__(kScanThreads) void pages_fork_assign_kernel(PagesPa
   }
 }
 
-__global__ __launch_bounds__(kScanThreads) void pages_grow_assign_kernel(PagesParams p) {
-  __shared__ int red[kScanThreads / kWave];
+__device__ __forceinline__ void grow_assign(const PagesParams& p, int* red) {
   const int t = threadIdx.x, lane = t & 63;
   const int free_pages = list_free(p, p.n_pages, red);
   int64_t base = 0;  // pages wanted by the rows before this round
@@ -246,8 +247,7 @@ __global__ __launch_bounds__(kScanThreads) void pages_grow_assign_kernel(PagesPa
   if (t == 0) *p.result = total;
 }
 
-__global__ __launch_bounds__(kScanThreads) void pages_compact_assign_kernel(PagesParams p) {
-  __shared__ int red[kScanThreads / kWave];
+__device__ __forceinline__ void compact_assign(const PagesParams& p, int* red) {
   const int words = (p.n_pages + 31) / 32;
   const int per = (words + kScanThreads - 1) / kScanThreads;
   const int w0 = threadIdx.x * per, w1 = w0 + per < words ? w0 + per : words;
@@ -279,6 +279,90 @@ __global__ __launch_bounds__(kScanThreads) void pages_compact_assign_kernel(Page
   if (threadIdx.x == 0) {
     *p.pairs = moves;
     *p.result = used;
+  }
+}
+
+template <int OP>
+__device__ __forceinline__ void assign(const PagesParams& p, int* red) {
+  if constexpr (OP == kFork) fork_assign(p, red);
+  if constexpr (OP == kGrow) grow_assign(p, red);
+  if constexpr (OP == kCompact) compact_assign(p, red);
+}
+
+template <int OP>
+__global__ __launch_bounds__(kScanThreads) void pages_assign_kernel(PagesParams p) {
+  __shared__ int red[kScanThreads / kWave];
+  assign<OP>(p, red);
+}
+
+// All of the bookkeeping in one workgroup, with the bitmap and the rows' wishes in
+// LDS: one launch instead of three (compaction: four), for states that one
+// compute unit walks through in a few microseconds.
+constexpr int kOneRows = 256, kOneEntries = 32 * 1024, kOnePages = 64 * 1024;
+
+template <int OP>
+__global__ __launch_bounds__(kScanThreads) void pages_one_kernel(PagesParams p) {
+  __shared__ int red[kScanThreads / kWave];
+  __shared__ uint32_t sBits[kOnePages / 32];
+  __shared__ int sFrom[kOneRows], sHeld[kOneRows], sNeed[kOneRows], sLast[kOneRows];
+  const int t = threadIdx.x;
+  p.bits = sBits;
+  p.need = sNeed;
+  p.last = sLast;
+  for (int i = t; i < (p.n_pages + 31) / 32; i += kScanThreads) sBits[i] = 0;
+  if (OP == kFork && p.refs)
+    for (int i = t; i < p.n_pages; i += kScanThreads) p.refs[i] = 0;
+  int tokens = 0;
+  if (t < p.rows) {
+    int from = t;
+    if constexpr (OP == kFork) {
+      from = p.parent[t];
+      if ((uint32_t)from >= (uint32_t)p.rows_in) from = -1;
+    }
+    tokens = from < 0 ? 0 : tokens_of(p, from);
+    sFrom[t] = from;
+    sHeld[t] = entries(p, tokens);
+    sNeed[t] = 0;
+    if constexpr (OP == kFork) p.lens_out[t] = tokens;
+    if constexpr (OP == kGrow) sNeed[t] = wanted_pages(p, t, tokens);
+  }
+  __syncthreads();
+  if constexpr (OP == kFork) {
+    if (t < p.rows && sFrom[t] >= 0 && tokens % p.page_size != 0) {
+      int later = 0;
+      for (int i = 0; i < t; ++i) later |= sFrom[i] == sFrom[t];
+      sNeed[t] = later;  // until the page is known to exist
+    }
+    __syncthreads();
+  }
+  for (int i = t; i < p.rows * p.width; i += kScanThreads) {
+    const int r = i / p.width, j = i - r * p.width;
+    int32_t id = -1;
+    if (j < sHeld[r]) {
+      id = p.table[(int64_t)sFrom[r] * p.width + j];
+      const bool names = names_page(p, id);
+      if (OP == kFork && j == sHeld[r] - 1 && sNeed[r]) {
+        // only this thread looks at this row's wish here
+        sLast[r] = id;
+        if (!names) sNeed[r] = 0;
+      } else if (names) {
+        atomicOr(&sBits[id >> 5], 1u << (id & 31));
+        if (OP == kFork && p.refs) atomicAdd(&p.refs[id], 1);
+      }
+    }
+    if constexpr (OP != kCompact) p.table_out[i] = id;
+  }
+  __syncthreads();
+  assign<OP>(p, red);
+  if constexpr (OP == kCompact) {
+    __syncthreads();  // the map is complete
+    const int used = *p.result;
+    for (int i = t; i < p.rows * p.width; i += kScanThreads) {
+      const int r = i / p.width, j = i - r * p.width;
+      int32_t id = j < sHeld[r] ? p.table[i] : -1;
+      if (names_page(p, id) && id >= used) id = p.map[id];
+      p.table_out[i] = id;
+    }
   }
 }
 
@@ -360,12 +444,6 @@ PagesParams params(const PagesArgs& a) {
   return p;
 }
 
-void clear(const PagesParams& p, hipStream_t s) {
-  const int64_t blocks = (p.n_pages + kPagesThreads - 1) / kPagesThreads;
-  hipLaunchKernelGGL(pages_clear_kernel, dim3((uint32_t)(blocks < 1024 ? blocks : 1024)),
-                     dim3(kPagesThreads), 0, s, p);
-}
-
 // `most`: an upper bound on the pairs.
 hipError_t copy(unsigned char* pool, int64_t planes, int64_t n_pages, int64_t page_bytes,
                 const int32_t* src, const int32_t* dst, const int32_t* count, int64_t most,
@@ -386,36 +464,44 @@ int64_t pages_workspace_bytes(int64_t rows, int64_t n_pages) {
   return up16(4 * ((n_pages + 31) / 32)) + 2 * up16(4 * rows) + 3 * up16(4 * n_pages) + 16;
 }
 
+namespace {
+
+// The bookkeeping of one operator: in one workgroup where the state is small.
+// Measured (us, one workgroup / separate launches): TODO
+template <int OP>
+hipError_t launch_state(const PagesParams& p, hipStream_t s) {
+  if (p.rows <= kOneRows && (int64_t)p.rows * p.width <= kOneEntries && p.n_pages <= kOnePages) {
+    hipLaunchKernelGGL(pages_one_kernel<OP>, dim3(1), dim3(kScanThreads), 0, s, p);
+    return hipGetLastError();
+  }
+  const int64_t blocks = (p.n_pages + kPagesThreads - 1) / kPagesThreads;
+  hipLaunchKernelGGL(pages_clear_kernel, dim3((uint32_t)(blocks < 1024 ? blocks : 1024)),
+                     dim3(kPagesThreads), 0, s, p);
+  if (p.rows > 0)
+    hipLaunchKernelGGL(pages_rows_kernel<OP>, dim3(p.rows), dim3(kPagesThreads), 0, s, p);
+  hipLaunchKernelGGL(pages_assign_kernel<OP>, dim3(1), dim3(kScanThreads), 0, s, p);
+  if (OP == kCompact && p.rows > 0)
+    hipLaunchKernelGGL(pages_retable_kernel, dim3(p.rows), dim3(kPagesThreads), 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_pages_fork(const PagesArgs& a, hipStream_t s) {
   const PagesParams p = params(a);
-  clear(p, s);
-  if (p.rows > 0)
-    hipLaunchKernelGGL(pages_rows_kernel<kFork>, dim3(p.rows), dim3(kPagesThreads), 0, s, p);
-  hipLaunchKernelGGL(pages_fork_assign_kernel, dim3(1), dim3(kScanThreads), 0, s, p);
-  const hipError_t e = hipGetLastError();
+  const hipError_t e = launch_state<kFork>(p, s);
   if (e != hipSuccess) return e;
   return copy(p.pool, p.planes, p.n_pages, p.page_bytes, p.src, p.dst, p.pairs,
               a.rows < a.n_pages ? a.rows : a.n_pages, s);
 }
 
 hipError_t launch_pages_grow(const PagesArgs& a, hipStream_t s) {
-  const PagesParams p = params(a);
-  clear(p, s);
-  if (p.rows > 0)
-    hipLaunchKernelGGL(pages_rows_kernel<kGrow>, dim3(p.rows), dim3(kPagesThreads), 0, s, p);
-  hipLaunchKernelGGL(pages_grow_assign_kernel, dim3(1), dim3(kScanThreads), 0, s, p);
-  return hipGetLastError();
+  return launch_state<kGrow>(params(a), s);
 }
 
 hipError_t launch_pages_compact(const PagesArgs& a, hipStream_t s) {
   const PagesParams p = params(a);
-  clear(p, s);
-  if (p.rows > 0)
-    hipLaunchKernelGGL(pages_rows_kernel<kCompact>, dim3(p.rows), dim3(kPagesThreads), 0, s, p);
-  hipLaunchKernelGGL(pages_compact_assign_kernel, dim3(1), dim3(kScanThreads), 0, s, p);
-  if (p.rows > 0)
-    hipLaunchKernelGGL(pages_retable_kernel, dim3(p.rows), dim3(kPagesThreads), 0, s, p);
-  const hipError_t e = hipGetLastError();
+  const hipError_t e = launch_state<kCompact>(p, s);
   if (e != hipSuccess) return e;
   return copy(p.pool, p.planes, p.n_pages, p.page_bytes, p.src, p.dst, p.pairs,
               a.n_pages / 2 + 1, s);
