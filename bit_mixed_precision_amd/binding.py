@@ -569,11 +569,12 @@ def _kind(t, name, where, f32=False):
 
 
 def _heads(t, name, where):
-    """Shape of a [tokens][heads][D] tensor, the numbers of a head adjacent."""
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+    """Shape and strides of a [tokens][heads][D] tensor, the numbers of a head adjacent."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or (strides[2] != 1 and shape[2] > 1):
         raise TQError(TQ_ERR_SHAPE, f"{where}: {name} must be [tokens][heads][D] with adjacent "
-                                    f"numbers, not {tuple(t.shape)} at strides {t.stride()}")
-    return t.shape
+                                    f"numbers, not {tuple(shape)} at strides {strides}")
+    return shape, strides
 
 
 def _same(t, name, like, shape, where, strided=False):
@@ -615,11 +616,22 @@ def _cache(k_pages, v_pages, like, D, where):
 
 def _table(table, where):
     """(n_pos, rot) of a cosine / sine table [n_pos][rot / 2][2]."""
-    if not isinstance(table, _torch.Tensor) or table.dim() != 3 or table.shape[2] != 2:
+    shape = table.shape if isinstance(table, _torch.Tensor) else ()
+    if len(shape) != 3 or shape[2] != 2:
         raise TQError(TQ_ERR_SHAPE, f"{where}: table must be [positions][rot / 2][2]")
     if table.dtype is not _torch.float32 or not table.is_contiguous():
         _need(table, "table", "f32", None, where)
-    return table.shape[0], 2 * table.shape[1]
+    return shape[0], 2 * shape[1]
+
+
+def _rows(t, name, where):
+    """(rows, width) of a contiguous int32 matrix."""
+    shape = t.shape if isinstance(t, _torch.Tensor) else ()
+    if len(shape) != 2:
+        raise TQError(TQ_ERR_SHAPE, f"{where}: {name} must be a 2-D tensor")
+    if t.dtype is not _I32T or not t.is_contiguous():
+        _need(t, name, "i32", None, where)
+    return shape
 
 
 def _empty(like, shape, dtype, stream):
@@ -627,9 +639,9 @@ def _empty(like, shape, dtype, stream):
     runs on: the allocator hands a freed block out again in the order of its own
     stream, so memory of the current stream must not be written on another one."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return _torch.empty(shape, dtype=dtype, device=like.device)
     with _torch.cuda.stream(_torch.cuda.ExternalStream(stream, like.device)):
-        return like.new_empty(shape, dtype=dtype)
+        return _torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _pieces(like, sizes, stream):
@@ -672,7 +684,7 @@ def tq_rope(X, table, positions, interleaved: bool = False, inverse: bool = Fals
     X; a new contiguous tensor when None."""
     where = "tq_rope"
     kind = _kind(X, "X", where, f32=True)
-    T, H, D = _heads(X, "X", where)
+    (T, H, D), xs = _heads(X, "X", where)
     n_pos, rot = _table(table, where)
     _int32(positions, "positions", (T,), where)
     if Y is not None:
@@ -683,7 +695,7 @@ def tq_rope(X, table, positions, interleaved: bool = False, inverse: bool = Fals
         _on_gpu(where, ("X", X), ("table", table), ("positions", positions), ("Y", Y))
     if Y is None:
         Y = _empty(X, (T, H, D), X.dtype, stream)
-    xs, ys = X.stride(), Y.stride()
+    ys = Y.stride()
     _launch(where, dev, lib.tq_rope, kind, X.data_ptr(), xs[0], xs[1], Y.data_ptr(), ys[0], ys[1],
             table.data_ptr(), n_pos, rot, positions.data_ptr(), T, H, D, interleaved, inverse,
             _raw_stream(stream, dev))
@@ -698,14 +710,12 @@ def tq_rope_append(QKV, table, positions, page_table, k_pages, v_pages, interlea
     [pages][slots][Hkv][D], any strides, numbers of a head adjacent."""
     where = "tq_rope_append"
     kind = _kind(QKV, "QKV", where)
-    T, H, D = _heads(QKV, "QKV", where)
-    xs = QKV.stride()
+    (T, H, D), xs = _heads(QKV, "QKV", where)
     if H > 1 and xs[1] != D:
         raise TQError(TQ_ERR_SHAPE, f"{where}: the heads of QKV must be adjacent")
     n_pos, rot = _table(table, where)
     _int32(positions, "positions", (T,), where)
-    n_seqs, width = _rank2(page_table, "page_table", where)
-    _int32(page_table, "page_table", (n_seqs, width), where)
+    n_seqs, width = _rows(page_table, "page_table", where)
     if seqs is not None:
         _int32(seqs, "seqs", (T,), where)
     P, size, Hkv, page_stride, row_stride, head_stride = _cache(k_pages, v_pages, QKV, D, where)
@@ -749,10 +759,11 @@ def tq_paged_attention(Q, k_pages, v_pages, page_table, lens, scale: float | Non
     and lse float32 [B][Hq] with return_lse.  scale: 1 / sqrt(D) when None."""
     where = "tq_paged_attention"
     kind = _kind(Q, "Q", where)
-    B, Hq, D = _heads(Q, "Q", where)
+    (B, Hq, D), qs = _heads(Q, "Q", where)
     P, size, Hkv, page_stride, row_stride, head_stride = _cache(k_pages, v_pages, Q, D, where)
-    width = _rank2(page_table, "page_table", where)[1]
-    _int32(page_table, "page_table", (B, width), where)
+    rows, width = _rows(page_table, "page_table", where)
+    if rows != B:
+        raise TQError(TQ_ERR_SHAPE, f"{where}: page_table has {rows} rows, Q {B}")
     _int32(lens, "lens", (B,), where)
     if out is not None:
         _same(out, "out", Q, (B, Hq, D), where)
@@ -776,7 +787,6 @@ def tq_paged_attention(Q, k_pages, v_pages, page_table, lens, scale: float | Non
     if out is None:
         out = _empty(Q, (B, Hq, D), Q.dtype, stream)
     lse = _empty(Q, (B, Hq), _torch.float32, stream) if return_lse else None
-    qs = Q.stride()
     _launch(where, dev, lib.tq_paged_attention, kind, Q.data_ptr(), qs[0], qs[1],
             k_pages.data_ptr(), v_pages.data_ptr(), P, size, page_stride, row_stride, head_stride,
             page_table.data_ptr(), width, lens.data_ptr(), B, Hq, Hkv, D,
@@ -797,8 +807,7 @@ def _pool(pool, where):
 
 
 def _state(page_table, lens, where):
-    rows, width = _rank2(page_table, "page_table", where)
-    _int32(page_table, "page_table", (rows, width), where)
+    rows, width = _rows(page_table, "page_table", where)
     _int32(lens, "lens", (rows,), where)
     return rows, width
 

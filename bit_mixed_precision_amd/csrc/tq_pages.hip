@@ -38,8 +38,9 @@ struct PagesParams {
   uint32_t* bits;   // ceil(n_pages / 32)
   int32_t* need;    // [rows] pages wanted by a row
   int32_t* last;    // [rows] fork: the page a row copies
-  int32_t* src;     // [n_pages]
-  int32_t* dst;     // [n_pages]: also the list of free pages
+  int32_t* src;     // [n_pages] copies: from
+  int32_t* dst;     // [n_pages] copies: to
+  int32_t* spare;   // [n_pages] free pages in ascending order
   int32_t* map;     // [n_pages] compact: where a page goes
   int32_t* pairs;   // [1] number of (src, dst)
 };
@@ -150,7 +151,7 @@ __device__ __forceinline__ uint32_t valid_bits(const PagesParams& p, int word) {
   return left >= 32 ? 0xffffffffu : (1u << left) - 1;
 }
 
-// One workgroup: ranks the free pages, in ascending order, into dst[0 .. limit)
+// One workgroup: ranks the free pages, in ascending order, into spare[0 .. limit)
 // and returns how many there are in all.
 __device__ __forceinline__ int list_free(const PagesParams& p, int limit, int* red) {
   const int words = (p.n_pages + 31) / 32;
@@ -163,36 +164,43 @@ __device__ __forceinline__ int list_free(const PagesParams& p, int limit, int* r
   for (int w = w0; w < w1 && rank < limit; ++w) {
     uint32_t f = ~p.bits[w] & valid_bits(p, w);
     while (f && rank < limit) {
-      p.dst[rank++] = w * 32 + __ffs(f) - 1;
+      p.spare[rank++] = w * 32 + __ffs(f) - 1;
       f &= f - 1;
     }
   }
-  __syncthreads();  // dst is complete for this workgroup
+  __syncthreads();  // the list is complete for this workgroup
   return total;
 }
 
 __device__ __forceinline__ void fork_assign(const PagesParams& p, int* red) {
   const int t = threadIdx.x;
-  int wanted = 0;
-  for (int r0 = 0; r0 < p.rows; r0 += kScanThreads) {
+  // wishes are 0 or 1; of the rows of the first round (mostly all) the rank is kept
+  const bool first = t < p.rows && p.need[t];
+  int wanted;
+  const int first_rank = scan_block(first, red, wanted);
+  const int first_total = wanted;
+  for (int r0 = kScanThreads; r0 < p.rows; r0 += kScanThreads) {
     int total;
     (void)scan_block(r0 + t < p.rows ? p.need[r0 + t] : 0, red, total);
     wanted += total;
   }
   const int free_pages = list_free(p, wanted, red);
-  int base = 0, kept = 0;
+  int base = 0;
   for (int r0 = 0; r0 < p.rows; r0 += kScanThreads) {
     const int r = r0 + t;
-    const int need = r < p.rows ? p.need[r] : 0;
-    int total;
-    const int rank = base + scan_block(need, red, total);
+    int need = first, rank = first_rank, total = first_total;
+    if (r0 > 0) {
+      need = r < p.rows ? p.need[r] : 0;
+      rank = base + scan_block(need, red, total);
+    }
     base += total;
     if (need) {
       const int tokens = p.lens_out[r];
       int32_t* out = p.table_out + (int64_t)r * p.width + entries(p, tokens) - 1;
       if (rank < free_pages) {
-        const int32_t id = p.dst[rank];
+        const int32_t id = p.spare[rank];
         p.src[rank] = p.last[r];
+        p.dst[rank] = id;
         *out = id;
         if (p.refs) p.refs[id] = 1;
       } else {
@@ -201,8 +209,8 @@ __device__ __forceinline__ void fork_assign(const PagesParams& p, int* red) {
       }
     }
   }
-  kept = wanted < free_pages ? wanted : free_pages;
   if (t == 0) {
+    const int kept = wanted < free_pages ? wanted : free_pages;
     *p.pairs = kept;
     *p.result = wanted - kept;
   }
@@ -239,7 +247,7 @@ __device__ __forceinline__ void grow_assign(const PagesParams& p, int* red) {
       const int from = __shfl((int)rank, k, kWave);
       const int row = r0 + (t & ~63) + k;
       int32_t* out = p.table_out + (int64_t)row * p.width + entries(p, tokens_of(p, row));
-      for (int i = lane; i < cnt; i += kWave) out[i] = p.dst[from + i];
+      for (int i = lane; i < cnt; i += kWave) out[i] = p.spare[from + i];
     }
   }
   int total;
@@ -296,114 +304,110 @@ __global__ __launch_bounds__(kScanThreads) void pages_assign_kernel(PagesParams 
 }
 
 // All of the bookkeeping in one workgroup, with the bitmap and the rows' wishes in
-// LDS: one launch instead of three (compaction: four), for states that one
-// compute unit walks through in a few microseconds.
-constexpr int kOneRows = 256, kOneEntries = 32 * 1024, kOnePages = 64 * 1024;
+// LDS: one launch instead of three, for states that one compute unit walks
+// through in a few microseconds.
+constexpr int kOneRows = 256, kOneEntries = 64 * 1024, kOnePages = 64 * 1024;
 
 template <int OP>
 __global__ __launch_bounds__(kScanThreads) void pages_one_kernel(PagesParams p) {
   __shared__ int red[kScanThreads / kWave];
   __shared__ uint32_t sBits[kOnePages / 32];
   __shared__ int sFrom[kOneRows], sHeld[kOneRows], sNeed[kOneRows], sLast[kOneRows];
+  __shared__ int sSpare[kOneRows];
   const int t = threadIdx.x;
   p.bits = sBits;
   p.need = sNeed;
   p.last = sLast;
+  if (OP == kFork) p.spare = sSpare;  // a page a row at most
   for (int i = t; i < (p.n_pages + 31) / 32; i += kScanThreads) sBits[i] = 0;
   if (OP == kFork && p.refs)
     for (int i = t; i < p.n_pages; i += kScanThreads) p.refs[i] = 0;
-  int tokens = 0;
   if (t < p.rows) {
     int from = t;
     if constexpr (OP == kFork) {
       from = p.parent[t];
       if ((uint32_t)from >= (uint32_t)p.rows_in) from = -1;
     }
-    tokens = from < 0 ? 0 : tokens_of(p, from);
+    const int tokens = from < 0 ? 0 : tokens_of(p, from);
     sFrom[t] = from;
     sHeld[t] = entries(p, tokens);
-    sNeed[t] = 0;
+    sNeed[t] = OP == kFork && from >= 0 && tokens % p.page_size != 0;  // may want a copy
     if constexpr (OP == kFork) p.lens_out[t] = tokens;
     if constexpr (OP == kGrow) sNeed[t] = wanted_pages(p, t, tokens);
   }
   __syncthreads();
-  if constexpr (OP == kFork) {
-    if (t < p.rows && sFrom[t] >= 0 && tokens % p.page_size != 0) {
+  const int lane = t & 63;
+  for (int r = t >> 6; r < p.rows; r += kScanThreads / kWave) {
+    const int held = sHeld[r];
+    bool wants = false;  // a copy of the last page: an earlier row continues the same one
+    if (OP == kFork && sNeed[r]) {
+      const int from = sFrom[r];
       int later = 0;
-      for (int i = 0; i < t; ++i) later |= sFrom[i] == sFrom[t];
-      sNeed[t] = later;  // until the page is known to exist
+      for (int i = lane; i < r; i += kWave) later |= sFrom[i] == from;
+      wants = __any(later);
+      if (lane == 0) sNeed[r] = wants;
     }
-    __syncthreads();
-  }
-  for (int i = t; i < p.rows * p.width; i += kScanThreads) {
-    const int r = i / p.width, j = i - r * p.width;
-    int32_t id = -1;
-    if (j < sHeld[r]) {
-      id = p.table[(int64_t)sFrom[r] * p.width + j];
-      const bool names = names_page(p, id);
-      if (OP == kFork && j == sHeld[r] - 1 && sNeed[r]) {
-        // only this thread looks at this row's wish here
-        sLast[r] = id;
-        if (!names) sNeed[r] = 0;
-      } else if (names) {
-        atomicOr(&sBits[id >> 5], 1u << (id & 31));
-        if (OP == kFork && p.refs) atomicAdd(&p.refs[id], 1);
+    const int32_t* row = p.table + (int64_t)(held ? sFrom[r] : 0) * p.width;
+    const int end = OP == kCompact ? held : p.width;
+#pragma unroll 4
+    for (int j = lane; j < end; j += kWave) {
+      int32_t id = -1;
+      if (j < held) {
+        id = row[j];
+        const bool names = names_page(p, id);
+        if (wants && j == held - 1) {
+          sLast[r] = id;
+          if (!names) sNeed[r] = 0;
+        } else if (names) {
+          atomicOr(&sBits[id >> 5], 1u << (id & 31));
+          if (OP == kFork && p.refs) atomicAdd(&p.refs[id], 1);
+        }
       }
+      if constexpr (OP != kCompact) p.table_out[(int64_t)r * p.width + j] = id;
     }
-    if constexpr (OP != kCompact) p.table_out[i] = id;
   }
   __syncthreads();
   assign<OP>(p, red);
-  if constexpr (OP == kCompact) {
-    __syncthreads();  // the map is complete
-    const int used = *p.result;
-    for (int i = t; i < p.rows * p.width; i += kScanThreads) {
-      const int r = i / p.width, j = i - r * p.width;
-      int32_t id = j < sHeld[r] ? p.table[i] : -1;
-      if (names_page(p, id) && id >= used) id = p.map[id];
-      p.table_out[i] = id;
-    }
-  }
-}
-
-// Rewrites the table after compaction: one workgroup per row.
-__global__ __launch_bounds__(kPagesThreads) void pages_retable_kernel(PagesParams p) {
-  const int r = blockIdx.x;
-  const int n = entries(p, tokens_of(p, r));
-  const int32_t* row = p.table + (int64_t)r * p.width;
-  int32_t* out = p.table_out + (int64_t)r * p.width;
-  const int used = *p.result;
-  for (int i = threadIdx.x; i < p.width; i += kPagesThreads) {
-    int32_t id = i < n ? row[i] : -1;
-    if (i < n && names_page(p, id) && id >= used) id = p.map[id];
-    out[i] = id;
-  }
 }
 
 constexpr int kCopyBytes = kPagesThreads * 16 * 4;  // bytes of one workgroup's step
 
-// pairs x planes x pieces of a page, taken in turn by a fixed grid.
-__global__ __launch_bounds__(kPagesThreads) void pages_copy_kernel(
-    unsigned char* pool, int64_t planes, int32_t n_pages, int64_t page_bytes, const int32_t* src,
-    const int32_t* dst, const int32_t* count, int64_t n) {
-  const int64_t pieces = (page_bytes + kCopyBytes - 1) / kCopyBytes;
-  const int64_t total = (count ? (int64_t)*count : n) * planes * pieces;
-  for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
+// Copies pairs x planes x pieces of a page, taken in turn by all but the first
+// `table_blocks` workgroups; those rewrite the table's rows after compaction.
+__global__ __launch_bounds__(kPagesThreads) void pages_move_kernel(PagesParams p, int64_t n,
+                                                                   int table_blocks) {
+  if ((int)blockIdx.x < table_blocks) {
+    const int used = *p.result;
+    for (int r = blockIdx.x; r < p.rows; r += table_blocks) {
+      const int held = entries(p, tokens_of(p, r));
+      const int64_t row = (int64_t)r * p.width;
+      for (int i = threadIdx.x; i < p.width; i += kPagesThreads) {
+        int32_t id = i < held ? p.table[row + i] : -1;
+        if (names_page(p, id) && id >= used) id = p.map[id];
+        p.table_out[row + i] = id;
+      }
+    }
+    return;
+  }
+  const int64_t blocks = gridDim.x - table_blocks;
+  const int64_t pieces = (p.page_bytes + kCopyBytes - 1) / kCopyBytes;
+  const int64_t total = (p.pairs ? (int64_t)*p.pairs : n) * p.planes * pieces;
+  for (int64_t i = (int)blockIdx.x - table_blocks; i < total; i += blocks) {
     const int64_t piece = i % pieces, rest = i / pieces;
-    const int64_t plane = rest % planes, pair = rest / planes;
-    const int32_t s = src[pair], d = dst[pair];
-    if ((uint32_t)s >= (uint32_t)n_pages || (uint32_t)d >= (uint32_t)n_pages) continue;
-    const unsigned char* from = pool + (plane * n_pages + s) * page_bytes;
-    unsigned char* to = pool + (plane * n_pages + d) * page_bytes;
+    const int64_t plane = rest % p.planes, pair = rest / p.planes;
+    const int32_t s = p.src[pair], d = p.dst[pair];
+    if (!names_page(p, s) || !names_page(p, d)) continue;
+    const unsigned char* from = p.pool + (plane * p.n_pages + s) * p.page_bytes;
+    unsigned char* to = p.pool + (plane * p.n_pages + d) * p.page_bytes;
     const int64_t at = piece * kCopyBytes + threadIdx.x * 16;
     u32x4 v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (at + k * kPagesThreads * 16 < page_bytes)
+      if (at + k * kPagesThreads * 16 < p.page_bytes)
         v[k] = *reinterpret_cast<const u32x4*>(from + at + k * kPagesThreads * 16);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (at + k * kPagesThreads * 16 < page_bytes)
+      if (at + k * kPagesThreads * 16 < p.page_bytes)
         *reinterpret_cast<u32x4*>(to + at + k * kPagesThreads * 16) = v[k];
   }
 }
@@ -439,29 +443,29 @@ PagesParams params(const PagesArgs& a) {
   p.last = reinterpret_cast<int32_t*>(take(a.rows));
   p.src = reinterpret_cast<int32_t*>(take(a.n_pages));
   p.dst = reinterpret_cast<int32_t*>(take(a.n_pages));
+  p.spare = reinterpret_cast<int32_t*>(take(a.n_pages));
   p.map = reinterpret_cast<int32_t*>(take(a.n_pages));
   p.pairs = reinterpret_cast<int32_t*>(take(1));
   return p;
 }
 
-// `most`: an upper bound on the pairs.
-hipError_t copy(unsigned char* pool, int64_t planes, int64_t n_pages, int64_t page_bytes,
-                const int32_t* src, const int32_t* dst, const int32_t* count, int64_t most,
-                hipStream_t s) {
-  const int64_t pieces = (page_bytes + kCopyBytes - 1) / kCopyBytes;
+// The copies, at most `most` of them, and the new table where `retable` is set.
+hipError_t move(const PagesParams& p, int64_t most, bool retable, hipStream_t s) {
+  const int64_t pieces = (p.page_bytes + kCopyBytes - 1) / kCopyBytes;
   const int64_t grid = 8 * device_cus();
-  if (most == 0 || planes == 0) return hipSuccess;
-  const int64_t items = most > grid ? grid : most * planes * pieces;  // no overflow: see limits
-  hipLaunchKernelGGL(pages_copy_kernel, dim3((uint32_t)(items < grid ? items : grid)),
-                     dim3(kPagesThreads), 0, s, pool, planes, (int32_t)n_pages, page_bytes, src, dst,
-                     count, most);
+  const int64_t items = most > grid && p.planes ? grid : most * p.planes * pieces;
+  const int table_blocks = !retable ? 0 : p.rows < 256 ? p.rows : 256;
+  const int64_t blocks = table_blocks + (items < grid ? items : grid);
+  if (blocks == 0) return hipSuccess;
+  hipLaunchKernelGGL(pages_move_kernel, dim3((uint32_t)blocks), dim3(kPagesThreads), 0, s, p, most,
+                     table_blocks);
   return hipGetLastError();
 }
 
 }  // namespace
 
 int64_t pages_workspace_bytes(int64_t rows, int64_t n_pages) {
-  return up16(4 * ((n_pages + 31) / 32)) + 2 * up16(4 * rows) + 3 * up16(4 * n_pages) + 16;
+  return up16(4 * ((n_pages + 31) / 32)) + 2 * up16(4 * rows) + 4 * up16(4 * n_pages) + 16;
 }
 
 namespace {
@@ -480,8 +484,6 @@ hipError_t launch_state(const PagesParams& p, hipStream_t s) {
   if (p.rows > 0)
     hipLaunchKernelGGL(pages_rows_kernel<OP>, dim3(p.rows), dim3(kPagesThreads), 0, s, p);
   hipLaunchKernelGGL(pages_assign_kernel<OP>, dim3(1), dim3(kScanThreads), 0, s, p);
-  if (OP == kCompact && p.rows > 0)
-    hipLaunchKernelGGL(pages_retable_kernel, dim3(p.rows), dim3(kPagesThreads), 0, s, p);
   return hipGetLastError();
 }
 
@@ -491,8 +493,7 @@ hipError_t launch_pages_fork(const PagesArgs& a, hipStream_t s) {
   const PagesParams p = params(a);
   const hipError_t e = launch_state<kFork>(p, s);
   if (e != hipSuccess) return e;
-  return copy(p.pool, p.planes, p.n_pages, p.page_bytes, p.src, p.dst, p.pairs,
-              a.rows < a.n_pages ? a.rows : a.n_pages, s);
+  return move(p, a.rows < a.n_pages ? a.rows : a.n_pages, false, s);
 }
 
 hipError_t launch_pages_grow(const PagesArgs& a, hipStream_t s) {
@@ -503,14 +504,20 @@ hipError_t launch_pages_compact(const PagesArgs& a, hipStream_t s) {
   const PagesParams p = params(a);
   const hipError_t e = launch_state<kCompact>(p, s);
   if (e != hipSuccess) return e;
-  return copy(p.pool, p.planes, p.n_pages, p.page_bytes, p.src, p.dst, p.pairs,
-              a.n_pages / 2 + 1, s);
+  return move(p, a.n_pages / 2 + 1, true, s);
 }
 
 hipError_t launch_pages_copy(unsigned char* pool, int64_t planes, int64_t n_pages,
                              int64_t page_bytes, const int32_t* src, const int32_t* dst, int64_t n,
                              hipStream_t s) {
-  return copy(pool, planes, n_pages, page_bytes, src, dst, nullptr, n, s);
+  PagesParams p{};
+  p.pool = pool;
+  p.planes = planes;
+  p.n_pages = (int32_t)n_pages;
+  p.page_bytes = page_bytes;
+  p.src = const_cast<int32_t*>(src);  // read only
+  p.dst = const_cast<int32_t*>(dst);
+  return move(p, n, false, s);
 }
 
 }  // namespace tq
