@@ -249,19 +249,32 @@ __device__ __forceinline__ void finish(const AttnParams& p, int b, int head, int
   if (p.lse && d == 0) p.lse[at] = lse_of<BF>(m, sum);
 }
 
+// Workgroups per CU, for which the registers are laid out: enough bytes in flight,
+// and more only spill.  Measured (us): heads of 128, 96 sequences of 2048 .. 8192
+// tokens, 8 key heads: 2 285, 3 322; heads of 64, 8 sequences of 32768, 8 key
+// heads: 2 110, 3 99, 4 114; heads of 256, the same with 2 key heads: 1 97, 2 131.
+__host__ __device__ constexpr int blocks_per_cu(int64_t D) { return D > 128 ? 1 : D > 64 ? 2 : 3; }
+
 // DV: 64, 128 or 256, the head dimension rounded up (D <= DV, D % 8 == 0).
 // UNI: the page size is a multiple of 16, so a half tile lies in one page and
 // its base address is uniform.
 template <bool BF, int DV, bool UNI>
-__global__ __launch_bounds__(kAttnThreads, DV == 256 ? 2 : 3) void paged_attention_kernel(
+__global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attention_kernel(
     AttnParams p) {
   constexpr int KS = DV / 32;             // MFMA steps of a score
   constexpr int NE = DV / 16;             // V operands (numbers per lane)
   constexpr int NV = DV == 256 ? 2 : 1;   // pieces of a head: LN numbers per lane each
   constexpr int LN = DV == 64 ? 4 : 8;
   constexpr int PW = LN * 16;             // numbers of a piece
+  constexpr int KC = DV / 8;              // 16-byte pieces of a key
+  constexpr int KR = kWave / KC;          // keys that one load covers
+  // Keys are loaded as whole rows, like values, and turned in LDS; heads of more
+  // than 128 numbers are loaded in operand order instead (64 bytes of 16 rows).
+  constexpr bool LDSK = DV <= 128;
   // partial sums of this workgroup's waves: [wave][first, last][heads][D + 4]
   extern __shared__ __attribute__((aligned(16))) float sO[];
+  // half a tile of keys on its way from load order to operand order, per wave
+  __shared__ u32x4 sK[LDSK ? kAttnWaves * 16 * KC : 1];
   __shared__ float sM[2 * kAttnWaves][kHeads], sL[2 * kAttnWaves][kHeads];
   __shared__ int sRow[2 * kAttnWaves], sEnds[2 * kAttnWaves], sLast[2 * kAttnWaves];
 
@@ -324,11 +337,11 @@ __global__ __launch_bounds__(kAttnThreads, DV == 256 ? 2 : 3) void paged_attenti
   u32x4 vreg[8][NV];  // DV == 64 uses the first two dwords of each
   const uint32_t rs = (uint32_t)p.row_stride;
   // byte offsets of this lane's pieces in a half tile, out of range past the head's end
-  const uint32_t koff = li * rs + g * 16;
+  const int kc = LDSK ? lane % KC : g, kr = LDSK ? lane / KC : li;  // its piece and its key
+  const uint32_t koff = kc * 8 < p.D ? kr * rs + kc * 16 : kOut;
   uint32_t voff[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) voff[j] = li * LN < p.D ? (g * 4 + j) * rs + li * (LN * 2) : kOut;
-  const bool kpart = g * 8 < p.D % 32;  // the step that holds the head's end
 
   // where a tile's tokens lie
   struct Place {
@@ -378,21 +391,27 @@ __global__ __launch_bounds__(kAttnThreads, DV == 256 ? 2 : 3) void paged_attenti
     for (int a = 0; a < 2; ++a) {
       if constexpr (UNI) {
         const auto r = base_of(p.K, c, w, a);
-        const int t = c.tile * kTileTokens + 16 * a + li;
-        const uint32_t off = (uint32_t)(t - c.r.lo) < span_of(c, w, a) ? koff : kOut;
+        const int t = c.tile * kTileTokens + 16 * a + kr;
+        const uint32_t span = span_of(c, w, a);
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
-          const bool in = i * 32 + 32 <= p.D || (i * 32 < p.D && kpart);
-          kreg[a][i] = load16(r, in ? off + i * 64 : kOut);
+          if constexpr (LDSK) {
+            const bool in = (uint32_t)(t + i * KR - c.r.lo) < span;
+            kreg[a][i] = load16(r, in ? koff + i * KR * rs : kOut);
+          } else {
+            const bool in = ((uint32_t)(t - c.r.lo) < span) & (i * 32 + g * 8 < p.D);
+            kreg[a][i] = load16(r, in ? koff + i * 64 : kOut);
+          }
         }
       } else {
-        const int64_t o = shfl64(w.off, 16 * a + li);
-        const unsigned char* k = p.K + (c.h / p.qtiles) * p.head_stride + o;
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
+          const int64_t o = shfl64(w.off, 16 * a + (LDSK ? i * KR : 0) + kr);
+          const int d = (LDSK ? 0 : i * 32) + kc * 8;
+          const unsigned char* k = p.K + (c.h / p.qtiles) * p.head_stride + o + d * 2;
           kreg[a][i] = u32x4{0, 0, 0, 0};
-          if (o >= 0 && i * 32 + g * 8 < p.D)
-            kreg[a][i] = *reinterpret_cast<const u32x4*>(k + i * 64 + g * 16);
+          if (o >= 0 && d < p.D)
+            kreg[a][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(k));
         }
       }
     }
@@ -428,9 +447,10 @@ __global__ __launch_bounds__(kAttnThreads, DV == 256 ? 2 : 3) void paged_attenti
             vreg[4 * a + j][i] = u32x4{0, 0, 0, 0};
             if (o >= 0 && i * PW + li * LN < p.D) {
               if constexpr (LN == 8) {
-                vreg[4 * a + j][i] = *reinterpret_cast<const u32x4*>(v + i * PW * 2);
+                vreg[4 * a + j][i] =
+                    __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(v + i * PW * 2));
               } else {
-                const u32x2 x = *reinterpret_cast<const u32x2*>(v);
+                const u32x2 x = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(v));
                 vreg[4 * a + j][i] = u32x4{x[0], x[1], 0, 0};
               }
             }
@@ -481,8 +501,22 @@ __global__ __launch_bounds__(kAttnThreads, DV == 256 ? 2 : 3) void paged_attenti
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
         s[a] = float4v{0, 0, 0, 0};
+        if constexpr (LDSK) {
+          // to operand order (lane li: key li, pieces 4 i + g); piece c of key t sits
+          // at c ^ t, so that 16 keys' reads of one piece spread over the banks
+          u32x4* turn = sK + wave * 16 * KC;
 #pragma unroll
-        for (int i = 0; i < KS; ++i) s[a] = mma<BF>(kreg[a][i], q[i], s[a]);
+          for (int i = 0; i < KS; ++i)
+            turn[(i * KR + kr) * KC + (kc ^ ((i * KR + kr) & (KC - 1)))] = kreg[a][i];
+          __builtin_amdgcn_wave_barrier();
+#pragma unroll
+          for (int i = 0; i < KS; ++i)
+            s[a] = mma<BF>(turn[li * KC + ((4 * i + g) ^ (li & (KC - 1)))], q[i], s[a]);
+          __builtin_amdgcn_wave_barrier();
+        } else {
+#pragma unroll
+          for (int i = 0; i < KS; ++i) s[a] = mma<BF>(kreg[a][i], q[i], s[a]);
+        }
       }
       if (more) load_k(next, w_next);
 
@@ -678,62 +712,122 @@ __global__ __launch_bounds__(kAttnThreads, DV == 256 ? 2 : 3) void paged_attenti
 }
 
 // Joins the partial sums of the rows that span workgroups of the first kernel:
-// one wave per query head of the row that workgroup blockIdx.x began and left
-// unfinished, D / 4 lanes on each part and as many parts at once as that allows.
+// one workgroup per four query heads of the row that workgroup blockIdx.x began
+// and left unfinished.  D / 4 lanes take a part, as many parts at once as that
+// allows, and the waves take turns.
+constexpr int kJoinHeads = 4;
+constexpr int kMostBlocks = 1024;  // of the first kernel: parts of a row at most
+
 template <bool BF>
 __global__ __launch_bounds__(kAttnThreads) void paged_attention_join_kernel(AttnParams p) {
+  __shared__ float sW[kMostBlocks * kJoinHeads];  // weight of each part
+  __shared__ float sRed[2][kAttnWaves][kJoinHeads];
+  __shared__ __attribute__((aligned(16))) float sV[kAttnWaves][kJoinHeads][256];
   const int2 own = p.owner[blockIdx.x];
   if (own.x < 0) return;
-  const int lane = threadIdx.x & 63;
-  const int hd = uni(blockIdx.y * kAttnWaves + (threadIdx.x >> 6));
+  const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int H = p.Hkv * p.qtiles;
   const int b = own.x / H, h = own.x - b * H;
   const int hk = h / p.qtiles, qt = h - hk * p.qtiles;
-  if (hd >= kHeads || qt * kHeads + hd >= p.G) return;
   const int slot_heads = p.G < kHeads ? p.G : kHeads;
+  const int hd0 = blockIdx.y * kJoinHeads;
+  const int rest = (p.G - qt * kHeads < kHeads ? p.G - qt * kHeads : kHeads) - hd0;
+  if (rest <= 0) return;
+  const int nh = rest < kJoinHeads ? rest : kJoinHeads;
   const int64_t size = slot_floats(slot_heads, p.D);
   const int n = own.y - (int)blockIdx.x + 1;
   // part 0 is this workgroup's second slot, the others the first slots that follow
   auto part = [&](int k) {
     return p.partial + (2 * ((int64_t)blockIdx.x + k) + (k == 0 ? 1 : 0)) * size;
   };
-  const int at_m = slot_heads * p.D + hd, at_l = at_m + slot_heads;
-  float m = -INFINITY;
-  for (int k = lane; k < n; k += kWave) m = fmaxf(m, part(k)[at_m]);
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, kWave));
-  const float base = m == -INFINITY ? 0.f : m;
-  float sum = 0.f;
-  for (int k = lane; k < n; k += kWave)
-    sum += __builtin_amdgcn_exp2f(part(k)[at_m] - base) * part(k)[at_l];
-  sum = wave_sum(sum);
+  // The first sums are under way while the weights are found: four parts of four
+  // heads at once; past the end the last part, left out.
   const int L = p.D / 4, conc = kWave / L;
   const int sub = lane / L, col = lane - sub * L;
-  float4v v = {0, 0, 0, 0};
+  const int step = kAttnWaves * conc;
+  float4v x[4][kJoinHeads];
+  auto fetch = [&](int k) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int ku = k + u * step;
+      const float* o = part(ku < n ? ku : n - 1) + hd0 * p.D + col * 4;
+#pragma unroll
+      for (int i = 0; i < kJoinHeads; ++i)
+        x[u][i] = *reinterpret_cast<const float4v*>(o + (i < nh ? i : 0) * p.D);
+    }
+  };
+  // maxima and sums: thread (k, j) looks after head j of the parts k, k + 64, ..
+  constexpr int kTurn = kAttnThreads / kJoinHeads;
+  const int j = tid % kJoinHeads, k0 = tid / kJoinHeads;
+  const int at_m = slot_heads * p.D + hd0 + (j < nh ? j : 0), at_l = at_m + slot_heads;
+  const float* mine = part(k0 < n ? k0 : n - 1);
+  const float m0 = mine[at_m], l0 = mine[at_l];
+  int kx = wave * conc + sub;
+  fetch(kx);
+  float m = m0;
+  for (int k = k0 + kTurn; k < n; k += kTurn) m = fmaxf(m, part(k)[at_m]);
+#pragma unroll
+  for (int off = kJoinHeads; off < kWave; off <<= 1) m = fmaxf(m, __shfl_xor(m, off, kWave));
+  if (lane < kJoinHeads) sRed[0][wave][lane] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kAttnWaves; ++w) m = fmaxf(m, sRed[0][w][j]);
+  const float base = m == -INFINITY ? 0.f : m;
+  float sum = 0.f;
+  for (int k = k0; k < n; k += kTurn) {
+    const float w = __builtin_amdgcn_exp2f((k == k0 ? m0 : part(k)[at_m]) - base);
+    sW[k * kJoinHeads + j] = w;
+    sum += w * (k == k0 ? l0 : part(k)[at_l]);
+  }
+#pragma unroll
+  for (int off = kJoinHeads; off < kWave; off <<= 1) sum += __shfl_xor(sum, off, kWave);
+  if (lane < kJoinHeads) sRed[1][wave][lane] = sum;
+  __syncthreads();
+  float4v v[kJoinHeads];
+#pragma unroll
+  for (int i = 0; i < kJoinHeads; ++i) v[i] = float4v{0, 0, 0, 0};
   if (sub < conc) {
-#pragma unroll 8
-    for (int k = sub; k < n; k += conc) {
-      const float* o = part(k);
-      const float f = __builtin_amdgcn_exp2f(o[at_m] - base);
-      v += f * *reinterpret_cast<const float4v*>(o + hd * p.D + col * 4);
+    while (kx < n) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int ku = kx + u * step;
+        if (ku < n) {
+#pragma unroll
+          for (int i = 0; i < kJoinHeads; ++i) v[i] += sW[ku * kJoinHeads + i] * x[u][i];
+        }
+      }
+      kx += 4 * step;
+      if (kx < n) fetch(kx);
     }
   }
-  float4v t = v;
-  for (int i = 1; i < conc; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) t[e] += __shfl(v[e], (col + i * L) & 63, kWave);
-  if (sub == 0) {
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int64_t head = (int64_t)b * p.Hq + hk * p.G + qt * kHeads + hd;
+  for (int i = 0; i < kJoinHeads; ++i) {
+    float4v t = v[i];
+    for (int u = 1; u < conc; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t[e] += __shfl(v[i][e], (col + u * L) & 63, kWave);
+    if (sub == 0) *reinterpret_cast<float4v*>(&sV[wave][i][col * 4]) = t;
+  }
+  __syncthreads();
+  if (wave < nh && lane < L) {
+    float4v t = {0, 0, 0, 0};
+    float total = 0.f, mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) {
+      t += *reinterpret_cast<const float4v*>(&sV[w][wave][lane * 4]);
+      total += sRed[1][w][wave];
+      mx = fmaxf(mx, sRed[0][w][wave]);
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    const int64_t head = (int64_t)b * p.Hq + hk * p.G + qt * kHeads + hd0 + wave;
     u32x2 u;
 #pragma unroll
     for (int e = 0; e < 2; ++e)
       u[e] = to16<BF>(t[2 * e] * inv) | ((uint32_t)to16<BF>(t[2 * e + 1] * inv) << 16);
-    *reinterpret_cast<u32x2*>(p.Out + (head * p.D + col * 4) * 2) = u;
-    if (p.lse && col == 0) p.lse[head] = lse_of<BF>(m, sum);
+    *reinterpret_cast<u32x2*>(p.Out + (head * p.D + lane * 4) * 2) = u;
+    if (p.lse && lane == 0) p.lse[head] = lse_of<BF>(mx, total);
   }
 }
-
 
 FastDiv fast_div(int64_t d) {
   uint32_t s = 0;
@@ -742,6 +836,9 @@ FastDiv fast_div(int64_t d) {
   return {(uint32_t)d, (uint32_t)m, 30 + s};
 }
 
+constexpr int64_t kLdsBytes = 160 * 1024;
+// What the kernel declares itself: the keys' turning buffer and small arrays.
+int64_t static_lds(int64_t D) { return D > 128 ? 2048 : D > 64 ? 18 * 1024 : 10 * 1024; }
 int64_t lds_bytes(int heads, int64_t D) { return 2 * kAttnWaves * heads * (D + 4) * 4; }
 
 struct Grid {
@@ -758,8 +855,10 @@ Grid attn_grid(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity) 
   if (capacity <= kAttnWaves * kTileTokens) return {B * H, 0, true};
   const int64_t tiles = capacity / kTileTokens + 2;  // a window may begin inside a tile
   const int64_t most = (B * H * tiles + kAttnWaves - 1) / kAttnWaves;
-  const int64_t by_lds = 155 * 1024 / (lds_bytes(heads, D) + 2048), by_regs = D > 128 ? 2 : 3;
-  const int64_t grid = device_cus() * (by_lds < by_regs ? by_lds : by_regs);
+  const int64_t by_lds = kLdsBytes / (lds_bytes(heads, D) + static_lds(D));
+  const int64_t by_regs = blocks_per_cu(D);
+  int64_t grid = device_cus() * (by_lds < by_regs ? by_lds : by_regs);
+  if (grid > kMostBlocks) grid = kMostBlocks;
   const int64_t blocks = most < grid ? most : grid;
   return {blocks, 2 * blocks, false};
 }
@@ -768,7 +867,7 @@ template <bool BF, int DV, bool UNI>
 hipError_t launch_kernel(const AttnParams& p, int64_t grid, hipStream_t s) {
   const auto fn = paged_attention_kernel<BF, DV, UNI>;
   const int lds = (int)lds_bytes(p.G < kHeads ? p.G : kHeads, p.D);
-  if (lds > 48 * 1024) {  // above what every kernel may use
+  if (lds + static_lds(p.D) > 64 * 1024) {  // above what every kernel may use
     static std::atomic<uint64_t> done{0};
     const hipError_t e = lds_limit_once(reinterpret_cast<const void*>(fn),
                                         (int)lds_bytes(kHeads, DV), done);
@@ -792,7 +891,7 @@ hipError_t launch_t(const AttnParams& p, int64_t grid, hipStream_t s) {
   if (e != hipSuccess || p.direct) return e;
   const int heads = p.G < kHeads ? p.G : kHeads;
   hipLaunchKernelGGL((paged_attention_join_kernel<BF>),
-                     dim3((uint32_t)grid, (heads + kAttnWaves - 1) / kAttnWaves),
+                     dim3((uint32_t)grid, (heads + kJoinHeads - 1) / kJoinHeads),
                      dim3(kAttnThreads), 0, s, p);
   return hipGetLastError();
 }
