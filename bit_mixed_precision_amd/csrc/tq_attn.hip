@@ -140,11 +140,27 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_at(const unsigned char* p
                                            (short)0, (int)kSpan, kBufferWord3);
 }
 
+// NT: non-temporal, for lines that one wave reads once.  Measured (us, with /
+// without): 96 sequences of 2048 .. 8192 tokens, 8 key heads of 128: 286 / 323;
+// heads of 80, whose rows share 128-byte lines: 150 / 130; 64 query heads on one
+// key head, read by four groups of heads: 45 / 41.
+constexpr int kNonTemporal = 2;
+template <bool NT>
 __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 2));
+  return __builtin_bit_cast(
+      u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, NT ? kNonTemporal : 0));
 }
+template <bool NT>
 __device__ __forceinline__ u32x2 load8(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 2));
+  return __builtin_bit_cast(
+      u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, NT ? kNonTemporal : 0));
+}
+template <bool NT, class T>
+__device__ __forceinline__ T load_at(const unsigned char* p) {
+  if constexpr (NT)
+    return __builtin_nontemporal_load(reinterpret_cast<const T*>(p));
+  else
+    return *reinterpret_cast<const T*>(p);
 }
 
 // Largest of the four lanes (li, g = 0..3) that hold one head.
@@ -258,7 +274,7 @@ __host__ __device__ constexpr int blocks_per_cu(int64_t D) { return D > 128 ? 1 
 // DV: 64, 128 or 256, the head dimension rounded up (D <= DV, D % 8 == 0).
 // UNI: the page size is a multiple of 16, so a half tile lies in one page and
 // its base address is uniform.
-template <bool BF, int DV, bool UNI>
+template <bool BF, int DV, bool UNI, bool NT>
 __global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attention_kernel(
     AttnParams p) {
   constexpr int KS = DV / 32;             // MFMA steps of a score
@@ -397,10 +413,10 @@ __global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attenti
         for (int i = 0; i < KS; ++i) {
           if constexpr (LDSK) {
             const bool in = (uint32_t)(t + i * KR - c.r.lo) < span;
-            kreg[a][i] = load16(r, in ? koff + i * KR * rs : kOut);
+            kreg[a][i] = load16<NT>(r, in ? koff + i * KR * rs : kOut);
           } else {
             const bool in = ((uint32_t)(t - c.r.lo) < span) & (i * 32 + g * 8 < p.D);
-            kreg[a][i] = load16(r, in ? koff + i * 64 : kOut);
+            kreg[a][i] = load16<NT>(r, in ? koff + i * 64 : kOut);
           }
         }
       } else {
@@ -411,7 +427,7 @@ __global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attenti
           const unsigned char* k = p.K + (c.h / p.qtiles) * p.head_stride + o + d * 2;
           kreg[a][i] = u32x4{0, 0, 0, 0};
           if (o >= 0 && d < p.D)
-            kreg[a][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(k));
+            kreg[a][i] = load_at<NT, u32x4>(k);
         }
       }
     }
@@ -430,9 +446,9 @@ __global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attenti
           for (int i = 0; i < NV; ++i) {
             const uint32_t o = i == 0 || i * PW + li * LN < p.D ? off + i * PW * 2 : kOut;
             if constexpr (LN == 8) {
-              vreg[4 * a + j][i] = load16(r, o);
+              vreg[4 * a + j][i] = load16<NT>(r, o);
             } else {
-              const u32x2 x = load8(r, o);
+              const u32x2 x = load8<NT>(r, o);
               vreg[4 * a + j][i] = u32x4{x[0], x[1], 0, 0};
             }
           }
@@ -447,10 +463,9 @@ __global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attenti
             vreg[4 * a + j][i] = u32x4{0, 0, 0, 0};
             if (o >= 0 && i * PW + li * LN < p.D) {
               if constexpr (LN == 8) {
-                vreg[4 * a + j][i] =
-                    __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(v + i * PW * 2));
+                vreg[4 * a + j][i] = load_at<NT, u32x4>(v + i * PW * 2);
               } else {
-                const u32x2 x = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(v));
+                const u32x2 x = load_at<NT, u32x2>(v);
                 vreg[4 * a + j][i] = u32x4{x[0], x[1], 0, 0};
               }
             }
@@ -863,9 +878,9 @@ Grid attn_grid(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity) 
   return {blocks, 2 * blocks, false};
 }
 
-template <bool BF, int DV, bool UNI>
+template <bool BF, int DV, bool UNI, bool NT>
 hipError_t launch_kernel(const AttnParams& p, int64_t grid, hipStream_t s) {
-  const auto fn = paged_attention_kernel<BF, DV, UNI>;
+  const auto fn = paged_attention_kernel<BF, DV, UNI, NT>;
   const int lds = (int)lds_bytes(p.G < kHeads ? p.G : kHeads, p.D);
   if (lds + static_lds(p.D) > 64 * 1024) {  // above what every kernel may use
     static std::atomic<uint64_t> done{0};
@@ -879,8 +894,16 @@ hipError_t launch_kernel(const AttnParams& p, int64_t grid, hipStream_t s) {
 
 template <bool BF, int DV>
 hipError_t launch_dv(const AttnParams& p, int64_t grid, hipStream_t s) {
-  return p.page.d % 16 == 0 ? launch_kernel<BF, DV, true>(p, grid, s)
-                            : launch_kernel<BF, DV, false>(p, grid, s);
+  // whole 128-byte lines that no other head or group of query heads reads
+  const uint64_t places = reinterpret_cast<uint64_t>(p.K) | reinterpret_cast<uint64_t>(p.V) |
+                          (uint64_t)(p.page_stride | p.row_stride | p.head_stride) |
+                          (uint64_t)p.D * 2;
+  const bool nt = p.qtiles == 1 && places % 128 == 0;
+  if (p.page.d % 16 == 0)
+    return nt ? launch_kernel<BF, DV, true, true>(p, grid, s)
+              : launch_kernel<BF, DV, true, false>(p, grid, s);
+  return nt ? launch_kernel<BF, DV, false, true>(p, grid, s)
+            : launch_kernel<BF, DV, false, false>(p, grid, s);
 }
 
 template <bool BF>

@@ -415,11 +415,12 @@ def test_attention_extreme_values():
     assert torch.all(torch.isnan(tq.tq_paged_attention(q, n3, v, pt, lens)))
 
 
-@pytest.mark.parametrize("dtype,size", [("f16", 64), ("bf16", 16), ("f16", 24)])
-def test_attention_long(dtype, size):
+@pytest.mark.parametrize("dtype,size,D", [("f16", 64, 128), ("bf16", 16, 128), ("f16", 24, 128),
+                                          ("f16", 16, 256), ("bf16", 32, 64), ("f16", 16, 80)])
+def test_attention_long(dtype, size, D):
     """One sequence over every workgroup (the split and its joining), against fp64
     on the GPU; the oracle's loops would take minutes."""
-    n, Hq, Hkv, D = 70001, 8, 2, 128
+    n, Hq, Hkv = 70001, 8, 2
     q, k, v, pt, lens = paged(10, dtype, [n], Hq, Hkv, D, size, poison=False)
     out, lse = tq.tq_paged_attention(q, k, v, pt, lens, return_lse=True)
     ids = pt[0, :-(-n // size)].long()
