@@ -15,8 +15,9 @@
 // half layout and V/2 pairs each in the interleaved one; the units after that
 // copy one vector of the rest.  With V = 8 (16-bit types) a lane moves 16 bytes
 // per access and 8 lanes cover a 128-number head as two whole 128-byte lines.
-// Heads of all tokens form one flattened list, so few heads or few tokens fill
-// the lanes alike.
+// Tokens and their heads form one flattened list, so few heads or few tokens fill
+// the lanes alike; with enough of both a thread takes two heads of its token for
+// one reading of the table.
 
 #include "tq.h"
 #include "tq_common.h"
@@ -48,10 +49,10 @@ struct RopeParams {
   int64_t x_tok, x_head, y_tok, y_head;  // elements
   const float2* table;
   const int32_t* pos;
-  uint32_t n_pos, rows;  // rows = T * H
-  int32_t rot, D;
+  uint32_t n_pos, rows;  // rows = T * slots
+  int32_t rot, H;
   int32_t turn_units, units;  // per head: turning, all
-  Div31 heads;
+  Div31 slots;                // threads that share a token's heads
   // appending
   int32_t Hq, Hkv;
   unsigned char* K;
@@ -69,140 +70,157 @@ struct alignas(sizeof(S) * V < 16 ? sizeof(S) * V : 16) Pack {
   S v[V];
 };
 
-// One row (token, head) and unit of one thread.
-template <class S, int V, bool INTER, bool INV, bool APPEND>
-struct RopeItem {
-  const S* x;
-  S* y;  // nullptr: not written
-  bool turn, zero;
-  int u;
-  uint32_t pos;
-  Pack<S, V> a, b;
+// Large calls (RPT > 1) store 16-byte pieces past the caches: what they write does
+// not stay there anyway.  Measured (us, with / without): 8192 tokens x 72 heads of
+// 128 in fp16 53 / 55, 16384 x 24 x 64 19 / 25, 4093 x 40 x 80 in fp32 18 / 20;
+// 8-byte pieces (20 pairs of 80 numbers) 52 / 44, which therefore go the usual way.
+template <int RPT, class S, int V>
+__device__ __forceinline__ void store(S* to, const Pack<S, V>& v) {
+  if constexpr (RPT > 1 && sizeof(S) * V == 16) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4*>(to));
+  } else {
+    *reinterpret_cast<Pack<S, V>*>(to) = v;
+  }
+}
 
-  __device__ __forceinline__ void locate(const RopeParams& p, uint32_t row, int unit) {
-    u = unit;
-    const uint32_t tok = p.heads.quot(row);
-    const int head = (int)(row - tok * p.heads.d);
-    const int32_t ps = p.pos[tok];
-    pos = (uint32_t)ps;
-    const bool ok = pos < p.n_pos;
-    zero = !ok;
-    turn = u < p.turn_units;
-    x = reinterpret_cast<const S*>(p.X) + tok * p.x_tok + head * p.x_head;
-    if constexpr (!APPEND) {
-      y = reinterpret_cast<S*>(p.Y) + tok * p.y_tok + head * p.y_head;
-    } else if (head < p.Hq) {
-      y = reinterpret_cast<S*>(p.Y) + tok * p.y_tok + head * p.y_head;
-    } else {
-      const bool key = head < p.Hq + p.Hkv;
-      if (!key) turn = false;
-      y = nullptr;
-      const uint32_t seq = p.seqs ? (uint32_t)p.seqs[tok] : tok;
-      const uint32_t pg = p.page.quot(ok ? pos : 0);
-      if (ok && seq < p.n_seqs && pg < p.width) {
-        const uint32_t id = (uint32_t)p.page_table[(int64_t)seq * p.width + pg];
-        if (id < p.n_pages)
-          y = reinterpret_cast<S*>(key ? p.K : p.Vp) + id * p.page_stride +
-              (pos - pg * p.page.d) * p.row_stride + (head - p.Hq - (key ? 0 : p.Hkv)) * p.head_stride;
-      }
-    }
-  }
-  // Numbers of the unit's two vectors (`second` also of units that copy, where
-  // they lie inside rot), and whether there is a second one.
-  __device__ __forceinline__ int first(const RopeParams& p) const {
-    if (u >= p.turn_units) return p.rot + (u - p.turn_units) * V;
-    return V == 1 && INTER ? 2 * u : u * V;
-  }
-  __device__ __forceinline__ int second(const RopeParams& p) const {
-    return V == 1 && INTER ? 2 * u + 1 : p.rot / 2 + u * V;
-  }
-  __device__ __forceinline__ void load(const RopeParams& p) {
-    a = *reinterpret_cast<const Pack<S, V>*>(x + first(p));
-    if (u < p.turn_units) b = *reinterpret_cast<const Pack<S, V>*>(x + second(p));
-  }
-  __device__ __forceinline__ static void turn_pair(float2 cs, S& p, S& q) {
-    const float sn = INV ? -cs.y : cs.y, fa = (float)p, fb = (float)q;
-    p = (S)(fa * cs.x - fb * sn);
-    q = (S)(fb * cs.x + fa * sn);
-  }
-  __device__ __forceinline__ void finish(const RopeParams& p) {
-    if (turn && !zero) {
-      const float2* t = p.table + (int64_t)pos * (p.rot / 2);
-      if constexpr (INTER && V > 1) {
-        const Pack<float2, V / 2> ca = *reinterpret_cast<const Pack<float2, V / 2>*>(t + u * (V / 2));
-        const Pack<float2, V / 2> cb =
-            *reinterpret_cast<const Pack<float2, V / 2>*>(t + p.rot / 4 + u * (V / 2));
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-          turn_pair(ca.v[i], a.v[2 * i], a.v[2 * i + 1]);
-          turn_pair(cb.v[i], b.v[2 * i], b.v[2 * i + 1]);
-        }
-      } else {
-        const Pack<float2, V> c = *reinterpret_cast<const Pack<float2, V>*>(t + u * V);
-#pragma unroll
-        for (int i = 0; i < V; ++i) turn_pair(c.v[i], a.v[i], b.v[i]);
-      }
-    }
-    if (zero) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) a.v[i] = b.v[i] = (S)0.f;
-    }
-    if (!y) return;
-    *reinterpret_cast<Pack<S, V>*>(y + first(p)) = a;
-    if (u < p.turn_units) *reinterpret_cast<Pack<S, V>*>(y + second(p)) = b;
-  }
-};
-
-// RPT rows per thread, their loads issued together.
+// One unit of RPT heads of a token: heads slot, slot + head_slots, ...  The
+// token's cosines and sines are read once for all of them, after the heads.
 template <class S, int V, bool INTER, bool INV, bool APPEND, int RPT>
 __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeParams p) {
   const int slots = kRopeThreads / p.units > 0 ? kRopeThreads / p.units : 1;
   const int slot = threadIdx.x / p.units;
-  for (int unit = threadIdx.x % p.units; unit < p.units; unit += kRopeThreads) {
-    if (slot >= slots) break;
-    RopeItem<S, V, INTER, INV, APPEND> it[RPT];
-    const uint64_t row0 = (uint64_t)blockIdx.x * (slots * RPT) + slot;
+  const uint64_t at = (uint64_t)blockIdx.x * slots + slot;
+  if (slot >= slots || at >= p.rows) return;
+  const uint32_t tok = p.slots.quot((uint32_t)at);
+  const int head0 = (int)((uint32_t)at - tok * p.slots.d);
+  const uint32_t pos = (uint32_t)p.pos[tok];
+  const bool known = pos < p.n_pos;
+  const S* x = reinterpret_cast<const S*>(p.X) + tok * p.x_tok;
+  S* y = reinterpret_cast<S*>(p.Y) + tok * p.y_tok;
+  int64_t slot_at = -1;  // appending: where the token's slot is in the cache
+  if constexpr (APPEND) {
+    const uint32_t seq = p.seqs ? (uint32_t)p.seqs[tok] : tok;
+    const uint32_t pg = p.page.quot(known ? pos : 0);
+    if (known && seq < p.n_seqs && pg < p.width) {
+      const uint32_t id = (uint32_t)p.page_table[(int64_t)seq * p.width + pg];
+      if (id < p.n_pages) slot_at = id * p.page_stride + (pos - pg * p.page.d) * p.row_stride;
+    }
+  }
+  // more units than threads: a thread takes every 256th
+  for (int u = threadIdx.x - slot * p.units; u < p.units; u += kRopeThreads) {
+    const bool turns = u < p.turn_units;
+    // numbers of the unit's two vectors; a copying unit has the first only
+    const int first = !turns ? p.rot + (u - p.turn_units) * V : V == 1 && INTER ? 2 * u : u * V;
+    const int second = !turns ? first : V == 1 && INTER ? 2 * u + 1 : p.rot / 2 + u * V;
+    Pack<S, V> a[RPT], b[RPT];
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
-      const uint64_t row = row0 + (uint64_t)i * slots;
-      if (row < p.rows) {
-        it[i].locate(p, (uint32_t)row, unit);
-        it[i].load(p);
+      const int head = head0 + i * (int)p.slots.d;
+      if (head < p.H) {
+        a[i] = *reinterpret_cast<const Pack<S, V>*>(x + head * p.x_head + first);
+        if (turns) b[i] = *reinterpret_cast<const Pack<S, V>*>(x + head * p.x_head + second);
       }
     }
+    Pack<float2, V> cs;
+    if (turns && known) {
+      const float2* t = p.table + (int64_t)pos * (p.rot / 2);
+      if constexpr (INTER && V > 1) {
+        const auto lo = *reinterpret_cast<const Pack<float2, V / 2>*>(t + u * (V / 2));
+        const auto hi = *reinterpret_cast<const Pack<float2, V / 2>*>(t + p.rot / 4 + u * (V / 2));
 #pragma unroll
-    for (int i = 0; i < RPT; ++i)
-      if (row0 + (uint64_t)i * slots < p.rows) it[i].finish(p);
+        for (int i = 0; i < V / 2; ++i) {
+          cs.v[i] = lo.v[i];
+          cs.v[V / 2 + i] = hi.v[i];
+        }
+      } else {
+        cs = *reinterpret_cast<const Pack<float2, V>*>(t + u * V);
+      }
+    }
+    auto turn = [&](float2 c, S& m, S& n) {
+      const float sn = INV ? -c.y : c.y, fm = (float)m, fn = (float)n;
+      // which product is fused is said here, and the results are kept in fp32 until
+      // their one conversion: every variant gives the same bits
+      float r0 = fmaf(fm, c.x, -(fn * sn)), r1 = fmaf(fn, c.x, fm * sn);
+      asm("" : "+v"(r0), "+v"(r1));
+      m = (S)r0;
+      n = (S)r1;
+    };
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const int head = head0 + i * (int)p.slots.d;
+      if (head >= p.H) continue;
+      S* to = y + head * p.y_head;
+      bool rotate = turns, write = true;
+      if constexpr (APPEND) {
+        if (head >= p.Hq) {  // a key or a value
+          const int kv = head - p.Hq;
+          const bool key = kv < p.Hkv;
+          rotate = turns && key;
+          write = slot_at >= 0;
+          to = reinterpret_cast<S*>(key ? p.K : p.Vp) + slot_at +
+               (key ? kv : kv - p.Hkv) * p.head_stride;
+        }
+      }
+      if (!known) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) a[i].v[e] = b[i].v[e] = (S)0.f;
+      } else if (rotate) {
+        if constexpr (INTER && V > 1) {
+#pragma unroll
+          for (int e = 0; e < V / 2; ++e) {
+            turn(cs.v[e], a[i].v[2 * e], a[i].v[2 * e + 1]);
+            turn(cs.v[V / 2 + e], b[i].v[2 * e], b[i].v[2 * e + 1]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; ++e) turn(cs.v[e], a[i].v[e], b[i].v[e]);
+        }
+      }
+      if (write) {
+        store<RPT, S, V>(to + first, a[i]);
+        if (turns) store<RPT, S, V>(to + second, b[i]);
+      }
+    }
   }
 }
 
-template <class S, int V, bool INTER, bool INV, bool APPEND>
-hipError_t launch_rows(const RopeParams& p, hipStream_t s) {
+template <class S, int V, bool INTER, bool INV, bool APPEND, int RPT>
+hipError_t launch_heads(RopeParams p, int64_t T, hipStream_t s) {
+  const int64_t head_slots = (p.H + RPT - 1) / RPT;
+  p.slots = Div31::of(head_slots);
+  p.rows = (uint32_t)(T * head_slots);
   const int slots = kRopeThreads / p.units > 0 ? kRopeThreads / p.units : 1;
-  const int64_t one = ((int64_t)p.rows + slots - 1) / slots;
-  if (one >= 8 * device_cus()) {
-    hipLaunchKernelGGL((rope_kernel<S, V, INTER, INV, APPEND, 4>), dim3((uint32_t)((one + 3) / 4)),
-                       dim3(kRopeThreads), 0, s, p);
-  } else {
-    hipLaunchKernelGGL((rope_kernel<S, V, INTER, INV, APPEND, 1>), dim3((uint32_t)one),
-                       dim3(kRopeThreads), 0, s, p);
-  }
+  hipLaunchKernelGGL((rope_kernel<S, V, INTER, INV, APPEND, RPT>),
+                     dim3((uint32_t)((p.rows + (int64_t)slots - 1) / slots)), dim3(kRopeThreads), 0,
+                     s, p);
   return hipGetLastError();
 }
 
+// Two heads a thread where that leaves the GPU full of waves.  Measured (us, 1 / 2 /
+// 3 / 4 heads): 8192 tokens x 72 heads of 128 in fp16 67 / 55 / 57 / 61.
+template <class S, int V, bool INTER, bool INV, bool APPEND>
+hipError_t launch_rows(const RopeParams& p, int64_t T, hipStream_t s) {
+  const int64_t waves = T * p.H * p.units / kWave;
+  if (waves >= 128 * device_cus())
+    return launch_heads<S, V, INTER, INV, APPEND, 2>(p, T, s);
+  return launch_heads<S, V, INTER, INV, APPEND, 1>(p, T, s);
+}
+
 template <class S, int V>
-hipError_t launch_kind(const RopeParams& p, bool inter, bool inv, bool append, hipStream_t s) {
+hipError_t launch_kind(const RopeParams& p, int64_t T, bool inter, bool inv, bool append,
+                       hipStream_t s) {
   if (append) {
     if constexpr (sizeof(S) == 2)
-      return inter ? launch_rows<S, V, true, false, true>(p, s)
-                   : launch_rows<S, V, false, false, true>(p, s);
+      return inter ? launch_rows<S, V, true, false, true>(p, T, s)
+                   : launch_rows<S, V, false, false, true>(p, T, s);
     return hipErrorInvalidValue;  // refused by the caller
   }
   if (inter)
-    return inv ? launch_rows<S, V, true, true, false>(p, s)
-               : launch_rows<S, V, true, false, false>(p, s);
-  return inv ? launch_rows<S, V, false, true, false>(p, s)
-             : launch_rows<S, V, false, false, false>(p, s);
+    return inv ? launch_rows<S, V, true, true, false>(p, T, s)
+               : launch_rows<S, V, true, false, false>(p, T, s);
+  return inv ? launch_rows<S, V, false, true, false>(p, T, s)
+             : launch_rows<S, V, false, false, false>(p, T, s);
 }
 
 // Whether vectors of V numbers of `size` bytes fit every address involved.
@@ -234,12 +252,10 @@ hipError_t launch_rope(int dtype, const RopeArgs& a, hipStream_t stream) {
   p.table = reinterpret_cast<const float2*>(a.table);
   p.pos = a.pos;
   p.n_pos = (uint32_t)a.n_pos;
-  p.rows = (uint32_t)(a.T * a.H);
   p.rot = (int32_t)a.rot;
-  p.D = (int32_t)a.D;
+  p.H = (int32_t)a.H;
   p.turn_units = (int32_t)(a.rot / 2 / V);
   p.units = p.turn_units + (int32_t)((a.D - a.rot) / V);
-  p.heads = Div31::of(a.H);
   const bool append = a.k_pages != nullptr;
   if (append) {
     p.Hq = (int32_t)a.Hq;
@@ -258,15 +274,15 @@ hipError_t launch_rope(int dtype, const RopeArgs& a, hipStream_t stream) {
   }
   const bool inter = a.interleaved, inv = a.inverse;
   if (dtype == TQ_F32)
-    return V == 4 ? launch_kind<float, 4>(p, inter, inv, append, stream)
-                  : launch_kind<float, 1>(p, inter, inv, append, stream);
+    return V == 4 ? launch_kind<float, 4>(p, a.T, inter, inv, append, stream)
+                  : launch_kind<float, 1>(p, a.T, inter, inv, append, stream);
   if (dtype == TQ_BF16)
-    return V == 8   ? launch_kind<__bf16, 8>(p, inter, inv, append, stream)
-           : V == 4 ? launch_kind<__bf16, 4>(p, inter, inv, append, stream)
-                    : launch_kind<__bf16, 1>(p, inter, inv, append, stream);
-  return V == 8   ? launch_kind<_Float16, 8>(p, inter, inv, append, stream)
-         : V == 4 ? launch_kind<_Float16, 4>(p, inter, inv, append, stream)
-                  : launch_kind<_Float16, 1>(p, inter, inv, append, stream);
+    return V == 8   ? launch_kind<__bf16, 8>(p, a.T, inter, inv, append, stream)
+           : V == 4 ? launch_kind<__bf16, 4>(p, a.T, inter, inv, append, stream)
+                    : launch_kind<__bf16, 1>(p, a.T, inter, inv, append, stream);
+  return V == 8   ? launch_kind<_Float16, 8>(p, a.T, inter, inv, append, stream)
+         : V == 4 ? launch_kind<_Float16, 4>(p, a.T, inter, inv, append, stream)
+                  : launch_kind<_Float16, 1>(p, a.T, inter, inv, append, stream);
 }
 
 }  // namespace tq
