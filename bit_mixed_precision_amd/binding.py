@@ -10,6 +10,7 @@ there is no fallback.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 import numpy as np
@@ -638,10 +639,12 @@ def _empty(like, shape, dtype, stream):
     """A new tensor on like's GPU whose memory belongs to the stream that the call
     runs on: the allocator hands a freed block out again in the order of its own
     stream, so memory of the current stream must not be written on another one."""
-    if stream is None:
-        return _torch.empty(shape, dtype=dtype, device=like.device)
-    with _torch.cuda.stream(_torch.cuda.ExternalStream(stream, like.device)):
-        return _torch.empty(shape, dtype=dtype, device=like.device)
+    device = like.device
+    if stream is None or stream == _torch._C._cuda_getCurrentRawStream(device.index):
+        return _torch.empty(shape, dtype=dtype, device=device)
+    with _torch.cuda.stream(_torch.cuda.default_stream(device) if stream == 0 else
+                            _torch.cuda.ExternalStream(stream, device)):
+        return _torch.empty(shape, dtype=dtype, device=device)
 
 
 def _pieces(like, sizes, stream):
@@ -750,6 +753,12 @@ def tq_paged_attention_workspace(B: int, Hq: int, Hkv: int, D: int, page_size: i
     return n
 
 
+@functools.lru_cache(maxsize=256)
+def _attention_workspace(dev, *shape):
+    with _torch.cuda.device(dev):  # the size follows the GPU's compute units
+        return lib.tq_paged_attention_workspace(*shape)
+
+
 def tq_paged_attention(Q, k_pages, v_pages, page_table, lens, scale: float | None = None,
                        window: int = 0, out=None, return_lse: bool = False, workspace=None,
                        stream=None):
@@ -778,7 +787,7 @@ def tq_paged_attention(Q, k_pages, v_pages, page_table, lens, scale: float | Non
                 ("page_table", page_table), ("lens", lens), ("out", out),
                 ("workspace", workspace))
     if workspace is None:
-        n = lib.tq_paged_attention_workspace(B, Hq, Hkv, D, size, width)
+        n = _attention_workspace(dev, B, Hq, Hkv, D, size, width)
         if n:
             _check(min(n, 0), where)
             workspace = _empty(Q, (n,), _torch.uint8, stream)
@@ -812,6 +821,7 @@ def _state(page_table, lens, where):
     return rows, width
 
 
+@functools.lru_cache(maxsize=256)
 def tq_pages_workspace(rows: int, n_pages: int) -> int:
     """Workspace bytes of tq_pages_fork, tq_pages_grow and tq_pages_compact."""
     n = int(lib.tq_pages_workspace(rows, n_pages))

@@ -100,21 +100,24 @@ __device__ __forceinline__ float4v mma(u32x4 a, u32x4 b, float4v c) {
 
 // Two floats as two 16-bit numbers (low half first) rounded toward zero, and
 // what that left of them, rounded the same way: hi + lo is within 2^-20 (fp16,
-// normal range) or 2^-14 (bf16) of the value.
+// normal range) or 2^-14 (bf16) of the value.  The remainder is never zero (at
+// least 2^-24 of weights scaled by 2^14, or 2^-100), so that an infinite value
+// times it stays infinite instead of becoming NaN.
 template <bool BF>
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
   if constexpr (BF) {
     const uint32_t xb = __builtin_bit_cast(uint32_t, x), yb = __builtin_bit_cast(uint32_t, y);
     hi = __builtin_amdgcn_perm(yb, xb, 0x07060302u);
-    const float xr = x - __builtin_bit_cast(float, xb & 0xffff0000u);
-    const float yr = y - __builtin_bit_cast(float, yb & 0xffff0000u);
+    const float xr = fmaxf(x - __builtin_bit_cast(float, xb & 0xffff0000u), 0x1p-100f);
+    const float yr = fmaxf(y - __builtin_bit_cast(float, yb & 0xffff0000u), 0x1p-100f);
     lo = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, yr), __builtin_bit_cast(uint32_t, xr),
                                0x07060302u);
   } else {
     const auto h = __builtin_amdgcn_cvt_pkrtz(x, y);
     hi = __builtin_bit_cast(uint32_t, h);
     lo = __builtin_bit_cast(uint32_t,
-                            __builtin_amdgcn_cvt_pkrtz(x - (float)h[0], y - (float)h[1]));
+                            __builtin_amdgcn_cvt_pkrtz(x - (float)h[0], y - (float)h[1])) |
+         0x00010001u;
   }
 }
 
@@ -329,10 +332,12 @@ __global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attenti
       cur.b = src * per;
       cur.r = range_of(p, cur.b);
       uint32_t n;
-      while (in_row >= (n = (uint32_t)(cur.r.t1 - cur.r.t0)) * H) {
+      // (the bounds on b hold whatever happens to the lengths meanwhile)
+      while (in_row >= (n = (uint32_t)(cur.r.t1 - cur.r.t0)) * H && cur.b + 1 < p.B) {
         in_row -= n * H;
         cur.r = range_of(p, ++cur.b);
       }
+      n = n > 0 ? n : 1;
       cur.h = in_row / n;
       cur.tile = cur.r.t0 + in_row % n;
     }
@@ -343,8 +348,10 @@ __global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attenti
     if (++c.tile < c.r.t1) return;
     if (++c.h == H) {
       c.h = 0;
-      do c.r = range_of(p, ++c.b);
-      while (c.r.t1 == c.r.t0);
+      while (c.b + 1 < p.B) {
+        c.r = range_of(p, ++c.b);
+        if (c.r.t1 > c.r.t0) break;
+      }
     }
     c.tile = c.r.t0;
   };
@@ -856,6 +863,7 @@ constexpr int64_t kLdsBytes = 160 * 1024;
 int64_t static_lds(int64_t D) { return D > 128 ? 2048 : D > 64 ? 18 * 1024 : 10 * 1024; }
 int64_t lds_bytes(int heads, int64_t D) { return 2 * kAttnWaves * heads * (D + 4) * 4; }
 
+constexpr int64_t kMostDirect = int64_t(1) << 20;  // workgroups of one launch
 struct Grid {
   int64_t blocks, partials;  // workgroups; partial sums they may leave
   bool direct;
@@ -867,7 +875,7 @@ struct Grid {
 Grid attn_grid(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity) {
   const int64_t G = Hq / Hkv, H = Hkv * ((G + kHeads - 1) / kHeads);
   const int heads = (int)(G < kHeads ? G : kHeads);
-  if (capacity <= kAttnWaves * kTileTokens) return {B * H, 0, true};
+  if (capacity <= kAttnWaves * kTileTokens && B * H <= kMostDirect) return {B * H, 0, true};
   const int64_t tiles = capacity / kTileTokens + 2;  // a window may begin inside a tile
   const int64_t most = (B * H * tiles + kAttnWaves - 1) / kAttnWaves;
   const int64_t by_lds = kLdsBytes / (lds_bytes(heads, D) + static_lds(D));

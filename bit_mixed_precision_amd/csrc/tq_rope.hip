@@ -28,6 +28,7 @@ namespace tq {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int64_t kMostBlocks = int64_t(1) << 23;  // of one launch; more than the heads of a token
 
 // n / d for 0 <= n < 2^31: exact with m = ceil(2^(31 + s) / d), s = ceil(log2 d).
 struct Div31 {
@@ -49,7 +50,7 @@ struct RopeParams {
   int64_t x_tok, x_head, y_tok, y_head;  // elements
   const float2* table;
   const int32_t* pos;
-  uint32_t n_pos, rows;  // rows = T * slots
+  uint32_t n_pos, rows, tok0;  // rows of this launch: tokens from tok0 x slots
   int32_t rot, H;
   int32_t turn_units, units;  // per head: turning, all
   Div31 slots;                // threads that share a token's heads
@@ -92,8 +93,9 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeParams p) {
   const int slot = threadIdx.x / p.units;
   const uint64_t at = (uint64_t)blockIdx.x * slots + slot;
   if (slot >= slots || at >= p.rows) return;
-  const uint32_t tok = p.slots.quot((uint32_t)at);
-  const int head0 = (int)((uint32_t)at - tok * p.slots.d);
+  const uint32_t in_launch = p.slots.quot((uint32_t)at);
+  const int head0 = (int)((uint32_t)at - in_launch * p.slots.d);
+  const uint32_t tok = p.tok0 + in_launch;
   const uint32_t pos = (uint32_t)p.pos[tok];
   const bool known = pos < p.n_pos;
   const S* x = reinterpret_cast<const S*>(p.X) + tok * p.x_tok;
@@ -189,12 +191,19 @@ template <class S, int V, bool INTER, bool INV, bool APPEND, int RPT>
 hipError_t launch_heads(RopeParams p, int64_t T, hipStream_t s) {
   const int64_t head_slots = (p.H + RPT - 1) / RPT;
   p.slots = Div31::of(head_slots);
-  p.rows = (uint32_t)(T * head_slots);
   const int slots = kRopeThreads / p.units > 0 ? kRopeThreads / p.units : 1;
-  hipLaunchKernelGGL((rope_kernel<S, V, INTER, INV, APPEND, RPT>),
-                     dim3((uint32_t)((p.rows + (int64_t)slots - 1) / slots)), dim3(kRopeThreads), 0,
-                     s, p);
-  return hipGetLastError();
+  // a launch holds fewer than 2^32 threads
+  const int64_t most = (kMostBlocks * slots) / head_slots;
+  for (int64_t t = 0; t < T; t += most) {
+    p.tok0 = (uint32_t)t;
+    p.rows = (uint32_t)((T - t < most ? T - t : most) * head_slots);
+    hipLaunchKernelGGL((rope_kernel<S, V, INTER, INV, APPEND, RPT>),
+                       dim3((uint32_t)((p.rows + (int64_t)slots - 1) / slots)),
+                       dim3(kRopeThreads), 0, s, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // Two heads a thread where that leaves the GPU full of waves.  Measured (us, 1 / 2 /

@@ -411,6 +411,10 @@ def test_attention_extreme_values():
     v2[row[0], 0, 0, 5] = float("inf")
     out = f64(tq.tq_paged_attention(q, k, v2, pt, lens))[0, 0]
     assert out[5] == np.inf and np.isfinite(np.delete(out, 5)).all()
+    # one token: its weight is exactly 1, nothing remains for the low part
+    for dt in (torch.float16, torch.bfloat16):
+        one = tq.tq_paged_attention(q.to(dt), k.to(dt), v2.to(dt), pt, i32([1]))
+        assert torch.equal(one[0, 0], v2[row[0], 0, 0].to(dt))
     n3[row[0], 0, 0, 5] = NAN
     assert torch.all(torch.isnan(tq.tq_paged_attention(q, n3, v, pt, lens)))
 
@@ -501,6 +505,10 @@ def test_attention_repeats_and_streams():
     got = [tq.tq_paged_attention(q, k, v, pt, lens, stream=side.cuda_stream) for _ in range(5)]
     side.synchronize()
     assert all(torch.equal(g, want) for g in got)
+    with torch.cuda.stream(side):  # stream 0 while another one is current
+        out = tq.tq_paged_attention(q, k, v, pt, lens, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
 
 
 def test_decode_ops_in_a_graph():
