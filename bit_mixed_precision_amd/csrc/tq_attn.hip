@@ -509,6 +509,7 @@ __global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attenti
     Cursor next = cur;
     int first_tile = cur.tile;
     bool first_row = true;
+    open_row(cur);  // queries do not wait for the page table
     w_cur = place_of(cur);
     load_k(cur, w_cur);
     load_v(cur, w_cur);
@@ -516,7 +517,6 @@ __global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attenti
       advance(next);
       w_next = place_of(next);
     }
-    open_row(cur);
     while (true) {
       const bool more = left > 1;
       float4v s[2];
@@ -666,22 +666,18 @@ __global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attenti
   // that began before, the second for one that goes on).
   __syncthreads();
   int owned = -1, last = 0;
-  for (int i = 0; i < 2 * kAttnWaves;) {
-    const int row = uni(sRow[i]);
-    if (row < 0) {
-      ++i;
-      continue;
-    }
-    int end = i + 1, ends = uni(sEnds[i]);
-    const bool begins = ends & 1;
-    for (int k = i + 1; k < 2 * kAttnWaves; ++k) {
-      const int other = uni(sRow[k]);
-      if (other < 0) continue;
-      if (other != row) break;
-      end = k + 1;
-      ends = uni(sEnds[k]);
-    }
-    const bool whole = begins && (ends & 2);
+  constexpr int kSlots = 2 * kAttnWaves;
+  const int row_of = lane < kSlots ? sRow[lane] : -1;
+  const int ends_of = sEnds[lane % kSlots], last_of = sLast[lane % kSlots];
+  uint32_t todo = (uint32_t)__ballot(row_of >= 0);
+  while (todo) {
+    const int i = __builtin_ctz(todo);
+    const int row = __builtin_amdgcn_readlane(row_of, i);
+    const uint32_t members = (uint32_t)__ballot(row_of == row);
+    todo &= ~members;
+    const bool begins = __builtin_amdgcn_readlane(ends_of, i) & 1;
+    const bool whole =
+        begins && (__builtin_amdgcn_readlane(ends_of, 31 - __builtin_clz(members)) & 2);
     const int b = row / H, h = row - b * H;
     const int hk = h / p.qtiles, qt = h - hk * p.qtiles;
     const int nh = p.G - qt * kHeads < kHeads ? p.G - qt * kHeads : kHeads;
@@ -689,18 +685,30 @@ __global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attenti
     const int units = p.D / 8;
     for (int j = tid; j < nh * units; j += kAttnThreads) {
       const int hd = j / units, d = (j - hd * units) * 8;
-      float mm = -INFINITY;
-      for (int k = i; k < end; ++k)
-        if (sRow[k] == row) mm = fmaxf(mm, sM[k][hd]);
-      const float base = mm == -INFINITY ? 0.f : mm;
-      float sum = 0.f, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      for (int k = i; k < end; ++k) {
-        if (sRow[k] != row) continue;
-        const float f = __builtin_amdgcn_exp2f(sM[k][hd] - base);
-        sum += f * sL[k][hd];
-        const float* o = sO + (k * slot_heads + hd) * row_floats + d;
+      // every slot is read, so that the reads overlap; only members count
+      float f[kSlots], mm = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += f * o[e];
+      for (int k = 0; k < kSlots; ++k) {
+        f[k] = members >> k & 1 ? sM[k][hd] : -INFINITY;
+        mm = fmaxf(mm, f[k]);
+      }
+      const float base = mm == -INFINITY ? 0.f : mm;
+      float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < kSlots; ++k) {
+        f[k] = __builtin_amdgcn_exp2f(f[k] - base);
+        const float lk = sL[k][hd];
+        const float* o = sO + (k * slot_heads + hd) * row_floats + d;
+        const float4v x = *reinterpret_cast<const float4v*>(o);
+        const float4v y = *reinterpret_cast<const float4v*>(o + 4);
+        if (members >> k & 1) {
+          sum += f[k] * lk;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] += f[k] * x[e];
+            v[e + 4] += f[k] * y[e];
+          }
+        }
       }
       if (whole) {
         finish<BF>(p, b, hk * p.G + qt * kHeads + hd, d, mm, sum, v);
@@ -716,9 +724,8 @@ __global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attenti
     }
     if (begins && !whole) {  // goes on in the following workgroups
       owned = row;
-      last = (int)(cut.part_of((uint32_t)sLast[i]) / kAttnWaves);
+      last = (int)(cut.part_of((uint32_t)__builtin_amdgcn_readlane(last_of, i)) / kAttnWaves);
     }
-    i = end;
   }
   if (!p.direct && tid == 0) p.owner[blockIdx.x] = make_int2(owned, last);
 
@@ -869,13 +876,20 @@ struct Grid {
   bool direct;
 };
 
+// Tiles a wave of a table's longest row, up to which every (sequence, head) has a
+// workgroup of its own and nothing is left to join.  Measured (us on the GPU, own
+// workgroup / split and joined), 8 sequences, 8 key heads of 128: 2 tiles 9.1 /
+// 12.9, 4 tiles 12.9 / 13.3, 8 tiles 21 / 16; 16 sequences, 4 key heads of 256: 4
+// tiles 22 / 17.
+constexpr int direct_tiles(int64_t D) { return D > 128 ? 2 : 4; }
+
 // Workgroups of the first kernel: as many as the GPU holds at once, or one for
-// each (sequence, head) where a table names at most four tiles a row: every wave
-// has one tile then and a join would only cost its launch.
+// each (sequence, head).
 Grid attn_grid(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity) {
   const int64_t G = Hq / Hkv, H = Hkv * ((G + kHeads - 1) / kHeads);
   const int heads = (int)(G < kHeads ? G : kHeads);
-  if (capacity <= kAttnWaves * kTileTokens && B * H <= kMostDirect) return {B * H, 0, true};
+  if (capacity <= direct_tiles(D) * kAttnWaves * kTileTokens && B * H <= kMostDirect)
+    return {B * H, 0, true};
   const int64_t tiles = capacity / kTileTokens + 2;  // a window may begin inside a tile
   const int64_t most = (B * H * tiles + kAttnWaves - 1) / kAttnWaves;
   const int64_t by_lds = kLdsBytes / (lds_bytes(heads, D) + static_lds(D));

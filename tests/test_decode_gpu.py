@@ -317,13 +317,14 @@ def test_attention_edges(dtype, Hq, Hkv, D, size, order):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
-@pytest.mark.parametrize("n", [1, 5, 31, 32, 33, 96, 128])
-def test_attention_short_tables(dtype, n):
-    """Tables of at most 128 tokens: one workgroup per head, no joining."""
+@pytest.mark.parametrize("n,D", [(1, 128), (5, 64), (31, 128), (32, 80), (33, 128), (96, 128), (128, 64),
+                                 (129, 128), (300, 128), (512, 128), (511, 64), (256, 256), (250, 192)])
+def test_attention_short_tables(dtype, n, D):
+    """Short tables: one workgroup per head, no joining."""
     size = 32
-    q, k, v, pt, lens = paged(n, dtype, [n, max(0, n - 3), 0, n], 8, 2, 128, size)
+    q, k, v, pt, lens = paged(n, dtype, [n, max(0, n - 3), 0, n, n // 2], 8, 2, D, size)
     pt = pt[:, :max(1, -(-n // size))].contiguous()
-    assert tq.tq_paged_attention_workspace(4, 8, 2, 128, size, pt.shape[1]) == 0
+    assert tq.tq_paged_attention_workspace(5, 8, 2, D, size, pt.shape[1]) == 0
     run_attention(q, k, v, pt, lens, dtype)
 
 

@@ -169,9 +169,11 @@ def test_paged_attention_refusals():
     for bad in (dict(dtype=2), dict(dtype=-1), dict(scale=float("inf")), dict(window=-1)):
         assert _attn(**bad) == tq.TQ_ERR_VALUE, bad
     assert tq.lib.tq_paged_attention_workspace(2, 8, 2, 12, 16, 4) == tq.TQ_ERR_SHAPE
-    # a table that cannot hold more than four tiles needs no workspace
-    assert tq.tq_paged_attention_workspace(2, 8, 2, 64, 16, 8) == 0
-    assert tq.tq_paged_attention_workspace(2, 8, 2, 64, 16, 9) > 0
+    # short tables need no workspace
+    assert tq.tq_paged_attention_workspace(2, 8, 2, 64, 16, 32) == 0
+    assert tq.tq_paged_attention_workspace(2, 8, 2, 64, 16, 33) > 0
+    assert tq.tq_paged_attention_workspace(2, 8, 2, 256, 16, 16) == 0
+    assert tq.tq_paged_attention_workspace(2, 8, 2, 256, 16, 17) > 0
 
 
 def test_pages_refusals():
