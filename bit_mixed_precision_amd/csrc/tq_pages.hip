@@ -38,6 +38,7 @@ struct PagesParams {
   uint32_t* bits;   // ceil(n_pages / 32)
   int32_t* need;    // [rows] pages wanted by a row
   int32_t* last;    // [rows] fork: the page a row copies
+  const int32_t* tokens;  // [rows] fork: lengths of the new rows
   int32_t* src;     // [n_pages] copies: from
   int32_t* dst;     // [n_pages] copies: to
   int32_t* spare;   // [n_pages] free pages in ascending order
@@ -55,7 +56,7 @@ __device__ __forceinline__ int tokens_of(const PagesParams& p, int row) {
   return n < 0 ? 0 : n < cap ? n : (int)cap;
 }
 __device__ __forceinline__ int entries(const PagesParams& p, int tokens) {
-  return (int)(((int64_t)tokens + p.page_size - 1) / p.page_size);
+  return (int)(((uint32_t)tokens + (uint32_t)p.page_size - 1) / (uint32_t)p.page_size);
 }
 
 // Pages that growing row r asks for; -1 if its row of the table is too short.
@@ -195,7 +196,7 @@ __device__ __forceinline__ void fork_assign(const PagesParams& p, int* red) {
     }
     base += total;
     if (need) {
-      const int tokens = p.lens_out[r];
+      const int tokens = p.tokens[r];
       int32_t* out = p.table_out + (int64_t)r * p.width + entries(p, tokens) - 1;
       if (rank < free_pages) {
         const int32_t id = p.spare[rank];
@@ -313,11 +314,12 @@ __global__ __launch_bounds__(kScanThreads) void pages_one_kernel(PagesParams p) 
   __shared__ int red[kScanThreads / kWave];
   __shared__ uint32_t sBits[kOnePages / 32];
   __shared__ int sFrom[kOneRows], sHeld[kOneRows], sNeed[kOneRows], sLast[kOneRows];
-  __shared__ int sSpare[kOneRows];
+  __shared__ int sSpare[kOneRows], sTokens[kOneRows];
   const int t = threadIdx.x;
   p.bits = sBits;
   p.need = sNeed;
   p.last = sLast;
+  p.tokens = sTokens;
   if (OP == kFork) p.spare = sSpare;  // a page a row at most
   for (int i = t; i < (p.n_pages + 31) / 32; i += kScanThreads) sBits[i] = 0;
   if (OP == kFork && p.refs)
@@ -332,38 +334,50 @@ __global__ __launch_bounds__(kScanThreads) void pages_one_kernel(PagesParams p) 
     sFrom[t] = from;
     sHeld[t] = entries(p, tokens);
     sNeed[t] = OP == kFork && from >= 0 && tokens % p.page_size != 0;  // may want a copy
+    sTokens[t] = tokens;
     if constexpr (OP == kFork) p.lens_out[t] = tokens;
     if constexpr (OP == kGrow) sNeed[t] = wanted_pages(p, t, tokens);
   }
   __syncthreads();
+  // a wave takes every 16th row, the first entries of four rows at a time
+  constexpr int kWaves = kScanThreads / kWave, kAtOnce = 4;
   const int lane = t & 63;
-  for (int r = t >> 6; r < p.rows; r += kScanThreads / kWave) {
-    const int held = sHeld[r];
-    bool wants = false;  // a copy of the last page: an earlier row continues the same one
-    if (OP == kFork && sNeed[r]) {
-      const int from = sFrom[r];
-      int later = 0;
-      for (int i = lane; i < r; i += kWave) later |= sFrom[i] == from;
-      wants = __any(later);
-      if (lane == 0) sNeed[r] = wants;
+  for (int r0 = t >> 6; r0 < p.rows; r0 += kWaves * kAtOnce) {
+    int32_t head[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int r = r0 + u * kWaves;
+      const int held = r < p.rows ? sHeld[r] : 0;
+      head[u] = lane < held ? p.table[(int64_t)sFrom[r] * p.width + lane] : -1;
     }
-    const int32_t* row = p.table + (int64_t)(held ? sFrom[r] : 0) * p.width;
-    const int end = OP == kCompact ? held : p.width;
-#pragma unroll 4
-    for (int j = lane; j < end; j += kWave) {
-      int32_t id = -1;
-      if (j < held) {
-        id = row[j];
-        const bool names = names_page(p, id);
-        if (wants && j == held - 1) {
-          sLast[r] = id;
-          if (!names) sNeed[r] = 0;
-        } else if (names) {
-          atomicOr(&sBits[id >> 5], 1u << (id & 31));
-          if (OP == kFork && p.refs) atomicAdd(&p.refs[id], 1);
-        }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int r = r0 + u * kWaves;
+      if (r >= p.rows) break;
+      const int held = sHeld[r];
+      bool wants = false;  // a copy of the last page: an earlier row continues the same one
+      if (OP == kFork && sNeed[r]) {
+        const int from = sFrom[r];
+        int later = 0;
+        for (int i = lane; i < r; i += kWave) later |= sFrom[i] == from;
+        wants = __any(later);
+        if (lane == 0) sNeed[r] = wants;
       }
-      if constexpr (OP != kCompact) p.table_out[(int64_t)r * p.width + j] = id;
+      const int end = OP == kCompact ? held : p.width;
+      for (int j = lane; j < end; j += kWave) {
+        int32_t id = j < kWave ? head[u] : j < held ? p.table[(int64_t)sFrom[r] * p.width + j] : -1;
+        if (j < held) {
+          const bool names = names_page(p, id);
+          if (wants && j == held - 1) {
+            sLast[r] = id;
+            if (!names) sNeed[r] = 0;
+          } else if (names) {
+            atomicOr(&sBits[id >> 5], 1u << (id & 31));
+            if (OP == kFork && p.refs) atomicAdd(&p.refs[id], 1);
+          }
+        }
+        if constexpr (OP != kCompact) p.table_out[(int64_t)r * p.width + j] = id;
+      }
     }
   }
   __syncthreads();
@@ -372,8 +386,35 @@ __global__ __launch_bounds__(kScanThreads) void pages_one_kernel(PagesParams p) 
 
 constexpr int kCopyBytes = kPagesThreads * 16 * 4;  // bytes of one workgroup's step
 
-// Copies pairs x planes x pieces of a page, taken in turn by all but the first
-// `table_blocks` workgroups; those rewrite the table's rows after compaction.
+// This workgroup's share of pairs x planes x pieces of a page, one in `blocks`.
+// I: an unsigned type that holds their number; 64-bit divisions take longer than
+// copying a piece.
+template <class I>
+__device__ __forceinline__ void copy_share(const PagesParams& p, I pairs, I pieces, I first,
+                                           I blocks) {
+  const I planes = (I)p.planes, total = pairs * planes * pieces;
+  for (I i = first; i < total; i += blocks) {
+    const I rest = i / pieces, piece = i - rest * pieces;
+    const I pair = rest / planes, plane = rest - pair * planes;
+    const int32_t s = p.src[pair], d = p.dst[pair];
+    if (!names_page(p, s) || !names_page(p, d)) continue;
+    const unsigned char* from = p.pool + ((int64_t)plane * p.n_pages + s) * p.page_bytes;
+    unsigned char* to = p.pool + ((int64_t)plane * p.n_pages + d) * p.page_bytes;
+    const int64_t at = (int64_t)piece * kCopyBytes + threadIdx.x * 16;
+    u32x4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (at + k * kPagesThreads * 16 < p.page_bytes)
+        v[k] = *reinterpret_cast<const u32x4*>(from + at + k * kPagesThreads * 16);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (at + k * kPagesThreads * 16 < p.page_bytes)
+        *reinterpret_cast<u32x4*>(to + at + k * kPagesThreads * 16) = v[k];
+  }
+}
+
+// The copies, taken in turn by all but the first `table_blocks` workgroups; those
+// rewrite the table's rows after compaction.
 __global__ __launch_bounds__(kPagesThreads) void pages_move_kernel(PagesParams p, int64_t n,
                                                                    int table_blocks) {
   if ((int)blockIdx.x < table_blocks) {
@@ -389,27 +430,13 @@ __global__ __launch_bounds__(kPagesThreads) void pages_move_kernel(PagesParams p
     }
     return;
   }
-  const int64_t blocks = gridDim.x - table_blocks;
+  const uint32_t blocks = gridDim.x - table_blocks, first = blockIdx.x - table_blocks;
   const int64_t pieces = (p.page_bytes + kCopyBytes - 1) / kCopyBytes;
-  const int64_t total = (p.pairs ? (int64_t)*p.pairs : n) * p.planes * pieces;
-  for (int64_t i = (int)blockIdx.x - table_blocks; i < total; i += blocks) {
-    const int64_t piece = i % pieces, rest = i / pieces;
-    const int64_t plane = rest % p.planes, pair = rest / p.planes;
-    const int32_t s = p.src[pair], d = p.dst[pair];
-    if (!names_page(p, s) || !names_page(p, d)) continue;
-    const unsigned char* from = p.pool + (plane * p.n_pages + s) * p.page_bytes;
-    unsigned char* to = p.pool + (plane * p.n_pages + d) * p.page_bytes;
-    const int64_t at = piece * kCopyBytes + threadIdx.x * 16;
-    u32x4 v[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (at + k * kPagesThreads * 16 < p.page_bytes)
-        v[k] = *reinterpret_cast<const u32x4*>(from + at + k * kPagesThreads * 16);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (at + k * kPagesThreads * 16 < p.page_bytes)
-        *reinterpret_cast<u32x4*>(to + at + k * kPagesThreads * 16) = v[k];
-  }
+  const int64_t pairs = p.pairs ? (int64_t)*p.pairs : n;
+  if (pairs * p.planes * pieces < INT32_MAX - (int64_t)blocks)
+    copy_share<uint32_t>(p, (uint32_t)pairs, (uint32_t)pieces, first, blocks);
+  else
+    copy_share<uint64_t>(p, pairs, pieces, first, blocks);
 }
 
 int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
@@ -430,6 +457,7 @@ PagesParams params(const PagesArgs& a) {
   p.add = a.add;
   p.table_out = a.table_out;
   p.lens_out = a.lens_out;
+  p.tokens = a.lens_out;
   p.refs = a.refs;
   p.result = a.result;
   unsigned char* w = static_cast<unsigned char*>(a.workspace);
