@@ -126,23 +126,25 @@ __global__ __launch_bounds__(kPagesThreads) void pages_rows_kernel(PagesParams p
 }
 
 // Exclusive prefix sum over the workgroup and its total.
-__device__ __forceinline__ int scan_block(int v, int* red, int& total) {
+template <class T>
+__device__ __forceinline__ T scan_block(T v, T* red, T& total) {
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
-  int inc = v;
+  T inc = v;
 #pragma unroll
   for (int off = 1; off < kWave; off <<= 1) {
-    const int o = __shfl_up(inc, off, kWave);
-    if (lane >= off) inc += o;
+    const T o = __shfl_up(inc, off, kWave);
+    inc += lane >= off ? o : T(0);
   }
   __syncthreads();  // red of the previous call has been read
   if (lane == 63) red[w] = inc;
   __syncthreads();
-  int before = inc - v;
+  T before = inc - v;
   total = 0;
 #pragma unroll
   for (int i = 0; i < kScanThreads / kWave; ++i) {
-    if (i < w) before += red[i];
-    total += red[i];
+    const T r = red[i];
+    before += i < w ? r : T(0);
+    total += r;
   }
   return before;
 }
@@ -178,7 +180,7 @@ __device__ __forceinline__ void fork_assign(const PagesParams& p, int* red) {
   // wishes are 0 or 1; of the rows of the first round (mostly all) the rank is kept
   const bool first = t < p.rows && p.need[t];
   int wanted;
-  const int first_rank = scan_block(first, red, wanted);
+  const int first_rank = scan_block((int)first, red, wanted);
   const int first_total = wanted;
   for (int r0 = kScanThreads; r0 < p.rows; r0 += kScanThreads) {
     int total;
@@ -218,37 +220,42 @@ __device__ __forceinline__ void fork_assign(const PagesParams& p, int* red) {
 }
 
 __device__ __forceinline__ void grow_assign(const PagesParams& p, int* red) {
+  __shared__ int64_t red64[kScanThreads / kWave];  // wishes add up past 32 bits
   const int t = threadIdx.x, lane = t & 63;
-  const int free_pages = list_free(p, p.n_pages, red);
+  auto wish = [&](int r) -> int64_t { return r < p.rows && p.need[r] > 0 ? p.need[r] : 0; };
+  int64_t wanted;
+  const int64_t first_rank = scan_block(wish(t), red64, wanted);
+  const int64_t first_total = wanted;
+  for (int r0 = kScanThreads; r0 < p.rows; r0 += kScanThreads) {
+    int64_t total;
+    (void)scan_block(wish(r0 + t), red64, total);
+    wanted += total;
+  }
+  const int free_pages = list_free(p, wanted < p.n_pages ? (int)wanted : p.n_pages, red);
   int64_t base = 0;  // pages wanted by the rows before this round
   int refused = 0;
   for (int r0 = 0; r0 < p.rows; r0 += kScanThreads) {
     const int r = r0 + t;
-    const int want = r < p.rows ? p.need[r] : 0;
-    // more pages than there are count as one more, so that sums stay small
-    const int need = want < 0 ? 0 : want <= p.n_pages ? want : p.n_pages + 1;
-    // rows are ranked one wave at a time: 64 (n_pages + 1) fits in 32 bits
-    int64_t rank = base;
-    for (int w = 0; w < kScanThreads / kWave; ++w) {
-      int total;
-      const int before = scan_block((t >> 6) == w ? need : 0, red, total);
-      if ((t >> 6) == w) rank = base + before;
-      base += total;
-    }
-    const bool ok = r < p.rows && want >= 0 && (need == 0 || rank + need <= free_pages);
+    const int64_t need = wish(r);
+    int64_t rank = first_rank, total = first_total;
+    if (r0 > 0) rank = base + scan_block(need, red64, total);
+    base += total;
+    const bool ok = r < p.rows && p.need[r] >= 0 && (need == 0 || rank + need <= free_pages);
+    int held = 0;
     if (r < p.rows) {
       const int tokens = tokens_of(p, r);
+      held = entries(p, tokens);
       p.lens_out[r] = ok ? tokens + (p.add[r] > 0 ? p.add[r] : 0) : tokens;
       refused += !ok;
     }
-    // the wave writes its rows' new pages together
-    for (int k = 0; k < kWave; ++k) {
-      const int cnt = __shfl(ok ? need : 0, k, kWave);
-      if (cnt == 0) continue;
-      const int from = __shfl((int)rank, k, kWave);
-      const int row = r0 + (t & ~63) + k;
-      int32_t* out = p.table_out + (int64_t)row * p.width + entries(p, tokens_of(p, row));
-      for (int i = lane; i < cnt; i += kWave) out[i] = p.spare[from + i];
+    // a row's page by its own thread, the pages of a row that wants more by its wave
+    const int cnt = ok ? (int)need : 0;
+    if (cnt == 1) p.table_out[(int64_t)r * p.width + held] = p.spare[rank];
+    for (uint64_t many = __ballot(cnt > 1); many; many &= many - 1) {
+      const int k = __builtin_ctzll(many);
+      const int n = __shfl(cnt, k, kWave), from = __shfl((int)rank, k, kWave);
+      int32_t* out = p.table_out + (int64_t)(r0 + (t & ~63) + k) * p.width + __shfl(held, k, kWave);
+      for (int i = lane; i < n; i += kWave) out[i] = p.spare[from + i];
     }
   }
   int total;
@@ -307,12 +314,17 @@ __global__ __launch_bounds__(kScanThreads) void pages_assign_kernel(PagesParams 
 // All of the bookkeeping in one workgroup, with the bitmap and the rows' wishes in
 // LDS: one launch instead of three, for states that one compute unit walks
 // through in a few microseconds.
-constexpr int kOneRows = 256, kOneEntries = 64 * 1024, kOnePages = 64 * 1024;
+constexpr int kOneRows = 256;
+// Forking counts the holders of every page in LDS too (atomics on memory from one
+// compute unit take 1.5 ns each: 256 x 128 entries 65 us).
+template <int OP>
+constexpr int one_pages() { return OP == kFork ? 8 * 1024 : 64 * 1024; }
 
 template <int OP>
 __global__ __launch_bounds__(kScanThreads) void pages_one_kernel(PagesParams p) {
   __shared__ int red[kScanThreads / kWave];
-  __shared__ uint32_t sBits[kOnePages / 32];
+  __shared__ uint32_t sBits[one_pages<OP>() / 32];
+  __shared__ int32_t sRefs[OP == kFork ? one_pages<OP>() : 1];
   __shared__ int sFrom[kOneRows], sHeld[kOneRows], sNeed[kOneRows], sLast[kOneRows];
   __shared__ int sSpare[kOneRows], sTokens[kOneRows];
   const int t = threadIdx.x;
@@ -322,8 +334,11 @@ __global__ __launch_bounds__(kScanThreads) void pages_one_kernel(PagesParams p) 
   p.tokens = sTokens;
   if (OP == kFork) p.spare = sSpare;  // a page a row at most
   for (int i = t; i < (p.n_pages + 31) / 32; i += kScanThreads) sBits[i] = 0;
-  if (OP == kFork && p.refs)
-    for (int i = t; i < p.n_pages; i += kScanThreads) p.refs[i] = 0;
+  int32_t* refs_out = p.refs;
+  if constexpr (OP == kFork) {
+    for (int i = t; i < p.n_pages; i += kScanThreads) sRefs[i] = 0;
+    p.refs = sRefs;
+  }
   if (t < p.rows) {
     int from = t;
     if constexpr (OP == kFork) {
@@ -373,7 +388,7 @@ __global__ __launch_bounds__(kScanThreads) void pages_one_kernel(PagesParams p) 
             if (!names) sNeed[r] = 0;
           } else if (names) {
             atomicOr(&sBits[id >> 5], 1u << (id & 31));
-            if (OP == kFork && p.refs) atomicAdd(&p.refs[id], 1);
+            if constexpr (OP == kFork) atomicAdd(&sRefs[id], 1);
           }
         }
         if constexpr (OP != kCompact) p.table_out[(int64_t)r * p.width + j] = id;
@@ -382,6 +397,10 @@ __global__ __launch_bounds__(kScanThreads) void pages_one_kernel(PagesParams p) 
   }
   __syncthreads();
   assign<OP>(p, red);
+  if (OP == kFork && refs_out) {
+    __syncthreads();
+    for (int i = t; i < p.n_pages; i += kScanThreads) refs_out[i] = sRefs[i];
+  }
 }
 
 constexpr int kCopyBytes = kPagesThreads * 16 * 4;  // bytes of one workgroup's step
@@ -499,10 +518,16 @@ int64_t pages_workspace_bytes(int64_t rows, int64_t n_pages) {
 namespace {
 
 // The bookkeeping of one operator: in one workgroup where the state is small.
-// Measured (us, one workgroup / separate launches): TODO
+// Measured (us on the GPU, one workgroup / separate launches), rows x width: fork
+// 4 x 10 5.9 / 8.9, 64 x 43 7.4 / 13.2, 48 x 884 11.5 / 10.2, 256 x 128 19 / 25; grow
+// 64 x 43 5.9 / 12.5, 256 x 256 21 / 16; compaction 4 x 10 7.9 / 10.4, 48 x 884
+// 9.1 / 12.5, 256 x 256 19.2 / 17.9.  Each further launch costs the caller some 2 us.
+constexpr int64_t kOneEntries = 48 * 1024;
+
 template <int OP>
 hipError_t launch_state(const PagesParams& p, hipStream_t s) {
-  if (p.rows <= kOneRows && (int64_t)p.rows * p.width <= kOneEntries && p.n_pages <= kOnePages) {
+  if (p.rows <= kOneRows && (int64_t)p.rows * p.width <= kOneEntries &&
+      p.n_pages <= one_pages<OP>()) {
     hipLaunchKernelGGL(pages_one_kernel<OP>, dim3(1), dim3(kScanThreads), 0, s, p);
     return hipGetLastError();
   }
