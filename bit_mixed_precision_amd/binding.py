@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes as C
 import functools
+import math
 import os
 
 import numpy as np
@@ -97,6 +98,18 @@ for _name, (_res, _args) in SIGNATURES.items():
     _fn = getattr(lib, _name)
     _fn.restype = _res
     _fn.argtypes = _args
+
+
+# The decode-side calls in their common form, compiled (csrc/torch/tq_torch.cpp);
+# each returns None for what it leaves to the functions below.
+if _torch is not None:
+    try:
+        from . import _tq_torch as _fast
+    except ImportError as e:
+        raise ImportError(f"_tq_torch.so is missing or does not load ({e}); build it with "
+                          "`python -m bit_mixed_precision_amd.build_lib`") from e
+    _fast.bind(getattr(_torch._C, "_cuda_getCurrentRawStream", lambda index: 0),
+               {_n: C.cast(getattr(lib, _n), C.c_void_p).value for _n in SIGNATURES})
 
 
 class TQError(RuntimeError):
@@ -551,8 +564,9 @@ def tq_kernel_name(fmt: int, M: int, N: int, K: int, path: int = TQ_PATH_AUTO) -
 
 # ------------------------------------------------------------------ decode
 #
-# These calls are a few microseconds of GPU work in a decode step, so the checks
-# look at every attribute once and leave the wording of a refusal to slow helpers.
+# These calls are a few microseconds of GPU work in a decode step: the common form
+# of each is compiled (_fast), and the functions here say what is wrong with any
+# other, or serve outputs, workspaces and streams that the caller brings.
 
 if _torch is not None:
     _KIND = {_torch.float16: TQ_F16, _torch.bfloat16: TQ_BF16, _torch.float32: TQ_F32}
@@ -652,6 +666,13 @@ def _pieces(like, sizes, stream):
     return _empty(like, (sum(sizes),), _I32T, stream).split_with_sizes(sizes)
 
 
+def _done(r, where):
+    """The result of a compiled call, or TQError for its status."""
+    if type(r) is int:
+        raise TQError(r, where)
+    return r
+
+
 def _launch(where, dev, fn, *args):
     """Call a C entry point with GPU `dev` current and raise for its status."""
     if _torch.cuda.current_device() != dev:
@@ -686,6 +707,10 @@ def tq_rope(X, table, positions, interleaved: bool = False, inverse: bool = Fals
     rot numbers of each head; inverse turns back, which is the gradient.  Y may be
     X; a new contiguous tensor when None."""
     where = "tq_rope"
+    if Y is None and stream is None:
+        r = _fast.rope(X, table, positions, interleaved, inverse)
+        if r is not None:
+            return _done(r, where)
     kind = _kind(X, "X", where, f32=True)
     (T, H, D), xs = _heads(X, "X", where)
     n_pos, rot = _table(table, where)
@@ -712,6 +737,11 @@ def tq_rope_append(QKV, table, positions, page_table, k_pages, v_pages, interlea
     paged cache, and return the queries [T][Hq][D].  k_pages, v_pages:
     [pages][slots][Hkv][D], any strides, numbers of a head adjacent."""
     where = "tq_rope_append"
+    if Q is None and stream is None:
+        r = _fast.rope_append(QKV, table, positions, page_table, k_pages, v_pages, interleaved,
+                              seqs)
+        if r is not None:
+            return _done(r, where)
     kind = _kind(QKV, "QKV", where)
     (T, H, D), xs = _heads(QKV, "QKV", where)
     if H > 1 and xs[1] != D:
@@ -767,6 +797,10 @@ def tq_paged_attention(Q, k_pages, v_pages, page_table, lens, scale: float | Non
     [pages][slots][Hkv][D] named by page_table [B][width].  Returns out [B][Hq][D],
     and lse float32 [B][Hq] with return_lse.  scale: 1 / sqrt(D) when None."""
     where = "tq_paged_attention"
+    if out is None and workspace is None and stream is None:
+        r = _fast.paged_attention(Q, k_pages, v_pages, page_table, lens, scale, window, return_lse)
+        if r is not None:
+            return _done(r, where)
     kind = _kind(Q, "Q", where)
     (B, Hq, D), qs = _heads(Q, "Q", where)
     P, size, Hkv, page_stride, row_stride, head_stride = _cache(k_pages, v_pages, Q, D, where)
@@ -799,7 +833,7 @@ def tq_paged_attention(Q, k_pages, v_pages, page_table, lens, scale: float | Non
     _launch(where, dev, lib.tq_paged_attention, kind, Q.data_ptr(), qs[0], qs[1],
             k_pages.data_ptr(), v_pages.data_ptr(), P, size, page_stride, row_stride, head_stride,
             page_table.data_ptr(), width, lens.data_ptr(), B, Hq, Hkv, D,
-            D ** -0.5 if scale is None else scale, window, out.data_ptr(),
+            1.0 / math.sqrt(D) if scale is None else scale, window, out.data_ptr(),
             None if lse is None else lse.data_ptr(),
             None if workspace is None else workspace.data_ptr(), n, _raw_stream(stream, dev))
     return (out, lse) if return_lse else out
@@ -836,6 +870,10 @@ def tq_pages_fork(pool, page_table, lens, parent, page_size: int, stream=None):
     lens [rows], parent [new rows].  Returns (page_table, lens, refs, short): the new
     state, how often each page is held, and the rows that found no free page."""
     where = "tq_pages_fork"
+    if stream is None:
+        r = _fast.pages_fork(pool, page_table, lens, parent, page_size)
+        if r is not None:
+            return _done(r, where)
     planes, P, size = _pool(pool, where)
     rows_in, width = _state(page_table, lens, where)
     if not isinstance(parent, _torch.Tensor) or parent.dim() != 1:
@@ -859,6 +897,10 @@ def tq_pages_grow(page_table, lens, add, n_pages: int, page_size: int, stream=No
     """Room for add[r] more tokens in row r, from the pages that no row holds.
     Returns (page_table, lens, short): the new state and how many rows were refused."""
     where = "tq_pages_grow"
+    if stream is None:
+        r = _fast.pages_grow(page_table, lens, add, n_pages, page_size)
+        if r is not None:
+            return _done(r, where)
     rows, width = _state(page_table, lens, where)
     _int32(add, "add", (rows,), where)
     dev = page_table.get_device()
@@ -876,6 +918,10 @@ def tq_pages_compact(pool, page_table, lens, page_size: int, stream=None):
     """Move the pages in use to the low end of the pool.  Returns (page_table, used):
     the new table and the number of pages in use (int32 [1]), all below it."""
     where = "tq_pages_compact"
+    if stream is None:
+        r = _fast.pages_compact(pool, page_table, lens, page_size)
+        if r is not None:
+            return _done(r, where)
     planes, P, size = _pool(pool, where)
     rows, width = _state(page_table, lens, where)
     dev = pool.get_device()

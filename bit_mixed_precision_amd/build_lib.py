@@ -1,4 +1,5 @@
-"""Build libtq.so (host packer + HIP kernels for gfx950) in the package folder.
+"""Build libtq.so (host packer + HIP kernels for gfx950) in the package folder,
+and beside it _tq_torch.so, the compiled part of the torch binding.
 
 Run ``python -m bit_mixed_precision_amd.build_lib`` or call ``build()``.  Host
 C++ is compiled with g++ (IEEE fp64, no contraction); device code with hipcc
@@ -27,6 +28,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libtq.so")
+TORCH_EXT = os.path.join(PKG, "_tq_torch.so")
+TORCH_SRC = os.path.join(CSRC, "torch", "tq_torch.cpp")
 SAN_BUILD = os.path.join(BUILD, "sanitize")
 SAN_LIB = os.path.join(SAN_BUILD, "libtq.so")
 CLANGXX = "/opt/rocm/llvm/bin/clang++"
@@ -65,6 +68,24 @@ def _hip_san_flags():
     return out
 
 
+def _torch_ext_cmd(out):
+    """The compiler call for _tq_torch.so; torch's libraries are already in the
+    process that loads it.  None without torch (host-only use)."""
+    import sysconfig
+    try:
+        import torch
+    except ImportError:
+        return None
+    root = os.path.dirname(torch.__file__)
+    # not HOST_FLAGS: torch's headers are not written for -Wextra
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I", INCLUDE,
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-isystem", os.path.join(root, "include"),
+            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            "-isystem", sysconfig.get_paths()["include"], TORCH_SRC, "-o", out,
+            "-L", os.path.join(root, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"]
+
+
 def build(verbose: bool = False, jobs: int | None = None, sanitize: bool = False) -> str:
     """Compile every source and link libtq.so; always rebuilds.  Returns the path
     (the sanitizer variant's when ``sanitize``)."""
@@ -86,6 +107,9 @@ def build(verbose: bool = False, jobs: int | None = None, sanitize: bool = False
         extra = _hip_san_flags() if sanitize else []
         cmds.append([HIPCC, *HIP_FLAGS, *extra, "-c", os.path.join(CSRC, f), "-o", o])
         objs.append(o)
+    ext = None if sanitize else _torch_ext_cmd(TORCH_EXT + ".tmp")
+    if ext:
+        cmds.append(ext)
     jobs = jobs or min(8, os.cpu_count() or 1)
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
         for out in ex.map(_run, cmds):
@@ -102,6 +126,8 @@ def build(verbose: bool = False, jobs: int | None = None, sanitize: bool = False
         _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-pthread", "-Wl,-z,defs",
               *objs, "-o", tmp])
     os.replace(tmp, target)
+    if ext:
+        os.replace(TORCH_EXT + ".tmp", TORCH_EXT)
     if verbose:
         print("built", target)
     return target

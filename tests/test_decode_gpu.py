@@ -512,6 +512,46 @@ def test_attention_repeats_and_streams():
     assert torch.equal(out, want)
 
 
+def test_compiled_and_python_calls_agree():
+    """The compiled form of each call and the Python one (taken when a stream is
+    named) give the same bits, and a refusal of the C ABI reaches the caller from both."""
+    q, k, v, pt, lens = paged(16, "bf16", [100, 700, 0], 8, 2, 64, 16, poison=False)
+    table = torch.from_numpy(tq.tq_rope_table(1024, 64)).cuda()
+    qkv, pool, parent = randn(2, "bf16", 3, 12, 64), torch.stack([k, v]), i32([1, 1, 0])
+    s = torch.cuda.current_stream().cuda_stream
+
+    def calls(**kw):
+        kc, vc = k.clone(), v.clone()
+        pc, pd = pool.clone(), pool.clone()
+        out = [tq.tq_rope(qkv[:, :10], table, lens, interleaved=True, **kw),
+               tq.tq_rope(qkv.float(), table, lens, inverse=True, **kw),
+               tq.tq_rope_append(qkv, table, i32([0, 1, 2]), pt, kc, vc, **kw), kc, vc,
+               tq.tq_rope_append(qkv, table, i32([0, 1, 2]), pt, kc, vc, True, i32([1, 0, 1]), **kw),
+               tq.tq_paged_attention(q, k, v, pt, lens, **kw),
+               *tq.tq_paged_attention(q, k, v, pt, lens, 0.5, 50, return_lse=True, **kw),
+               *tq.tq_pages_fork(pc, pt, lens, parent, 16, **kw), pc,
+               *tq.tq_pages_grow(pt, lens, i32([1, 90, 5]), k.shape[0], 16, **kw),
+               *tq.tq_pages_compact(pd, pt, lens, 16, **kw), pd]
+        return out
+
+    a, b = calls(), calls(stream=s)
+    assert len(a) == len(b)
+    for x, y in zip(a, b):
+        assert x.dtype == y.dtype and x.shape == y.shape and torch.equal(x, y)
+    for kw in ({}, {"stream": s}):
+        for bad in (lambda: tq.tq_pages_fork(pool, pt, lens, parent, 0, **kw),
+                    lambda: tq.tq_pages_grow(pt, lens, lens, 0, 16, **kw),
+                    lambda: tq.tq_pages_compact(pool, pt, lens, -1, **kw),
+                    lambda: tq.tq_paged_attention(q, k, v, pt, lens, window=-1, **kw),
+                    lambda: tq.tq_paged_attention(q, k, v, pt, lens, float("nan"), **kw),
+                    lambda: tq.tq_paged_attention(q.cpu(), k, v, pt, lens, **kw),
+                    lambda: tq.tq_rope(qkv, table, lens.cpu(), **kw),
+                    lambda: tq.tq_rope(qkv.double(), table, lens, **kw),
+                    lambda: tq.tq_rope_append(qkv, table, lens, pt, k, v.half(), **kw)):
+            with pytest.raises(tq.TQError):
+                bad()
+
+
 def test_decode_ops_in_a_graph():
     """Append, attention and the page operators captured once and replayed, against
     the eager results, with eager work between the replays."""
