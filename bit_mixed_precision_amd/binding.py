@@ -100,7 +100,7 @@ for _name, (_res, _args) in SIGNATURES.items():
     _fn.argtypes = _args
 
 
-# The decode-side calls in their common form, compiled (csrc/torch/tq_torch.cpp);
+# The decode-side calls in their common form, compiled (csrc_decode/tq_torch.cc);
 # each returns None for what it leaves to the functions below.
 if _torch is not None:
     try:

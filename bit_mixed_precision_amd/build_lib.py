@@ -24,12 +24,13 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-CSRC = os.path.join(PKG, "csrc")
+CSRC = os.path.join(PKG, "csrc")                # the ternary products
+CSRC_DECODE = os.path.join(PKG, "csrc_decode")  # the decode-side operators
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libtq.so")
 TORCH_EXT = os.path.join(PKG, "_tq_torch.so")
-TORCH_SRC = os.path.join(CSRC, "torch", "tq_torch.cpp")
+TORCH_SRC = os.path.join(CSRC_DECODE, "tq_torch.cc")
 SAN_BUILD = os.path.join(BUILD, "sanitize")
 SAN_LIB = os.path.join(SAN_BUILD, "libtq.so")
 CLANGXX = "/opt/rocm/llvm/bin/clang++"
@@ -40,17 +41,17 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-ffp-contract=off", "-Wall", "-Wextra",
-              "-I", INCLUDE, "-I", CSRC, "-pthread"]
+              "-I", INCLUDE, "-I", CSRC, "-I", CSRC_DECODE, "-pthread"]
 HIP_FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
              "-Wno-unused-command-line-argument",
-             "-I", INCLUDE, "-I", CSRC]
+             "-I", INCLUDE, "-I", CSRC, "-I", CSRC_DECODE]
 
 
 def _sources():
-    host = sorted(f for f in os.listdir(CSRC) if f.endswith(".cpp"))
-    dev = sorted(f for f in os.listdir(CSRC) if f.endswith(".hip"))
-    return host, dev
+    """Paths of the host (.cpp) and device (.hip) sources of libtq.so."""
+    every = [os.path.join(d, f) for d in (CSRC, CSRC_DECODE) for f in sorted(os.listdir(d))]
+    return [f for f in every if f.endswith(".cpp")], [f for f in every if f.endswith(".hip")]
 
 
 def _run(cmd):
@@ -96,16 +97,16 @@ def build(verbose: bool = False, jobs: int | None = None, sanitize: bool = False
     host, dev = _sources()
     cmds, objs = [], []
     for f in host:
-        o = os.path.join(out_dir, f + ".o")
+        o = os.path.join(out_dir, os.path.basename(f) + ".o")
         if sanitize:
-            cmds.append([CLANGXX, *HOST_FLAGS, *SAN_FLAGS, "-c", os.path.join(CSRC, f), "-o", o])
+            cmds.append([CLANGXX, *HOST_FLAGS, *SAN_FLAGS, "-c", f, "-o", o])
         else:
-            cmds.append(["g++", *HOST_FLAGS, "-c", os.path.join(CSRC, f), "-o", o])
+            cmds.append(["g++", *HOST_FLAGS, "-c", f, "-o", o])
         objs.append(o)
     for f in dev:
-        o = os.path.join(out_dir, f + ".o")
+        o = os.path.join(out_dir, os.path.basename(f) + ".o")
         extra = _hip_san_flags() if sanitize else []
-        cmds.append([HIPCC, *HIP_FLAGS, *extra, "-c", os.path.join(CSRC, f), "-o", o])
+        cmds.append([HIPCC, *HIP_FLAGS, *extra, "-c", f, "-o", o])
         objs.append(o)
     ext = None if sanitize else _torch_ext_cmd(TORCH_EXT + ".tmp")
     if ext:

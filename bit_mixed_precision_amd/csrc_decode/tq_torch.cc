@@ -26,14 +26,17 @@
 
 namespace {
 
-decltype(&tq_rope) c_rope;
-decltype(&tq_rope_append) c_rope_append;
-decltype(&tq_paged_attention) c_paged_attention;
-decltype(&tq_paged_attention_workspace) c_paged_attention_workspace;
-decltype(&tq_pages_workspace) c_pages_workspace;
-decltype(&tq_pages_fork) c_pages_fork;
-decltype(&tq_pages_grow) c_pages_grow;
-decltype(&tq_pages_compact) c_pages_compact;
+struct Entries {
+  decltype(&tq_rope) rope;
+  decltype(&tq_rope_append) rope_append;
+  decltype(&tq_paged_attention) paged_attention;
+  decltype(&tq_paged_attention_workspace) paged_attention_workspace;
+  decltype(&tq_pages_workspace) pages_workspace;
+  decltype(&tq_pages_fork) pages_fork;
+  decltype(&tq_pages_grow) pages_grow;
+  decltype(&tq_pages_compact) pages_compact;
+};
+Entries c{};
 PyObject* raw_stream = nullptr;  // device index -> HIP stream as an int
 
 // A tensor argument, or nullptr.
@@ -162,7 +165,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* s = stream_of(d, &ok);
     if (!ok) return nullptr;
     at::Tensor y = at::empty(x.sizes(), x.options());
-    const int st = c_rope(k, x.data_ptr(), x.stride(0), x.stride(1), y.data_ptr(), y.stride(0),
+    const int st = c.rope(k, x.data_ptr(), x.stride(0), x.stride(1), y.data_ptr(), y.stride(0),
                           y.stride(1), ptr<float>(table), table.size(0), 2 * table.size(1),
                           ptr<int32_t>(pos), x.size(0), x.size(1), x.size(2), inter, inv, s);
     return st == TQ_OK ? THPVariable_Wrap(y) : PyLong_FromLong(st);
@@ -190,7 +193,7 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* s = stream_of(d, &ok);
     if (!ok) return nullptr;
     at::Tensor q = at::empty({T, Hq, D}, x.options());
-    const int st = c_rope_append(
+    const int st = c.rope_append(
         kd, x.data_ptr(), x.stride(0), ptr<float>(table), table.size(0), 2 * table.size(1),
         ptr<int32_t>(pos), seqs ? ptr<int32_t>(*seqs) : nullptr, ptr<int32_t>(pages),
         pages.size(0), pages.size(1), k.data_ptr(), v.data_ptr(), k.size(0), k.size(1),
@@ -216,7 +219,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const long long window = PyLong_AsLongLong(a[6]);
     if (window == -1 && PyErr_Occurred()) return nullptr;
     const int64_t bytes =
-        c_paged_attention_workspace(B, Hq, k.size(2), D, k.size(1), pages.size(1));
+        c.paged_attention_workspace(B, Hq, k.size(2), D, k.size(1), pages.size(1));
     if (bytes < 0) return PyLong_FromLong((long)bytes);
     bool ok;
     void* s = stream_of(d, &ok);
@@ -224,7 +227,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor out = at::empty({B, Hq, D}, q.options()), lse, ws;
     if (with_lse) lse = at::empty({B, Hq}, q.options().dtype(at::kFloat));
     if (bytes > 0) ws = at::empty({bytes}, q.options().dtype(at::kByte));
-    const int st = c_paged_attention(
+    const int st = c.paged_attention(
         kd, q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), v.data_ptr(), k.size(0),
         k.size(1), k.stride(0), k.stride(1), k.stride(2), ptr<int32_t>(pages), pages.size(1),
         ptr<int32_t>(lens), B, Hq, k.size(2), D, scale, window, out.data_ptr(),
@@ -249,7 +252,7 @@ PyObject* pages_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const long long size = PyLong_AsLongLong(a[4]);
     if (size == -1 && PyErr_Occurred()) return nullptr;
     const int64_t rows = parent.size(0), width = table.size(1);
-    const int64_t bytes = c_pages_workspace(rows, pages);
+    const int64_t bytes = c.pages_workspace(rows, pages);
     if (bytes < 0) return PyLong_FromLong((long)bytes);
     bool ok;
     void* s = stream_of(d, &ok);
@@ -258,7 +261,7 @@ PyObject* pages_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor ws = at::empty({bytes / 4}, o), table_out = at::empty({rows, width}, o),
                lens_out = at::empty({rows}, o), refs = at::empty({pages}, o),
                lacking = at::empty({1}, o);
-    const int st = c_pages_fork(pool.data_ptr(), planes, pages, page_bytes, ptr<int32_t>(table),
+    const int st = c.pages_fork(pool.data_ptr(), planes, pages, page_bytes, ptr<int32_t>(table),
                                 ptr<int32_t>(lens), table.size(0), ptr<int32_t>(parent), rows,
                                 width, size, ptr<int32_t>(table_out), ptr<int32_t>(lens_out),
                                 ptr<int32_t>(refs), ptr<int32_t>(lacking), ws.data_ptr(), bytes, s);
@@ -280,7 +283,7 @@ PyObject* pages_grow(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const long long pages = PyLong_AsLongLong(a[3]), size = PyLong_AsLongLong(a[4]);
     if (PyErr_Occurred()) return nullptr;
     const int64_t rows = table.size(0), width = table.size(1);
-    const int64_t bytes = c_pages_workspace(rows, pages);
+    const int64_t bytes = c.pages_workspace(rows, pages);
     if (bytes < 0) return PyLong_FromLong((long)bytes);
     bool ok;
     void* s = stream_of(d, &ok);
@@ -288,7 +291,7 @@ PyObject* pages_grow(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto o = lens.options();
     at::Tensor ws = at::empty({bytes / 4}, o), table_out = at::empty({rows, width}, o),
                lens_out = at::empty({rows}, o), lacking = at::empty({1}, o);
-    const int st = c_pages_grow(ptr<int32_t>(table), ptr<int32_t>(lens), ptr<int32_t>(add), rows,
+    const int st = c.pages_grow(ptr<int32_t>(table), ptr<int32_t>(lens), ptr<int32_t>(add), rows,
                                 width, size, pages, ptr<int32_t>(table_out),
                                 ptr<int32_t>(lens_out), ptr<int32_t>(lacking), ws.data_ptr(),
                                 bytes, s);
@@ -310,7 +313,7 @@ PyObject* pages_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const long long size = PyLong_AsLongLong(a[3]);
     if (size == -1 && PyErr_Occurred()) return nullptr;
     const int64_t rows = table.size(0), width = table.size(1);
-    const int64_t bytes = c_pages_workspace(rows, pages);
+    const int64_t bytes = c.pages_workspace(rows, pages);
     if (bytes < 0) return PyLong_FromLong((long)bytes);
     bool ok;
     void* s = stream_of(d, &ok);
@@ -318,7 +321,7 @@ PyObject* pages_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto o = lens.options();
     at::Tensor ws = at::empty({bytes / 4}, o), table_out = at::empty({rows, width}, o),
                used = at::empty({1}, o);
-    const int st = c_pages_compact(pool.data_ptr(), planes, pages, page_bytes, ptr<int32_t>(table),
+    const int st = c.pages_compact(pool.data_ptr(), planes, pages, page_bytes, ptr<int32_t>(table),
                                    ptr<int32_t>(lens), rows, width, size, ptr<int32_t>(table_out),
                                    ptr<int32_t>(used), ws.data_ptr(), bytes, s);
     return st == TQ_OK ? tuple({table_out, used}) : PyLong_FromLong(st);
@@ -342,12 +345,14 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     std::memcpy(fn, &p, sizeof p);
     return true;
   };
-  if (!take("tq_rope", &c_rope) || !take("tq_rope_append", &c_rope_append) ||
-      !take("tq_paged_attention", &c_paged_attention) ||
-      !take("tq_paged_attention_workspace", &c_paged_attention_workspace) ||
-      !take("tq_pages_workspace", &c_pages_workspace) || !take("tq_pages_fork", &c_pages_fork) ||
-      !take("tq_pages_grow", &c_pages_grow) || !take("tq_pages_compact", &c_pages_compact))
+  Entries e{};  // all or nothing
+  if (!take("tq_rope", &e.rope) || !take("tq_rope_append", &e.rope_append) ||
+      !take("tq_paged_attention", &e.paged_attention) ||
+      !take("tq_paged_attention_workspace", &e.paged_attention_workspace) ||
+      !take("tq_pages_workspace", &e.pages_workspace) || !take("tq_pages_fork", &e.pages_fork) ||
+      !take("tq_pages_grow", &e.pages_grow) || !take("tq_pages_compact", &e.pages_compact))
     return nullptr;
+  c = e;
   Py_INCREF(a[0]);
   Py_XDECREF(raw_stream);
   raw_stream = a[0];

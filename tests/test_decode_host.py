@@ -284,6 +284,31 @@ def test_binding_refusals():
     assert _status(tq.tq_pages_copy, pool, pos, pos) == D
 
 
+def test_compiled_calls_leave_the_rest_to_python():
+    """The compiled functions return None, and do nothing, for anything but tensors
+    on the current GPU: the Python path then words the refusal."""
+    f = tq._fast
+    X, pos = torch.zeros(3, 4, 16, dtype=torch.float16), torch.zeros(3, dtype=torch.int32)
+    tab, pt = torch.zeros(8, 8, 2), torch.zeros(3, 4, dtype=torch.int32)
+    k, pool = torch.zeros(5, 16, 2, 16, dtype=torch.float16), torch.zeros(2, 5, 16, 16)
+    assert f.rope(X, tab, pos, False, False) is None
+    assert f.rope(None, tab, pos, False, False) is None
+    assert f.rope(X, tab) is None and f.rope() is None
+    assert f.rope_append(X, tab, pos, pt, k, k, False, None) is None
+    assert f.rope_append(X, tab, pos, pt, k, k, False, 3) is None
+    assert f.paged_attention(X, k, k, pt, pos, None, 0, True) is None
+    assert f.paged_attention(X, k, k, pt, pos, "a", 0, True) is None
+    assert f.pages_fork(pool, pt, pos, pos, 16) is None
+    assert f.pages_grow(pt, pos, pos, 5, 16) is None
+    assert f.pages_compact(pool, pt, pos, 16) is None
+    with pytest.raises(TypeError):
+        f.bind()
+    with pytest.raises(KeyError):
+        f.bind(lambda i: 0, {"tq_rope": 1})
+    # what was bound before still is
+    assert f.rope(X, tab, pos, False, False) is None
+
+
 def test_division_constants():
     """The multiply-and-shift divisions of the kernels, t / d for t < 2^30 and n / d
     for n < 2^31, at every divisor's most critical dividends."""
