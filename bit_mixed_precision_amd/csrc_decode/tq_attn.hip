@@ -95,6 +95,7 @@ struct AttnParams {
   FastDiv page;
   int32_t n_pages, width, B, Hq, Hkv, D, G, qtiles, window;
   int32_t direct;  // one workgroup per (sequence, head): nothing is split
+  int32_t full;    // tiles of 16 KB in pages of whole half tiles, two workgroups per CU
   float scale;
 };
 
@@ -284,10 +285,23 @@ __device__ __forceinline__ void finish(const AttnParams& p, int b, int head, int
 }
 
 // Workgroups per CU, for which the registers are laid out: enough bytes in flight,
-// and more only spill.  Measured (us): heads of 128, 96 sequences of 2048 .. 8192
-// tokens, 8 key heads: 2 285, 3 322; heads of 64, 8 sequences of 32768, 8 key
-// heads: 2 110, 3 99, 4 114; heads of 256, the same with 2 key heads: 1 97, 2 131.
-__host__ __device__ constexpr int blocks_per_cu(int64_t D) { return D > 128 ? 1 : D > 64 ? 2 : 3; }
+// and more only spill or crowd.  Measured (us): heads of 128, 96 sequences of 2048
+// .. 8192 tokens, 8 key heads: 2 285, 3 322; heads of 64, 64 sequences of up to 4096,
+// 24 key heads: 2 163, 3 180; heads of 256, 8 sequences of 32768, 2 key heads: 1 97,
+// 2 131.
+__host__ __device__ constexpr int blocks_per_cu(int64_t D) { return D > 128 ? 1 : 2; }
+
+// Waves that share the tiles, of those that run: half of them, one workgroup per
+// CU, where each has many tiles that are fetched without a detour (p.full: 16 KB a
+// tile, pages of whole half tiles), which keeps 64 KB of a CU in flight as it is.
+// Measured (us, half / all): one sequence of 131072 tokens, 8 key heads of 128: 90 /
+// 100, 96 sequences of 2048 .. 8192: 274 / 280; with fewer tiles a wave the other way
+// round: 32 sequences of up to 1024 tokens (2.5 a wave) 26.2 / 24.4, 128 of them (10)
+// 65.3 / 63.8; heads of 80 161 / 126, pages of 24 108 / 98.
+constexpr uint32_t kManyTiles = 12;
+__device__ __forceinline__ uint32_t waves_for(const AttnParams& p, uint32_t units, uint32_t waves) {
+  return p.full && units / kManyTiles >= waves ? waves / 2 : waves;
+}
 
 // DV: 64, 128 or 256, the head dimension rounded up (D <= DV, D % 8 == 0).
 // UNI: the page size is a multiple of 16, so a half tile lies in one page and
@@ -334,7 +348,7 @@ __global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attenti
     const int per = (p.B + kWave - 1) / kWave;
     uint32_t mine, total;
     const uint32_t before = scan_tiles(p, lane, per, mine, total);
-    cut = Cut(total * H, gridDim.x * kAttnWaves);
+    cut = Cut(total * H, waves_for(p, total * H, gridDim.x * kAttnWaves));
     const uint32_t part = blockIdx.x * kAttnWaves + wave;
     left = 0;
     if (part < cut.parts) {
@@ -994,6 +1008,7 @@ hipError_t launch_paged_attention(int dtype, const AttnArgs& a, hipStream_t stre
   p.scale = a.scale_log2;
   const Grid g = attn_grid(a.B, a.Hq, a.Hkv, a.D, a.width * a.page_size);
   p.direct = g.direct;
+  p.full = a.D == 128 && a.page_size % 16 == 0 && g.blocks >= 2 * device_cus();
   p.owner = reinterpret_cast<int2*>(
       p.partial + g.partials * slot_floats(p.G < kHeads ? p.G : kHeads, p.D));
   return dtype == TQ_BF16 ? launch_t<true>(p, g.blocks, stream)

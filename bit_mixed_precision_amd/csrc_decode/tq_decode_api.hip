@@ -52,6 +52,27 @@ bool distinct(int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t len) {
   return n_large == 1 || large >= run;
 }
 
+// The same for the heads of the slots of the pages of a cache, whose strides are
+// nested in some order.
+bool distinct_cache(int64_t n_pages, int64_t page, int64_t page_size, int64_t row, int64_t heads,
+                    int64_t head, int64_t len) {
+  struct Level {
+    int64_t n, stride;
+  } l[3] = {{n_pages, page}, {page_size, row}, {heads, head}};
+  int64_t reach = len;  // elements from the first to past the last so far
+  bool done[3] = {l[0].n == 1, l[1].n == 1, l[2].n == 1};
+  for (int i = 0; i < 3; ++i) {
+    int least = -1;
+    for (int k = 0; k < 3; ++k)
+      if (!done[k] && (least < 0 || l[k].stride < l[least].stride)) least = k;
+    if (least < 0) break;
+    if (l[least].stride < reach) return false;
+    reach += l[least].stride * (l[least].n - 1);
+    done[least] = true;
+  }
+  return true;
+}
+
 int rope_shapes(int64_t n_pos, int64_t rot, int64_t T, int64_t H, int64_t D) {
   if (n_pos < 0 || n_pos > kMaxTokens || D > kMaxHeadDim || rot < 2 || rot % 2 || rot > D ||
       T > kMaxTokens || H > kMaxHeads || T * H > INT32_MAX)
@@ -143,7 +164,8 @@ int tq_rope_append(int dtype, const void* QKV, int64_t qkv_tok, const float* tab
       !stride_ok(head_stride) || n_pages < 1 || n_pages > INT32_MAX || n_seqs < 1 ||
       n_seqs > INT32_MAX || width < 1 || page_size < 1 || width > kMaxTokens ||
       page_size > kMaxTokens || width * page_size > kMaxTokens ||
-      page_stride > INT64_MAX / 4 / n_pages || row_stride > INT64_MAX / 4 / page_size)
+      page_stride > INT64_MAX / 4 / n_pages || row_stride > INT64_MAX / 4 / page_size ||
+      !distinct_cache(n_pages, page_stride, page_size, row_stride, Hkv, head_stride, D))
     return TQ_ERR_SHAPE;
   if (!aligned(QKV, 2) || !aligned(Q, 2) || !aligned(k_pages, 2) || !aligned(v_pages, 2) ||
       !aligned(table, 8) || !aligned(pos, 4) || !aligned(seqs, 4) || !aligned(page_table, 4))

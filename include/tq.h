@@ -420,7 +420,8 @@ int tq_rope(int dtype, const void* X, int64_t x_tok, int64_t x_head, void* Y, in
  * [0, n_seqs), the position is past the table's width, or the page is outside
  * [0, n_pages).  Two tokens of one call must not name the same slot.
  * Errors as tq_rope's, and TQ_ERR_SHAPE for page geometry (page_size < 1,
- * negative strides, width * page_size > 2^30). */
+ * negative strides, width * page_size > 2^30, strides that let two numbers of a
+ * cache share an address). */
 int tq_rope_append(int dtype, const void* QKV, int64_t qkv_tok, const float* table, int64_t n_pos,
                    int64_t rot, const int32_t* pos, const int32_t* seqs, const int32_t* page_table,
                    int64_t n_seqs, int64_t width, void* k_pages, void* v_pages, int64_t n_pages,
@@ -439,7 +440,7 @@ int tq_rope_append(int dtype, const void* QKV, int64_t qkv_tok, const float* tab
  * [0, n_pages) counts as absent: its tokens are left out.  What the cache holds
  * in other slots, NaN included, has no influence.
  * fp16 or bfloat16 in and out, fp32 scores, weights and sums.  The same bits on
- * every run.
+ * every run.  Outputs and workspace must not overlap the inputs.
  * D a multiple of 8, 8 <= D <= 256; Hq a multiple of Hkv, Hq <= 2^12; B <=
  * 2^20; width * page_size <= 2^30; B * Hkv * ceil(Hq / Hkv / 16) * (width *
  * page_size / 32 + 2) < 2^31; strides multiples of 8, row_stride <= 2^24;

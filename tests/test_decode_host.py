@@ -139,8 +139,13 @@ def test_rope_append_refusals():
     assert _append(X=None, T=0) == tq.TQ_OK
     for bad in (dict(T=-1), dict(rot=17), dict(Hq=0), dict(Hkv=0), dict(P=0), dict(ps=0),
                 dict(width=0), dict(width=1 << 20, ps=1 << 11), dict(n_seqs=0), dict(pst=-8),
-                dict(hst=-1), dict(pst=1 << 46, P=1 << 30)):
+                dict(hst=-1), dict(pst=1 << 46, P=1 << 30), dict(hst=0), dict(hst=15),
+                dict(rst=16), dict(pst=0), dict(pst=511), dict(hst=512, rst=16, pst=767)):
         assert _append(**bad) == tq.TQ_ERR_SHAPE, bad
+    # heads outside slots, slots outside pages: any nesting is a cache (refused later)
+    for good in (dict(hst=256, rst=16, pst=512), dict(hst=144, rst=9 * 2 * 16, pst=16),
+                 dict(pst=513), dict(P=1, pst=0)):
+        assert _append(**good, dtype=2) == tq.TQ_ERR_VALUE, good
     for bad in (dict(X=A + 1), dict(k=A + 1), dict(pt=A + 2), dict(seqs=A + 1)):
         assert _append(**bad) == tq.TQ_ERR_ALIGN, bad
     for bad in (dict(dtype=2), dict(inter=3)):
