@@ -48,6 +48,7 @@ struct PagesParams {
   int32_t* spare;   // [n_pages] free pages in ascending order
   int32_t* map;     // [n_pages] compact: where a page goes
   int32_t* pairs;   // [1] number of (src, dst)
+  bool writes;      // this workgroup writes the outputs
 };
 
 __device__ __forceinline__ bool names_page(const PagesParams& p, int32_t id) {
@@ -208,9 +209,9 @@ __device__ __forceinline__ void fork_assign(const PagesParams& p, int* red) {
         const int32_t id = p.spare[rank];
         p.src[rank] = p.last[r];
         p.dst[rank] = id;
-        *out = id;
+        if (p.writes) *out = id;
         if (p.refs) p.refs[id] = 1;
-      } else {
+      } else if (p.writes) {
         *out = -1;
         p.lens_out[r] = tokens / p.page_size * p.page_size;
       }
@@ -315,30 +316,100 @@ __global__ __launch_bounds__(kScanThreads) void pages_assign_kernel(PagesParams 
   assign<OP>(p, red);
 }
 
+// Bytes that a workgroup of T threads copies at a time, and such pieces of a page.
+template <int T>
+__host__ __device__ __forceinline__ int64_t pieces_of(int64_t page_bytes) {
+  return (page_bytes + T * 64 - 1) / (T * 64);
+}
+
+// This workgroup's share of pairs x planes x pieces of a page, one in `blocks`.
+// I: an unsigned type that holds their number; 64-bit divisions take longer than
+// copying a piece.
+template <int T, class I>
+__device__ __forceinline__ void copy_share(const PagesParams& p, I pairs, I pieces, I first,
+                                           I blocks) {
+  const I planes = (I)p.planes, total = pairs * planes * pieces;
+  for (I i = first; i < total; i += blocks) {
+    const I rest = i / pieces, piece = i - rest * pieces;
+    const I pair = rest / planes, plane = rest - pair * planes;
+    const int32_t s = p.src[pair], d = p.dst[pair];
+    if (!names_page(p, s) || !names_page(p, d)) continue;
+    const unsigned char* from = p.pool + ((int64_t)plane * p.n_pages + s) * p.page_bytes;
+    unsigned char* to = p.pool + ((int64_t)plane * p.n_pages + d) * p.page_bytes;
+    const int64_t at = (int64_t)piece * (T * 64) + threadIdx.x * 16;
+    u32x4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (at + k * T * 16 < p.page_bytes)
+        v[k] = *reinterpret_cast<const u32x4*>(from + at + k * T * 16);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (at + k * T * 16 < p.page_bytes)
+        *reinterpret_cast<u32x4*>(to + at + k * T * 16) = v[k];
+  }
+}
+
+template <int T>
+__device__ __forceinline__ void copy_turns(const PagesParams& p, int64_t pairs, uint32_t first,
+                                           uint32_t blocks) {
+  const int64_t pieces = pieces_of<T>(p.page_bytes);
+  if (pairs * p.planes * pieces < INT32_MAX - (int64_t)blocks)
+    copy_share<T, uint32_t>(p, (uint32_t)pairs, (uint32_t)pieces, first, blocks);
+  else
+    copy_share<T, uint64_t>(p, pairs, pieces, first, blocks);
+}
+
+// Row r of the table after compaction, by the threads of a workgroup.
+__device__ __forceinline__ void retable_row(const PagesParams& p, int r, int held, int used,
+                                            int thread, int threads) {
+  const int64_t row = (int64_t)r * p.width;
+  for (int i = thread; i < p.width; i += threads) {
+    int32_t id = i < held ? p.table[row + i] : -1;
+    if (names_page(p, id) && id >= used) id = p.map[id];
+    p.table_out[row + i] = id;
+  }
+}
+
 // All of the bookkeeping in one workgroup, with the bitmap and the rows' wishes in
 // LDS: one launch instead of three, for states that one compute unit walks
-// through in a few microseconds.
+// through in a few microseconds.  INSIDE (fork, compact): every workgroup does it
+// for itself, the first writes the results and the others copy the pages, so that
+// nothing else has to be launched.
 constexpr int kOneRows = 256;
 // Forking counts the holders of every page in LDS too (atomics on memory from one
 // compute unit take 1.5 ns each: 256 x 128 entries 65 us).
-template <int OP>
-constexpr int one_pages() { return OP == kFork ? 8 * 1024 : 64 * 1024; }
+template <int OP, bool INSIDE>
+constexpr int one_pages() {
+  return OP == kFork ? 8 * 1024 : INSIDE ? 4 * 1024 : 64 * 1024;
+}
 
-template <int OP>
+template <int OP, bool INSIDE>
 __global__ __launch_bounds__(kScanThreads) void pages_one_kernel(PagesParams p) {
+  constexpr int kPages = one_pages<OP, INSIDE>();
+  constexpr int kPairs = !INSIDE ? 1 : OP == kFork ? kOneRows : kPages / 2;
   __shared__ int red[kScanThreads / kWave];
-  __shared__ uint32_t sBits[one_pages<OP>() / 32];
-  __shared__ int32_t sRefs[OP == kFork ? one_pages<OP>() : 1];
+  __shared__ uint32_t sBits[kPages / 32];
+  __shared__ int32_t sRefs[OP == kFork ? kPages : 1];
   __shared__ int sFrom[kOneRows], sHeld[kOneRows], sNeed[kOneRows], sLast[kOneRows];
   __shared__ int sSpare[kOneRows], sTokens[kOneRows];
+  __shared__ int32_t sSrc[kPairs], sDst[kPairs], sMap[INSIDE && OP == kCompact ? kPages : 1];
+  __shared__ int32_t sPairs, sResult;
   const int t = threadIdx.x;
+  int32_t *const refs_out = p.refs, *const result_out = p.result;
+  p.writes = !INSIDE || blockIdx.x == 0;
   p.bits = sBits;
   p.need = sNeed;
   p.last = sLast;
   p.tokens = sTokens;
   if (OP == kFork) p.spare = sSpare;  // a page a row at most
+  if constexpr (INSIDE) {
+    p.src = sSrc;
+    p.dst = sDst;
+    p.map = sMap;
+    p.pairs = &sPairs;
+    p.result = &sResult;
+  }
   for (int i = t; i < (p.n_pages + 31) / 32; i += kScanThreads) sBits[i] = 0;
-  int32_t* refs_out = p.refs;
   if constexpr (OP == kFork) {
     for (int i = t; i < p.n_pages; i += kScanThreads) sRefs[i] = 0;
     p.refs = sRefs;
@@ -354,7 +425,7 @@ __global__ __launch_bounds__(kScanThreads) void pages_one_kernel(PagesParams p) 
     sHeld[t] = entries(p, tokens);
     sNeed[t] = OP == kFork && from >= 0 && tokens % p.page_size != 0;  // may want a copy
     sTokens[t] = tokens;
-    if constexpr (OP == kFork) p.lens_out[t] = tokens;
+    if (OP == kFork && p.writes) p.lens_out[t] = tokens;
     if constexpr (OP == kGrow) sNeed[t] = wanted_pages(p, t, tokens);
   }
   __syncthreads();
@@ -382,7 +453,7 @@ __global__ __launch_bounds__(kScanThreads) void pages_one_kernel(PagesParams p) 
         wants = __any(later);
         if (lane == 0) sNeed[r] = wants;
       }
-      const int end = OP == kCompact ? held : p.width;
+      const int end = OP == kCompact || !p.writes ? held : p.width;
       for (int j = lane; j < end; j += kWave) {
         int32_t id = j < kWave ? head[u] : j < held ? p.table[(int64_t)sFrom[r] * p.width + j] : -1;
         if (j < held) {
@@ -395,44 +466,24 @@ __global__ __launch_bounds__(kScanThreads) void pages_one_kernel(PagesParams p) 
             if constexpr (OP == kFork) atomicAdd(&sRefs[id], 1);
           }
         }
-        if constexpr (OP != kCompact) p.table_out[(int64_t)r * p.width + j] = id;
+        if (OP != kCompact && p.writes) p.table_out[(int64_t)r * p.width + j] = id;
       }
     }
   }
   __syncthreads();
   assign<OP>(p, red);
-  if (OP == kFork && refs_out) {
-    __syncthreads();
+  __syncthreads();
+  if (OP == kFork && p.writes && refs_out)
     for (int i = t; i < p.n_pages; i += kScanThreads) refs_out[i] = sRefs[i];
-  }
-}
-
-constexpr int kCopyBytes = kPagesThreads * 16 * 4;  // bytes of one workgroup's step
-
-// This workgroup's share of pairs x planes x pieces of a page, one in `blocks`.
-// I: an unsigned type that holds their number; 64-bit divisions take longer than
-// copying a piece.
-template <class I>
-__device__ __forceinline__ void copy_share(const PagesParams& p, I pairs, I pieces, I first,
-                                           I blocks) {
-  const I planes = (I)p.planes, total = pairs * planes * pieces;
-  for (I i = first; i < total; i += blocks) {
-    const I rest = i / pieces, piece = i - rest * pieces;
-    const I pair = rest / planes, plane = rest - pair * planes;
-    const int32_t s = p.src[pair], d = p.dst[pair];
-    if (!names_page(p, s) || !names_page(p, d)) continue;
-    const unsigned char* from = p.pool + ((int64_t)plane * p.n_pages + s) * p.page_bytes;
-    unsigned char* to = p.pool + ((int64_t)plane * p.n_pages + d) * p.page_bytes;
-    const int64_t at = (int64_t)piece * kCopyBytes + threadIdx.x * 16;
-    u32x4 v[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (at + k * kPagesThreads * 16 < p.page_bytes)
-        v[k] = *reinterpret_cast<const u32x4*>(from + at + k * kPagesThreads * 16);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (at + k * kPagesThreads * 16 < p.page_bytes)
-        *reinterpret_cast<u32x4*>(to + at + k * kPagesThreads * 16) = v[k];
+  if constexpr (INSIDE) {
+    if (blockIdx.x > 0) {
+      copy_turns<kScanThreads>(p, sPairs, blockIdx.x - 1, gridDim.x - 1);
+      return;
+    }
+    if (t == 0) *result_out = sResult;
+    if constexpr (OP == kCompact)
+      for (int r = t >> 6; r < p.rows; r += kWaves)
+        retable_row(p, r, sHeld[r], sResult, lane, kWave);
   }
 }
 
@@ -442,24 +493,12 @@ __global__ __launch_bounds__(kPagesThreads) void pages_move_kernel(PagesParams p
                                                                    int table_blocks) {
   if ((int)blockIdx.x < table_blocks) {
     const int used = *p.result;
-    for (int r = blockIdx.x; r < p.rows; r += table_blocks) {
-      const int held = entries(p, tokens_of(p, r));
-      const int64_t row = (int64_t)r * p.width;
-      for (int i = threadIdx.x; i < p.width; i += kPagesThreads) {
-        int32_t id = i < held ? p.table[row + i] : -1;
-        if (names_page(p, id) && id >= used) id = p.map[id];
-        p.table_out[row + i] = id;
-      }
-    }
+    for (int r = blockIdx.x; r < p.rows; r += table_blocks)
+      retable_row(p, r, entries(p, tokens_of(p, r)), used, threadIdx.x, kPagesThreads);
     return;
   }
-  const uint32_t blocks = gridDim.x - table_blocks, first = blockIdx.x - table_blocks;
-  const int64_t pieces = (p.page_bytes + kCopyBytes - 1) / kCopyBytes;
-  const int64_t pairs = p.pairs ? (int64_t)*p.pairs : n;
-  if (pairs * p.planes * pieces < INT32_MAX - (int64_t)blocks)
-    copy_share<uint32_t>(p, (uint32_t)pairs, (uint32_t)pieces, first, blocks);
-  else
-    copy_share<uint64_t>(p, pairs, pieces, first, blocks);
+  copy_turns<kPagesThreads>(p, p.pairs ? (int64_t)*p.pairs : n, blockIdx.x - table_blocks,
+                            gridDim.x - table_blocks);
 }
 
 int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
@@ -497,14 +536,15 @@ PagesParams params(const PagesArgs& a) {
   p.spare = reinterpret_cast<int32_t*>(take(a.n_pages));
   p.map = reinterpret_cast<int32_t*>(take(a.n_pages));
   p.pairs = reinterpret_cast<int32_t*>(take(1));
+  p.writes = true;
   return p;
 }
 
 // The copies, at most `most` of them, and the new table where `retable` is set.
 hipError_t move(const PagesParams& p, int64_t most, bool retable, hipStream_t s) {
-  const int64_t pieces = (p.page_bytes + kCopyBytes - 1) / kCopyBytes;
   const int64_t grid = 8 * device_cus();
-  const int64_t items = most > grid && p.planes ? grid : most * p.planes * pieces;
+  const int64_t items =
+      most > grid && p.planes ? grid : most * p.planes * pieces_of<kPagesThreads>(p.page_bytes);
   const int table_blocks = !retable ? 0 : p.rows < 256 ? p.rows : 256;
   const int64_t blocks = table_blocks + (items < grid ? items : grid);
   if (blocks == 0) return hipSuccess;
@@ -531,8 +571,8 @@ constexpr int64_t kOneEntries = 48 * 1024;
 template <int OP>
 hipError_t launch_state(const PagesParams& p, hipStream_t s) {
   if (p.rows <= kOneRows && (int64_t)p.rows * p.width <= kOneEntries &&
-      p.n_pages <= one_pages<OP>()) {
-    hipLaunchKernelGGL(pages_one_kernel<OP>, dim3(1), dim3(kScanThreads), 0, s, p);
+      p.n_pages <= one_pages<OP, false>()) {
+    hipLaunchKernelGGL((pages_one_kernel<OP, false>), dim3(1), dim3(kScanThreads), 0, s, p);
     return hipGetLastError();
   }
   const int64_t blocks = (p.n_pages + kPagesThreads - 1) / kPagesThreads;
@@ -544,13 +584,34 @@ hipError_t launch_state(const PagesParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Bookkeeping and copies (`most` of them at most): in one launch where both are
+// small, because every workgroup then does the bookkeeping.  Measured (us on the GPU,
+// one launch / two; rows x width, planes): fork 4 x 10, 8 6.0 / 7.3, 64 x 128, 2 8.4 /
+// 10.4, 32 x 16, 16 8.9 / 9.8; compaction 3 x 64, 4 7.6 / 8.5, 64 x 43, 8 23.6 / 24.4.
+// Beyond the limits the bookkeeping of many workgroups gets in its own way: fork 64
+// x 43, 32 23 / 18, 256 x 32, 2 40 / 18.
+constexpr int64_t kInsideRows = 64, kInsideEntries = 8 * 1024, kInsideItems = 512;
+constexpr int64_t kInsideBlocks = 128;
+
+template <int OP>
+hipError_t launch_pages(const PagesParams& p, int64_t most, hipStream_t s) {
+  const int64_t pieces = pieces_of<kScanThreads>(p.page_bytes);
+  if (p.rows <= kInsideRows && (int64_t)p.rows * p.width <= kInsideEntries &&
+      p.n_pages <= one_pages<OP, true>() && most * p.planes * pieces <= kInsideItems) {
+    const int64_t items = most * p.planes * pieces;
+    hipLaunchKernelGGL((pages_one_kernel<OP, true>),
+                       dim3((uint32_t)(1 + (items < kInsideBlocks ? items : kInsideBlocks))),
+                       dim3(kScanThreads), 0, s, p);
+    return hipGetLastError();
+  }
+  const hipError_t e = launch_state<OP>(p, s);
+  return e != hipSuccess ? e : move(p, most, OP == kCompact, s);
+}
+
 }  // namespace
 
 hipError_t launch_pages_fork(const PagesArgs& a, hipStream_t s) {
-  const PagesParams p = params(a);
-  const hipError_t e = launch_state<kFork>(p, s);
-  if (e != hipSuccess) return e;
-  return move(p, a.rows < a.n_pages ? a.rows : a.n_pages, false, s);
+  return launch_pages<kFork>(params(a), a.rows < a.n_pages ? a.rows : a.n_pages, s);
 }
 
 hipError_t launch_pages_grow(const PagesArgs& a, hipStream_t s) {
@@ -558,10 +619,7 @@ hipError_t launch_pages_grow(const PagesArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_pages_compact(const PagesArgs& a, hipStream_t s) {
-  const PagesParams p = params(a);
-  const hipError_t e = launch_state<kCompact>(p, s);
-  if (e != hipSuccess) return e;
-  return move(p, a.n_pages / 2 + 1, true, s);
+  return launch_pages<kCompact>(params(a), a.n_pages / 2, s);
 }
 
 hipError_t launch_pages_copy(unsigned char* pool, int64_t planes, int64_t n_pages,
