@@ -47,11 +47,11 @@
 // kernel (no atomics: the same bits on every run).
 //
 // Measured: 96 sequences of 2048 .. 8192 tokens, 64 query / 8 key-value heads of
-// 128, pages of 16, 1.75 GB: 282 us, 6.2 TB/s (89% of what a plain read reaches on
+// 128, pages of 16, 1.75 GB: 273 us, 6.4 TB/s (92% of what a plain read reaches on
 // this card, 6.97 TB/s; HBM reads by the counters 1.00 of the algorithmic bytes);
-// one sequence of 131072 tokens, 537 MB: 100 us, of which the join takes 8; 37
-// ragged sequences of up to 4096 tokens, 24 heads of 64 in bf16, 116 MB: 32 us (25 in
-// the first kernel, whose start and end weigh more); one of 97 tokens: 6.1 us, four
+// one sequence of 131072 tokens, 537 MB: 90 us, of which the join takes 5; 37
+// ragged sequences of up to 4096 tokens, 24 heads of 64 in bf16, 116 MB: 31 us (25 in
+// the first kernel, whose start and end weigh more); one of 97 tokens: 6.2 us, four
 // dependent memory latencies and the launch.
 
 #include <atomic>

@@ -5,13 +5,16 @@
 // (bit-wise or and integer counts only, so the order of the atomics does not
 // show), one workgroup ranks its free (or used) bits by popcounts and a prefix
 // sum, and the data moves in a last launch that reads the list of pairs and
-// their number from device memory: no call waits for the host.
+// their number from device memory: no call waits for the host.  Small states take
+// fewer launches: the bookkeeping by one workgroup in LDS, or by every workgroup
+// that copies, each for itself.
 //
 // Bound: the copied pages, read and written once per plane.  Measured: compacting a
 // pool of 2048 pages in 16 planes, 500 moved, 524 MB: 114 us a call, of which the
 // copies take 105 (5.0 TB/s; a plain copy reaches 4.9); forking 16 requests of 4
-// beams, 32 pages copied in 32 planes, 67 MB: 15-17 us; one request of 4 beams 11 us,
-// two launches and the bookkeeping's chain of dependent reads.
+// beams, 32 pages copied in 32 planes, 67 MB: 15 us on the GPU, 8 of them the copies;
+// one request of 4 beams 6 us (8 us a call), the bookkeeping's chain of dependent
+// reads.
 
 #include "tq.h"
 #include "tq_common.h"
