@@ -116,16 +116,19 @@ __device__ __forceinline__ float4v mma(u32x4 a, u32x4 b, float4v c) {
 
 // Two floats as two 16-bit numbers (low half first) rounded toward zero, and
 // what that left of them, rounded the same way: hi + lo is within 2^-20 (fp16,
-// normal range) or 2^-14 (bf16) of the value.  The remainder is never zero (at
-// least 2^-24 of weights scaled by 2^14, or 2^-100), so that an infinite value
-// times it stays infinite instead of becoming NaN.
+// normal range) or 2^-14 (bf16) of the value.  The remainder of a weight is never
+// zero (at least 2^-24 of weights scaled by 2^14 in fp16; in bf16 2^-126, the
+// least weight there is, unless the weight is zero), so that an infinite value times
+// it stays infinite instead of becoming NaN.
 template <bool BF>
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
   if constexpr (BF) {
     const uint32_t xb = __builtin_bit_cast(uint32_t, x), yb = __builtin_bit_cast(uint32_t, y);
     hi = __builtin_amdgcn_perm(yb, xb, 0x07060302u);
-    const float xr = fmaxf(x - __builtin_bit_cast(float, xb & 0xffff0000u), 0x1p-100f);
-    const float yr = fmaxf(y - __builtin_bit_cast(float, yb & 0xffff0000u), 0x1p-100f);
+    const float xr = __builtin_amdgcn_fmed3f(
+        x - __builtin_bit_cast(float, xb & 0xffff0000u), 0x1p-126f, x);
+    const float yr = __builtin_amdgcn_fmed3f(
+        y - __builtin_bit_cast(float, yb & 0xffff0000u), 0x1p-126f, y);
     lo = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, yr), __builtin_bit_cast(uint32_t, xr),
                                0x07060302u);
   } else {

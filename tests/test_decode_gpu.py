@@ -420,6 +420,18 @@ def test_attention_extreme_values():
     assert torch.all(torch.isnan(tq.tq_paged_attention(q, n3, v, pt, lens)))
 
 
+@pytest.mark.parametrize("D,size", [(64, 16), (128, 24), (256, 32)])
+def test_attention_weight_of_zero(D, size):
+    """A bf16 token of weight e^-400 leaves no trace, however large its value."""
+    q, k, v, pt, lens = paged(12, "bf16", [70], 3, 1, D, size)
+    q[:] = 1
+    k.zero_()
+    v[pt[0, 0].long(), 3] = 3e38
+    k[pt[0, 0].long(), 3] = -400 / D  # exact in bf16
+    assert torch.all(k[pt[0, 0].long(), 3].float() == -400 / D)
+    run_attention(q, k, v, pt, lens, "bf16", scale=1.0)
+
+
 @pytest.mark.parametrize("dtype,size,D", [("f16", 64, 128), ("bf16", 16, 128), ("f16", 24, 128),
                                           ("f16", 16, 256), ("bf16", 32, 64), ("f16", 16, 80)])
 def test_attention_long(dtype, size, D):
