@@ -714,6 +714,41 @@ def test_pages_compact(rows, width, P, size):
         assert torch.equal(t2, t) and int(u2) == used and torch.equal(pool, want_pool)
 
 
+# Either side of the sizes at which the bookkeeping changes its form (one launch for
+# everything, one workgroup in LDS, three kernels), with pages of one and two pieces.
+@pytest.mark.parametrize("rows,width,P,size,planes,D", [
+    (64, 12, 1000, 4, 2, 8), (65, 12, 1000, 4, 2, 8), (64, 12, 1000, 4, 9, 8),
+    (256, 5, 1500, 3, 1, 8), (257, 5, 1500, 3, 1, 8), (64, 128, 600, 2, 1, 8),
+    (63, 131, 600, 2, 1, 8), (10, 40, 4096, 2, 1, 8), (10, 40, 4097, 2, 1, 8),
+    (10, 40, 8192, 2, 1, 8), (10, 40, 8193, 2, 1, 8), (12, 4, 60, 33, 3, 1000),
+    (70, 4, 350, 33, 2, 1000), (3, 400, 1100, 1, 1, 8)])
+def test_pages_forms(rows, width, P, size, planes, D):
+    rng = np.random.default_rng(rows + P)
+    table, lens = random_state(rng, rows, width, P, size)
+    table_dev, lens_dev = i32(table), i32(lens)
+    pool = make_pool(5, planes, P, size, D=D)
+    want_t, used, moves = pages_compact_ref(table, lens, P, size)
+    want_pool = pool.clone()
+    for s, d in moves:
+        want_pool[:, d] = pool[:, s]
+    t, u = tq.tq_pages_compact(pool, table_dev, lens_dev, size)
+    assert np.array_equal(t.cpu().numpy(), want_t) and int(u) == used
+    assert torch.equal(pool, want_pool)
+    parent = rng.integers(0, max(1, rows // 2), rows)
+    want_t, want_n, refs, short, copies = pages_fork_ref(table, lens, parent, P, size)
+    for s, d in copies:
+        want_pool[:, d] = pool[:, s]
+    t, n, r, sh = tq.tq_pages_fork(pool, table_dev, lens_dev, i32(parent), size)
+    assert np.array_equal(t.cpu().numpy(), want_t) and np.array_equal(n.cpu().numpy(), want_n)
+    assert np.array_equal(r.cpu().numpy(), refs) and int(sh) == short
+    assert torch.equal(pool, want_pool)
+    add = rng.integers(0, 2 * size + 1, rows)
+    want = pages_grow_ref(table, lens, add, P, size)
+    t, n, refused = tq.tq_pages_grow(table_dev, lens_dev, i32(add), P, size)
+    assert np.array_equal(t.cpu().numpy(), want[0])
+    assert np.array_equal(n.cpu().numpy(), want[1]) and int(refused) == want[2]
+
+
 @pytest.mark.parametrize("shape", [(1, 2, 8), (3, 9, 16, 1, 24), (2, 5, 64, 4, 128), (1, 300, 8)])
 def test_pages_copy(shape):
     pool = randn(1, "f16", *shape)
