@@ -44,7 +44,9 @@
 // lengths.  Rows that begin and end in a wave are written by it; what is left of
 // the others, two parts a wave at most, joins in LDS at the end of the workgroup,
 // and a row that spans workgroups leaves its sums in the workspace for the joining
-// kernel (no atomics: the same bits on every run).
+// kernel (no atomics: the same bits on every run).  Where every row is short (by the
+// table's width or the window) and they are not too many, each has a workgroup of
+// its own instead and one launch does.
 //
 // Measured: 96 sequences of 2048 .. 8192 tokens, 64 query / 8 key-value heads of
 // 128, pages of 16, 1.75 GB: 273 us, 6.4 TB/s (92% of what a plain read reaches on
@@ -210,15 +212,22 @@ __device__ __forceinline__ int32_t read_const(const int32_t* p, int64_t i) {
 struct Range {
   int lo, hi, t0, t1;
 };
-__device__ __forceinline__ Range range_of(const AttnParams& p, int b) {
+__device__ __forceinline__ Range range_of_len(const AttnParams& p, int len) {
   const int cap = p.width * (int)p.page.d;
-  const int len = read_const(p.lens, b);
   const int n = len < 0 ? 0 : len;
   const int hi = n < cap ? n : cap;
   const int from = p.window > 0 && n > p.window ? n - p.window : 0;
   const int lo = from < hi ? from : hi;
   const int t0 = lo / kTileTokens;
   return {lo, hi, t0, lo < hi ? (hi + kTileTokens - 1) / kTileTokens : t0};
+}
+__device__ __forceinline__ Range range_of(const AttnParams& p, int b) {
+  return range_of_len(p, read_const(p.lens, b));
+}
+// Tiles of sequence b, 0 where it is left out; the read does not wait for `in`.
+__device__ __forceinline__ uint32_t tiles_of(const AttnParams& p, int b, bool in) {
+  const Range r = range_of(p, b < p.B ? b : p.B - 1);
+  return in && b < p.B ? r.t1 - r.t0 : 0;
 }
 
 // The flattened list of `units` tiles (sequence, then head, then tile) cut into
@@ -238,24 +247,34 @@ struct Cut {
   }
 };
 
+// Sum over this lane and those before it.
+__device__ __forceinline__ uint32_t scan_wave(uint32_t v, int lane) {
+#pragma unroll
+  for (int off = 1; off < kWave; off <<= 1) {
+    const uint32_t o = __shfl_up(v, off, kWave);
+    v += lane >= off ? o : 0;
+  }
+  return v;
+}
+
+// Sequences a lane, up to which a wave walks through them one by one.  Measured
+// (us, walking / 64 at a time): 256 sequences of up to 32 tokens (4 a lane), 8 key
+// heads of 128: 10.0 / 10.4, 4096 of one key head (64 a lane) 35.7 / 28.8.
+constexpr int kFewLengths = 8;
+
 // Every wave by itself: the number of tiles of all sequences, and those before
 // this lane's; lane i looks after the sequences [i * per, (i + 1) * per).
 __device__ __forceinline__ uint32_t scan_tiles(const AttnParams& p, int lane, int per,
                                                uint32_t& mine, uint32_t& total) {
-  mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int b = lane * per + i;
-    if (b < p.B) {
-      const Range r = range_of(p, b);
-      mine += r.t1 - r.t0;
-    }
-  }
-  uint32_t inc = mine;
+  mine = tiles_of(p, lane * per, true);
+  for (int i = 1; i < per; i += 8) {  // eight lengths at a time are under way
+    uint32_t n[8];
 #pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) {
-    const uint32_t o = __shfl_up(inc, off, kWave);
-    inc += lane >= off ? o : 0;
+    for (int u = 0; u < 8; ++u) n[u] = tiles_of(p, lane * per + i + u, i + u < per);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) mine += n[u];
   }
+  const uint32_t inc = scan_wave(mine, lane);
   total = uni((int)__shfl(inc, 63, kWave));
   return inc - mine;
 }
@@ -322,7 +341,8 @@ __global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attenti
   // Keys are loaded as whole rows, like values, and turned in LDS; heads of more
   // than 128 numbers are loaded in operand order instead (64 bytes of 16 rows).
   constexpr bool LDSK = DV <= 128;
-  // partial sums of this workgroup's waves: [wave][first, last][heads][D + 4]
+  // partial sums of this workgroup's waves: [wave][first, last][heads][D + 4], or,
+  // direct, [wave][heads][D + 4]
   extern __shared__ __attribute__((aligned(16))) float sO[];
   // half a tile of keys on its way from load order to operand order, per wave
   __shared__ u32x4 sK[LDSK ? kAttnWaves * 16 * KC : 1];
@@ -362,6 +382,19 @@ __global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attenti
       const int src = __builtin_ctzll(has);
       uint32_t in_row = at - (uint32_t)__builtin_amdgcn_readlane((int)before, src) * H;
       cur.b = src * per;
+      // which of that lane's sequences: one by one, or, of many, 64 at a time
+      for (int i = 0; per > kFewLengths && i < per; i += kWave) {
+        const uint32_t n = tiles_of(p, src * per + i + lane, i + lane < per);
+        const uint32_t inc = scan_wave(n, lane);
+        const uint64_t hit = __ballot(in_row < inc * H);
+        if (hit) {
+          const int k = __builtin_ctzll(hit);
+          cur.b = src * per + i + k;
+          in_row -= (uint32_t)__builtin_amdgcn_readlane((int)(inc - n), k) * H;
+          break;
+        }
+        in_row -= (uint32_t)__builtin_amdgcn_readlane((int)inc, kWave - 1) * H;
+      }
       cur.r = range_of(p, cur.b);
       uint32_t n;
       // (the bounds on b hold whatever happens to the lengths meanwhile)
@@ -651,7 +684,7 @@ __global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attenti
               }
           }
         } else {
-          const int slot = 2 * wave + (first_row ? 0 : 1);
+          const int slot = p.direct ? wave : 2 * wave + (first_row ? 0 : 1);
           if (li < heads) {
             float* o = sO + (slot * slot_heads + li) * row_floats;
 #pragma unroll
@@ -730,7 +763,8 @@ __global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attenti
       for (int k = 0; k < kSlots; ++k) {
         f[k] = __builtin_amdgcn_exp2f(f[k] - base);
         const float lk = sL[k][hd];
-        const float* o = sO + (k * slot_heads + hd) * row_floats + d;
+        const int at = p.direct ? k % kAttnWaves : k;  // direct: a part a wave
+        const float* o = sO + (at * slot_heads + hd) * row_floats + d;
         const float4v x = *reinterpret_cast<const float4v*>(o);
         const float4v y = *reinterpret_cast<const float4v*>(o + 4);
         if (members >> k & 1) {
@@ -761,14 +795,23 @@ __global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attenti
   }
   if (!p.direct && tid == 0) p.owner[blockIdx.x] = make_int2(owned, last);
 
-  // sequences without tokens: zeros and -inf, spread over the workgroups
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    const Range r = range_of(p, b);
-    if (r.hi > r.lo) continue;
-    uint16_t* o = reinterpret_cast<uint16_t*>(p.Out) + (int64_t)b * p.Hq * p.D;
+  // sequences without tokens: zeros and -inf
+  auto clear = [&](int64_t b) {
+    uint16_t* o = reinterpret_cast<uint16_t*>(p.Out) + b * p.Hq * p.D;
     for (int i = tid; i < p.Hq * p.D; i += kAttnThreads) o[i] = 0;
     if (p.lse)
-      for (int i = tid; i < p.Hq; i += kAttnThreads) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
+      for (int i = tid; i < p.Hq; i += kAttnThreads) p.lse[b * p.Hq + i] = -INFINITY;
+  };
+  if (p.direct) {
+    if (cur.h == 0 && cur.r.hi <= cur.r.lo) clear(cur.b);
+    return;
+  }
+  // spread over the workgroups and looked for 64 at a time
+  for (int64_t b0 = blockIdx.x; b0 < p.B; b0 += (int64_t)gridDim.x * kWave) {
+    const int64_t mine = b0 + (int64_t)gridDim.x * lane;
+    const Range r = range_of(p, (int)(mine < p.B ? mine : b0));
+    for (uint64_t none = __ballot(mine < p.B && r.hi <= r.lo); none; none &= none - 1)
+      clear(b0 + (int64_t)gridDim.x * __builtin_ctzll(none));
   }
 }
 
@@ -900,31 +943,54 @@ FastDiv fast_div(int64_t d) {
 constexpr int64_t kLdsBytes = 160 * 1024;
 // What the kernel declares itself: the keys' turning buffer and small arrays.
 int64_t static_lds(int64_t D) { return D > 128 ? 2048 : D > 64 ? 18 * 1024 : 10 * 1024; }
-int64_t lds_bytes(int heads, int64_t D) { return 2 * kAttnWaves * heads * (D + 4) * 4; }
+int64_t lds_bytes(int heads, int64_t D, bool direct) {
+  return (direct ? 1 : 2) * kAttnWaves * heads * (D + 4) * 4;
+}
 
-constexpr int64_t kMostDirect = int64_t(1) << 20;  // workgroups of one launch
 struct Grid {
   int64_t blocks, partials;  // workgroups; partial sums they may leave
   bool direct;
 };
 
-// Tiles a wave of a table's longest row, up to which every (sequence, head) has a
-// workgroup of its own and nothing is left to join.  Measured (us on the GPU, own
-// workgroup / split and joined), 8 sequences, 8 key heads of 128: 2 tiles 9.1 /
-// 12.9, 4 tiles 12.9 / 13.3, 8 tiles 21 / 16; 16 sequences, 4 key heads of 256: 4
-// tiles 22 / 17.
+// Tiles a wave of the longest row, up to which a (sequence, head) has a workgroup of
+// its own and nothing is left to join.  Measured (us on the GPU, own workgroup /
+// split and joined), 8 sequences, 8 key heads of 128: 2 tiles 9.1 / 12.9, 4 tiles 12.9
+// / 13.3, 8 tiles 21 / 16; 16 sequences, 4 key heads of 256: 4 tiles 22 / 17.
 constexpr int direct_tiles(int64_t D) { return D > 128 ? 2 : 4; }
+
+// Workgroups of their own per CU, up to which that holds: more of them come in
+// rounds, each of which waits for memory from its start, where the split kernel
+// fetches a row's first tile during the row before.  Measured (us, own / split; up to
+// 32, 128, 256 tokens): 8 key heads of 64, 4 query heads each, 256 sequences (8 a CU) 8 /
+// 9, 14 / 22, 22 / 28, 512 (16) 14 / 13, 26 / 31, 38 / 42, 1024 (32) 26 / 20, 44 / 46, 70 /
+// 70; of 128, 128 sequences (4) 8 / 8, 14 / 19, 23 / 26, 256 (8) 15 / 10, 27 / 27, 41 / 40;
+// of 256, 64 sequences (2) 10 / 10, 20 / 23, 28 / 28, 128 (4) 20 / 12, 35 / 30, 53 / 43.
+// With one row a sequence the split kernel has a length and a page to find for each:
+// 4096 sequences, one key head of 64 14 / 25, 24 / 42, 35 / 54, of 128 29 / 27, 49 / 54,
+// 71 / 79; of 256 83 / 37, 139 / 89, 206 / 147.
+bool direct_rows(int64_t B, int64_t H, int heads, int64_t D) {
+  if (H == 1 && D <= 128) return true;
+  const int64_t by_lds = kLdsBytes / (lds_bytes(heads, D, true) + static_lds(D));
+  const int64_t by_regs = D > 128 ? 1 : D > 64 ? 2 : 4;  // at once
+  const int64_t rounds = D > 64 ? 2 : 4;
+  return B * H <= device_cus() * rounds * (by_lds < by_regs ? by_lds : by_regs);
+}
 
 // Workgroups of the first kernel: as many as the GPU holds at once, or one for
 // each (sequence, head).
-Grid attn_grid(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity) {
+Grid attn_grid(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity, int64_t window) {
   const int64_t G = Hq / Hkv, H = Hkv * ((G + kHeads - 1) / kHeads);
   const int heads = (int)(G < kHeads ? G : kHeads);
-  if (capacity <= direct_tiles(D) * kAttnWaves * kTileTokens && B * H <= kMostDirect)
+  // tiles of a row; a window may begin inside one
+  int64_t tiles = (capacity + kTileTokens - 1) / kTileTokens;
+  if (window > 0 && window < capacity) {
+    const int64_t seen = (window + kTileTokens - 2) / kTileTokens + 1;
+    if (seen < tiles) tiles = seen;
+  }
+  if (tiles <= direct_tiles(D) * kAttnWaves && direct_rows(B, H, heads, D))
     return {B * H, 0, true};
-  const int64_t tiles = capacity / kTileTokens + 2;  // a window may begin inside a tile
   const int64_t most = (B * H * tiles + kAttnWaves - 1) / kAttnWaves;
-  const int64_t by_lds = kLdsBytes / (lds_bytes(heads, D) + static_lds(D));
+  const int64_t by_lds = kLdsBytes / (lds_bytes(heads, D, false) + static_lds(D));
   const int64_t by_regs = blocks_per_cu(D);
   int64_t grid = device_cus() * (by_lds < by_regs ? by_lds : by_regs);
   if (grid > kMostBlocks) grid = kMostBlocks;
@@ -935,11 +1001,11 @@ Grid attn_grid(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity) 
 template <bool BF, int DV, bool UNI, bool NT>
 hipError_t launch_kernel(const AttnParams& p, int64_t grid, hipStream_t s) {
   const auto fn = paged_attention_kernel<BF, DV, UNI, NT>;
-  const int lds = (int)lds_bytes(p.G < kHeads ? p.G : kHeads, p.D);
+  const int lds = (int)lds_bytes(p.G < kHeads ? p.G : kHeads, p.D, p.direct);
   if (lds + static_lds(p.D) > 64 * 1024) {  // above what every kernel may use
     static std::atomic<uint64_t> done{0};
     const hipError_t e = lds_limit_once(reinterpret_cast<const void*>(fn),
-                                        (int)lds_bytes(kHeads, DV), done);
+                                        (int)lds_bytes(kHeads, DV, false), done);
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL(fn, dim3((uint32_t)grid), dim3(kAttnThreads), lds, s, p);
@@ -976,7 +1042,7 @@ hipError_t launch_t(const AttnParams& p, int64_t grid, hipStream_t s) {
 }  // namespace
 
 int64_t attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity) {
-  const Grid g = attn_grid(B, Hq, Hkv, D, capacity);
+  const Grid g = attn_grid(B, Hq, Hkv, D, capacity, 0);  // a window takes no more
   const int64_t G = Hq / Hkv;
   if (g.direct) return 0;
   return g.partials * slot_floats((int)(G < kHeads ? G : kHeads), (int)D) * (int64_t)sizeof(float) +
@@ -1009,7 +1075,7 @@ hipError_t launch_paged_attention(int dtype, const AttnArgs& a, hipStream_t stre
   p.qtiles = (p.G + kHeads - 1) / kHeads;
   p.window = (int32_t)a.window;
   p.scale = a.scale_log2;
-  const Grid g = attn_grid(a.B, a.Hq, a.Hkv, a.D, a.width * a.page_size);
+  const Grid g = attn_grid(a.B, a.Hq, a.Hkv, a.D, a.width * a.page_size, a.window);
   p.direct = g.direct;
   p.full = a.D == 128 && a.page_size % 16 == 0 && g.blocks >= 2 * device_cus();
   p.owner = reinterpret_cast<int2*>(

@@ -420,6 +420,26 @@ def test_attention_extreme_values():
     assert torch.all(torch.isnan(tq.tq_paged_attention(q, n3, v, pt, lens)))
 
 
+# Rows kept to a workgroup each, and rows split over all of them: either side of the
+# number of rows, of the table's length and of the window's at which that changes;
+# one, a few and many lengths a lane.
+@pytest.mark.parametrize("B,Hq,Hkv,D,longest,window", [
+    (150, 8, 8, 128, 60, 0), (128, 64, 8, 128, 40, 0), (129, 64, 8, 128, 40, 0),
+    (33, 32, 2, 256, 40, 0), (300, 8, 8, 64, 50, 0), (700, 8, 8, 64, 40, 0),
+    (1500, 2, 1, 64, 30, 0), (1200, 1, 1, 256, 30, 0), (2, 48, 3, 128, 512, 0),
+    (2, 48, 3, 128, 513, 0), (6, 8, 2, 128, 1500, 482), (6, 8, 2, 128, 1500, 483),
+    (6, 8, 2, 256, 1500, 226), (6, 8, 2, 256, 1500, 227), (70, 16, 1, 64, 400, 33),
+    (5, 5, 5, 80, 900, 1)])
+def test_attention_many_rows(B, Hq, Hkv, D, longest, window):
+    rng = np.random.default_rng(B + D)
+    lens = rng.integers(0, longest + 1, B)
+    lens[rng.integers(0, B, B // 5)] = 0
+    lens[-1] = longest
+    q, k, v, pt, lens = paged(13, "bf16" if D == 64 else "f16", lens, Hq, Hkv, D, 16)
+    run_attention(q, k, v, pt[:, :-(-longest // 16)].contiguous(), lens,
+                  "bf16" if D == 64 else "f16", window=window)
+
+
 @pytest.mark.parametrize("D,size", [(64, 16), (128, 24), (256, 32)])
 def test_attention_weight_of_zero(D, size):
     """A bf16 token of weight e^-400 leaves no trace, however large its value."""
