@@ -319,7 +319,7 @@ __host__ __device__ constexpr int blocks_per_cu(int64_t D) { return D > 128 ? 1 
 // tile, pages of whole half tiles), which keeps 64 KB of a CU in flight as it is.
 // Measured (us, half / all): one sequence of 131072 tokens, 8 key heads of 128: 90 /
 // 100, 96 sequences of 2048 .. 8192: 274 / 280; with fewer tiles a wave the other way
-// round: 32 sequences of up to 1024 tokens (2.5 a wave) 26.2 / 24.4, 128 of them (10)
+// round: 32 sequences of up to 1024 tokens, if split (2.5 a wave) 26.2 / 24.4, 128 (10)
 // 65.3 / 63.8; heads of 80 161 / 126, pages of 24 108 / 98.
 constexpr uint32_t kManyTiles = 12;
 __device__ __forceinline__ uint32_t waves_for(const AttnParams& p, uint32_t units, uint32_t waves) {
@@ -963,10 +963,16 @@ struct Grid {
 };
 
 // Tiles a wave of the longest row, up to which a (sequence, head) has a workgroup of
-// its own and nothing is left to join.  Measured (us on the GPU, own workgroup /
-// split and joined), 8 sequences, 8 key heads of 128: 2 tiles 9.1 / 12.9, 4 tiles 12.9
-// / 13.3, 8 tiles 21 / 16; 16 sequences, 4 key heads of 256: 4 tiles 22 / 17.
-constexpr int direct_tiles(int64_t D) { return D > 128 ? 2 : 4; }
+// its own and nothing is left to join; more of them where the rows alone occupy half
+// the CUs.  Measured (us on the GPU, own workgroup / split and joined; rows of up to
+// 512, 768, 1024, 2048 tokens), 8 key heads of 128: 4 sequences 9.6 / 11.5, 12.1 /
+// 11.4, 14.8 / 11.8, 26 / 14; 16 sequences 9.8 / 13.4, 13.3 / 15.7, 16.5 / 17.0, 29 /
+// 25; 64 sequences 19 / 25, 26 / 30, 32 / 37, 63 / 63; of 64, 16 sequences 8.1 / 13.1,
+// 9.8 / 13.7, 11.7 / 14.1, 20 / 18; of 256, up to 256 tokens 4 sequences 10.9 / 14.3, 64
+// 26 / 28, up to 512 15.7 / 14.8, 42 / 40.
+int64_t direct_tiles(int64_t rows, int64_t D) {
+  return D > 128 ? 2 : 2 * rows >= device_cus() ? 8 : 4;
+}
 
 // Workgroups of their own per CU, up to which that holds: more of them come in
 // rounds, each of which waits for memory from its start, where the split kernel
@@ -997,7 +1003,7 @@ Grid attn_grid(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity, 
     const int64_t seen = (window + kTileTokens - 2) / kTileTokens + 1;
     if (seen < tiles) tiles = seen;
   }
-  if (tiles <= direct_tiles(D) * kAttnWaves && direct_rows(B, H, heads, D))
+  if (tiles <= direct_tiles(B * H, D) * kAttnWaves && direct_rows(B, H, heads, D))
     return {B * H, 0, true};
   const int64_t most = (B * H * tiles + kAttnWaves - 1) / kAttnWaves;
   const int64_t by_lds = kLdsBytes / (lds_bytes(heads, D, false) + static_lds(D));

@@ -429,6 +429,8 @@ def test_attention_extreme_values():
     (1500, 2, 1, 64, 30, 0), (1200, 1, 1, 256, 30, 0), (2, 48, 3, 128, 512, 0),
     (2, 48, 3, 128, 513, 0), (6, 8, 2, 128, 1500, 482), (6, 8, 2, 128, 1500, 483),
     (6, 8, 2, 256, 1500, 226), (6, 8, 2, 256, 1500, 227), (70, 16, 1, 64, 400, 33),
+    (64, 2, 2, 128, 1024, 0), (64, 2, 2, 128, 1025, 0), (128, 3, 1, 80, 1024, 900),
+    (63, 2, 2, 64, 1000, 0),
     (5, 5, 5, 80, 900, 1)])
 def test_attention_many_rows(B, Hq, Hkv, D, longest, window):
     rng = np.random.default_rng(B + D)
