@@ -60,6 +60,7 @@
 #include <type_traits>
 
 #include "tq.h"
+#include "tq_attn_slots.h"
 #include "tq_common.h"
 #include "tq_decode.h"
 #include "tq_kernels.h"
@@ -70,7 +71,6 @@ namespace {
 
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 
-constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = kAttnWaves * kWave;
 constexpr int kTileTokens = 32;
 constexpr int kHeads = 16;                // query heads per workgroup
@@ -353,8 +353,8 @@ __global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attenti
   extern __shared__ __attribute__((aligned(16))) float sO[];
   // half a tile of keys on its way from load order to operand order, per wave
   __shared__ u32x4 sK[LDSK ? kAttnWaves * 16 * KC : 1];
-  __shared__ float sM[2 * kAttnWaves][kHeads], sL[2 * kAttnWaves][kHeads];
-  __shared__ int sRow[2 * kAttnWaves], sEnds[2 * kAttnWaves], sLast[2 * kAttnWaves];
+  __shared__ float sM[kAttnSlots][kHeads], sL[kAttnSlots][kHeads];
+  __shared__ int sRow[kAttnSlots], sEnds[kAttnSlots], sLast[kAttnSlots];
 
   const int tid = threadIdx.x;
   const int wave = uni(tid >> 6);
@@ -414,7 +414,11 @@ __global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attenti
       cur.tile = cur.r.t0 + in_row % n;
     }
   }
-  if (lane < 2) sRow[2 * wave + lane] = -1;
+  // its own slots are empty (written by the lane that fills them later: there is no
+  // barrier in between)
+  if (lane == 0)
+#pragma unroll
+    for (int part = 0; part < kAttnParts; ++part) sRow[attn_slot(wave, part)] = -1;
 
   auto advance = [&](Cursor& c) {  // only where another tile follows
     if (++c.tile < c.r.t1 || DIRECT) return;
@@ -693,9 +697,9 @@ __global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attenti
               }
           }
         } else {
-          const int slot = DIRECT ? wave : 2 * wave + (first_row ? 0 : 1);
+          const int slot = attn_slot(wave, DIRECT || first_row ? 0 : 1);
           if (li < heads) {
-            float* o = sO + (slot * slot_heads + li) * row_floats;
+            float* o = sO + (attn_sums_at(DIRECT, slot) * slot_heads + li) * row_floats;
 #pragma unroll
             for (int c = 0; c < NV; ++c)
 #pragma unroll
@@ -741,9 +745,9 @@ __global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attenti
   // that began before, the second for one that goes on).
   __syncthreads();
   int owned = -1, last = 0;
-  constexpr int kSlots = 2 * kAttnWaves;
-  const int row_of = lane < kSlots ? sRow[lane] : -1;
-  const int ends_of = sEnds[lane % kSlots], last_of = sLast[lane % kSlots];
+  constexpr int kStep = DIRECT ? kAttnParts : 1;  // direct: no second parts
+  const int row_of = lane < kAttnSlots ? sRow[lane] : -1;
+  const int ends_of = sEnds[lane % kAttnSlots], last_of = sLast[lane % kAttnSlots];
   uint32_t todo = (uint32_t)__ballot(row_of >= 0);
   while (todo) {
     const int i = __builtin_ctz(todo);
@@ -761,20 +765,19 @@ __global__ __launch_bounds__(kAttnThreads, blocks_per_cu(DV)) void paged_attenti
     for (int j = tid; j < nh * units; j += kAttnThreads) {
       const int hd = j / units, d = (j - hd * units) * 8;
       // every slot is read, so that the reads overlap; only members count
-      float f[kSlots], mm = -INFINITY, sum = 0.f;
+      float f[kAttnSlots], mm = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int k = 0; k < kSlots; ++k) {
+      for (int k = 0; k < kAttnSlots; k += kStep) {
         f[k] = members >> k & 1 ? sM[k][hd] : -INFINITY;
         mm = fmaxf(mm, f[k]);
       }
       const float base = mm == -INFINITY ? 0.f : mm;
       float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-      for (int k = 0; k < kSlots; ++k) {
+      for (int k = 0; k < kAttnSlots; k += kStep) {
         f[k] = __builtin_amdgcn_exp2f(f[k] - base);
         const float lk = sL[k][hd];
-        const int at = DIRECT ? k % kAttnWaves : k;  // direct: a part a wave
-        const float* o = sO + (at * slot_heads + hd) * row_floats + d;
+        const float* o = sO + (attn_sums_at(DIRECT, k) * slot_heads + hd) * row_floats + d;
         const float4v x = *reinterpret_cast<const float4v*>(o);
         const float4v y = *reinterpret_cast<const float4v*>(o + 4);
         if (members >> k & 1) {
@@ -954,7 +957,7 @@ constexpr int64_t kLdsBytes = 160 * 1024;
 // What the kernel declares itself: the keys' turning buffer and small arrays.
 int64_t static_lds(int64_t D) { return D > 128 ? 2048 : D > 64 ? 18 * 1024 : 10 * 1024; }
 int64_t lds_bytes(int heads, int64_t D, bool direct) {
-  return (direct ? 1 : 2) * kAttnWaves * heads * (D + 4) * 4;
+  return (attn_sums_at(direct, kAttnSlots - 1) + 1) * heads * (D + 4) * 4;
 }
 
 struct Grid {
