@@ -27,9 +27,11 @@
 //    its 8 tokens and turns them into A operands (8 tokens of one number) with 4
 //    v_perm_b32 each.  O^T keeps lane = head, so rescaling and the final division
 //    need no exchange.
-//  * P is split into two 16-bit numbers (high part and remainder), so rounding
-//    it to the cache's type costs no accuracy; fp16 exponents are shifted by 14
-//    so that weights down to 2^-28 of the largest keep all their bits.
+//  * P enters the product as two 16-bit numbers, cut and remainder, the latter
+//    rounded to nearest (to within 2^-22 of a weight in fp16, 2^-16 in bf16: one
+//    number, 2^-12 and 2^-9, would add as much error as the output's own rounding; a
+//    third would cost another product); fp16 exponents are shifted by 14 so that
+//    weights down to 2^-28 of the largest keep all their bits.
 //  * The next tile's K is loaded after this tile's scores, its V after this tile's
 //    sums, also across the end of a row: the registers of one tile and the loads of
 //    the next are the same, and a CU keeps some 100 KB in flight.
@@ -70,6 +72,10 @@ namespace tq {
 namespace {
 
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef float float2v __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kAttnThreads = kAttnWaves * kWave;
 constexpr int kTileTokens = 32;
@@ -117,12 +123,13 @@ __device__ __forceinline__ float4v mma(u32x4 a, u32x4 b, float4v c) {
                                                   __builtin_bit_cast(half8, b), c, 0, 0, 0);
 }
 
-// Two floats as two 16-bit numbers (low half first) rounded toward zero, and
-// what that left of them, rounded the same way: hi + lo is within 2^-20 (fp16,
-// normal range) or 2^-14 (bf16) of the value.  The remainder of a weight is never
-// zero (at least 2^-24 of weights scaled by 2^14 in fp16; in bf16 2^-126, the
-// least weight there is, unless the weight is zero), so that an infinite value times
-// it stays infinite instead of becoming NaN.
+// Two floats x >= 0 as two 16-bit numbers each (low half first): x cut, and what
+// that left of it, rounded to nearest, so that the errors of many weights do not add
+// up to one side: hi + lo is within 2^-22 (fp16, normal range) or 2^-16 (bf16) of x.
+// The first is cut, not rounded, for the second to have no sign, and the second of a
+// weight is never zero (at least 2^-24 of weights scaled by 2^14 in fp16; in bf16
+// 2^-126, the least weight there is, unless the weight is zero): an infinite value
+// times them stays infinite instead of becoming NaN.
 template <bool BF>
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
   if constexpr (BF) {
@@ -132,14 +139,13 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
         x - __builtin_bit_cast(float, xb & 0xffff0000u), 0x1p-126f, x);
     const float yr = __builtin_amdgcn_fmed3f(
         y - __builtin_bit_cast(float, yb & 0xffff0000u), 0x1p-126f, y);
-    lo = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, yr), __builtin_bit_cast(uint32_t, xr),
-                               0x07060302u);
+    lo = __builtin_bit_cast(uint32_t, __builtin_convertvector((float2v{xr, yr}), bf2));
   } else {
     const auto h = __builtin_amdgcn_cvt_pkrtz(x, y);
     hi = __builtin_bit_cast(uint32_t, h);
-    lo = __builtin_bit_cast(uint32_t,
-                            __builtin_amdgcn_cvt_pkrtz(x - (float)h[0], y - (float)h[1])) |
-         0x00010001u;
+    const float2v rest = {x - (float)h[0], y - (float)h[1]};
+    const u16x2 r = __builtin_bit_cast(u16x2, __builtin_convertvector(rest, half2v));
+    lo = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(r, u16x2{1, 1}));
   }
 }
 

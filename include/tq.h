@@ -440,8 +440,9 @@ int tq_rope_append(int dtype, const void* QKV, int64_t qkv_tok, const float* tab
  * [0, n_pages) counts as absent: its tokens are left out.  What the cache holds
  * in other slots, NaN included, has no influence.
  * fp16 or bfloat16 in and out, fp32 scores, weights and sums; each weight enters
- * the product with v to within 2^-20 (fp16; 2^-14 bfloat16) of itself, in fp16 or
- * within 2^-38 of the row's largest.  The same bits on every run.  Outputs and workspace must not overlap the inputs.
+ * the product with v as two 16-bit numbers, rounded to within 2^-22 (fp16; 2^-16
+ * bfloat16) of itself, in fp16 or within 2^-38 of the row's largest.  The same bits
+ * on every run.  Outputs and workspace must not overlap the inputs.
  * D a multiple of 8, 8 <= D <= 256; Hq a multiple of Hkv, Hq <= 2^12; B <=
  * 2^20; width * page_size <= 2^30; B * Hkv * ceil(Hq / Hkv / 16) * (width *
  * page_size / 32 + 2) < 2^31; strides multiples of 8, row_stride <= 2^24;

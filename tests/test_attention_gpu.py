@@ -31,3 +31,51 @@ def test_attention_own_workgroups_repeat(dtype, B, Hq, Hkv, D, longest):
         out, lse = tq.tq_paged_attention(q, k, v, pt, lens, return_lse=True, **stream)
         side.synchronize()
         assert torch.equal(out, want) and torch.equal(lse, lw), i
+
+
+def exact_rows(dtype, tokens, seed=0):
+    """64 sequences of `tokens` slots with a page each, one head of 8 numbers: q is
+    (y, 0, ..), y in dtype, all keys 0 but the last one, -(1, 0, ..): scores 0 and -y."""
+    rng = np.random.default_rng(seed)
+    B, t = 64, {"f16": torch.float16, "bf16": torch.bfloat16}[dtype]
+    size = -(-tokens // 16) * 16
+    y = torch.from_numpy(rng.uniform(0.1, 3.0, B)).to(t)
+    q = torch.zeros(B, 1, 8, dtype=t)
+    q[:, 0, 0] = y
+    k, v = torch.zeros(B, size, 1, 8, dtype=t), torch.zeros(B, size, 1, 8, dtype=t)
+    k[:, tokens - 1, 0, 0] = -1
+    pt = torch.arange(B, dtype=torch.int32)[:, None]
+    lens = torch.full((B,), tokens, dtype=torch.int32)
+    return y.double().numpy(), q, k, v, pt, lens
+
+
+def truncated(x, bits):
+    """x > 0 cut to so many significant bits."""
+    e = np.frexp(x)[1] - bits
+    return np.ldexp(np.floor(np.ldexp(x, -e)), e)
+
+
+@pytest.mark.parametrize("dtype,bits,weight_bits", [("f16", 11, 22), ("bf16", 8, 16)])
+def test_attention_weights_are_rounded_to_nearest(dtype, bits, weight_bits):
+    """A weight w = e^-y of two 16-bit numbers is off by 2^-weight_bits of itself at
+    most.  Two tokens of weight 1 carry the two leading pieces of w, cut, with the
+    opposite sign, so that what is left is of the size of the error.  Besides: the
+    score's product and scaling (2^-24 y each) and the fp32 exponential and sums, at
+    most (3 + 16) 2^-23 of sum w |v| as in test_decode_gpu.py."""
+    y, q, k, v, pt, lens = exact_rows(dtype, 3)
+    w = np.exp(-y)
+    first = truncated(w, bits)
+    second = truncated(w - first, bits)
+    at = torch.tensor([5])
+    for t, x in enumerate((-first, -second, np.ones_like(w))):
+        v[:, t, 0, at] = torch.from_numpy(256 * x)[:, None].to(v.dtype)
+        assert np.array_equal(v[:, t, 0, 5].double().numpy(), 256 * x)  # exact in the type
+    out = tq.tq_paged_attention(*(x.cuda() for x in (q, k, v, pt, lens)), scale=1.0)
+    got = out[:, 0, 5].double().cpu().numpy()
+    total = 2 + w
+    want = 256 * (w - first - second) / total
+    before = 256 / total * w * (2.0 ** -weight_bits + 2 * 2.0 ** -24 * y) \
+        + 256 * 2 * w / total * (3 + 16) * 2.0 ** -23
+    ulp = np.ldexp(1.0, np.frexp(np.abs(want) + before)[1] - 1 - bits)
+    err = np.abs(got - want)
+    assert np.all(err <= before + np.maximum(ulp, 2.0 ** -25)), float((err / before).max())
