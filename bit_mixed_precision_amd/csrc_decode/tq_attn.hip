@@ -75,7 +75,6 @@ typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef float float2v __attribute__((ext_vector_type(2)));
-typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kAttnThreads = kAttnWaves * kWave;
 constexpr int kTileTokens = 32;
@@ -126,27 +125,31 @@ __device__ __forceinline__ float4v mma(u32x4 a, u32x4 b, float4v c) {
 // Two floats x >= 0 as two 16-bit numbers each (low half first): x cut, and what
 // that left of it, rounded to nearest, so that the errors of many weights do not add
 // up to one side: hi + lo is within 2^-22 (fp16, normal range) or 2^-16 (bf16) of x.
-// The first is cut, not rounded, for the second to have no sign, and the second of a
-// weight is never zero (at least 2^-24 of weights scaled by 2^14 in fp16; in bf16
-// 2^-126, the least weight there is, unless the weight is zero): an infinite value
-// times them stays infinite instead of becoming NaN.
+// The first is cut, not rounded, for the second to have no sign, and the second is
+// no less than `least` wherever x is not: an infinite value times them then stays
+// infinite instead of becoming NaN.  Below that x has one number only, or none: a
+// token without weight adds nothing, however large its value.  `least`: 2^-126 in
+// bf16 (the least weight there is); in fp16 the type's own 2^-24, of weights scaled by
+// 2^14.
 template <bool BF>
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  constexpr float least = BF ? 0x1p-126f : 0x1p-24f;
+  float xh, yh;
   if constexpr (BF) {
     const uint32_t xb = __builtin_bit_cast(uint32_t, x), yb = __builtin_bit_cast(uint32_t, y);
     hi = __builtin_amdgcn_perm(yb, xb, 0x07060302u);
-    const float xr = __builtin_amdgcn_fmed3f(
-        x - __builtin_bit_cast(float, xb & 0xffff0000u), 0x1p-126f, x);
-    const float yr = __builtin_amdgcn_fmed3f(
-        y - __builtin_bit_cast(float, yb & 0xffff0000u), 0x1p-126f, y);
-    lo = __builtin_bit_cast(uint32_t, __builtin_convertvector((float2v{xr, yr}), bf2));
+    xh = __builtin_bit_cast(float, xb & 0xffff0000u);
+    yh = __builtin_bit_cast(float, yb & 0xffff0000u);
   } else {
     const auto h = __builtin_amdgcn_cvt_pkrtz(x, y);
     hi = __builtin_bit_cast(uint32_t, h);
-    const float2v rest = {x - (float)h[0], y - (float)h[1]};
-    const u16x2 r = __builtin_bit_cast(u16x2, __builtin_convertvector(rest, half2v));
-    lo = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(r, u16x2{1, 1}));
+    xh = (float)h[0];
+    yh = (float)h[1];
   }
+  const float2v rest = {__builtin_amdgcn_fmed3f(x - xh, least, x),
+                        __builtin_amdgcn_fmed3f(y - yh, least, y)};
+  using half2 = std::conditional_t<BF, bf2, half2v>;
+  lo = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, half2));
 }
 
 template <bool BF>

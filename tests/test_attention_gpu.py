@@ -79,3 +79,32 @@ def test_attention_weights_are_rounded_to_nearest(dtype, bits, weight_bits):
     ulp = np.ldexp(1.0, np.frexp(np.abs(want) + before)[1] - 1 - bits)
     err = np.abs(got - want)
     assert np.all(err <= before + np.maximum(ulp, 2.0 ** -25)), float((err / before).max())
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D,size,n", [(64, 16, 1000), (128, 24, 300), (256, 32, 1500)])
+def test_attention_many_tokens_without_weight(dtype, D, size, n):
+    """One token of a small value has all the weight; the others, of weight e^-400 (0
+    in fp32) and large values of one sign, leave no trace, however many they are."""
+    q, k, v, pt, lens = paged(D, dtype, [n, 1, 40], 3, 1, D, size)
+    q[:] = 1
+    used = ~torch.isnan(k)
+    k[used], v[used] = -400 / D, 6e4  # the key is exact in both types
+    assert float(k[used][0]) == -400 / D
+    first = pt[:, 0].long()
+    k[first, 0], v[first, 0] = 0, 1e-3
+    run_attention(q, k, v, pt, lens, dtype, scale=1.0)
+
+
+def test_attention_infinite_values_of_small_weights():
+    """An infinite value stays infinite down to weights of 2^-38 (fp16) or 2^-126
+    (bf16) of the largest, also where nothing remains of the weight for its second number."""
+    for dtype, exps in (("f16", (0, 1, 12, 24, 37, 38)), ("bf16", (0, 1, 24, 37, 100, 125))):
+        for e in exps:
+            q, k, v, pt, lens = paged(e, dtype, [20], 1, 1, 64, 16, poison=False)
+            q.zero_(), k.zero_()
+            q[..., 0], k[pt[0, 0].long(), 3, 0, 0] = 1, -e
+            v[pt[0, 0].long(), 3, 0, 7] = float("inf")
+            out = tq.tq_paged_attention(q, k, v, pt, lens, scale=float(np.log(2.0)))[0, 0]
+            assert out[7] == float("inf"), (dtype, e)
+            assert torch.isfinite(out[torch.arange(64) != 7]).all()
