@@ -12,7 +12,10 @@ namespace {
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
 constexpr int64_t kMaxHeadDim = int64_t(1) << 16;
 constexpr int64_t kMaxHeads = int64_t(1) << 16;
-constexpr int64_t kMaxStride = int64_t(1) << 46;  // elements: byte offsets stay far below 2^63
+constexpr int64_t kMaxStride = int64_t(1) << 46;  // elements
+// Elements that the steps of one dimension may span: the byte offsets of three
+// dimensions of four-byte numbers add up to less than 2^62.
+constexpr int64_t kMaxReach = int64_t(1) << 58;
 constexpr int64_t kMaxAttnBatch = int64_t(1) << 20;
 constexpr int64_t kMaxAttnHeads = int64_t(1) << 12;
 constexpr int64_t kMaxRowStride = int64_t(1) << 24;  // 16 rows within 32-bit buffer offsets
@@ -22,7 +25,8 @@ constexpr int64_t kMaxPlanes = int64_t(1) << 16;
 constexpr int64_t kMaxPageBytes = int64_t(1) << 30;
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-bool stride_ok(int64_t s) { return s >= 0 && s <= kMaxStride; }
+// Stride s of a dimension of n >= 1 entries.
+bool stride_ok(int64_t n, int64_t s) { return s >= 0 && s <= kMaxStride && s <= kMaxReach / n; }
 
 int device_ready() {
   int dev = -1;
@@ -41,7 +45,8 @@ int finish(hipError_t e) {
   return TQ_OK;
 }
 
-// No two of n1 x n2 runs of `len` elements at strides s1, s2 share an element.
+// No two of n1 x n2 runs of `len` elements at strides s1, s2 (stride_ok) share an
+// element.
 bool distinct(int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t len) {
   if (n1 == 1) s1 = kMaxStride;  // a stride that is never taken
   if (n2 == 1) s2 = kMaxStride;
@@ -118,8 +123,8 @@ int tq_rope(int dtype, const void* X, int64_t x_tok, int64_t x_head, void* Y, in
   if (!X || !Y || (!table && n_pos != 0) || !pos) return TQ_ERR_NULL;
   int st = rope_shapes(n_pos, rot, T, H, D);
   if (st != TQ_OK) return st;
-  if (!stride_ok(x_tok) || !stride_ok(x_head) || !stride_ok(y_tok) || !stride_ok(y_head) ||
-      !distinct(T, y_tok, H, y_head, D))
+  if (!stride_ok(T, x_tok) || !stride_ok(H, x_head) || !stride_ok(T, y_tok) ||
+      !stride_ok(H, y_head) || !distinct(T, y_tok, H, y_head, D))
     return TQ_ERR_SHAPE;
   if (X == Y && ((T > 1 && x_tok != y_tok) || (H > 1 && x_head != y_head))) return TQ_ERR_SHAPE;
   const uintptr_t size = dtype == TQ_F32 ? 4 : 2;
@@ -160,11 +165,11 @@ int tq_rope_append(int dtype, const void* QKV, int64_t qkv_tok, const float* tab
   if (Hq < 1 || Hkv < 1 || Hq > kMaxHeads || Hkv > kMaxHeads) return TQ_ERR_SHAPE;
   int st = rope_shapes(n_pos, rot, T, Hq + 2 * Hkv, D);
   if (st != TQ_OK) return st;
-  if (!stride_ok(qkv_tok) || !stride_ok(page_stride) || !stride_ok(row_stride) ||
-      !stride_ok(head_stride) || n_pages < 1 || n_pages > INT32_MAX || n_seqs < 1 ||
-      n_seqs > INT32_MAX || width < 1 || page_size < 1 || width > kMaxTokens ||
-      page_size > kMaxTokens || width * page_size > kMaxTokens ||
-      page_stride > INT64_MAX / 4 / n_pages || row_stride > INT64_MAX / 4 / page_size ||
+  if (n_pages < 1 || n_pages > INT32_MAX || n_seqs < 1 || n_seqs > INT32_MAX || width < 1 ||
+      page_size < 1 || width > kMaxTokens || page_size > kMaxTokens ||
+      width * page_size > kMaxTokens || !stride_ok(T, qkv_tok) ||
+      !stride_ok(n_pages, page_stride) || !stride_ok(page_size, row_stride) ||
+      !stride_ok(Hkv, head_stride) ||
       !distinct_cache(n_pages, page_stride, page_size, row_stride, Hkv, head_stride, D))
     return TQ_ERR_SHAPE;
   if (!aligned(QKV, 2) || !aligned(Q, 2) || !aligned(k_pages, 2) || !aligned(v_pages, 2) ||
@@ -222,10 +227,10 @@ int tq_paged_attention(int dtype, const void* Q, int64_t q_tok, int64_t q_head,
   if (!Q || !k_pages || !v_pages || !page_table || !lens || !Out) return TQ_ERR_NULL;
   int st = attn_shapes(B, Hq, Hkv, D, page_size, width);
   if (st != TQ_OK) return st;
-  if (!stride_ok(q_tok) || !stride_ok(q_head) || !stride_ok(page_stride) ||
-      !stride_ok(row_stride) || !stride_ok(head_stride) || row_stride > kMaxRowStride ||
-      q_tok % 8 || q_head % 8 || page_stride % 8 || row_stride % 8 || head_stride % 8 ||
-      n_pages < 1 || n_pages > INT32_MAX || page_stride > INT64_MAX / 4 / n_pages)
+  if (n_pages < 1 || n_pages > INT32_MAX || !stride_ok(B, q_tok) || !stride_ok(Hq, q_head) ||
+      !stride_ok(n_pages, page_stride) || !stride_ok(page_size, row_stride) ||
+      !stride_ok(Hkv, head_stride) || row_stride > kMaxRowStride || q_tok % 8 || q_head % 8 ||
+      page_stride % 8 || row_stride % 8 || head_stride % 8)
     return TQ_ERR_SHAPE;
   const int64_t wants = tq::attn_workspace_bytes(B, Hq, Hkv, D, width * page_size);
   if (workspace_bytes < wants) return TQ_ERR_SHAPE;

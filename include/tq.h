@@ -351,7 +351,8 @@ int tq_gemm_tq1_tile(const void* X, const void* qs, int64_t ldq, const void* sca
  * and LLaMA-style attention; the operators are the standard ones, stated below.
  *
  * Types: fp16, bfloat16 and, for tq_rope, fp32 (tq_dtype).  Strides are in
- * elements.  Device entry points enqueue on `stream` and return; they never
+ * elements, 0 to 2^46, and a stride times the entries of its dimension is at most
+ * 2^58.  Device entry points enqueue on `stream` and return; they never
  * allocate, synchronize or use memory that is not an argument, and can be
  * captured in a HIP graph.
  *
