@@ -13,6 +13,8 @@ import ctypes as C
 import functools
 import math
 import os
+import types
+import warnings
 
 import numpy as np
 
@@ -101,15 +103,29 @@ for _name, (_res, _args) in SIGNATURES.items():
 
 
 # The decode-side calls in their common form, compiled (csrc_decode/tq_torch.cc);
-# each returns None for what it leaves to the functions below.
-if _torch is not None:
+# each returns None for what it leaves to the functions below.  Those serve every
+# call, on the same kernels: without the compiled forms, or where they were built for
+# another torch, a call takes some 5 us more of the host, and nothing else changes.
+def _compiled_calls():
     try:
-        from . import _tq_torch as _fast
+        from . import _tq_torch as fast
+        built_for = getattr(fast, "torch_version", None)
+        if built_for != _torch.__version__:
+            raise ImportError(f"built for torch {built_for}, this is {_torch.__version__}")
     except ImportError as e:
-        raise ImportError(f"_tq_torch.so is missing or does not load ({e}); build it with "
-                          "`python -m bit_mixed_precision_amd.build_lib`") from e
-    _fast.bind(getattr(_torch._C, "_cuda_getCurrentRawStream", lambda index: 0),
-               {_n: C.cast(getattr(lib, _n), C.c_void_p).value for _n in SIGNATURES})
+        warnings.warn(f"_tq_torch.so is missing or does not load ({e}): the decode-side calls are "
+                      "made from Python; build it with "
+                      "`python -m bit_mixed_precision_amd.build_lib`", RuntimeWarning, stacklevel=3)
+        return types.SimpleNamespace(**{n: lambda *a: None for n in (
+            "rope", "rope_append", "paged_attention", "pages_fork", "pages_grow",
+            "pages_compact")})
+    fast.bind(getattr(_torch._C, "_cuda_getCurrentRawStream", lambda index: 0),
+              {n: C.cast(getattr(lib, n), C.c_void_p).value for n in SIGNATURES})
+    return fast
+
+
+if _torch is not None:
+    _fast = _compiled_calls()
 
 
 class TQError(RuntimeError):

@@ -71,16 +71,24 @@ def _hip_san_flags():
 
 def _torch_ext_cmd(out):
     """The compiler call for _tq_torch.so; torch's libraries are already in the
-    process that loads it.  None without torch (host-only use)."""
+    process that loads it.  None without torch (host-only use) or without the
+    headers of torch or Python: libtq.so does not need it, and the binding makes the
+    same calls from Python."""
     import sysconfig
     try:
         import torch
     except ImportError:
         return None
     root = os.path.dirname(torch.__file__)
+    for header in (os.path.join(root, "include", "ATen", "ATen.h"),
+                   os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        if not os.path.exists(header):
+            print(f"{header} is missing: _tq_torch.so is left out", file=sys.stderr)
+            return None
     # not HOST_FLAGS: torch's headers are not written for -Wextra
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I", INCLUDE,
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f'-DTQ_TORCH_VERSION="{torch.__version__}"',
             "-isystem", os.path.join(root, "include"),
             "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
             "-isystem", sysconfig.get_paths()["include"], TORCH_SRC, "-o", out,

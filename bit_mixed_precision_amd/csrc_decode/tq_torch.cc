@@ -371,4 +371,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tq_torch",
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__tq_torch() { return PyModule_Create(&module); }
+// torch_version: the torch whose headers this was compiled with; binding.py calls
+// nothing here under any other.
+PyMODINIT_FUNC PyInit__tq_torch() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", TQ_TORCH_VERSION) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
