@@ -599,6 +599,16 @@ def _kind(t, name, where, f32=False):
     return k
 
 
+def _flag(v, name, where):
+    """A bool, or 0 or 1, as an int."""
+    try:
+        if v == 0 or v == 1:
+            return int(v)
+    except (RuntimeError, TypeError, ValueError):  # an array or a tensor of several
+        pass
+    raise TQError(TQ_ERR_VALUE, f"{where}: {name} must be True or False, not {v!r}")
+
+
 def _heads(t, name, where):
     """Shape and strides of a [tokens][heads][D] tensor, the numbers of a head adjacent."""
     shape, strides = t.shape, t.stride()
@@ -728,6 +738,7 @@ def tq_rope(X, table, positions, interleaved: bool = False, inverse: bool = Fals
         if r is not None:
             return _done(r, where)
     kind = _kind(X, "X", where, f32=True)
+    interleaved, inverse = _flag(interleaved, "interleaved", where), _flag(inverse, "inverse", where)
     (T, H, D), xs = _heads(X, "X", where)
     n_pos, rot = _table(table, where)
     _int32(positions, "positions", (T,), where)
@@ -759,6 +770,7 @@ def tq_rope_append(QKV, table, positions, page_table, k_pages, v_pages, interlea
         if r is not None:
             return _done(r, where)
     kind = _kind(QKV, "QKV", where)
+    interleaved = _flag(interleaved, "interleaved", where)
     (T, H, D), xs = _heads(QKV, "QKV", where)
     if H > 1 and xs[1] != D:
         raise TQError(TQ_ERR_SHAPE, f"{where}: the heads of QKV must be adjacent")

@@ -60,6 +60,15 @@ int kind(const at::Tensor& t, bool f32) {
   }
 }
 
+// A flag that the C ABI takes as it is: a bool, or the int 0 or 1; -1 for the rest,
+// which binding.py looks at.
+int flag(PyObject* o) {
+  if (!PyLong_Check(o)) return -1;  // bools are ints
+  int overflow = 0;
+  const long v = PyLong_AsLongAndOverflow(o, &overflow);
+  return !overflow && (v == 0 || v == 1) ? (int)v : -1;
+}
+
 bool on(const at::Tensor& t, const at::Device& d) { return t.device() == d; }
 
 // t is on the GPU that is current.
@@ -156,11 +165,11 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor* t[3];
     if (n != 5 || !tensors(a, {0, 1, 2}, t)) return none();
     const at::Tensor &x = *t[0], &table = *t[1], &pos = *t[2];
-    const int k = kind(x, true), inter = PyObject_IsTrue(a[3]), inv = PyObject_IsTrue(a[4]);
+    const int k = kind(x, true), inter = flag(a[3]), inv = flag(a[4]);
     const at::Device d = x.device();
     if (k < 0 || inter < 0 || inv < 0 || !current(x) || !heads(x) || !angles(table, d) ||
         !int32s(pos, {x.size(0)}, d))
-      return PyErr_Occurred() ? nullptr : none();
+      return none();
     bool ok;
     void* s = stream_of(d, &ok);
     if (!ok) return nullptr;
@@ -180,13 +189,13 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor &x = *t[0], &table = *t[1], &pos = *t[2], &pages = *t[3], &k = *t[4],
                      &v = *t[5];
     const at::Tensor* seqs = a[7] == Py_None ? nullptr : tensor(a[7]);
-    const int kd = kind(x, false), inter = PyObject_IsTrue(a[6]);
+    const int kd = kind(x, false), inter = flag(a[6]);
     const at::Device d = x.device();
     if (kd < 0 || inter < 0 || (a[7] != Py_None && !seqs) || !current(x) || !heads(x) ||
         (x.size(1) > 1 && x.stride(1) != x.size(2)) || !angles(table, d) || !matrix(pages, d) ||
         !int32s(pos, {x.size(0)}, d) || (seqs && !int32s(*seqs, {x.size(0)}, d)) ||
         !cache(k, v, x, d))
-      return PyErr_Occurred() ? nullptr : none();
+      return none();
     const int64_t T = x.size(0), D = x.size(2), Hkv = k.size(2), Hq = x.size(1) - 2 * Hkv;
     if (Hq < 1) return none();
     bool ok;

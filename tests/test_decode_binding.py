@@ -5,6 +5,7 @@ import os
 import subprocess
 import sys
 
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -67,3 +68,33 @@ def test_build_without_headers(monkeypatch, tmp_path):
     paths = dict(sysconfig.get_paths(), include=str(tmp_path))
     monkeypatch.setattr(sysconfig, "get_paths", lambda: paths)
     assert build_lib._torch_ext_cmd("x.so") is None
+
+
+FLAGS = [2, -1, None, "yes", [1], 0.5, 1 << 70, torch.ones(2)]
+
+
+@pytest.mark.parametrize("device", ["cpu", pytest.param("cuda", marks=pytest.mark.gpu)])
+def test_flags(device):
+    """interleaved and inverse: a bool, or 0 or 1, in both forms of a call; on the CPU
+    the refusal of the flag comes before that of the device."""
+    h = dict(dtype=torch.float16, device=device)
+    i = dict(dtype=torch.int32, device=device)
+    X, pos = torch.ones(3, 8, 16, **h), torch.ones(3, **i)
+    table = torch.from_numpy(tq.tq_rope_table(8, 16)).to(device)
+    k, pt = torch.zeros(5, 16, 2, 16, **h), torch.zeros(3, 4, **i)
+    forms = [{}] if device == "cpu" else [{}, {"stream": torch.cuda.current_stream().cuda_stream}]
+    calls = [lambda f, kw: tq.tq_rope(X, table, pos, interleaved=f, **kw),
+             lambda f, kw: tq.tq_rope(X, table, pos, inverse=f, **kw),
+             lambda f, kw: tq.tq_rope_append(X, table, pos, pt, k, k.clone(), f, **kw)]
+    for call in calls:
+        for kw in forms:
+            for bad in FLAGS:
+                with pytest.raises(tq.TQError) as e:
+                    call(bad, kw)
+                assert e.value.status == tq.TQ_ERR_VALUE, bad
+        if device == "cuda":
+            for value in (False, True):
+                want = call(value, {})
+                for same in (int(value), np.bool_(value), float(value), torch.tensor(value)):
+                    for kw in forms:
+                        assert torch.equal(call(same, kw), want)
