@@ -641,6 +641,9 @@ def _int32(t, name, shape, where):
 def _cache(k_pages, v_pages, like, D, where):
     """(n_pages, page_size, Hkv, page, row and head stride) of the two halves of a
     paged cache [pages][slots][Hkv][D], any order in memory, numbers adjacent."""
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if not isinstance(t, _torch.Tensor):
+            raise TQError(TQ_ERR_VALUE, f"{where}: {name} must be a torch tensor")
     ks, kst = k_pages.shape, k_pages.stride()
     if not (k_pages.dtype is v_pages.dtype is like.dtype and len(ks) == 4 and ks[3] == D
             and kst[3] == 1 and v_pages.shape == ks and v_pages.stride() == kst):

@@ -98,3 +98,23 @@ def test_flags(device):
                 for same in (int(value), np.bool_(value), float(value), torch.tensor(value)):
                     for kw in forms:
                         assert torch.equal(call(same, kw), want)
+
+
+def test_arguments_that_are_no_tensors():
+    """Every tensor argument in turn replaced by None, an array and a list: TQError, not
+    whatever the first attribute access gives."""
+    h, i = dict(dtype=torch.float16), dict(dtype=torch.int32)
+    x, pos, pt = torch.zeros(3, 8, 16, **h), torch.zeros(3, **i), torch.zeros(3, 4, **i)
+    table, k = torch.zeros(8, 8, 2), torch.zeros(5, 16, 2, 16, **h)
+    pool = torch.zeros(2, 5, 16, 16, **h)
+    calls = [(tq.tq_rope, (x, table, pos)), (tq.tq_rope_append, (x, table, pos, pt, k, k)),
+             (tq.tq_paged_attention, (x, k, k, pt, pos)), (tq.tq_pages_fork, (pool, pt, pos, pos)),
+             (tq.tq_pages_grow, (pt, pos, pos)), (tq.tq_pages_compact, (pool, pt, pos)),
+             (tq.tq_pages_copy, (pool, pos, pos))]
+    rest = {tq.tq_pages_fork: (16,), tq.tq_pages_grow: (5, 16), tq.tq_pages_compact: (16,)}
+    for fn, args in calls:
+        for n in range(len(args)):
+            for bad in (None, np.zeros((3, 4), np.int32), [1, 2]):
+                with pytest.raises(tq.TQError) as e:
+                    fn(*args[:n], bad, *args[n + 1:], *rest.get(fn, ()))
+                assert e.value.status in (tq.TQ_ERR_VALUE, tq.TQ_ERR_SHAPE), (fn, n)
