@@ -1,5 +1,6 @@
 // C ABI of the decode-side operators (include/tq.h): argument checks.
 
+#include <float.h>
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -238,7 +239,9 @@ int tq_paged_attention(int dtype, const void* Q, int64_t q_tok, int64_t q_head,
   if (!aligned(Q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(Out, 16) ||
       !aligned(workspace, 16) || !aligned(page_table, 4) || !aligned(lens, 4) || !aligned(lse, 4))
     return TQ_ERR_ALIGN;
-  if ((dtype != TQ_F16 && dtype != TQ_BF16) || !isfinite(scale) || window < 0) return TQ_ERR_VALUE;
+  const double scale_log2 = scale * 1.4426950408889634;  // the kernels hold it in fp32
+  if ((dtype != TQ_F16 && dtype != TQ_BF16) || !(fabs(scale_log2) <= FLT_MAX) || window < 0)
+    return TQ_ERR_VALUE;
   st = device_ready();
   if (st != TQ_OK) return st;
   tq::AttnArgs a{};
@@ -259,7 +262,7 @@ int tq_paged_attention(int dtype, const void* Q, int64_t q_tok, int64_t q_head,
   a.Hq = Hq;
   a.Hkv = Hkv;
   a.D = D;
-  a.scale_log2 = (float)(scale * 1.4426950408889634);
+  a.scale_log2 = (float)scale_log2;
   a.window = window > INT32_MAX ? 0 : window;  // longer than any sequence
   a.Out = Out;
   a.lse = lse;

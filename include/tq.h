@@ -454,7 +454,7 @@ int tq_rope_append(int dtype, const void* QKV, int64_t qkv_tok, const float* tab
  * bytes, 16-byte aligned, contents irrelevant; calls that overlap on one
  * workspace race.
  * Errors: TQ_ERR_NULL, TQ_ERR_SHAPE (a workspace that is too small included),
- * TQ_ERR_ALIGN, TQ_ERR_VALUE (dtype, scale not finite, window < 0),
+ * TQ_ERR_ALIGN, TQ_ERR_VALUE (dtype, scale log2(e) not finite in fp32, window < 0),
  * TQ_ERR_DEVICE.  B = 0 is a no-op. */
 int tq_paged_attention(int dtype, const void* Q, int64_t q_tok, int64_t q_head,
                        const void* k_pages, const void* v_pages, int64_t n_pages,

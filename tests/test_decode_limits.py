@@ -44,3 +44,10 @@ def test_strides_that_leave_64_bits():
                 dict(Hq=1 << 12, Hkv=1 << 12, hst=1 << 46 | 8), dict(P=1 << 30, pst=1 << 30)):
         assert attn(**bad) == S, bad
     assert attn(P=1 << 30, pst=1 << 27) == V
+
+
+def test_scale_past_fp32():
+    """The kernels hold scale log2(e) in fp32: a finite scale that leaves its range would
+    make 0 * inf of a score of zero."""
+    for bad in (3e38, -3e38, 1e39, 1e308, float("nan")):
+        assert attn(scale=bad, dtype=0) == V, bad
