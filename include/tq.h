@@ -404,7 +404,7 @@ int tq_rope_table(int64_t n_pos, int64_t rot, double theta, int scaling, double 
  * out as zeros.  table: fp32 [n_pos][rot / 2][2], device, 8-byte aligned (NULL
  * when n_pos = 0).
  * T = 0 or H = 0 is a no-op.  D <= 2^16, rot even, 2 <= rot <= D, H <= 2^16,
- * T <= 2^30.  Errors: TQ_ERR_NULL, TQ_ERR_SHAPE, TQ_ERR_ALIGN (X or Y not
+ * T <= 2^30, T H < 2^31.  Errors: TQ_ERR_NULL, TQ_ERR_SHAPE, TQ_ERR_ALIGN (X or Y not
  * aligned to an element), TQ_ERR_VALUE (dtype, interleaved, inverse). */
 int tq_rope(int dtype, const void* X, int64_t x_tok, int64_t x_head, void* Y, int64_t y_tok,
             int64_t y_head, const float* table, int64_t n_pos, int64_t rot, const int32_t* pos,
@@ -420,6 +420,7 @@ int tq_rope(int dtype, const void* X, int64_t x_tok, int64_t x_head, void* Y, in
  * it is written to the cache; nor is it where the row is outside
  * [0, n_seqs), the position is past the table's width, or the page is outside
  * [0, n_pages).  Two tokens of one call must not name the same slot.
+ * Limits as tq_rope's with H = Hq + 2 Hkv, and Hq, Hkv >= 1.
  * Errors as tq_rope's, and TQ_ERR_SHAPE for page geometry (page_size < 1,
  * negative strides, width * page_size > 2^30, strides that let two numbers of a
  * cache share an address). */

@@ -51,3 +51,12 @@ def test_scale_past_fp32():
     make 0 * inf of a score of zero."""
     for bad in (3e38, -3e38, 1e39, 1e308, float("nan")):
         assert attn(scale=bad, dtype=0) == V, bad
+
+
+def test_tokens_times_heads():
+    """Both sides of the documented limit T H < 2^31, appending with Hq + 2 Hkv heads."""
+    far = dict(yt=1 << 20, yh=16)
+    assert rope(T=1 << 16, H=(1 << 15) - 1, **far) == V and rope(T=1 << 16, H=1 << 15, **far) == S
+    assert rope(T=(1 << 30), H=1, yt=16) == V and rope(T=(1 << 30), H=2, yt=32) == S
+    assert append(T=1 << 28, Hq=5, Hkv=1, xt=112) == V
+    assert append(T=1 << 28, Hq=6, Hkv=1, xt=128) == S
