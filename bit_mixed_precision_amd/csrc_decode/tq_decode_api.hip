@@ -26,6 +26,10 @@ constexpr int64_t kMaxPlanes = int64_t(1) << 16;
 constexpr int64_t kMaxPageBytes = int64_t(1) << 30;
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+// The stride of a dimension of one entry is never taken: whatever a caller has there
+// (a view of a tensor may hold any number) stands for 0.
+int64_t step(int64_t n, int64_t s) { return n == 1 ? 0 : s; }
+
 // Stride s of a dimension of n >= 1 entries.
 bool stride_ok(int64_t n, int64_t s) { return s >= 0 && s <= kMaxStride && s <= kMaxReach / n; }
 
@@ -124,10 +128,14 @@ int tq_rope(int dtype, const void* X, int64_t x_tok, int64_t x_head, void* Y, in
   if (!X || !Y || (!table && n_pos != 0) || !pos) return TQ_ERR_NULL;
   int st = rope_shapes(n_pos, rot, T, H, D);
   if (st != TQ_OK) return st;
+  x_tok = step(T, x_tok);
+  x_head = step(H, x_head);
+  y_tok = step(T, y_tok);
+  y_head = step(H, y_head);
   if (!stride_ok(T, x_tok) || !stride_ok(H, x_head) || !stride_ok(T, y_tok) ||
       !stride_ok(H, y_head) || !distinct(T, y_tok, H, y_head, D))
     return TQ_ERR_SHAPE;
-  if (X == Y && ((T > 1 && x_tok != y_tok) || (H > 1 && x_head != y_head))) return TQ_ERR_SHAPE;
+  if (X == Y && (x_tok != y_tok || x_head != y_head)) return TQ_ERR_SHAPE;
   const uintptr_t size = dtype == TQ_F32 ? 4 : 2;
   if (!aligned(X, size) || !aligned(Y, size) || !aligned(table, 8) || !aligned(pos, 4))
     return TQ_ERR_ALIGN;
@@ -166,6 +174,10 @@ int tq_rope_append(int dtype, const void* QKV, int64_t qkv_tok, const float* tab
   if (Hq < 1 || Hkv < 1 || Hq > kMaxHeads || Hkv > kMaxHeads) return TQ_ERR_SHAPE;
   int st = rope_shapes(n_pos, rot, T, Hq + 2 * Hkv, D);
   if (st != TQ_OK) return st;
+  qkv_tok = step(T, qkv_tok);
+  page_stride = step(n_pages, page_stride);
+  row_stride = step(page_size, row_stride);
+  head_stride = step(Hkv, head_stride);
   if (n_pages < 1 || n_pages > INT32_MAX || n_seqs < 1 || n_seqs > INT32_MAX || width < 1 ||
       page_size < 1 || width > kMaxTokens || page_size > kMaxTokens ||
       width * page_size > kMaxTokens || !stride_ok(T, qkv_tok) ||
@@ -228,6 +240,11 @@ int tq_paged_attention(int dtype, const void* Q, int64_t q_tok, int64_t q_head,
   if (!Q || !k_pages || !v_pages || !page_table || !lens || !Out) return TQ_ERR_NULL;
   int st = attn_shapes(B, Hq, Hkv, D, page_size, width);
   if (st != TQ_OK) return st;
+  q_tok = step(B, q_tok);
+  q_head = step(Hq, q_head);
+  page_stride = step(n_pages, page_stride);
+  row_stride = step(page_size, row_stride);
+  head_stride = step(Hkv, head_stride);
   if (n_pages < 1 || n_pages > INT32_MAX || !stride_ok(B, q_tok) || !stride_ok(Hq, q_head) ||
       !stride_ok(n_pages, page_stride) || !stride_ok(page_size, row_stride) ||
       !stride_ok(Hkv, head_stride) || row_stride > kMaxRowStride || q_tok % 8 || q_head % 8 ||

@@ -352,7 +352,7 @@ int tq_gemm_tq1_tile(const void* X, const void* qs, int64_t ldq, const void* sca
  *
  * Types: fp16, bfloat16 and, for tq_rope, fp32 (tq_dtype).  Strides are in
  * elements, 0 to 2^46, and a stride times the entries of its dimension is at most
- * 2^58.  Device entry points enqueue on `stream` and return; they never
+ * 2^58; the stride of a dimension of one entry is not looked at.  Device entry points enqueue on `stream` and return; they never
  * allocate, synchronize or use memory that is not an argument, and can be
  * captured in a HIP graph.
  *

@@ -108,3 +108,24 @@ def test_attention_infinite_values_of_small_weights():
             out = tq.tq_paged_attention(q, k, v, pt, lens, scale=float(np.log(2.0)))[0, 0]
             assert out[7] == float("inf"), (dtype, e)
             assert torch.isfinite(out[torch.arange(64) != 7]).all()
+
+
+def test_single_slot_pages_in_a_turned_cache():
+    """Pages of one token in a cache made as [1][pages][heads][D]: the stride between the
+    slots of a page is that of the whole cache, and is never taken."""
+    P, Hkv, D = 70000, 2, 128
+    q, k, v, pt, lens = paged(1, "f16", [50, 7, 0], 4, Hkv, D, 1, poison=False)
+    n = k.shape[0]
+    big = [torch.zeros(1, P, Hkv, D, dtype=torch.float16, device="cuda") for _ in range(2)]
+    for b, x in zip(big, (k, v)):
+        b[0, :n] = x[:, 0]
+    kt, vt = (b.transpose(0, 1) for b in big)
+    assert kt.stride(1) == P * Hkv * D > 1 << 24
+    want = tq.tq_paged_attention(q, k, v, pt, lens)
+    assert torch.equal(tq.tq_paged_attention(q, kt, vt, pt, lens), want)
+    table = torch.from_numpy(tq.tq_rope_table(64, D)).cuda()
+    qkv = torch.randn(3, 4 + 2 * Hkv, D, device="cuda").half()
+    pos = torch.tensor([3, 6, 0], dtype=torch.int32, device="cuda")
+    assert torch.equal(tq.tq_rope_append(qkv, table, pos, pt, kt, vt),
+                       tq.tq_rope_append(qkv, table, pos, pt, k, v))
+    assert torch.equal(kt[:n], k) and torch.equal(vt[:n], v)

@@ -60,3 +60,14 @@ def test_tokens_times_heads():
     assert rope(T=(1 << 30), H=1, yt=16) == V and rope(T=(1 << 30), H=2, yt=32) == S
     assert append(T=1 << 28, Hq=5, Hkv=1, xt=112) == V
     assert append(T=1 << 28, Hq=6, Hkv=1, xt=128) == S
+
+
+def test_strides_of_single_entries():
+    """The stride of a dimension of one entry is never taken, so it need not fit."""
+    assert rope(T=1, xt=-1, yt=(1 << 46) + 1) == V and rope(H=1, xh=-1, yh=-5) == V
+    assert append(T=1, xt=-1) == V and append(ps=1, rst=-1, width=64, pst=32) == V
+    assert append(P=1, pst=-1) == V and append(Hkv=1, Hq=6, hst=-1) == V
+    assert attn(B=1, qt=3) == V and attn(ps=1, rst=(1 << 24) + 8) == V and attn(P=1, pst=-4) == V
+    assert attn(Hq=1, Hkv=1, qh=3, hst=5) == V
+    # of two entries it is
+    assert attn(B=2, qt=3) == S and attn(ps=2, rst=(1 << 24) + 8) == S and attn(P=2, pst=-4) == S
