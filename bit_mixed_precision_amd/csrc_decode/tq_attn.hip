@@ -103,7 +103,8 @@ struct AttnParams {
   FastDiv page;
   int32_t n_pages, width, B, Hq, Hkv, D, G, qtiles, window;
   int32_t direct;  // one workgroup per (sequence, head): nothing is split
-  int32_t full;    // tiles of 16 KB in pages of whole half tiles, two workgroups per CU
+  int32_t full;    // tiles of 16 KB or more in whole lines and pages of whole half tiles,
+                   // two workgroups per CU
   float scale;
 };
 
@@ -325,11 +326,16 @@ __host__ __device__ constexpr int blocks_per_cu(int64_t D) { return D > 128 ? 1 
 
 // Waves that share the tiles, of those that run: half of them, one workgroup per
 // CU, where each has many tiles that are fetched without a detour (p.full: 16 KB a
-// tile, pages of whole half tiles), which keeps 64 KB of a CU in flight as it is.
-// Measured (us, half / all): one sequence of 131072 tokens, 8 key heads of 128: 90 /
-// 100, 96 sequences of 2048 .. 8192: 274 / 280; with fewer tiles a wave the other way
-// round: 32 sequences of up to 1024 tokens, if split (2.5 a wave) 26.2 / 24.4, 128 (10)
-// 65.3 / 63.8; heads of 80 161 / 126, pages of 24 108 / 98.
+// tile in whole lines, pages of whole half tiles), which keeps 64 KB of a CU in flight
+// as it is.  Measured (us, half / all): one sequence of 131072 tokens, 8 key heads of
+// 128: 93 / 102, 96 sequences of 2048 .. 8192: 285 / 294, 8 of 32768: 176 / 187 (but 64 of
+// 4096, 24 key heads: 492 / 481); with fewer tiles a wave the other way round: 32
+// sequences of up to 1024 tokens, if split (2.5 a wave) 26.2 / 24.4, 128 (10) 65.3 / 63.8;
+// pages of 24 108 / 98.  Smaller heads keep less in flight, and those of 72 .. 120 share
+// lines: the same 131072 tokens, heads of 64 75 / 54, 80 89 / 72, 96 93 / 84, 104 96 / 91,
+// 112 98 / 103, 120 101 / 105; 32 sequences of 8192, 2 key heads of 80 84 / 62, 96 83 / 70,
+// 104 104 / 74, 112 104 / 79, 120 113 / 84, 128 84 / 84; the 96 sequences, heads of 64 208 /
+// 144, 80 280 / 276, 96 286 / 300, 104 352 / 376, 112 367 / 384, 120 399 / 411.
 constexpr uint32_t kManyTiles = 12;
 __device__ __forceinline__ uint32_t waves_for(const AttnParams& p, uint32_t units, uint32_t waves) {
   return p.full && units / kManyTiles >= waves ? waves / 2 : waves;
@@ -1040,13 +1046,17 @@ hipError_t launch_kernel(const AttnParams& p, int64_t grid, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool BF, int DV>
-hipError_t launch_dv(const AttnParams& p, int64_t grid, hipStream_t s) {
-  // whole 128-byte lines that no other head or group of query heads reads
+// Rows of whole 128-byte lines that no other head or group of query heads reads.
+bool whole_lines(const AttnParams& p) {
   const uint64_t places = reinterpret_cast<uint64_t>(p.K) | reinterpret_cast<uint64_t>(p.V) |
                           (uint64_t)(p.page_stride | p.row_stride | p.head_stride) |
                           (uint64_t)p.D * 2;
-  const bool nt = p.qtiles == 1 && places % 128 == 0;
+  return p.qtiles == 1 && places % 128 == 0;
+}
+
+template <bool BF, int DV>
+hipError_t launch_dv(const AttnParams& p, int64_t grid, hipStream_t s) {
+  const bool nt = whole_lines(p);
   const auto form = [&](auto uni, auto lines) {
     return p.direct ? launch_kernel<BF, DV, uni, lines, true>(p, grid, s)
                     : launch_kernel<BF, DV, uni, lines, false>(p, grid, s);
@@ -1108,7 +1118,7 @@ hipError_t launch_paged_attention(int dtype, const AttnArgs& a, hipStream_t stre
   p.scale = a.scale_log2;
   const Grid g = attn_grid(a.B, a.Hq, a.Hkv, a.D, a.width * a.page_size, a.window);
   p.direct = g.direct;
-  p.full = a.D == 128 && a.page_size % 16 == 0 && g.blocks >= 2 * device_cus();
+  p.full = a.D > 64 && whole_lines(p) && a.page_size % 16 == 0 && g.blocks >= 2 * device_cus();
   p.owner = reinterpret_cast<int2*>(
       p.partial + g.partials * slot_floats(p.G < kHeads ? p.G : kHeads, p.D));
   return dtype == TQ_BF16 ? launch_t<true>(p, g.blocks, stream)

@@ -9,7 +9,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 tq = pytest.importorskip("bit_mixed_precision_amd.binding")
 
-from test_decode_gpu import paged, run_attention  # noqa: E402
+from test_decode_gpu import check_attention, f64, paged, run_attention  # noqa: E402
 
 
 @pytest.mark.parametrize("dtype,B,Hq,Hkv,D,longest", [
@@ -129,3 +129,45 @@ def test_single_slot_pages_in_a_turned_cache():
     assert torch.equal(tq.tq_rope_append(qkv, table, pos, pt, kt, vt),
                        tq.tq_rope_append(qkv, table, pos, pt, k, v))
     assert torch.equal(kt[:n], k) and torch.equal(vt[:n], v)
+
+
+def check_on_gpu(q, k, v, pt, lens, dtype):
+    """Every row and head against fp64 on the GPU (products of matrix and vector), for
+    caches over which the oracle's loops would take minutes."""
+    size, Hkv, D = k.shape[1:]
+    G = q.shape[1] // Hkv
+    out, lse = tq.tq_paged_attention(q, k, v, pt, lens, return_lse=True)
+    for b, n in enumerate(lens.tolist()):
+        if n == 0:
+            assert torch.all(out[b] == 0) and torch.all(lse[b] == -float("inf"))
+            continue
+        ids = pt[b, :-(-n // size)].long()
+        for h in range(Hkv):
+            kk, vv = (x[ids, :, h].flatten(0, 1)[:n].double() for x in (k, v))
+            vt = vv.t().contiguous()
+            for g in range(G):
+                qh = q[b, h * G + g].double()
+                s = kk @ qh / D ** 0.5
+                w = torch.softmax(s, 0)
+                ref = (f64(vt @ w)[None, None], f64(torch.logsumexp(s, 0))[None, None],
+                       np.array([[float((kk.abs() @ qh.abs()).max()) / D ** 0.5]]),
+                       f64(vt.abs() @ w)[None, None])
+                at = slice(h * G + g, h * G + g + 1)
+                check_attention(out[b:b + 1, at], lse[b:b + 1, at], ref, dtype, D, n)
+    again = tq.tq_paged_attention(q, k, v, pt, lens)
+    assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("dtype,D,size,shift", [
+    ("f16", 128, 16, 0), ("bf16", 128, 64, 0),  # whole lines: half of the waves work
+    ("f16", 128, 16, 8),                        # lines shared between heads
+    ("f16", 120, 16, 0), ("bf16", 104, 32, 0), ("f16", 128, 24, 0), ("f16", 256, 16, 0)])
+def test_attention_many_tiles_a_wave(dtype, D, size, shift):
+    """More than 12 tiles for every wave of the GPU, in rows that begin and end anywhere."""
+    q, k, v, pt, lens = paged(21, dtype, [60001, 0, 41000, 3, 33, 7000], 8, 8, D, size,
+                              poison=False)
+    if shift:
+        k, v = (torch.cat([torch.zeros(shift, dtype=x.dtype, device="cuda"), x.flatten()])
+                [shift:].view(x.shape) for x in (k, v))
+        assert k.data_ptr() % 128 == 2 * shift
+    check_on_gpu(q, k, v, pt, lens, dtype)
