@@ -849,6 +849,36 @@ def stack_cpu_baseline(cols=256):
 
 # ----------------------------------------------------------------------------- main
 
+def line_of(out):
+    """The one JSON line of the sweep: every figure of `out`, its tables with one short
+    row a call (what a row leaves out follows from its sizes, or is in --tables-out), so
+    that the line stays below 8 KB, which is what a log's tail holds."""
+    def pick(row, *keys):
+        return {k: row[k] for k in keys if k in row}
+
+    out = dict(out)
+    out["calls"] = [pick(r, "fmt", "M", "N", "us", "TBps", "TFLOPps", "roof_frac")
+                    for r in out["calls"]]
+    if "context" in out:
+        out["context"] = dict(out["context"], fp16_matmul=[
+            pick(r, "M", "N", "us", "tq2_us") for r in out["context"]["fp16_matmul"]])
+    if "other_configs" in out:
+        short = {}
+        for name, rows in out["other_configs"].items():
+            if isinstance(rows, list):
+                by = {}
+                for r in rows:
+                    by.setdefault(r["linear"], pick(r, "linear", "N", "K"))[r["fmt"] + "_us"] = r["us"]
+                rows = list(by.values())
+            short[name] = rows
+        out["other_configs"] = short
+    if "tq1_vs_tq2_same_weights" in out:
+        out["tq1_vs_tq2_same_weights"] = [
+            dict(pick(r, "p", "M", "N"), tq1_us=r["tq1"]["us"], tq2_us=r["tq2"]["us"])
+            for r in out["tq1_vs_tq2_same_weights"]]
+    return json.dumps(out)
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--gpus", type=int, default=1)
@@ -862,6 +892,8 @@ def main():
                     help="skip the timing of the 1024 x 1024 GEMV, the 3B-class layer and the "
                          "TQ1-vs-TQ2 zero-fraction sweep")
     ap.add_argument("--calls-out", default=None, help="also write the per-call table here (JSON)")
+    ap.add_argument("--tables-out", default=None,
+                    help="also write the line with its tables in full here (JSON)")
     ap.add_argument("--bwd", action="store_true",
                     help="QAT backward dX = dY (s.T) at the 70B layer shapes, 4096 tokens")
     ap.add_argument("--stack", action="store_true",
@@ -1022,7 +1054,10 @@ def main():
     if args.calls_out:
         with open(args.calls_out, "w") as f:
             json.dump(per_call, f, indent=1)
-    print(json.dumps(out), flush=True)
+    if args.tables_out:
+        with open(args.tables_out, "w") as f:
+            json.dump(out, f, indent=1)
+    print(line_of(out), flush=True)
 
 
 if __name__ == "__main__":
