@@ -734,7 +734,10 @@ def tq_rope(X, table, positions, interleaved: bool = False, inverse: bool = Fals
     """Rotary positions: X [T][H][D] (fp16, bfloat16 or float32; a view with any
     strides, numbers of a head adjacent) turned by table[positions] over the first
     rot numbers of each head; inverse turns back, which is the gradient.  Y may be
-    X; a new contiguous tensor when None."""
+    X; a new contiguous tensor when None.  Like every call here it is unknown to
+    autograd: the result of an X that requires a gradient requires none, and a
+    torch.autograd.Function that is to carry one calls this with inverse in its
+    backward."""
     where = "tq_rope"
     if Y is None and stream is None:
         r = _fast.rope(X, table, positions, interleaved, inverse)

@@ -51,7 +51,7 @@
 // its own instead and one launch does.
 //
 // Measured: 96 sequences of 2048 .. 8192 tokens, 64 query / 8 key-value heads of
-// 128, pages of 16, 1.75 GB: 273 us, 6.4 TB/s (92% of what a plain read reaches on
+// 128, pages of 16, 1.75 GB: 274 us, 6.4 TB/s (92% of what a plain read reaches on
 // this card, 6.97 TB/s; HBM reads by the counters 1.00 of the algorithmic bytes);
 // one sequence of 131072 tokens, 537 MB: 90 us, of which the join takes 5; 37
 // ragged sequences of up to 4096 tokens, 24 heads of 64 in bf16, 116 MB: 31 us (25 in
@@ -319,9 +319,9 @@ __device__ __forceinline__ void finish(const AttnParams& p, int b, int head, int
 
 // Workgroups per CU, for which the registers are laid out: enough bytes in flight,
 // and more only spill or crowd.  Measured (us): heads of 128, 96 sequences of 2048
-// .. 8192 tokens, 8 key heads: 2 285, 3 322; heads of 64, 64 sequences of up to 4096,
-// 24 key heads: 2 163, 3 180; heads of 256, 8 sequences of 32768, 2 key heads: 1 97,
-// 2 131.
+// .. 8192 tokens, 8 key heads: 2 274, 3 314; heads of 64, 64 sequences of 1024 .. 4096,
+// 24 key heads: 2 167, 3 173 (but 8 of 32768, 8 key heads: 104, 98); heads of 256, 8
+// sequences of 32768, 2 key heads: 1 98, 2 124.
 __host__ __device__ constexpr int blocks_per_cu(int64_t D) { return D > 128 ? 1 : 2; }
 
 // Waves that share the tiles, of those that run: half of them, one workgroup per

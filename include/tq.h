@@ -480,6 +480,9 @@ int64_t tq_paged_attention_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t
  * of n_pages pages of page_bytes contiguous bytes each; a page's copy is made
  * in every plane.  page_bytes a multiple of 16, pool 16-byte aligned.
  * Entries outside [0, n_pages) name no page: they are kept and never followed.
+ * Two rows may share the pages that both have filled.  A caller that cuts a length
+ * back into such a page has to give that row a page of its own (tq_pages_copy) before
+ * it appends there: neither forking nor growing looks for it.
  * workspace: tq_pages_workspace(rows, n_pages) bytes, 16-byte aligned.
  * Limits: rows <= 2^16, width * page_size <= 2^30, n_pages <= 2^24, planes <=
  * 2^16, page_bytes <= 2^30.  Free pages are taken in ascending order for rows
