@@ -444,10 +444,10 @@ int tq_rope_append(int dtype, const void* QKV, int64_t qkv_tok, const float* tab
  * fp16 or bfloat16 in and out, fp32 scores, weights and sums; each weight enters
  * the product with v as two 16-bit numbers, rounded to within 2^-22 (fp16; 2^-16
  * bfloat16) of itself, in fp16 or within 2^-38 of the row's largest.  A weight of
- * zero adds nothing, however large its (finite) value; in fp16 nor does one below
- * 2^-39 of the row's largest.  An infinite value gives an infinite result, or NaN where
- * its weight is zero or, in fp16, below 2^-38 of the largest.  The same bits on every
- * run.  Outputs and workspace must not overlap the inputs.
+ * zero adds nothing, however large its (finite) value; in fp16 one below 2^-39 of the
+ * row's largest may add nothing.  An infinite value gives an infinite result, or NaN
+ * where its weight is zero, and in fp16 it may where it is below 2^-38 of the largest.
+ * The same bits on every run.  Outputs and workspace must not overlap the inputs.
  * D a multiple of 8, 8 <= D <= 256; Hq a multiple of Hkv, Hq <= 2^12; B <=
  * 2^20; width * page_size <= 2^30; B * Hkv * ceil(Hq / Hkv / 16) * (width *
  * page_size / 32 + 2) < 2^31; strides multiples of 8, row_stride <= 2^24;
