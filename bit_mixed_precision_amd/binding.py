@@ -88,6 +88,11 @@ SIGNATURES = {
                                 _I64, _P, _I64, _I64, _I64, _I64, _D, _I64, _P, _P, _P, _I64,
                                 _P]),
     "tq_paged_attention_workspace": (_I64, [_I64, _I64, _I64, _I64, _I64, _I64]),
+    "tq_tree_mask": (_I, [_P, _I64, _I64, _P, _P, _P]),
+    "tq_tree_attention": (_I, [_I, _P, _I64, _I64, _I64, _P, _P, _I64, _I64, _I64, _I64, _I64, _P,
+                               _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _D, _I64, _P,
+                               _P, _P, _I64, _P]),
+    "tq_tree_attention_workspace": (_I64, [_I64, _I64, _I64, _I64, _I64, _I64, _I64]),
     "tq_pages_fork": (_I, [_P, _I64, _I64, _I64, _P, _P, _I64, _P, _I64, _I64, _I64, _P, _P, _P,
                            _P, _P, _I64, _P]),
     "tq_pages_grow": (_I, [_P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _P]),
@@ -117,8 +122,8 @@ def _compiled_calls():
                       "made from Python; build it with "
                       "`python -m bit_mixed_precision_amd.build_lib`", RuntimeWarning, stacklevel=3)
         return types.SimpleNamespace(**{n: lambda *a: None for n in (
-            "rope", "rope_append", "paged_attention", "pages_fork", "pages_grow",
-            "pages_compact")})
+            "rope", "rope_append", "paged_attention", "tree_mask", "tree_attention", "pages_fork",
+            "pages_grow", "pages_compact")})
     fast.bind(getattr(_torch._C, "_cuda_getCurrentRawStream", lambda index: 0),
               {n: C.cast(getattr(lib, n), C.c_void_p).value for n in SIGNATURES})
     return fast
@@ -713,6 +718,17 @@ def _launch(where, dev, fn, *args):
         raise TQError(st, where)
 
 
+def _address(t):
+    """The address of a tensor that may be None."""
+    return None if t is None else t.data_ptr()
+
+
+def _all_on(where, dev, *named):
+    """Every (name, tensor) that is not None on GPU `dev`, the first one's."""
+    if dev < 0 or any(t is not None and t.get_device() != dev for _, t in named):
+        _on_gpu(where, *named)
+
+
 def _raw_stream(stream, dev):
     if stream is not None:
         return stream
@@ -870,6 +886,117 @@ def tq_paged_attention(Q, k_pages, v_pages, page_table, lens, scale: float | Non
             1.0 / math.sqrt(D) if scale is None else scale, window, out.data_ptr(),
             None if lse is None else lse.data_ptr(),
             None if workspace is None else workspace.data_ptr(), n, _raw_stream(stream, dev))
+    return (out, lse) if return_lse else out
+
+
+def _nodes(Q, where):
+    """Shape and strides of queries [B][T][Hq][D], the numbers of a head adjacent."""
+    shape, strides = Q.shape, Q.stride()
+    if len(shape) != 4 or (strides[3] != 1 and shape[3] > 1):
+        raise TQError(TQ_ERR_SHAPE, f"{where}: Q must be [sequences][nodes][heads][D] with adjacent "
+                                    f"numbers, not {tuple(shape)} at strides {strides}")
+    return shape, strides
+
+
+def _mask(mask, B, T, where):
+    """Words between the sequences of a mask [B][T][ceil(T / 64)], or 0 for one of
+    [T][ceil(T / 64)] or [1][T][..] that serves all."""
+    words = (T + 63) // 64
+    if not isinstance(mask, _torch.Tensor) or mask.dtype is not _torch.int64:
+        raise TQError(TQ_ERR_VALUE, f"{where}: mask must be an int64 tensor")
+    shape = tuple(mask.shape)
+    if shape not in ((B, T, words), (1, T, words), (T, words)) or not mask.is_contiguous():
+        raise TQError(TQ_ERR_SHAPE, f"{where}: mask must be a contiguous [{B}][{T}][{words}] or "
+                                    f"[{T}][{words}], not {shape}")
+    return T * words if len(shape) == 3 and shape[0] > 1 else 0
+
+
+def tq_tree_mask(parents, stream=None):
+    """The paths of drafted trees: parents int32 [B][T], node i below node parents[i] < i
+    or, with any other number, below the last cached token.  Returns (mask, depth):
+    int64 [B][T][ceil(T / 64)], bit j of node i set where j is i or above it, and int32
+    [B][T], the number of nodes above i.  For tq_tree_attention and, with the lengths
+    added, for the positions of the nodes."""
+    where = "tq_tree_mask"
+    if stream is None:
+        r = _fast.tree_mask(parents)
+        if r is not None:
+            return _done(r, where)
+    B, T = _rows(parents, "parents", where)
+    dev = parents.get_device()
+    if dev < 0:
+        _on_gpu(where, ("parents", parents))
+    mask = _empty(parents, (B, T, (T + 63) // 64), _torch.int64, stream)
+    depth = _empty(parents, (B, T), _I32T, stream)
+    _launch(where, dev, lib.tq_tree_mask, parents.data_ptr(), B, T, mask.data_ptr(),
+            depth.data_ptr(), _raw_stream(stream, dev))
+    return mask, depth
+
+
+def tq_tree_attention_workspace(B: int, T: int, Hq: int, Hkv: int, D: int, page_size: int,
+                                width: int) -> int:
+    """Workspace bytes of tq_tree_attention on the current GPU."""
+    n = int(lib.tq_tree_attention_workspace(B, T, Hq, Hkv, D, page_size, width))
+    _check(min(n, 0), "tq_tree_attention_workspace")
+    return n
+
+
+@functools.lru_cache(maxsize=256)
+def _tree_workspace(dev, *shape):
+    with _torch.cuda.device(dev):  # the size follows the GPU's compute units
+        return lib.tq_tree_attention_workspace(*shape)
+
+
+def tq_tree_attention(Q, k_pages, v_pages, page_table, lens, mask=None, nodes=None,
+                      scale: float | None = None, window: int = 0, out=None,
+                      return_lse: bool = False, workspace=None, stream=None):
+    """Attention of several new tokens per sequence: Q [B][T][Hq][D], the nodes of a
+    drafted tree, whose keys and values lie in the slots lens[b], lens[b] + 1, ... of the
+    paged cache k_pages, v_pages [pages][slots][Hkv][D] named by page_table [B][width].
+    Node i sees the lens[b] cached tokens (the last of `window` on its path, 0: all) and
+    the nodes whose bits mask sets for it (tq_tree_mask; [T][words] for all sequences
+    alike; None: the nodes up to i).  nodes int32 [B]: how many of the T there are (None:
+    all); rows of the others come out as zeros with lse -inf.  Returns out [B][T][Hq][D],
+    and lse float32 [B][T][Hq] with return_lse.  scale: 1 / sqrt(D) when None."""
+    where = "tq_tree_attention"
+    if out is None and workspace is None and stream is None:
+        r = _fast.tree_attention(Q, k_pages, v_pages, page_table, lens, mask, nodes, scale, window,
+                                 return_lse)
+        if r is not None:
+            return _done(r, where)
+    kind = _kind(Q, "Q", where)
+    (B, T, Hq, D), qs = _nodes(Q, where)
+    P, size, Hkv, page_stride, row_stride, head_stride = _cache(k_pages, v_pages, Q, D, where)
+    rows, width = _rows(page_table, "page_table", where)
+    if rows != B:
+        raise TQError(TQ_ERR_SHAPE, f"{where}: page_table has {rows} rows, Q {B}")
+    _int32(lens, "lens", (B,), where)
+    if nodes is not None:
+        _int32(nodes, "nodes", (B,), where)
+    mask_seq = 0 if mask is None else _mask(mask, B, T, where)
+    if out is not None:
+        _same(out, "out", Q, (B, T, Hq, D), where)
+    if workspace is not None:
+        _need(workspace, "workspace", "u8", None, where)
+    dev = Q.get_device()
+    _all_on(where, dev, ("Q", Q), ("k_pages", k_pages), ("v_pages", v_pages),
+            ("page_table", page_table), ("lens", lens), ("mask", mask), ("nodes", nodes),
+            ("out", out), ("workspace", workspace))
+    if workspace is None:
+        n = _tree_workspace(dev, B, T, Hq, Hkv, D, size, width)
+        if n:
+            _check(min(n, 0), where)
+            workspace = _empty(Q, (n,), _torch.uint8, stream)
+    else:
+        n = workspace.numel()
+    if out is None:
+        out = _empty(Q, (B, T, Hq, D), Q.dtype, stream)
+    lse = _empty(Q, (B, T, Hq), _torch.float32, stream) if return_lse else None
+    _launch(where, dev, lib.tq_tree_attention, kind, Q.data_ptr(), qs[0], qs[1], qs[2],
+            k_pages.data_ptr(), v_pages.data_ptr(), P, size, page_stride, row_stride, head_stride,
+            page_table.data_ptr(), width, lens.data_ptr(), _address(nodes), _address(mask),
+            mask_seq, B, T, Hq, Hkv, D, 1.0 / math.sqrt(D) if scale is None else scale, window,
+            out.data_ptr(), _address(lse), _address(workspace), n, _raw_stream(stream, dev))
     return (out, lse) if return_lse else out
 
 

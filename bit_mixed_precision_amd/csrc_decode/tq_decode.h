@@ -50,6 +50,32 @@ struct AttnArgs {
 int64_t attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity);
 hipError_t launch_paged_attention(int dtype, const AttnArgs& a, hipStream_t stream);
 
+// Several new tokens per sequence: the nodes of a drafted tree.
+struct TreeArgs {
+  const void* Q;  // [B][T][Hq][D]
+  int64_t q_seq, q_tok, q_head;
+  const void* k_pages;
+  const void* v_pages;
+  int64_t n_pages, page_size, page_stride, row_stride, head_stride;
+  const int32_t* page_table;  // [B][width]
+  int64_t width;
+  const int32_t* lens;   // [B]: cached tokens before the nodes
+  const int32_t* nodes;  // [B] or nullptr: T
+  const void* mask;      // 64-bit words [B][T][ceil(T / 64)] or nullptr: chains
+  int64_t mask_seq;      // words; 0: one tree for all
+  int64_t B, T, Hq, Hkv, D;
+  float scale_log2;
+  int64_t window;
+  void* Out;   // [B][T][Hq][D]
+  float* lse;  // [B][T][Hq] or nullptr
+  void* workspace;
+};
+int64_t tree_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                             int64_t capacity);
+hipError_t launch_tree_attention(int dtype, const TreeArgs& a, hipStream_t stream);
+hipError_t launch_tree_mask(const int32_t* parents, int64_t B, int64_t T, void* mask,
+                            int32_t* depth, hipStream_t stream);
+
 // Page bookkeeping.  A sequence of `len` tokens holds the first
 // ceil(len / page_size) entries of its row of the page table.
 struct PagesArgs {

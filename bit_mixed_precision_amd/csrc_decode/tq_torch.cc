@@ -31,6 +31,9 @@ struct Entries {
   decltype(&tq_rope_append) rope_append;
   decltype(&tq_paged_attention) paged_attention;
   decltype(&tq_paged_attention_workspace) paged_attention_workspace;
+  decltype(&tq_tree_mask) tree_mask;
+  decltype(&tq_tree_attention) tree_attention;
+  decltype(&tq_tree_attention_workspace) tree_attention_workspace;
   decltype(&tq_pages_workspace) pages_workspace;
   decltype(&tq_pages_fork) pages_fork;
   decltype(&tq_pages_grow) pages_grow;
@@ -85,6 +88,9 @@ bool int32s(const at::Tensor& t, at::IntArrayRef shape, const at::Device& d) {
 // [tokens][heads][D], the numbers of a head adjacent
 bool heads(const at::Tensor& t) { return t.dim() == 3 && (t.stride(2) == 1 || t.size(2) <= 1); }
 
+// [sequences][nodes][heads][D], the numbers of a head adjacent
+bool queries(const at::Tensor& t) { return t.dim() == 4 && (t.stride(3) == 1 || t.size(3) <= 1); }
+
 // cosines and sines [positions][rot / 2][2]
 bool angles(const at::Tensor& t, const at::Device& d) {
   return t.dim() == 3 && t.size(2) == 2 && t.scalar_type() == at::kFloat && t.is_contiguous() &&
@@ -95,9 +101,26 @@ bool matrix(const at::Tensor& t, const at::Device& d) {
   return t.dim() == 2 && t.scalar_type() == at::kInt && t.is_contiguous() && on(t, d);
 }
 
+// int64 words [B][T][ceil(T / 64)] or [T][ceil(T / 64)] of a mask; *seq: words between
+// sequences
+bool mask_of(const at::Tensor& t, int64_t B, int64_t T, const at::Device& d, int64_t* seq) {
+  const int64_t words = (T + 63) / 64, n = t.dim();
+  if (t.scalar_type() != at::kLong || !t.is_contiguous() || !on(t, d) || n < 2 || n > 3 ||
+      t.size(n - 2) != T || t.size(n - 1) != words || (n == 3 && t.size(0) != B && t.size(0) != 1))
+    return false;
+  *seq = n == 3 && t.size(0) > 1 ? T * words : 0;
+  return true;
+}
+
+// A tensor argument or None: false for anything else.
+bool optional(PyObject* o, const at::Tensor** t) {
+  *t = o == Py_None ? nullptr : tensor(o);
+  return o == Py_None || *t;
+}
+
 // the halves of a paged cache [pages][slots][heads][D], as like's type
 bool cache(const at::Tensor& k, const at::Tensor& v, const at::Tensor& like, const at::Device& d) {
-  return k.dim() == 4 && k.size(3) == like.size(2) && (k.stride(3) == 1 || k.size(3) <= 1) &&
+  return k.dim() == 4 && k.size(3) == like.size(-1) && (k.stride(3) == 1 || k.size(3) <= 1) &&
          k.scalar_type() == like.scalar_type() && v.scalar_type() == like.scalar_type() &&
          k.sizes() == v.sizes() && k.strides() == v.strides() && on(k, d) && on(v, d);
 }
@@ -246,6 +269,65 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// (parents)
+PyObject* tree_mask(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const at::Tensor* parents = n == 1 ? tensor(a[0]) : nullptr;
+    if (!parents || !current(*parents) || !matrix(*parents, parents->device())) return none();
+    const int64_t B = parents->size(0), T = parents->size(1);
+    bool ok;
+    void* s = stream_of(parents->device(), &ok);
+    if (!ok) return nullptr;
+    at::Tensor mask = at::empty({B, T, (T + 63) / 64}, parents->options().dtype(at::kLong)),
+               depth = at::empty({B, T}, parents->options());
+    const int st = c.tree_mask(ptr<int32_t>(*parents), B, T, ptr<int64_t>(mask),
+                               ptr<int32_t>(depth), s);
+    return st == TQ_OK ? tuple({mask, depth}) : PyLong_FromLong(st);
+  });
+}
+
+// (Q, k_pages, v_pages, page_table, lens, mask or None, nodes or None, scale or None,
+//  window, return_lse)
+PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const at::Tensor *t[5], *mask, *nodes;
+    if (n != 10 || !tensors(a, {0, 1, 2, 3, 4}, t) || !optional(a[5], &mask) ||
+        !optional(a[6], &nodes) || !PyLong_Check(a[8]) || !(a[7] == Py_None || PyFloat_Check(a[7])))
+      return none();
+    const at::Tensor &q = *t[0], &k = *t[1], &v = *t[2], &pages = *t[3], &lens = *t[4];
+    const int kd = kind(q, false), with_lse = PyObject_IsTrue(a[9]);
+    const at::Device d = q.device();
+    if (kd < 0 || with_lse < 0 || !current(q) || !queries(q) || !matrix(pages, d) ||
+        pages.size(0) != q.size(0) || !int32s(lens, {q.size(0)}, d) || !cache(k, v, q, d) ||
+        (nodes && !int32s(*nodes, {q.size(0)}, d)))
+      return PyErr_Occurred() ? nullptr : none();
+    const int64_t B = q.size(0), T = q.size(1), Hq = q.size(2), D = q.size(3);
+    int64_t mask_seq = 0;
+    if (mask && !mask_of(*mask, B, T, d, &mask_seq)) return none();
+    const double scale = a[7] == Py_None ? 1.0 / std::sqrt((double)D) : PyFloat_AS_DOUBLE(a[7]);
+    const long long window = PyLong_AsLongLong(a[8]);
+    if (window == -1 && PyErr_Occurred()) return nullptr;
+    const int64_t bytes =
+        c.tree_attention_workspace(B, T, Hq, k.size(2), D, k.size(1), pages.size(1));
+    if (bytes < 0) return PyLong_FromLong((long)bytes);
+    bool ok;
+    void* s = stream_of(d, &ok);
+    if (!ok) return nullptr;
+    at::Tensor out = at::empty({B, T, Hq, D}, q.options()), lse, ws;
+    if (with_lse) lse = at::empty({B, T, Hq}, q.options().dtype(at::kFloat));
+    if (bytes > 0) ws = at::empty({bytes}, q.options().dtype(at::kByte));
+    const int st = c.tree_attention(
+        kd, q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), k.data_ptr(), v.data_ptr(),
+        k.size(0), k.size(1), k.stride(0), k.stride(1), k.stride(2), ptr<int32_t>(pages),
+        pages.size(1), ptr<int32_t>(lens), nodes ? ptr<int32_t>(*nodes) : nullptr,
+        mask ? ptr<int64_t>(*mask) : nullptr, mask_seq, B, T, Hq, k.size(2), D, scale, window,
+        out.data_ptr(), with_lse ? ptr<float>(lse) : nullptr, bytes > 0 ? ws.data_ptr() : nullptr,
+        bytes, s);
+    if (st != TQ_OK) return PyLong_FromLong(st);
+    return with_lse ? tuple({out, lse}) : THPVariable_Wrap(out);
+  });
+}
+
 // (pool, page_table, lens, parent, page_size)
 PyObject* pages_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
@@ -358,6 +440,8 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!take("tq_rope", &e.rope) || !take("tq_rope_append", &e.rope_append) ||
       !take("tq_paged_attention", &e.paged_attention) ||
       !take("tq_paged_attention_workspace", &e.paged_attention_workspace) ||
+      !take("tq_tree_mask", &e.tree_mask) || !take("tq_tree_attention", &e.tree_attention) ||
+      !take("tq_tree_attention_workspace", &e.tree_attention_workspace) ||
       !take("tq_pages_workspace", &e.pages_workspace) || !take("tq_pages_fork", &e.pages_fork) ||
       !take("tq_pages_grow", &e.pages_grow) || !take("tq_pages_compact", &e.pages_compact))
     return nullptr;
@@ -372,6 +456,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   { #name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr }
 PyMethodDef methods[] = {TQ_METHOD(bind),          TQ_METHOD(rope),
                          TQ_METHOD(rope_append),   TQ_METHOD(paged_attention),
+                         TQ_METHOD(tree_mask),     TQ_METHOD(tree_attention),
                          TQ_METHOD(pages_fork),    TQ_METHOD(pages_grow),
                          TQ_METHOD(pages_compact), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tq_torch",

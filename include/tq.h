@@ -470,6 +470,55 @@ int tq_paged_attention(int dtype, const void* Q, int64_t q_tok, int64_t q_head,
 int64_t tq_paged_attention_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
                                      int64_t page_size, int64_t width);
 
+/* The paths of drafted trees: parents int32 [B][T], node i hanging on node parents[i]
+ * < i of its tree, or on the last cached token where parents[i] is anything else.  mask: 64-bit
+ * words [B][T][ceil(T / 64)]; bit j % 64 of word j / 64 of node i is set where j is i
+ * or a node above it, all other bits are clear.  depth int32 [B][T] or NULL: the number
+ * of nodes above i, which with the sequence's length is the node's position.
+ * All device pointers.  T <= 256, B <= 2^20; B = 0 or T = 0 is a no-op.  Errors:
+ * TQ_ERR_NULL, TQ_ERR_SHAPE, TQ_ERR_ALIGN (mask to 8 bytes), TQ_ERR_DEVICE. */
+int tq_tree_mask(const int32_t* parents, int64_t B, int64_t T, int64_t* mask, int32_t* depth,
+                 void* stream);
+
+/* Attention of several new tokens per sequence over the paged cache: sequence b has
+ * lens[b] cached tokens (negative counts as 0) and the first nodes[b] of T nodes
+ * (NULL: all; below 0 none), whose keys and values lie in the slots lens[b],
+ * lens[b] + 1, ... after them.
+ *   out[b][i][h] = sum_t w_t v[t][h / G],  w = softmax_t(scale q[b][i][h] . k[t][h / G])
+ * over the cached tokens and the tokens lens[b] + j of the nodes j < nodes[b] whose bit
+ * is set for node i in mask (words as tq_tree_mask writes them, sequence b's at mask +
+ * mask_seq b, mask_seq = 0: one tree for all; any bits will do, also none; NULL: a
+ * chain, j <= i).  With a window (0: none, otherwise at least T) a node that sees s
+ * nodes sees only the last window - s cached tokens.  At most width * page_size tokens
+ * are read, and an absent page's tokens are left out, as by tq_paged_attention.
+ * Rows of nodes that are not there, and of nodes that see no token, are zeros with
+ * lse = -inf.  Q: number d of head h of node i of sequence b at q_seq b + q_tok i +
+ * q_head h + d; Out [B][T][Hq][D]; lse fp32 [B][T][Hq] or NULL.
+ * fp16 or bfloat16 in and out, fp32 scores, weights and sums.  Up to 32 rows (T G <= 32) a
+ * weight enters the product with v as two 16-bit numbers, as in tq_paged_attention; with
+ * more rows as one, rounded to nearest (2^-11 of itself in fp16, 2^-8 in bfloat16, and
+ * in fp16 within 2^-38 of the row's largest).  A token that a node does not see has no
+ * influence on it, whatever its key and value hold.  The same bits on every run.
+ * Outputs and workspace must not overlap the inputs.
+ * Limits as tq_paged_attention's, and T <= 256; B * Hkv * ceil(T G / 32) * (width *
+ * page_size / 64 + 2) < 2^31.  workspace: tq_tree_attention_workspace(...) bytes,
+ * 16-byte aligned, contents irrelevant; calls that overlap on one workspace race.
+ * Errors: as tq_paged_attention's; TQ_ERR_SHAPE for a window below T.  B = 0 or T = 0
+ * is a no-op. */
+int tq_tree_attention(int dtype, const void* Q, int64_t q_seq, int64_t q_tok, int64_t q_head,
+                      const void* k_pages, const void* v_pages, int64_t n_pages,
+                      int64_t page_size, int64_t page_stride, int64_t row_stride,
+                      int64_t head_stride, const int32_t* page_table, int64_t width,
+                      const int32_t* lens, const int32_t* nodes, const int64_t* mask,
+                      int64_t mask_seq, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                      double scale, int64_t window, void* Out, float* lse, void* workspace,
+                      int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of tq_tree_attention for tables of `width` pages; TQ_ERR_SHAPE for
+ * shapes it refuses. */
+int64_t tq_tree_attention_workspace(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                                    int64_t page_size, int64_t width);
+
 /* The pages of a cache.  The page table and the lengths are the whole state: a
  * page is free when no row holds it, and a page held by several rows is shared.
  * The functions read one state and write another, so a step can be repeated and

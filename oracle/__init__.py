@@ -33,3 +33,11 @@ from .decode_oracle import (  # noqa: F401,E402
     pages_grow_ref,
     pages_compact_ref,
 )
+from .tree_oracle import (  # noqa: F401,E402
+    tree_paths_ref,
+    mask_words_ref,
+    tree_attention_ref,
+    cache_weights_ref,
+    cache_select_ref,
+    pages_keep_ref,
+)
