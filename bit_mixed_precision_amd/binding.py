@@ -93,6 +93,17 @@ SIGNATURES = {
                                _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _D, _I64, _P,
                                _P, _P, _I64, _P]),
     "tq_tree_attention_workspace": (_I64, [_I64, _I64, _I64, _I64, _I64, _I64, _I64]),
+    "tq_rope_append_at": (_I, [_I, _P, _I64, _P, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _P, _P,
+                               _I64, _I64, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I, _P]),
+    "tq_cache_weights": (_I, [_I, _P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I64, _P, _I64,
+                              _P, _P, _P, _I64, _P, _I64, _I64, _I64, _I64, _I64, _D, _I64, _D, _P,
+                              _I64, _I64, _I64, _P]),
+    "tq_cache_select": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I64, _P, _P, _P,
+                             _P, _I64, _P]),
+    "tq_cache_select_workspace": (_I64, [_I64, _I64, _I64]),
+    "tq_pages_keep": (_I, [_P, _I64, _I64, _I64, _P, _P, _I64, _I64, _I64, _P, _I64, _I64, _I64,
+                           _P, _P, _P, _P, _P, _P, _I64, _P]),
+    "tq_pages_keep_workspace": (_I64, [_I64, _I64, _I64]),
     "tq_pages_fork": (_I, [_P, _I64, _I64, _I64, _P, _P, _I64, _P, _I64, _I64, _I64, _P, _P, _P,
                            _P, _P, _I64, _P]),
     "tq_pages_grow": (_I, [_P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _P]),
@@ -122,8 +133,9 @@ def _compiled_calls():
                       "made from Python; build it with "
                       "`python -m bit_mixed_precision_amd.build_lib`", RuntimeWarning, stacklevel=3)
         return types.SimpleNamespace(**{n: lambda *a: None for n in (
-            "rope", "rope_append", "paged_attention", "tree_mask", "tree_attention", "pages_fork",
-            "pages_grow", "pages_compact")})
+            "rope", "rope_append", "paged_attention", "tree_mask", "tree_attention",
+            "cache_weights", "cache_select", "pages_fork", "pages_grow", "pages_compact",
+            "pages_keep")})
     fast.bind(getattr(_torch._C, "_cuda_getCurrentRawStream", lambda index: 0),
               {n: C.cast(getattr(lib, n), C.c_void_p).value for n in SIGNATURES})
     return fast
@@ -780,15 +792,15 @@ def tq_rope(X, table, positions, interleaved: bool = False, inverse: bool = Fals
 
 
 def tq_rope_append(QKV, table, positions, page_table, k_pages, v_pages, interleaved: bool = False,
-                   seqs=None, Q=None, stream=None):
+                   seqs=None, Q=None, stream=None, slots=None):
     """Rotate the query and key heads of QKV [T][Hq + 2 Hkv][D], write the keys and
-    values of token t into slot positions[t] of row seqs[t] (t when None) of the
-    paged cache, and return the queries [T][Hq][D].  k_pages, v_pages:
+    values of token t into slot slots[t] (positions[t] when None) of row seqs[t] (t when
+    None) of the paged cache, and return the queries [T][Hq][D].  k_pages, v_pages:
     [pages][slots][Hkv][D], any strides, numbers of a head adjacent."""
     where = "tq_rope_append"
     if Q is None and stream is None:
         r = _fast.rope_append(QKV, table, positions, page_table, k_pages, v_pages, interleaved,
-                              seqs)
+                              seqs, slots)
         if r is not None:
             return _done(r, where)
     kind = _kind(QKV, "QKV", where)
@@ -801,6 +813,8 @@ def tq_rope_append(QKV, table, positions, page_table, k_pages, v_pages, interlea
     n_seqs, width = _rows(page_table, "page_table", where)
     if seqs is not None:
         _int32(seqs, "seqs", (T,), where)
+    if slots is not None:
+        _int32(slots, "slots", (T,), where)
     P, size, Hkv, page_stride, row_stride, head_stride = _cache(k_pages, v_pages, QKV, D, where)
     Hq = H - 2 * Hkv
     if Hq < 1:
@@ -811,14 +825,15 @@ def tq_rope_append(QKV, table, positions, page_table, k_pages, v_pages, interlea
     if dev < 0 or not (table.get_device() == positions.get_device() == page_table.get_device()
                        == k_pages.get_device() == v_pages.get_device() == dev) or (
             seqs is not None and seqs.get_device() != dev) or (
+            slots is not None and slots.get_device() != dev) or (
             Q is not None and Q.get_device() != dev):
         _on_gpu(where, ("QKV", QKV), ("table", table), ("positions", positions),
-                ("page_table", page_table), ("seqs", seqs), ("k_pages", k_pages),
-                ("v_pages", v_pages), ("Q", Q))
+                ("page_table", page_table), ("seqs", seqs), ("slots", slots),
+                ("k_pages", k_pages), ("v_pages", v_pages), ("Q", Q))
     if Q is None:
         Q = _empty(QKV, (T, Hq, D), QKV.dtype, stream)
-    _launch(where, dev, lib.tq_rope_append, kind, QKV.data_ptr(), xs[0], table.data_ptr(), n_pos,
-            rot, positions.data_ptr(), None if seqs is None else seqs.data_ptr(),
+    _launch(where, dev, lib.tq_rope_append_at, kind, QKV.data_ptr(), xs[0], table.data_ptr(), n_pos,
+            rot, positions.data_ptr(), _address(slots), _address(seqs),
             page_table.data_ptr(), n_seqs, width, k_pages.data_ptr(), v_pages.data_ptr(), P, size,
             page_stride, row_stride, head_stride, Q.data_ptr(), T, Hq, Hkv, D, interleaved,
             _raw_stream(stream, dev))
@@ -1000,6 +1015,98 @@ def tq_tree_attention(Q, k_pages, v_pages, page_table, lens, mask=None, nodes=No
     return (out, lse) if return_lse else out
 
 
+def tq_cache_weights(Q, k_pages, page_table, lens, lse, scores, mask=None, nodes=None,
+                     scale: float | None = None, window: int = 0, decay: float = 1.0, stream=None):
+    """Add to scores float32 [B][Hkv][S] the attention weight that the nodes Q
+    [B][T][Hq][D] give to every token of the paged cache, after multiplying the sums of
+    the lens[b] cached tokens by decay; the nodes' own tokens begin anew.  Arguments as
+    tq_tree_attention's, whose lse [B][T][Hq] this takes; a row with lse = -inf adds
+    nothing.  In place; returns scores."""
+    where = "tq_cache_weights"
+    if stream is None:
+        r = _fast.cache_weights(Q, k_pages, page_table, lens, lse, scores, mask, nodes, scale,
+                                window, decay)
+        if r is not None:
+            return _done(r, where)
+    kind = _kind(Q, "Q", where)
+    (B, T, Hq, D), qs = _nodes(Q, where)
+    P, size, Hkv, page_stride, row_stride, head_stride = _cache(k_pages, k_pages, Q, D, where)
+    rows, width = _rows(page_table, "page_table", where)
+    if rows != B:
+        raise TQError(TQ_ERR_SHAPE, f"{where}: page_table has {rows} rows, Q {B}")
+    _int32(lens, "lens", (B,), where)
+    if nodes is not None:
+        _int32(nodes, "nodes", (B,), where)
+    mask_seq = 0 if mask is None else _mask(mask, B, T, where)
+    _need(lse, "lse", "f32", (B, T, Hq), where)
+    S, s_seq, s_head = _sums(scores, B, Hkv, where)
+    dev = Q.get_device()
+    _all_on(where, dev, ("Q", Q), ("k_pages", k_pages), ("page_table", page_table), ("lens", lens),
+            ("lse", lse), ("scores", scores), ("mask", mask), ("nodes", nodes))
+    _launch(where, dev, lib.tq_cache_weights, kind, Q.data_ptr(), qs[0], qs[1], qs[2],
+            k_pages.data_ptr(), P, size, page_stride, row_stride, head_stride,
+            page_table.data_ptr(), width, lens.data_ptr(), _address(nodes), _address(mask),
+            mask_seq, lse.data_ptr(), B, T, Hq, Hkv, D,
+            1.0 / math.sqrt(D) if scale is None else scale, window, decay, scores.data_ptr(),
+            s_seq, s_head, S, _raw_stream(stream, dev))
+    return scores
+
+
+def _sums(scores, B, H, where):
+    """(S, stride of a sequence, of a head) of scores [B][H][S], numbers adjacent; B and H
+    None: as they are."""
+    if not isinstance(scores, _torch.Tensor) or scores.dtype is not _torch.float32:
+        raise TQError(TQ_ERR_VALUE, f"{where}: scores must be a float32 tensor")
+    shape, strides = tuple(scores.shape), scores.stride()
+    if len(shape) != 3 or (B is not None and shape[:2] != (B, H)) or (
+            shape[2] > 1 and strides[2] != 1):
+        raise TQError(TQ_ERR_SHAPE, f"{where}: scores must be [sequences][heads][tokens] with "
+                                    f"adjacent numbers, not {shape} at strides {strides}")
+    return shape[2], strides[0], strides[1]
+
+
+def tq_cache_select_workspace(B: int, H: int, S: int) -> int:
+    """Workspace bytes of tq_cache_select on the current GPU."""
+    n = int(lib.tq_cache_select_workspace(B, H, S))
+    _check(min(n, 0), "tq_cache_select_workspace")
+    return n
+
+
+@functools.lru_cache(maxsize=256)
+def _select_workspace(dev, *shape):
+    with _torch.cuda.device(dev):
+        return lib.tq_cache_select_workspace(*shape)
+
+
+def tq_cache_select(scores, lens, budget: int, recent: int = 0, sinks: int = 0, stream=None):
+    """Which of the lens[b] tokens of every sequence and head stay within `budget`: the first
+    `sinks`, the last `recent`, and of the others those of the largest scores float32
+    [B][H][S] (equal ones by the lowest index).  Returns (keep, counts, sums): int32
+    [B][H][budget] ascending indexes, then -1; int32 [B] how many; float32
+    [B][H][budget] their scores, then 0.  For tq_pages_keep."""
+    where = "tq_cache_select"
+    if stream is None:
+        r = _fast.cache_select(scores, lens, budget, recent, sinks)
+        if r is not None:
+            return _done(r, where)
+    S, s_seq, s_head = _sums(scores, None, None, where)
+    B, H = scores.shape[:2]
+    _int32(lens, "lens", (B,), where)
+    dev = scores.get_device()
+    _all_on(where, dev, ("scores", scores), ("lens", lens))
+    n = _select_workspace(dev, B, H, S)
+    _check(min(n, 0), where)
+    if budget < 0 or budget > 1 << 30:
+        raise TQError(TQ_ERR_SHAPE, f"{where}: a budget of {budget}")
+    workspace = _empty(scores, (n,), _torch.uint8, stream) if n else None
+    keep, counts = _empty(scores, (B, H, budget), _I32T, stream), _empty(scores, (B,), _I32T, stream)
+    sums = _empty(scores, (B, H, budget), _torch.float32, stream)
+    _launch(where, dev, lib.tq_cache_select, scores.data_ptr(), s_seq, s_head, S, lens.data_ptr(),
+            B, H, budget, recent, sinks, keep.data_ptr(), counts.data_ptr(), sums.data_ptr(),
+            _address(workspace), n, _raw_stream(stream, dev))
+    return keep, counts, sums
+
+
 def _pool(pool, where):
     """(planes, n_pages, bytes of a page) of a contiguous pool [planes][pages]..."""
     if not isinstance(pool, _torch.Tensor) or pool.dim() < 3 or not pool.is_contiguous():
@@ -1094,6 +1201,51 @@ def tq_pages_compact(pool, page_table, lens, page_size: int, stream=None):
             page_table.data_ptr(), lens.data_ptr(), rows, width, page_size, table_out.data_ptr(),
             used.data_ptr(), ws.data_ptr(), n, _raw_stream(stream, dev))
     return table_out.view(rows, width), used
+
+
+@functools.lru_cache(maxsize=256)
+def tq_pages_keep_workspace(rows: int, width: int, n_pages: int) -> int:
+    """Workspace bytes of tq_pages_keep."""
+    n = int(lib.tq_pages_keep_workspace(rows, width, n_pages))
+    _check(min(n, 0), "tq_pages_keep_workspace")
+    return n
+
+
+def tq_pages_keep(pool, page_table, lens, keep, counts, page_size: int, base=None, stream=None):
+    """Move the tokens that stay together: row r keeps its first base[r] tokens (0 when
+    None) and then the counts[r] tokens that keep lists in ascending order, int32 [rows][n],
+    [rows][heads][n] (each head its own) or [groups][rows][heads][n] (each run of
+    planes / groups planes of the pool [planes][pages][page_size][heads].. too); pages past
+    the last token are released, and pages that other rows hold too are replaced by free
+    ones before they are written.  Returns (page_table, lens, short): the new state and how
+    many rows found too few free pages and stay as they are."""
+    where = "tq_pages_keep"
+    if stream is None:
+        r = _fast.pages_keep(pool, page_table, lens, keep, counts, page_size, base)
+        if r is not None:
+            return _done(r, where)
+    planes, P, size = _pool(pool, where)
+    rows, width = _state(page_table, lens, where)
+    if not isinstance(keep, _torch.Tensor) or not 2 <= keep.dim() <= 4:
+        raise TQError(TQ_ERR_SHAPE, f"{where}: keep must be a tensor of 2 to 4 dimensions")
+    shape = tuple(keep.shape)
+    groups = shape[0] if len(shape) == 4 else 1
+    heads = shape[-2] if len(shape) > 2 else 1
+    _int32(keep, "keep", {2: (rows, shape[-1]), 3: (rows, heads, shape[-1]),
+                          4: (groups, rows, heads, shape[-1])}[len(shape)], where)
+    _int32(counts, "counts", (rows,), where)
+    if base is not None:
+        _int32(base, "base", (rows,), where)
+    dev = pool.get_device()
+    _all_on(where, dev, ("pool", pool), ("page_table", page_table), ("lens", lens), ("keep", keep),
+            ("counts", counts), ("base", base))
+    n = tq_pages_keep_workspace(rows, width, P)
+    ws, table_out, lens_out, short = _pieces(lens, (n // 4, rows * width, rows, 1), stream)
+    _launch(where, dev, lib.tq_pages_keep, pool.data_ptr(), planes, P, size, page_table.data_ptr(),
+            lens.data_ptr(), rows, width, page_size, keep.data_ptr(), groups, heads, shape[-1],
+            counts.data_ptr(), _address(base), table_out.data_ptr(), lens_out.data_ptr(),
+            short.data_ptr(), ws.data_ptr(), n, _raw_stream(stream, dev))
+    return table_out.view(rows, width), lens_out, short
 
 
 def tq_pages_copy(pool, src, dst, stream=None):

@@ -28,6 +28,7 @@ struct RopeArgs {
   const int32_t* page_table;  // [n_seqs][width]
   int64_t width, n_seqs;
   const int32_t* seqs;  // [T] or nullptr: token t belongs to sequence t
+  const int32_t* places;  // [T] or nullptr: a token's slot is its position
 };
 hipError_t launch_rope(int dtype, const RopeArgs& a, hipStream_t stream);
 
@@ -76,6 +77,29 @@ hipError_t launch_tree_attention(int dtype, const TreeArgs& a, hipStream_t strea
 hipError_t launch_tree_mask(const int32_t* parents, int64_t B, int64_t T, void* mask,
                             int32_t* depth, hipStream_t stream);
 
+// What the cached tokens receive of it.
+struct WeightsArgs {
+  TreeArgs tree;  // without v_pages, Out, lse and workspace
+  const float* lse;  // [B][T][Hq]
+  float* scores;     // [B][Hkv][S]
+  int64_t s_seq, s_head, S;
+  float decay;
+};
+hipError_t launch_cache_weights(int dtype, const WeightsArgs& a, hipStream_t stream);
+
+struct SelectArgs {
+  const float* scores;  // [B][H][S]
+  int64_t s_seq, s_head, S;
+  const int32_t* lens;  // [B]
+  int64_t B, H, budget, recent, sinks;
+  int32_t* keep;    // [B][H][budget]
+  int32_t* counts;  // [B]
+  float* sums;      // [B][H][budget] or nullptr
+  void* workspace;
+};
+int64_t select_workspace_bytes(int64_t B, int64_t H, int64_t S);
+hipError_t launch_cache_select(const SelectArgs& a, hipStream_t stream);
+
 // Page bookkeeping.  A sequence of `len` tokens holds the first
 // ceil(len / page_size) entries of its row of the page table.
 struct PagesArgs {
@@ -93,6 +117,17 @@ struct PagesArgs {
   void* workspace;
 };
 int64_t pages_workspace_bytes(int64_t rows, int64_t n_pages);
+
+// Tokens that stay, moved together.
+struct KeepArgs {
+  PagesArgs pages;      // without parent, add and refs
+  const int32_t* keep;  // [groups][rows][heads][n]
+  int64_t groups, heads, n;
+  const int32_t* counts;  // [rows]
+  const int32_t* base;    // [rows] or nullptr: 0
+};
+int64_t keep_workspace_bytes(int64_t rows, int64_t width, int64_t n_pages);
+hipError_t launch_pages_keep(const KeepArgs& a, hipStream_t stream);
 hipError_t launch_pages_fork(const PagesArgs& a, hipStream_t stream);
 hipError_t launch_pages_grow(const PagesArgs& a, hipStream_t stream);
 hipError_t launch_pages_compact(const PagesArgs& a, hipStream_t stream);

@@ -55,15 +55,17 @@ int tq_rope(int dtype, const void* X, int64_t x_tok, int64_t x_head, void* Y, in
   return finish(tq::launch_rope(dtype, a, static_cast<hipStream_t>(stream)));
 }
 
-int tq_rope_append(int dtype, const void* QKV, int64_t qkv_tok, const float* table, int64_t n_pos,
-                   int64_t rot, const int32_t* pos, const int32_t* seqs, const int32_t* page_table,
-                   int64_t n_seqs, int64_t width, void* k_pages, void* v_pages, int64_t n_pages,
-                   int64_t page_size, int64_t page_stride, int64_t row_stride,
-                   int64_t head_stride, void* Q, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
-                   int interleaved, void* stream) {
+int tq_rope_append_at(int dtype, const void* QKV, int64_t qkv_tok, const float* table,
+                      int64_t n_pos, int64_t rot, const int32_t* pos, const int32_t* slots,
+                      const int32_t* seqs, const int32_t* page_table, int64_t n_seqs,
+                      int64_t width, void* k_pages, void* v_pages, int64_t n_pages,
+                      int64_t page_size, int64_t page_stride, int64_t row_stride,
+                      int64_t head_stride, void* Q, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                      int interleaved, void* stream) {
   if (T < 0) return TQ_ERR_SHAPE;
   if (T == 0) return TQ_OK;
-  if (!QKV || (!table && n_pos != 0) || !pos || !page_table || !k_pages || !v_pages || !Q) return TQ_ERR_NULL;
+  if (!QKV || (!table && n_pos != 0) || !pos || !page_table || !k_pages || !v_pages || !Q)
+    return TQ_ERR_NULL;
   if (Hq < 1 || Hkv < 1 || Hq > kMaxHeads || Hkv > kMaxHeads) return TQ_ERR_SHAPE;
   int st = rope_shapes(n_pos, rot, T, Hq + 2 * Hkv, D);
   if (st != TQ_OK) return st;
@@ -79,7 +81,7 @@ int tq_rope_append(int dtype, const void* QKV, int64_t qkv_tok, const float* tab
       !distinct_cache(n_pages, page_stride, page_size, row_stride, Hkv, head_stride, D))
     return TQ_ERR_SHAPE;
   if (!aligned(QKV, 2) || !aligned(Q, 2) || !aligned(k_pages, 2) || !aligned(v_pages, 2) ||
-      !aligned(table, 8) || !aligned(pos, 4) || !aligned(seqs, 4) || !aligned(page_table, 4))
+      !aligned(table, 8) || !aligned(pos, 4) || !aligned(seqs, 4) || !aligned(slots, 4) || !aligned(page_table, 4))
     return TQ_ERR_ALIGN;
   if ((dtype != TQ_F16 && dtype != TQ_BF16) || (interleaved & ~1)) return TQ_ERR_VALUE;
   st = device_ready();
@@ -112,7 +114,19 @@ int tq_rope_append(int dtype, const void* QKV, int64_t qkv_tok, const float* tab
   a.width = width;
   a.n_seqs = n_seqs;
   a.seqs = seqs;
+  a.places = slots;
   return finish(tq::launch_rope(dtype, a, static_cast<hipStream_t>(stream)));
+}
+
+int tq_rope_append(int dtype, const void* QKV, int64_t qkv_tok, const float* table, int64_t n_pos,
+                   int64_t rot, const int32_t* pos, const int32_t* seqs, const int32_t* page_table,
+                   int64_t n_seqs, int64_t width, void* k_pages, void* v_pages, int64_t n_pages,
+                   int64_t page_size, int64_t page_stride, int64_t row_stride,
+                   int64_t head_stride, void* Q, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                   int interleaved, void* stream) {
+  return tq_rope_append_at(dtype, QKV, qkv_tok, table, n_pos, rot, pos, nullptr, seqs, page_table,
+                           n_seqs, width, k_pages, v_pages, n_pages, page_size, page_stride,
+                           row_stride, head_stride, Q, T, Hq, Hkv, D, interleaved, stream);
 }
 
 int64_t tq_paged_attention_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D,

@@ -21,6 +21,7 @@
 #include "tq_common.h"
 #include "tq_decode.h"
 #include "tq_kernels.h"
+#include "tq_scan.h"
 
 namespace tq {
 namespace {
@@ -28,7 +29,6 @@ namespace {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kPagesThreads = 256;
-constexpr int kScanThreads = 1024;
 
 struct PagesParams {
   unsigned char* pool;
@@ -132,30 +132,6 @@ __global__ __launch_bounds__(kPagesThreads) void pages_rows_kernel(PagesParams p
     }
     if constexpr (OP != kCompact) out[i] = id;
   }
-}
-
-// Exclusive prefix sum over the workgroup and its total.
-template <class T>
-__device__ __forceinline__ T scan_block(T v, T* red, T& total) {
-  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
-  T inc = v;
-#pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) {
-    const T o = __shfl_up(inc, off, kWave);
-    inc += lane >= off ? o : T(0);
-  }
-  __syncthreads();  // red of the previous call has been read
-  if (lane == 63) red[w] = inc;
-  __syncthreads();
-  T before = inc - v;
-  total = 0;
-#pragma unroll
-  for (int i = 0; i < kScanThreads / kWave; ++i) {
-    const T r = red[i];
-    before += i < w ? r : T(0);
-    total += r;
-  }
-  return before;
 }
 
 __device__ __forceinline__ uint32_t valid_bits(const PagesParams& p, int word) {

@@ -68,6 +68,7 @@ struct RopeParams {
   uint32_t n_pages, width, n_seqs;
   const int32_t* page_table;
   const int32_t* seqs;
+  const int32_t* places;  // [T] or nullptr: the token's slot is its position
 };
 
 // V numbers moved as one access (two or more of 16 bytes where they are longer).
@@ -108,10 +109,12 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeParams p) {
   int64_t slot_at = -1;  // appending: where the token's slot is in the cache
   if constexpr (APPEND) {
     const uint32_t seq = p.seqs ? (uint32_t)p.seqs[tok] : tok;
-    const uint32_t pg = p.page.quot(known ? pos : 0);
-    if (known && seq < p.n_seqs && pg < p.width) {
+    const uint32_t place = p.places ? (uint32_t)p.places[tok] : pos;
+    const bool placed = known && place <= (uint32_t)INT32_MAX;
+    const uint32_t pg = p.page.quot(placed ? place : 0);
+    if (placed && seq < p.n_seqs && pg < p.width) {
       const uint32_t id = (uint32_t)p.page_table[(int64_t)seq * p.width + pg];
-      if (id < p.n_pages) slot_at = id * p.page_stride + (pos - pg * p.page.d) * p.row_stride;
+      if (id < p.n_pages) slot_at = id * p.page_stride + (place - pg * p.page.d) * p.row_stride;
     }
   }
   // more units than threads: a thread takes every 256th
@@ -285,6 +288,7 @@ hipError_t launch_rope(int dtype, const RopeArgs& a, hipStream_t stream) {
     p.n_seqs = (uint32_t)a.n_seqs;
     p.page_table = a.page_table;
     p.seqs = a.seqs;
+    p.places = a.places;
   }
   const bool inter = a.interleaved, inv = a.inverse;
   if (dtype == TQ_F32)

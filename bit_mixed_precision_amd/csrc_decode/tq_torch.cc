@@ -28,7 +28,7 @@ namespace {
 
 struct Entries {
   decltype(&tq_rope) rope;
-  decltype(&tq_rope_append) rope_append;
+  decltype(&tq_rope_append_at) rope_append;
   decltype(&tq_paged_attention) paged_attention;
   decltype(&tq_paged_attention_workspace) paged_attention_workspace;
   decltype(&tq_tree_mask) tree_mask;
@@ -38,6 +38,11 @@ struct Entries {
   decltype(&tq_pages_fork) pages_fork;
   decltype(&tq_pages_grow) pages_grow;
   decltype(&tq_pages_compact) pages_compact;
+  decltype(&tq_cache_weights) cache_weights;
+  decltype(&tq_cache_select) cache_select;
+  decltype(&tq_cache_select_workspace) cache_select_workspace;
+  decltype(&tq_pages_keep) pages_keep;
+  decltype(&tq_pages_keep_workspace) pages_keep_workspace;
 };
 Entries c{};
 PyObject* raw_stream = nullptr;  // device index -> HIP stream as an int
@@ -204,19 +209,22 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (QKV, table, positions, page_table, k_pages, v_pages, interleaved, seqs or None)
+// (QKV, table, positions, page_table, k_pages, v_pages, interleaved, seqs or None, slots or
+//  None)
 PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    const at::Tensor* t[6];
-    if (n != 8 || !tensors(a, {0, 1, 2, 3, 4, 5}, t)) return none();
+    const at::Tensor *t[6], *seqs, *slots;
+    if (n != 9 || !tensors(a, {0, 1, 2, 3, 4, 5}, t) || !optional(a[7], &seqs) ||
+        !optional(a[8], &slots))
+      return none();
     const at::Tensor &x = *t[0], &table = *t[1], &pos = *t[2], &pages = *t[3], &k = *t[4],
                      &v = *t[5];
-    const at::Tensor* seqs = a[7] == Py_None ? nullptr : tensor(a[7]);
     const int kd = kind(x, false), inter = flag(a[6]);
     const at::Device d = x.device();
-    if (kd < 0 || inter < 0 || (a[7] != Py_None && !seqs) || !current(x) || !heads(x) ||
+    if (kd < 0 || inter < 0 || !current(x) || !heads(x) ||
         (x.size(1) > 1 && x.stride(1) != x.size(2)) || !angles(table, d) || !matrix(pages, d) ||
         !int32s(pos, {x.size(0)}, d) || (seqs && !int32s(*seqs, {x.size(0)}, d)) ||
+        (slots && !int32s(*slots, {x.size(0)}, d)) ||
         !cache(k, v, x, d))
       return none();
     const int64_t T = x.size(0), D = x.size(2), Hkv = k.size(2), Hq = x.size(1) - 2 * Hkv;
@@ -227,8 +235,8 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor q = at::empty({T, Hq, D}, x.options());
     const int st = c.rope_append(
         kd, x.data_ptr(), x.stride(0), ptr<float>(table), table.size(0), 2 * table.size(1),
-        ptr<int32_t>(pos), seqs ? ptr<int32_t>(*seqs) : nullptr, ptr<int32_t>(pages),
-        pages.size(0), pages.size(1), k.data_ptr(), v.data_ptr(), k.size(0), k.size(1),
+        ptr<int32_t>(pos), slots ? ptr<int32_t>(*slots) : nullptr,
+        seqs ? ptr<int32_t>(*seqs) : nullptr, ptr<int32_t>(pages), pages.size(0), pages.size(1), k.data_ptr(), v.data_ptr(), k.size(0), k.size(1),
         k.stride(0), k.stride(1), k.stride(2), q.data_ptr(), T, Hq, Hkv, D, inter, s);
     return st == TQ_OK ? THPVariable_Wrap(q) : PyLong_FromLong(st);
   });
@@ -419,6 +427,124 @@ PyObject* pages_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// sums [sequences][heads][tokens], the numbers of a head adjacent
+bool sums_of(const at::Tensor& t, const at::Device& d) {
+  return t.dim() == 3 && t.scalar_type() == at::kFloat && (t.stride(2) == 1 || t.size(2) <= 1) &&
+         on(t, d);
+}
+
+// (Q, k_pages, page_table, lens, lse, scores, mask or None, nodes or None, scale or None,
+//  window, decay)
+PyObject* cache_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const at::Tensor *t[6], *mask, *nodes;
+    if (n != 11 || !tensors(a, {0, 1, 2, 3, 4, 5}, t) || !optional(a[6], &mask) ||
+        !optional(a[7], &nodes) || !(a[8] == Py_None || PyFloat_Check(a[8])) ||
+        !PyLong_Check(a[9]) || !PyFloat_Check(a[10]))
+      return none();
+    const at::Tensor &q = *t[0], &k = *t[1], &pages = *t[2], &lens = *t[3], &lse = *t[4],
+                     &scores = *t[5];
+    const int kd = kind(q, false);
+    const at::Device d = q.device();
+    if (kd < 0 || !current(q) || !queries(q) || !matrix(pages, d) || pages.size(0) != q.size(0) ||
+        !int32s(lens, {q.size(0)}, d) || !cache(k, k, q, d) ||
+        (nodes && !int32s(*nodes, {q.size(0)}, d)) || !sums_of(scores, d) ||
+        scores.size(0) != q.size(0) || scores.size(1) != k.size(2) ||
+        lse.scalar_type() != at::kFloat || !lse.is_contiguous() || !on(lse, d) ||
+        lse.sizes() != q.sizes().slice(0, 3))
+      return none();
+    const int64_t B = q.size(0), T = q.size(1), Hq = q.size(2), D = q.size(3);
+    int64_t mask_seq = 0;
+    if (mask && !mask_of(*mask, B, T, d, &mask_seq)) return none();
+    const double scale = a[8] == Py_None ? 1.0 / std::sqrt((double)D) : PyFloat_AS_DOUBLE(a[8]);
+    const long long window = PyLong_AsLongLong(a[9]);
+    if (window == -1 && PyErr_Occurred()) return nullptr;
+    bool ok;
+    void* s = stream_of(d, &ok);
+    if (!ok) return nullptr;
+    const int st = c.cache_weights(
+        kd, q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), k.data_ptr(), k.size(0),
+        k.size(1), k.stride(0), k.stride(1), k.stride(2), ptr<int32_t>(pages), pages.size(1),
+        ptr<int32_t>(lens), nodes ? ptr<int32_t>(*nodes) : nullptr,
+        mask ? ptr<int64_t>(*mask) : nullptr, mask_seq, ptr<float>(lse), B, T, Hq, k.size(2), D,
+        scale, window, PyFloat_AS_DOUBLE(a[10]), ptr<float>(scores), scores.stride(0),
+        scores.stride(1), scores.size(2), s);
+    if (st != TQ_OK) return PyLong_FromLong(st);
+    Py_INCREF(a[5]);
+    return a[5];
+  });
+}
+
+// (scores, lens, budget, recent, sinks)
+PyObject* cache_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const at::Tensor* t[2];
+    if (n != 5 || !tensors(a, {0, 1}, t) || !PyLong_Check(a[2]) || !PyLong_Check(a[3]) ||
+        !PyLong_Check(a[4]))
+      return none();
+    const at::Tensor &scores = *t[0], &lens = *t[1];
+    const at::Device d = scores.device();
+    if (!current(scores) || !sums_of(scores, d) || !int32s(lens, {scores.size(0)}, d))
+      return none();
+    const long long budget = PyLong_AsLongLong(a[2]), recent = PyLong_AsLongLong(a[3]),
+                    sinks = PyLong_AsLongLong(a[4]);
+    if (PyErr_Occurred()) return nullptr;
+    const int64_t B = scores.size(0), H = scores.size(1), S = scores.size(2);
+    const int64_t bytes = c.cache_select_workspace(B, H, S);
+    if (bytes < 0) return PyLong_FromLong((long)bytes);
+    if (budget < 0 || budget > int64_t(1) << 30) return none();
+    bool ok;
+    void* s = stream_of(d, &ok);
+    if (!ok) return nullptr;
+    at::Tensor keep = at::empty({B, H, budget}, lens.options()),
+               counts = at::empty({B}, lens.options()),
+               sums = at::empty({B, H, budget}, scores.options()), ws;
+    if (bytes > 0) ws = at::empty({bytes}, lens.options().dtype(at::kByte));
+    const int st = c.cache_select(ptr<float>(scores), scores.stride(0), scores.stride(1), S,
+                                  ptr<int32_t>(lens), B, H, budget, recent, sinks,
+                                  ptr<int32_t>(keep), ptr<int32_t>(counts), ptr<float>(sums),
+                                  bytes > 0 ? ws.data_ptr() : nullptr, bytes, s);
+    return st == TQ_OK ? tuple({keep, counts, sums}) : PyLong_FromLong(st);
+  });
+}
+
+// (pool, page_table, lens, keep, counts, page_size, base or None)
+PyObject* pages_keep(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const at::Tensor *t[5], *base;
+    if (n != 7 || !tensors(a, {0, 1, 2, 3, 4}, t) || !PyLong_Check(a[5]) || !optional(a[6], &base))
+      return none();
+    const at::Tensor &pool = *t[0], &table = *t[1], &lens = *t[2], &keep = *t[3], &counts = *t[4];
+    const at::Device d = pool.device();
+    int64_t planes, pages, page_bytes;
+    if (!current(pool) || !pool_of(pool, &planes, &pages, &page_bytes) || !matrix(table, d))
+      return none();
+    const int64_t rows = table.size(0), width = table.size(1), dims = keep.dim();
+    if (!int32s(lens, {rows}, d) || !int32s(counts, {rows}, d) ||
+        (base && !int32s(*base, {rows}, d)) || dims < 2 || dims > 4 ||
+        !int32s(keep, keep.sizes(), d) || keep.size(dims == 4 ? 1 : 0) != rows)
+      return none();
+    const int64_t groups = dims == 4 ? keep.size(0) : 1, heads = dims > 2 ? keep.size(dims - 2) : 1;
+    const long long size = PyLong_AsLongLong(a[5]);
+    if (size == -1 && PyErr_Occurred()) return nullptr;
+    const int64_t bytes = c.pages_keep_workspace(rows, width, pages);
+    if (bytes < 0) return PyLong_FromLong((long)bytes);
+    bool ok;
+    void* s = stream_of(d, &ok);
+    if (!ok) return nullptr;
+    const auto o = lens.options();
+    at::Tensor ws = at::empty({bytes / 4}, o), table_out = at::empty({rows, width}, o),
+               lens_out = at::empty({rows}, o), lacking = at::empty({1}, o);
+    const int st = c.pages_keep(pool.data_ptr(), planes, pages, page_bytes, ptr<int32_t>(table),
+                                ptr<int32_t>(lens), rows, width, size, ptr<int32_t>(keep), groups,
+                                heads, keep.size(dims - 1), ptr<int32_t>(counts),
+                                base ? ptr<int32_t>(*base) : nullptr, ptr<int32_t>(table_out),
+                                ptr<int32_t>(lens_out), ptr<int32_t>(lacking), ws.data_ptr(),
+                                bytes, s);
+    return st == TQ_OK ? tuple({table_out, lens_out, lacking}) : PyLong_FromLong(st);
+  });
+}
+
 // bind(raw_stream, {name: address}): what the functions call
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 2 || !PyDict_Check(a[1])) {
@@ -437,13 +563,17 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return true;
   };
   Entries e{};  // all or nothing
-  if (!take("tq_rope", &e.rope) || !take("tq_rope_append", &e.rope_append) ||
+  if (!take("tq_rope", &e.rope) || !take("tq_rope_append_at", &e.rope_append) ||
       !take("tq_paged_attention", &e.paged_attention) ||
       !take("tq_paged_attention_workspace", &e.paged_attention_workspace) ||
       !take("tq_tree_mask", &e.tree_mask) || !take("tq_tree_attention", &e.tree_attention) ||
       !take("tq_tree_attention_workspace", &e.tree_attention_workspace) ||
       !take("tq_pages_workspace", &e.pages_workspace) || !take("tq_pages_fork", &e.pages_fork) ||
-      !take("tq_pages_grow", &e.pages_grow) || !take("tq_pages_compact", &e.pages_compact))
+      !take("tq_pages_grow", &e.pages_grow) || !take("tq_pages_compact", &e.pages_compact) ||
+      !take("tq_cache_weights", &e.cache_weights) || !take("tq_cache_select", &e.cache_select) ||
+      !take("tq_cache_select_workspace", &e.cache_select_workspace) ||
+      !take("tq_pages_keep", &e.pages_keep) ||
+      !take("tq_pages_keep_workspace", &e.pages_keep_workspace))
     return nullptr;
   c = e;
   Py_INCREF(a[0]);
@@ -457,8 +587,10 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef methods[] = {TQ_METHOD(bind),          TQ_METHOD(rope),
                          TQ_METHOD(rope_append),   TQ_METHOD(paged_attention),
                          TQ_METHOD(tree_mask),     TQ_METHOD(tree_attention),
+                         TQ_METHOD(cache_weights), TQ_METHOD(cache_select),
                          TQ_METHOD(pages_fork),    TQ_METHOD(pages_grow),
-                         TQ_METHOD(pages_compact), {nullptr, nullptr, 0, nullptr}};
+                         TQ_METHOD(pages_compact), TQ_METHOD(pages_keep),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tq_torch",
                       "Decode-side calls of libtq.so in their common form.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

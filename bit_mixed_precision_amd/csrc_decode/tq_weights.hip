@@ -1,0 +1,319 @@
+// The attention weight that every cached token receives, added to a running sum: what
+// an eviction goes by.
+//
+//     w[b][h][t] = sum over nodes i and heads g of the group of
+//                  exp(scale * q[b][i][hG + g] . k[t][h] - lse[b][i][hG + g])
+//     scores[b][h][t] = decay * scores[b][h][t] + w   (cached tokens)
+//                     = w                             (the nodes' own tokens)
+//
+// The normalizing sums are known (the attention before returned them), so tokens do not
+// depend on each other and nothing is split or joined: a wave holds some tokens' keys in
+// registers and walks through the rows (node, head of the group).
+
+#include <atomic>
+
+#include "tq.h"
+#include "tq_attn_dev.h"
+#include "tq_common.h"
+#include "tq_decode.h"
+#include "tq_kernels.h"
+#include "tq_mfma.h"
+
+namespace tq {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kMaskWords = 4;
+constexpr int kMaxNodes = 64 * kMaskWords;
+
+struct WeightsParams {
+  const unsigned char* Q;
+  const unsigned char* K;
+  int64_t q_seq, q_tok, q_head;                  // bytes
+  int64_t page_stride, row_stride, head_stride;  // bytes
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* nodes;
+  const uint64_t* mask;
+  int64_t mask_seq;  // words
+  const float* lse;  // [B][T][Hq]
+  float* scores;
+  int64_t s_seq, s_head;  // numbers
+  FastDiv page, group;
+  int32_t n_pages, width, B, T, words, Hq, Hkv, D, G, window, S;
+  int32_t tiles;  // not 0: of the longest sequence; every tile has a workgroup
+  float scale, decay;
+};
+
+template <bool BF>
+__device__ __forceinline__ float4v mma16(u32x4 a, u32x4 b, float4v c) {
+  if constexpr (BF)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a),
+                                                   __builtin_bit_cast(bf8, b), c, 0, 0, 0);
+  else
+    return mfma16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c);
+}
+
+// A sequence: n cached tokens, m nodes, tokens [lo, hi) that any node may see, the
+// tiles [t0, t1) of UT tokens whose sums change.
+struct Seq {
+  int n, m, lo, hi, t0, t1;
+};
+template <int UT>
+__device__ __forceinline__ Seq read_seq(const WeightsParams& p, int b) {
+  Seq s;
+  const int len = read_const(p.lens, b), nodes = p.nodes ? read_const(p.nodes, b) : p.T;
+  const int cap = p.width * (int)p.page.d;
+  s.n = len < 0 ? 0 : len < cap ? len : cap;
+  s.m = nodes < 0 ? 0 : nodes < p.T ? nodes : p.T;
+  s.hi = s.n + s.m < cap ? s.n + s.m : cap;
+  s.lo = p.window > 0 && s.n > p.window ? s.n - p.window : 0;
+  const int last = s.hi < p.S ? s.hi : p.S;
+  s.t0 = p.decay == 1.f ? s.lo / UT : 0;
+  s.t1 = s.m == 0 && p.decay == 1.f ? s.t0 : (last + UT - 1) / UT;
+  if (s.t1 < s.t0) s.t1 = s.t0;
+  return s;
+}
+
+// DV: 64, 128 or 256, the head dimension rounded up.  NT: 16-token tiles of a wave.
+template <bool BF, int DV, int NT>
+__global__ __launch_bounds__(kThreads) void cache_weights_kernel(WeightsParams p) {
+  constexpr int KS = DV / 32, UT = 16 * NT * kWaves;
+  extern __shared__ float sLse[];  // [rows], times log2 e; +inf: the row adds nothing
+  __shared__ uint64_t sBits[kMaxNodes][kMaskWords];
+  __shared__ int sLow[kMaxNodes];
+
+  const int tid = threadIdx.x;
+  const int wave = uni(tid >> 6), lane = tid & 63, li = lane & 15, g = lane >> 4;
+
+  int b = 0, h = 0, tile = 0;
+  uint32_t left = 1;
+  Seq s;
+  if (p.tiles > 0) {
+    const int row = blockIdx.x / p.tiles;
+    tile = blockIdx.x - row * p.tiles;
+    b = row / p.Hkv;
+    h = row - b * p.Hkv;
+    s = read_seq<UT>(p, b);
+    tile += s.t0;
+    if (tile >= s.t1) return;
+  } else {
+    const int per = (p.B + kWave - 1) / kWave;
+    auto tiles_of = [&](int x, bool in) -> uint32_t {
+      const Seq q = read_seq<UT>(p, x < p.B ? x : p.B - 1);
+      return in && x < p.B ? q.t1 - q.t0 : 0;
+    };
+    uint32_t mine = 0;
+    for (int i = 0; i < per; ++i) mine += tiles_of(lane * per + i, true);
+    const uint32_t inc = scan_wave(mine, lane);
+    const Cut cut((uint32_t)uni((int)__shfl(inc, 63, kWave)) * p.Hkv, gridDim.x);
+    if (blockIdx.x >= cut.parts) return;
+    uint32_t at = cut.start(blockIdx.x);
+    left = cut.start(blockIdx.x + 1) - at;
+    const uint64_t has = __ballot(at < inc * p.Hkv);
+    const int src = has ? __builtin_ctzll(has) : 0;
+    at -= (uint32_t)__builtin_amdgcn_readlane((int)(inc - mine), src) * p.Hkv;
+    b = src * per;
+    for (int i = 0; per > 1 && i < per; i += kWave) {
+      const uint32_t n = tiles_of(src * per + i + lane, i + lane < per);
+      const uint32_t run = scan_wave(n, lane);
+      const uint64_t hit = __ballot(at < run * p.Hkv);
+      if (hit) {
+        const int k = __builtin_ctzll(hit);
+        b = src * per + i + k;
+        at -= (uint32_t)__builtin_amdgcn_readlane((int)(run - n), k) * p.Hkv;
+        break;
+      }
+      at -= (uint32_t)__builtin_amdgcn_readlane((int)run, kWave - 1) * p.Hkv;
+    }
+    if (b >= p.B) b = p.B - 1;
+    s = read_seq<UT>(p, b);
+    const uint32_t n = s.t1 > s.t0 ? s.t1 - s.t0 : 1;
+    h = at / n < (uint32_t)p.Hkv ? at / n : p.Hkv - 1;
+    tile = s.t0 + at % n;
+  }
+
+  bool fresh = true;
+  for (; left > 0; --left) {
+    const int rows = s.m * p.G;
+    if (fresh) {
+      __syncthreads();  // what the rows before needed has been read
+      for (int r = tid; r < rows; r += kThreads) {
+        const int i = div_page(p.group, r);
+        const float l = p.lse[((int64_t)b * p.T + i) * p.Hq + h * p.G + (r - i * p.G)];
+        sLse[r] = fabsf(l) < INFINITY ? l * kLog2e : INFINITY;
+      }
+      for (int i = tid; i < s.m; i += kThreads) {
+        int seen = 0;
+        for (int w = 0; w < kMaskWords; ++w) {
+          const int valid = s.m - w * 64, upto = i + 1 - w * 64;
+          const uint64_t some = valid >= 64 ? ~0ull : valid <= 0 ? 0ull : (1ull << valid) - 1;
+          uint64_t bits = upto >= 64 ? ~0ull : upto <= 0 ? 0ull : (1ull << upto) - 1;
+          if (p.mask) bits = w < p.words ? p.mask[b * p.mask_seq + (int64_t)i * p.words + w] : 0;
+          sBits[i][w] = bits & some;
+          seen += __popcll(bits & some);
+        }
+        const int low = p.window > 0 ? s.n + seen - p.window : 0;
+        sLow[i] = low > 0 ? low : 0;
+      }
+      __syncthreads();
+    }
+    const int t0 = tile * UT + wave * 16 * NT;
+    // Keys as the B operand: lane li holds token t0 + 16 n + li
+    u32x4 k[NT][KS];
+    bool there[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int t = t0 + 16 * n + li;
+      const bool in = t >= s.lo && t < s.hi;
+      const int pg = div_page(p.page, in ? t : 0);
+      const int id = in ? p.table[(int64_t)b * p.width + pg] : -1;
+      there[n] = (uint32_t)id < (uint32_t)p.n_pages;
+      const unsigned char* kp = p.K + id * p.page_stride +
+                                (t - pg * (int)p.page.d) * p.row_stride + h * p.head_stride;
+#pragma unroll
+      for (int x = 0; x < KS; ++x) {
+        const int d = 32 * x + 8 * g;
+        k[n][x] = u32x4{0, 0, 0, 0};
+        if (there[n] && d < p.D) k[n][x] = *reinterpret_cast<const u32x4*>(kp + d * 2);
+      }
+    }
+    float sum[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) sum[n] = 0.f;
+    const bool edge = t0 + 16 * NT > s.n || (p.window > 0 && t0 < s.n + s.m - p.window);
+    for (int r0 = 0; r0 < rows; r0 += 16) {
+      // queries as the A operand: lane li holds row r0 + li
+      const int row = r0 + li;
+      const int i = div_page(p.group, row < rows ? row : 0);
+      const unsigned char* qp = p.Q + b * p.q_seq + i * p.q_tok +
+                                (int64_t)(h * p.G + ((row < rows ? row : 0) - i * p.G)) * p.q_head;
+      u32x4 q[KS];
+#pragma unroll
+      for (int x = 0; x < KS; ++x) {
+        const int d = 32 * x + 8 * g;
+        q[x] = u32x4{0, 0, 0, 0};
+        if (row < rows && d < p.D) q[x] = *reinterpret_cast<const u32x4*>(qp + d * 2);
+      }
+      float ls[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int rj = r0 + 4 * g + j;
+        ls[j] = rj < rows ? sLse[rj] : INFINITY;
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float4v c = {0, 0, 0, 0};
+#pragma unroll
+        for (int x = 0; x < KS; ++x) c = mma16<BF>(q[x], k[n][x], c);
+        const int t = t0 + 16 * n + li;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          bool ok = ls[j] < INFINITY && there[n];
+          if (edge && ok) {
+            const int node = div_page(p.group, r0 + 4 * g + j), at = t - s.n;
+            ok = at < 0 ? t >= sLow[node]
+                        : at < kMaxNodes && (sBits[node][at >> 6] >> (at & 63) & 1);
+          }
+          const float w = __builtin_amdgcn_exp2f(fmaf(c[j], p.scale, -ls[j]));
+          sum[n] += ok ? w : 0.f;
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      sum[n] += __shfl_xor(sum[n], 16, kWave);
+      sum[n] += __shfl_xor(sum[n], 32, kWave);
+    }
+    // lane group g writes the tiles g, g + 4, ..
+#pragma unroll
+    for (int n0 = 0; n0 < NT; n0 += 4) {
+      float w = sum[n0];
+#pragma unroll
+      for (int n = 1; n < 4; ++n)
+        if (n0 + n < NT) w = g == n ? sum[n0 + n] : w;
+      const int t = t0 + 16 * (n0 + g) + li;
+      if (n0 + g < NT && t < s.hi && t < p.S) {
+        float* to = p.scores + b * p.s_seq + h * p.s_head + t;
+        *to = t < s.n ? fmaf(p.decay, *to, w) : w;
+      }
+    }
+    fresh = false;
+    if (++tile >= s.t1 && left > 1) {
+      fresh = true;
+      if (++h == p.Hkv) {
+        h = 0;
+        while (b + 1 < p.B) {
+          s = read_seq<UT>(p, ++b);
+          if (s.t1 > s.t0) break;
+        }
+      }
+      tile = s.t0;
+    }
+  }
+}
+
+template <bool BF, int DV, int NT>
+hipError_t launch_nt(WeightsParams p, hipStream_t s) {
+  constexpr int64_t UT = 16 * NT * kWaves;
+  int64_t cap = (int64_t)p.width * p.page.d;
+  if (cap > p.S) cap = p.S;
+  const int64_t tiles = (cap + UT - 1) / UT, all = (int64_t)p.B * p.Hkv * tiles;
+  const int64_t most = 4 * (int64_t)device_cus();
+  if (all == 0) return hipSuccess;
+  p.tiles = all <= 2 * most ? (int32_t)tiles : 0;
+  const int lds = p.T * p.G * 4;
+  hipLaunchKernelGGL((cache_weights_kernel<BF, DV, NT>),
+                     dim3((uint32_t)(p.tiles || all < most ? all : most)), dim3(kThreads), lds, s, p);
+  return hipGetLastError();
+}
+
+template <bool BF>
+hipError_t launch_weights(const WeightsParams& p, hipStream_t s) {
+  return p.D <= 64    ? launch_nt<BF, 64, 2>(p, s)
+         : p.D <= 128 ? launch_nt<BF, 128, 2>(p, s)
+                      : launch_nt<BF, 256, 2>(p, s);
+}
+
+}  // namespace
+
+hipError_t launch_cache_weights(int dtype, const WeightsArgs& a, hipStream_t stream) {
+  WeightsParams p{};
+  const TreeArgs& t = a.tree;
+  p.Q = static_cast<const unsigned char*>(t.Q);
+  p.K = static_cast<const unsigned char*>(t.k_pages);
+  p.q_seq = 2 * t.q_seq;
+  p.q_tok = 2 * t.q_tok;
+  p.q_head = 2 * t.q_head;
+  p.page_stride = 2 * t.page_stride;
+  p.row_stride = 2 * t.row_stride;
+  p.head_stride = 2 * t.head_stride;
+  p.table = t.page_table;
+  p.lens = t.lens;
+  p.nodes = t.nodes;
+  p.mask = static_cast<const uint64_t*>(t.mask);
+  p.mask_seq = t.mask_seq;
+  p.lse = a.lse;
+  p.scores = a.scores;
+  p.s_seq = a.s_seq;
+  p.s_head = a.s_head;
+  p.page = fast_div(t.page_size);
+  p.group = fast_div(t.Hq / t.Hkv);
+  p.n_pages = (int32_t)t.n_pages;
+  p.width = (int32_t)t.width;
+  p.B = (int32_t)t.B;
+  p.T = (int32_t)t.T;
+  p.words = (int32_t)((t.T + 63) / 64);
+  p.Hq = (int32_t)t.Hq;
+  p.Hkv = (int32_t)t.Hkv;
+  p.D = (int32_t)t.D;
+  p.G = (int32_t)(t.Hq / t.Hkv);
+  p.window = (int32_t)t.window;
+  p.S = (int32_t)a.S;
+  p.scale = t.scale_log2;
+  p.decay = a.decay;
+  return dtype == TQ_BF16 ? launch_weights<true>(p, stream) : launch_weights<false>(p, stream);
+}
+
+}  // namespace tq

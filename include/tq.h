@@ -431,6 +431,19 @@ int tq_rope_append(int dtype, const void* QKV, int64_t qkv_tok, const float* tab
                    int64_t head_stride, void* Q, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
                    int interleaved, void* stream);
 
+/* tq_rope_append where a token's slot is not its position: the drafted nodes of a tree,
+ * whose positions go by their depth, and caches that have lost tokens.  slots int32 [T],
+ * device, or NULL: positions.  Keys and values of token t go to slot slots[t] of its row;
+ * queries and keys are turned by position pos[t].  A slot outside the table's width, or
+ * negative, is not written.  Everything else as tq_rope_append. */
+int tq_rope_append_at(int dtype, const void* QKV, int64_t qkv_tok, const float* table,
+                      int64_t n_pos, int64_t rot, const int32_t* pos, const int32_t* slots,
+                      const int32_t* seqs, const int32_t* page_table, int64_t n_seqs,
+                      int64_t width, void* k_pages, void* v_pages, int64_t n_pages,
+                      int64_t page_size, int64_t page_stride, int64_t row_stride,
+                      int64_t head_stride, void* Q, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                      int interleaved, void* stream);
+
 /* Attention of one new token per sequence over the paged cache:
  *   out[b][h] = sum_t w_t v[t][h / G],  w = softmax_t(scale q[b][h] . k[t][h / G])
  * over the tokens t in [max(0, len - window), len) of sequence b (window = 0:
@@ -519,6 +532,47 @@ int tq_tree_attention(int dtype, const void* Q, int64_t q_seq, int64_t q_tok, in
 int64_t tq_tree_attention_workspace(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
                                     int64_t page_size, int64_t width);
 
+/* What an eviction goes by: the attention weight that every cached token receives,
+ * added to a running sum.  Arguments as tq_tree_attention's (T = 1: one new token per
+ * sequence, lens not counting it); lse fp32 [B][T][Hq] is what that call returned.
+ *   w[b][h][t] = sum over nodes i and query heads j of head h's group of
+ *                exp(scale q[b][i][j] . k[t][h] - lse[b][i][j]) over the tokens i sees
+ *   scores[b][h][t] = decay scores[b][h][t] + w   for the lens[b] cached tokens,
+ *                   = w                           for the nodes' own tokens,
+ * in place; numbers of tokens past those, and of tokens from S on, stay as they are.  A
+ * row whose lse is infinite or no number adds nothing (tokens that a verification has
+ * rejected: lse = -inf).  scores fp32, number t of head h of sequence b at s_seq b +
+ * s_head h + t, none of which may share an address.  fp32 sums, in an order that does
+ * not change from run to run.
+ * Limits as tq_tree_attention's, T G <= 8192, S <= 2^30.  Errors likewise; TQ_ERR_VALUE
+ * for a decay outside [0, 1].  B, T or S = 0 is a no-op. */
+int tq_cache_weights(int dtype, const void* Q, int64_t q_seq, int64_t q_tok, int64_t q_head,
+                     const void* k_pages, int64_t n_pages, int64_t page_size, int64_t page_stride,
+                     int64_t row_stride, int64_t head_stride, const int32_t* page_table,
+                     int64_t width, const int32_t* lens, const int32_t* nodes, const int64_t* mask,
+                     int64_t mask_seq, const float* lse, int64_t B, int64_t T, int64_t Hq,
+                     int64_t Hkv, int64_t D, double scale, int64_t window, double decay,
+                     float* scores, int64_t s_seq, int64_t s_head, int64_t S, void* stream);
+
+/* Which tokens stay: of each sequence and head, with n = lens[b] tokens (negative counts
+ * as 0, and S at most) all, where n <= budget, else `budget` of them: the first `sinks`,
+ * the last `recent`, and of the others those of the largest scores (equal ones by the
+ * lowest index; NaN counts as -inf, -0 as 0).  scores fp32, number t of head h of
+ * sequence b at s_seq b + s_head h + t, t < S.
+ * keep int32 [B][H][budget]: their indexes, ascending, then -1; counts int32 [B]:
+ * min(n, budget); sums fp32 [B][H][budget] or NULL: their scores, then 0.
+ * All device pointers.  sinks + recent <= budget <= 2^30, S <= 2^30, B H <= 2^22.
+ * workspace: tq_cache_select_workspace(...) bytes, 16-byte aligned; outputs and
+ * workspace must not overlap the inputs.  Errors: TQ_ERR_NULL, TQ_ERR_SHAPE,
+ * TQ_ERR_ALIGN, TQ_ERR_DEVICE.  B = 0 or H = 0 is a no-op. */
+int tq_cache_select(const float* scores, int64_t s_seq, int64_t s_head, int64_t S,
+                    const int32_t* lens, int64_t B, int64_t H, int64_t budget, int64_t recent,
+                    int64_t sinks, int32_t* keep, int32_t* counts, float* sums, void* workspace,
+                    int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of tq_cache_select; TQ_ERR_SHAPE for shapes it refuses. */
+int64_t tq_cache_select_workspace(int64_t B, int64_t H, int64_t S);
+
 /* The pages of a cache.  The page table and the lengths are the whole state: a
  * page is free when no row holds it, and a page held by several rows is shared.
  * The functions read one state and write another, so a step can be repeated and
@@ -575,6 +629,33 @@ int tq_pages_compact(void* pool, int64_t planes, int64_t n_pages, int64_t page_b
  * page must not be a destination twice, nor both a source and a destination. */
 int tq_pages_copy(void* pool, int64_t planes, int64_t n_pages, int64_t page_bytes,
                   const int32_t* src, const int32_t* dst, int64_t n, void* stream);
+
+/* Keeping some tokens: row r keeps its first base[r] tokens (base NULL: 0; clipped to its
+ * length) and then the counts[r] tokens that keep lists (clipped to n and to what
+ * the row has after base[r]); they move together, and pages past the last one are
+ * released.  What an eviction leaves (tq_cache_select's indexes), or the accepted path of
+ * a tree: base the length before the nodes, keep base + the path's nodes.
+ * A token is `heads` parts of page_bytes / page_size / heads bytes, each with a list of
+ * its own, and every run of planes / groups planes likewise: keep int32
+ * [groups][rows][heads][n].  Slot base[r] + i gets token keep[..][i].  Lists ascend, so
+ * that entry i is base[r] + i at least; an entry below that, or past the row's length,
+ * leaves its slot as it is.  Slots past the last token, and those of pages that a row
+ * releases, stay as they are.
+ * A page that is held by more than one table entry is not written: where a token in it
+ * would change, the row gets a free page in its place, with its kept tokens.  A row that
+ * needs more pages, together with those before it, than are free keeps its tokens, length
+ * and pages, and short_out int32 [1] counts such rows.  lens_out int32 [rows]: base +
+ * counts.  page_bytes a multiple of page_size * heads * 16, planes one of groups; heads
+ * <= 2^16.  workspace: tq_pages_keep_workspace(rows, width, n_pages) bytes. */
+int tq_pages_keep(void* pool, int64_t planes, int64_t n_pages, int64_t page_bytes,
+                  const int32_t* table, const int32_t* lens, int64_t rows, int64_t width,
+                  int64_t page_size, const int32_t* keep, int64_t groups, int64_t heads, int64_t n,
+                  const int32_t* counts, const int32_t* base, int32_t* table_out,
+                  int32_t* lens_out, int32_t* short_out, void* workspace, int64_t workspace_bytes,
+                  void* stream);
+
+/* Workspace bytes of tq_pages_keep; TQ_ERR_SHAPE for sizes that it refuses. */
+int64_t tq_pages_keep_workspace(int64_t rows, int64_t width, int64_t n_pages);
 
 /* Workspace bytes of fork, grow and compact; TQ_ERR_SHAPE for sizes that they
  * refuse. */
