@@ -11,6 +11,8 @@
 // The m * G queries that share a key-value head are the rows of one matrix product
 // each with K and V; a row block of them and a run of tokens are a unit of work.
 
+#include <math.h>
+
 #include <atomic>
 #include <type_traits>
 
@@ -50,8 +52,9 @@ struct TreeParams {
   FastDiv page, group;
   int32_t n_pages, width, B, T, words, Hq, Hkv, D, G, window;
   int32_t direct;  // one workgroup per row block: nothing is split
+  int32_t runs;    // 16 tokens lie in one page
   float scale;     // not negative
-  uint32_t flip;   // sign bit where the caller's scale is negative
+  uint32_t flip;   // sign bits of two numbers where the caller's scale is negative: of the queries
 };
 
 // Floats of one partial result: rows x D numbers, maxima, sums.
@@ -79,6 +82,41 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 __device__ __forceinline__ int64_t shfl64(int64_t v, int src) {
   const int lo = __shfl((int)v, src, kWave), hi = __shfl((int)(v >> 32), src, kWave);
   return ((int64_t)hi << 32) | (uint32_t)lo;
+}
+
+constexpr uint32_t kOut = 0x80000000u;   // a lane offset past every buffer
+constexpr uint32_t kSpan = 0x7ffffffcu;  // bytes a buffer resource covers
+constexpr int kNoLoads = 0x0f70;         // s_waitcnt: until no vector load is under way
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_at(const unsigned char* p) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(((uint64_t)hi << 32) | lo),
+                                           (short)0, (int)kSpan, kBufferWord3);
+}
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+// 16 bytes at the resource's base + off to LDS: lane l writes the bytes dst + 16 l.  In
+// assembly, because the compiler would otherwise wait for these copies before every
+// transposing read of LDS, of whatever buffer; waited for by kNoLoads.  (Nothing is
+// returned to a register.  A copy needs one state between the write of m0 and itself.)
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, int off, unsigned char* dst) {
+  const uint32_t to = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)dst;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(to), "v"(off), "s"(r) : "memory", "m0");
+}
+
+// A value that the compiler takes for a new one: what follows from it is computed where it
+// stands, instead of being kept in registers through the whole loop.
+__device__ __forceinline__ int anew(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+__device__ __forceinline__ int anew_uniform(int v) {
+  asm volatile("" : "+s"(v));
+  return v;
 }
 
 // The low n bits, n of any value.
@@ -155,10 +193,13 @@ struct Shape {
   static constexpr int TEAMS = kTreeWaves / TEAM;
   static constexpr int UT = TT * TEAMS;            // tokens of a unit
   static constexpr int ROWS = kTeamRows * TEAM;    // rows of a block
-  static constexpr int PER = TT * PC / (kWave * TEAM);  // pieces of K (and of V) a thread loads
+  static constexpr int HALVES = TT / 16 / TEAM;         // runs of 16 tokens that a wave loads
+  static constexpr int PH = 16 * PC / kWave;            // pieces of such a run, per thread
+  static constexpr int PER = HALVES * PH;               // pieces of K (and of V) per thread
   static constexpr int TILE = TT * DP * 2;         // bytes of K (and of V)
   static constexpr int PAD = DP + 4;               // floats of a row of sums in LDS
-  static constexpr int TILES = 2 * TILE * TEAMS;
+  static constexpr int BUFFERS = TEAM == 4 ? 2 : 1;
+  static constexpr int TILES = 2 * TILE * TEAMS * BUFFERS;
   static constexpr int JOIN = TEAM == 4 ? 0 : kTreeWaves * kTeamRows * PAD * 4;
   static constexpr int LDS = TILES > JOIN ? TILES : JOIN;
   // A weight as two 16-bit numbers where memory sets the pace, as one with many rows,
@@ -185,7 +226,7 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
     TreeParams p) {
   using S = Shape<DP, TEAM>;
   constexpr int KS = S::KS, NE = S::NE, PC = S::PC, TT = S::TT, SUB = S::SUB, UT = S::UT;
-  constexpr int ROWS = S::ROWS, PER = S::PER;
+  constexpr int ROWS = S::ROWS, PER = S::PER, PH = S::PH;
   extern __shared__ __attribute__((aligned(16))) unsigned char sTiles[];
   // what a row sees of the nodes, and its first cached token
   __shared__ uint64_t sBits[kTreeWaves][kTeamRows][kMaskWords];
@@ -196,18 +237,17 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
   const int tid = threadIdx.x;
   const int wave = uni(tid >> 6), lane = tid & 63, col = lane & 31, half = lane >> 5;
   const int team = wave / TEAM;
-  const int tl = TEAM == 4 ? tid : lane;  // this thread in its team
-  unsigned char* const sK = sTiles + team * 2 * S::TILE;
-  unsigned char* const sV = sK + S::TILE;
+  const int run16 = TEAM == 4 ? wave : 0;  // the first run of 16 tokens that this wave loads
+  unsigned char* const sTeam = sTiles + team * 2 * S::TILE * S::BUFFERS;
 
-  // this workgroup's run of units
+  // This workgroup's run of units: of the list (row block, sequence, head, tile), one of
+  // gridDim.x equal ones.
   Unit cur{};
   uint32_t left = 0, run_end = 0;
   Cut cut(0, 1);
   if (p.direct) {
-    const int per_block = p.B * p.Hkv;
-    cur.r = blockIdx.x / per_block;
-    const int rest = blockIdx.x - cur.r * per_block;
+    const int rows = p.B * p.Hkv, rest = blockIdx.x % rows;
+    cur.r = blockIdx.x / rows;
     cur.b = rest / p.Hkv;
     cur.h = rest - cur.b * p.Hkv;
     cur.s = read_seq<UT, ROWS>(p, cur.b);
@@ -219,14 +259,11 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
       const Seq s = read_seq<UT, ROWS>(p, b < p.B ? b : p.B - 1);
       return in && b < p.B && s.blocks > r ? s.t1 - s.t0 : 0;
     };
-    uint32_t all = 0, most = 0;  // tiles x blocks, blocks
+    uint32_t all = 0;  // tiles x blocks
     for (int i = 0; i < per; ++i) {
       const int b = lane * per + i;
       const Seq s = read_seq<UT, ROWS>(p, b < p.B ? b : p.B - 1);
-      if (b < p.B) {
-        all += (uint32_t)(s.t1 - s.t0) * s.blocks;
-        most = (uint32_t)s.blocks > most ? s.blocks : most;
-      }
+      if (b < p.B) all += (uint32_t)(s.t1 - s.t0) * s.blocks;
     }
     all = uni((int)__shfl(scan_wave(all, lane), 63, kWave));
     cut = Cut(all * p.Hkv, gridDim.x);
@@ -235,18 +272,17 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
       run_end = cut.start(blockIdx.x + 1);
       left = run_end - at;
       // the row block, the lane that looks after the sequence, the sequence
-      const int lanes = (p.B + per - 1) / per;
       uint32_t mine = 0, inc = 0;
-      for (cur.r = 0;; ++cur.r) {
+      for (;; ++cur.r) {
         mine = 0;
         for (int i = 0; i < per; ++i) mine += tiles_of(lane * per + i, true, cur.r);
         inc = scan_wave(mine, lane);
         const uint32_t total = uni((int)__shfl(inc, 63, kWave)) * (uint32_t)p.Hkv;
-        // (the bound holds whatever happens to the lengths meanwhile)
+        // (the bounds here hold whatever happens to the lengths meanwhile)
         if (at < total || cur.r >= p.T * p.G / ROWS) break;
         at -= total;
       }
-      const uint64_t has = __ballot(at < inc * p.Hkv && lane < lanes);
+      const uint64_t has = __ballot(at < inc * p.Hkv);
       const int src = has ? __builtin_ctzll(has) : 0;
       at -= (uint32_t)__builtin_amdgcn_readlane((int)(inc - mine), src) * p.Hkv;
       cur.b = src * per;
@@ -270,15 +306,17 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
       if (cur.h >= p.Hkv) cur.h = p.Hkv - 1;
     }
   }
-
-  auto advance = [&](Unit& c) {  // only where another unit follows
-    if (++c.tile < c.s.t1) return;
+  // The first unit after c's row (of a row block, sequence and head).
+  auto next_row = [&](Unit& c) {
     if (++c.h == p.Hkv) {
       c.h = 0;
       while (true) {
         if (++c.b == p.B) {
           c.b = 0;
-          if (++c.r > p.T * p.G / ROWS) break;  // past the end (the lengths have changed)
+          if (++c.r > p.T * p.G / ROWS) {  // past the end (the lengths have changed)
+            left = 0;
+            return;
+          }
         }
         c.s = read_seq<UT, ROWS>(p, c.b);
         if (c.s.t1 > c.s.t0 && c.s.blocks > c.r) break;
@@ -287,40 +325,22 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
     c.tile = c.s.t0;
   };
 
-  // This lane's token of the team's tile: the page it lies in, as the table has it.
-  auto first_token = [&](const Unit& c) { return c.tile * UT + team * TT; };
-  auto page_id = [&](const Unit& c) {
-    const int t = first_token(c) + (lane & (TT - 1));
+  auto first_token = [&](int tile) { return tile * UT + team * TT; };
+  // The page of this lane's token of the team's tile, as the table has it.
+  auto page_id = [&](const Unit& c, int tile) {
+    const int t = first_token(tile) + (lane & (TT - 1));
     const bool in = t >= c.s.lo && t < c.s.hi;
     return p.table[(int64_t)c.b * p.width + div_page(p.page, in ? t : c.s.lo)];
   };
-  u32x4 kreg[PER], vreg[PER];
-  uint64_t present_next = 0;
-  auto load = [&](const Unit& c, int id) {
-    const int t = first_token(c) + (lane & (TT - 1));
-    const bool ok = t >= c.s.lo && t < c.s.hi && (uint32_t)id < (uint32_t)p.n_pages;
-    const int slot = t - (int)(div_page(p.page, ok ? t : 0) * p.page.d);
-    const int64_t off = ok ? id * p.page_stride + slot * p.row_stride + c.h * p.head_stride : -1;
-    present_next = __ballot(ok);
-#pragma unroll
-    for (int u = 0; u < PER; ++u) {
-      const int x = u * kWave * TEAM + tl, row = x / PC, piece = x - row * PC;
-      const int64_t o = shfl64(off, row);
-      kreg[u] = vreg[u] = u32x4{0, 0, 0, 0};
-      if (o >= 0 && piece * 8 < p.D) {
-        kreg[u] = *reinterpret_cast<const u32x4*>(p.K + o + piece * 16);
-        vreg[u] = *reinterpret_cast<const u32x4*>(p.V + o + piece * 16);
-      }
-    }
-  };
   // Whether some row may not see some present token of the tile.
-  auto edge = [&](const Unit& c) {
-    const int a = first_token(c);
-    return a + TT > c.s.n || (p.window > 0 && a < c.s.n + c.s.m - p.window);
+  auto edge = [&](const Seq& s, int tile) {
+    const int a = first_token(tile);
+    return a + TT > s.n || (p.window > 0 && a < s.n + s.m - p.window);
   };
-  // Of such a tile only the finite values: a weight of zero times infinity would reach
-  // rows that do not see the token.  close_row adds what is left out here.
-  auto stage = [&](bool at_edge) {
+  // Of a tile at an edge only the finite values go to LDS: a weight of zero times infinity
+  // would reach rows that do not see the token.  close_row adds what is left out here.
+  u32x4 kreg[PER], vreg[PER];
+  auto stage = [&](bool at_edge, unsigned char* buf) {
     if (at_edge) {
       bool odd = false;
 #pragma unroll
@@ -333,16 +353,66 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
         }
       if (odd) sOdd[team] = 1;  // every writer writes 1
     }
+    const int ln = TEAM == 1 ? lane : anew(lane);
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
-      const int x = u * kWave * TEAM + tl, row = x / PC, piece = x - row * PC;
-      *reinterpret_cast<u32x4*>(sK + row * DP * 2 + S::k_at(row, piece) * 16) = kreg[u];
-      *reinterpret_cast<u32x4*>(sV + row * DP * 2 + S::v_at(row, piece) * 16) = vreg[u];
+      const int x = u % PH * kWave + ln, row = 16 * (run16 + u / PH) + x / PC, piece = x % PC;
+      *reinterpret_cast<u32x4*>(buf + (row * PC + S::k_at(row, piece)) * 16) = kreg[u];
+      *reinterpret_cast<u32x4*>(buf + S::TILE + (row * PC + S::v_at(row, piece)) * 16) = vreg[u];
     }
   };
-  auto team_sync = [&] {
-    if constexpr (TEAM == 4) __syncthreads();
-    else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  // Fetches a tile.  A wave takes runs of 16 tokens, lane x their pieces x, x + 64, ..  Teams
+  // of four copy straight to LDS where every token is there, none is at an edge and a
+  // run lies in one page: where a piece lies in LDS is turned, so a lane fetches what
+  // belongs to its place.  Other tiles, and those of single waves, go through registers.
+  uint64_t present = 0;  // tokens that are there, of the tile last fetched
+  constexpr uint64_t kFull = TT == 64 ? ~0ull : 0xffffffffull;
+  auto fetch = [&](const Unit& c, int tile, int id, unsigned char* buf) {
+    const int a = first_token(tile);
+    const int t = a + (lane & (TT - 1));
+    const bool ok = t >= c.s.lo && t < c.s.hi && (uint32_t)id < (uint32_t)p.n_pages;
+    const bool at_edge = edge(c.s, tile);
+    present = __ballot(ok) & kFull;
+    const int64_t head = c.h * p.head_stride;
+    const int D = anew_uniform(p.D), ln = anew(lane);
+    if (p.runs && present == kFull && !at_edge) {
+#pragma unroll
+      for (int r = 0; r < S::HALVES; ++r) {
+        const int first = a + 16 * (run16 + r);
+        const int slot = first - (int)(div_page(p.page, first) * p.page.d);
+        const int64_t at = __builtin_amdgcn_readlane(id, 16 * (run16 + r)) * p.page_stride +
+                           slot * p.row_stride + head;
+        const auto rk = rsrc_at(p.K + at), rv = rsrc_at(p.V + at);
+#pragma unroll
+        for (int u = 0; u < PH; ++u) {
+          const int x = u * kWave + ln, row = x / PC, place = x - row * PC;
+          if constexpr (TEAM == 4) {
+            unsigned char* to = buf + (run16 * 16 * PC + u * kWave) * 16;
+            const int kp = S::k_at(row, place), vp = S::v_at(row, place);
+            if (kp * 8 < D) dma16(rk, row * (int)p.row_stride + kp * 16, to);
+            if (vp * 8 < D) dma16(rv, row * (int)p.row_stride + vp * 16, to + S::TILE);
+          } else {
+            const uint32_t off = place * 8 < D ? row * (uint32_t)p.row_stride + place * 16 : kOut;
+            kreg[r * PH + u] = load16(rk, off);
+            vreg[r * PH + u] = load16(rv, off);
+          }
+        }
+      }
+      return;
+    }
+    const int slot = t - (int)(div_page(p.page, ok ? t : 0) * p.page.d);
+    const int64_t off = ok ? id * p.page_stride + slot * p.row_stride + head : -1;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int x = u % PH * kWave + ln, row = x / PC, piece = x - row * PC;
+      const int64_t o = shfl64(off, 16 * (run16 + u / PH) + row);
+      kreg[u] = vreg[u] = u32x4{0, 0, 0, 0};
+      if (o >= 0 && piece * 8 < D) {
+        kreg[u] = *reinterpret_cast<const u32x4*>(p.K + o + piece * 16);
+        vreg[u] = *reinterpret_cast<const u32x4*>(p.V + o + piece * 16);
+      }
+    }
+    if constexpr (TEAM == 4) stage(at_edge, buf);
   };
 
   u32x4 q[KS];
@@ -350,6 +420,7 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
   float m = -INFINITY, l = 0.f;
   int row0 = 0;  // of this wave
   auto open_row = [&](const Unit& c) {
+    const int col = anew(lane & 31), half = anew(lane >> 5);
     row0 = c.r * ROWS + (TEAM == 4 ? wave * kTeamRows : 0);
     const int row = row0 + col;
     const bool real = row < c.s.m * p.G;
@@ -360,6 +431,8 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
       const int d = k * 16 + half * 8;
       q[k] = u32x4{0, 0, 0, 0};
       if (real && d < p.D) q[k] = *reinterpret_cast<const u32x4*>(qp + d * 2);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[k][i] ^= p.flip;
     }
     int seen = 0;
     for (int w = 0; w < kMaskWords; ++w) {
@@ -389,6 +462,7 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
   };
   // Tokens a .. a + 31 that this lane's row sees, one bit each.
   auto sees = [&](const Unit& c, int a, uint32_t present) {
+    const int col = anew(lane & 31);
     const uint32_t cached = below(c.s.n - a) & ~below(sLow[wave][col] - a);
     const int j = a - c.s.n;  // the node of bit 0
     uint32_t drafted = 0;
@@ -401,13 +475,13 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
     return present & (cached | drafted);
   };
   // O^T += V^T P^T, from the A operands that `turn` makes of V's
-  auto v_operand = [&](int e, int s, int u) {
+  auto v_operand = [&](const unsigned char* sV, int e, int s, int u) {
     const int i = lane & 15;
     const int t = 32 * s + 16 * u + 4 * half + (i >> 2);
     const int piece = 4 * e + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
     typedef __attribute__((address_space(3))) s16x4* lds4;
-    const unsigned char* a = sV + t * DP * 2 + S::v_at(t, piece) * 16 + (i & 1) * 8;
-    const unsigned char* b = sV + (t + 8) * DP * 2 + S::v_at(t + 8, piece) * 16 + (i & 1) * 8;
+    const unsigned char* a = sV + (t * PC + S::v_at(t, piece)) * 16 + (i & 1) * 8;
+    const unsigned char* b = sV + ((t + 8) * PC + S::v_at(t + 8, piece)) * 16 + (i & 1) * 8;
     const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)a);
     const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)b);
     const u32x2 xu = __builtin_bit_cast(u32x2, x), yu = __builtin_bit_cast(u32x2, y);
@@ -426,23 +500,25 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
   // The infinite values and NaN that stage has left out, of the tiles from `first` to
   // c's, for the rows that see their tokens.
   auto add_odd = [&](const Unit& c, int first) {
+    const int half = anew(lane >> 5);
     Unit x = c;
     for (x.tile = first; x.tile <= c.tile; ++x.tile) {
-      if (!edge(x)) continue;
+      if (!edge(c.s, x.tile)) continue;
       for (int k = 0; k < TT; ++k) {
-        const int t = first_token(x) + k;
+        const int t = first_token(x.tile) + k;
         if (t < c.s.lo || t >= c.s.hi) continue;
         const int pg = div_page(p.page, t);
         const int id = p.table[(int64_t)c.b * p.width + pg];
         if ((uint32_t)id >= (uint32_t)p.n_pages || !(sees(c, t, 1u) & 1)) continue;
         const unsigned char* v = p.V + id * p.page_stride + (t - pg * (int)p.page.d) * p.row_stride +
                                  c.h * p.head_stride;
+        const int D = anew_uniform(p.D);
 #pragma unroll
         for (int e = 0; e < NE; ++e)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int d = 32 * e + 8 * r + 4 * half;
-            if (d >= p.D) continue;
+            if (d >= D) continue;
             const u32x2 u = *reinterpret_cast<const u32x2*>(v + d * 2);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -454,6 +530,7 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
     }
   };
   auto close_row = [&](const Unit& c, int first_tile, bool begins, bool ends) {
+    const int col = anew(lane & 31), half = anew(lane >> 5), tid = anew(threadIdx.x);
     if (sOdd[team]) add_odd(c, first_tile);
     const bool whole = begins && ends;
     float* const part = p.direct ? nullptr : part_of(begins ? 1 : 0);
@@ -530,118 +607,136 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
     }
   };
 
-  int owned = -1, last = 0;
-  if (tid < S::TEAMS) sOdd[tid] = 0;
-  __syncthreads();
-  if (left > 0) {
-    int first_tile = cur.tile;
-    Unit next = cur;
-    open_row(cur);
-    load(cur, page_id(cur));
-    int id_next = 0;
-    if (left > 1) {
-      advance(next);
-      id_next = page_id(next);
-    }
-    stage(edge(cur));
-    uint64_t present = present_next;
-    if (left > 1) load(next, id_next);
-    team_sync();
-    while (true) {
-      const bool more = left > 1;
-      const int a0 = first_token(cur);
-      f32x16 s[SUB];
+  // One tile: scores, weights, and their product with V.
+  auto compute = [&](const Unit& c, int tile, uint64_t there, const unsigned char* sK) {
+    const unsigned char* const sV = sK + S::TILE;
+    const int a0 = first_token(tile);
+    // Reads of LDS are issued well ahead of their use and kept there: a read that
+    // is waited for takes longer than a matrix instruction.
+    u32x4 k[KS][SUB];
+#pragma unroll
+    for (int i = 0; i < KS; ++i)
 #pragma unroll
       for (int x = 0; x < SUB; ++x) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s[x][r] = 0.f;
         const int t = 32 * x + col;
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-          s[x] = mma32<BF>(*reinterpret_cast<const u32x4*>(sK + t * DP * 2 + S::k_at(t, 2 * k + half) * 16),
-                           q[k], s[x]);
+        k[i][x] = *reinterpret_cast<const u32x4*>(sK + (t * PC + S::k_at(t, 2 * i + half)) * 16);
       }
-      if (p.flip)
+    __builtin_amdgcn_sched_barrier(0);
+    f32x16 s[SUB];
 #pragma unroll
-        for (int x = 0; x < SUB; ++x)
+    for (int x = 0; x < SUB; ++x)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) s[x][r] = -s[x][r];
-      constexpr uint64_t kFull = TT == 64 ? ~0ull : 0xffffffffull;
-      const uint64_t there = TT == 64 ? present : present & kFull;
-      const bool masks = there != kFull || a0 + TT > cur.s.n ||
-                         (p.window > 0 && a0 < cur.s.n + cur.s.m - p.window);
-      if (masks) {
+      for (int r = 0; r < 16; ++r) s[x][r] = 0.f;
 #pragma unroll
-        for (int x = 0; x < SUB; ++x) {
-          const uint32_t see = sees(cur, a0 + 32 * x, (uint32_t)(there >> (32 * x))) >> (4 * half);
+    for (int i = 0; i < KS; ++i)
 #pragma unroll
-          for (int r = 0; r < 16; ++r)
-            s[x][r] = see >> (8 * (r >> 2) + (r & 3)) & 1 ? s[x][r] : -INFINITY;
+      for (int x = 0; x < SUB; ++x) s[x] = mma32<BF>(k[i][x], q[i], s[x]);
+    u32x4 v[NE][SUB * 2];
+    auto read_v = [&](int e) {
+#pragma unroll
+      for (int y = 0; y < SUB * 2; ++y) v[e][y] = v_operand(sV, e, y / 2, y % 2);
+    };
+    read_v(0);
+    if constexpr (NE > 1) read_v(1);
+    __builtin_amdgcn_sched_barrier(0);
+    if (there != kFull || edge(c.s, tile)) {
+#pragma unroll
+      for (int x = 0; x < SUB; ++x) {
+        const uint32_t see = sees(c, a0 + 32 * x, (uint32_t)(there >> (32 * x))) >> (4 * half);
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          s[x][r] = see >> (8 * (r >> 2) + (r & 3)) & 1 ? s[x][r] : -INFINITY;
+      }
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int x = 0; x < SUB; ++x)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[x][r]);
+    top = fmaxf(top, __shfl_xor(top, 32, kWave));
+    if (!__all(top <= m)) {
+      const float mn = fmaxf(m, top);
+      const float alpha = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - mn) * p.scale);
+      m = mn;
+      l *= alpha;
+#pragma unroll
+      for (int e = 0; e < NE; ++e) acc[e] *= alpha;
+    }
+    const float base = (m == -INFINITY ? 0.f : m * p.scale) - kShift<BF>;
+    u32x4 hi[SUB][2], lo[SUB][2];
+#pragma unroll
+    for (int x = 0; x < SUB; ++x)
+#pragma unroll
+      for (int r = 0; r < 16; r += 2) {
+        const float w0 = __builtin_amdgcn_exp2f(fmaf(s[x][r], p.scale, -base));
+        const float w1 = __builtin_amdgcn_exp2f(fmaf(s[x][r + 1], p.scale, -base));
+        l += w0 + w1;
+        uint32_t h2, l2 = 0;
+        if constexpr (S::SPLIT) split2<BF>(w0, w1, h2, l2);
+        else h2 = pack2<BF>(w0, w1);
+        hi[x][r / 8][r % 8 / 2] = h2;
+        lo[x][r / 8][r % 8 / 2] = l2;
+      }
+#pragma unroll
+    for (int e = 0; e < NE; ++e) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (e + 2 < NE) read_v(e + 2);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int y = 0; y < SUB * 2; ++y) {
+        acc[e] = mma32<BF>(v[e][y], hi[y / 2][y % 2], acc[e]);
+        if constexpr (S::SPLIT) acc[e] = mma32<BF>(v[e][y], lo[y / 2][y % 2], acc[e]);
+      }
+    }
+  };
+
+  int owned = -1, last = 0;
+  if (tid < S::TEAMS) sOdd[tid] = 0;
+  if (S::BUFFERS == 2 && p.D < DP)  // direct copies leave the numbers past a head's end out
+    for (int i = tid; i < S::TILES / 16; i += kTreeThreads)
+      *reinterpret_cast<u32x4*>(sTiles + i * 16) = u32x4{0, 0, 0, 0};
+  __syncthreads();
+  if (left > 0) {
+    unsigned char* buf = sTeam;
+    int id = page_id(cur, cur.tile);
+    fetch(cur, cur.tile, id, buf);
+    while (true) {
+      // the tiles [first, end) of one row
+      const int first = cur.tile;
+      const int end = (uint32_t)(cur.s.t1 - first) < left ? cur.s.t1 : first + (int)left;
+      left -= end - first;
+      const bool begins = first == cur.s.t0, ends = end == cur.s.t1;
+      const uint32_t row_end = run_end - left + (cur.s.t1 - end);  // the unit after this row
+      Unit next = cur;
+      if (left > 0) next_row(next);
+      id = end - first > 1 ? page_id(cur, first + 1) : left > 0 ? page_id(next, next.tile) : 0;
+      open_row(cur);
+      for (int tile = first; tile < end; ++tile) {
+        const uint64_t there = present;
+        if (TEAM == 4) {
+          __builtin_amdgcn_s_waitcnt(kNoLoads);
+          __syncthreads();  // this tile is there, and the one before it has been read
+        } else {
+          stage(edge(cur.s, tile), buf);
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         }
-      }
-      float top = s[0][0];
-#pragma unroll
-      for (int x = 0; x < SUB; ++x)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[x][r]);
-      top = fmaxf(top, __shfl_xor(top, 32, kWave));
-      if (!__all(top <= m)) {
-        const float mn = fmaxf(m, top);
-        const float alpha = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - mn) * p.scale);
-        m = mn;
-        l *= alpha;
-#pragma unroll
-        for (int e = 0; e < NE; ++e) acc[e] *= alpha;
-      }
-      const float base = (m == -INFINITY ? 0.f : m * p.scale) - kShift<BF>;
-      u32x4 hi[SUB][2], lo[SUB][2];
-#pragma unroll
-      for (int x = 0; x < SUB; ++x)
-#pragma unroll
-        for (int r = 0; r < 16; r += 2) {
-          const float w0 = __builtin_amdgcn_exp2f(fmaf(s[x][r], p.scale, -base));
-          const float w1 = __builtin_amdgcn_exp2f(fmaf(s[x][r + 1], p.scale, -base));
-          l += w0 + w1;
-          uint32_t h2, l2 = 0;
-          if constexpr (S::SPLIT) split2<BF>(w0, w1, h2, l2);
-          else h2 = pack2<BF>(w0, w1);
-          hi[x][r / 8][r % 8 / 2] = h2;
-          lo[x][r / 8][r % 8 / 2] = l2;
+        unsigned char* const to = S::BUFFERS == 1 ? buf : buf == sTeam ? sTeam + 2 * S::TILE : sTeam;
+        const bool here = tile + 1 < end;  // the tile that follows is this row's
+        if (here || left > 0) {
+          fetch(here ? cur : next, here ? tile + 1 : next.tile, id, to);
+          if (here) id = tile + 2 < end ? page_id(cur, tile + 2) : left > 0 ? page_id(next, next.tile) : 0;
         }
-#pragma unroll
-      for (int e = 0; e < NE; ++e)
-#pragma unroll
-        for (int x = 0; x < SUB; ++x)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const u32x4 v = v_operand(e, x, u);
-            acc[e] = mma32<BF>(v, hi[x][u], acc[e]);
-            if constexpr (S::SPLIT) acc[e] = mma32<BF>(v, lo[x][u], acc[e]);
-          }
-      --left;
-      const bool ends = cur.tile + 1 == cur.s.t1;
-      if (ends || !more) {
-        const bool begins = first_tile == cur.s.t0;
-        close_row(cur, first_tile, begins, ends);
-        if (begins && !ends) {  // goes on in the following workgroups
-          owned = (cur.r * p.B + cur.b) * p.Hkv + cur.h;
-          last = (int)cut.part_of(run_end - left - 1 + (cur.s.t1 - cur.tile - 1));
-        }
+        compute(cur, tile, there, buf);
+        buf = to;
       }
-      if (!more) break;
-      team_sync();  // the tile has been read
-      stage(edge(next));
-      present = present_next;
+      cur.tile = end - 1;
+      close_row(cur, first, begins, ends);
+      if (begins && !ends) {  // goes on in the following workgroups
+        owned = (cur.r * p.B + cur.b) * p.Hkv + cur.h;
+        last = (int)cut.part_of(row_end - 1);
+      }
+      if (left == 0) break;
       cur = next;
-      if (ends) {
-        first_tile = cur.tile;
-        open_row(cur);
-      }
-      if (left > 1) {
-        advance(next);
-        load(next, page_id(next));
-      }
-      team_sync();
     }
   }
   if (!p.direct && tid == 0) p.owner[blockIdx.x] = make_int2(owned, last);
@@ -662,61 +757,97 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
   }
 }
 
-// Joins the partial results of the row blocks that span workgroups: one workgroup for
-// RPW rows of the block that workgroup blockIdx.x began and left unfinished, a wave's
-// lanes over the numbers of a row and, as far as they reach, over its parts.
-template <bool BF, int ROWS>
+// Joins the partial results of the row blocks that span workgroups: one workgroup for RJ
+// rows of the block that workgroup blockIdx.x began and left unfinished.  A group of lanes,
+// a power of two that holds D / 4, takes a row's numbers; where there are more groups than
+// rows, they share a row's parts.
+template <int DP>
+constexpr int join_lanes() {
+  return DP <= 64 ? 16 : DP <= 128 ? 32 : 64;
+}
+template <bool BF, int DP, int ROWS, int RJ>
 __global__ __launch_bounds__(kTreeThreads) void tree_join_kernel(TreeParams p) {
-  __shared__ float sAcc[kTreeWaves][256], sMax[kTreeWaves], sSum[kTreeWaves];
+  constexpr int CL = join_lanes<DP>(), GROUPS = kTreeThreads / CL;
+  constexpr int SHARE = GROUPS > RJ ? GROUPS / RJ : 1;  // groups that share a row
+  constexpr int ML = kTreeThreads / RJ;                 // threads that look for a row's maximum
+  extern __shared__ float sW[];                         // [parts][RJ]: weights of the parts
+  __shared__ float sRed[2][RJ][ML];
+  __shared__ __attribute__((aligned(16))) float sV[SHARE > 1 ? GROUPS * CL * 4 : 4];
   const int2 own = p.owner[blockIdx.x];
   if (own.x < 0) return;
   const int h = own.x % p.Hkv, rest = own.x / p.Hkv, b = rest % p.B, r = rest / p.B;
   const int nodes = p.nodes ? p.nodes[b] : p.T;
-  const int m = nodes < p.T ? nodes : p.T;
-  const int row = r * ROWS + blockIdx.y;
-  if (row >= m * p.G) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
+  const int in0 = blockIdx.y * RJ, row0 = r * ROWS + in0;
+  const int rows = (nodes < p.T ? nodes : p.T) * p.G - row0;
+  if (rows <= 0) return;
+  const int tid = threadIdx.x;
   const int64_t size = part_floats(ROWS, p.D);
   const int n = own.y - (int)blockIdx.x + 1;
   // part 0 is this workgroup's second slot, the others the first slots that follow
   auto part = [&](int k) {
     return p.partial + (2 * ((int64_t)blockIdx.x + k) + (k == 0 ? 1 : 0)) * size;
   };
-  const int at_m = ROWS * p.D + blockIdx.y, at_l = at_m + ROWS;
-  float mm = -INFINITY;
-  for (int k = tid; k < n; k += kTreeThreads) mm = fmaxf(mm, part(k)[at_m]);
+  {
+    const int j = tid % RJ, k0 = tid / RJ;
+    const int at_m = ROWS * p.D + in0 + j, at_l = at_m + ROWS;
+    float m = -INFINITY, sum = 0.f;
+    if (j < rows)
+      for (int k = k0; k < n; k += ML) m = fmaxf(m, part(k)[at_m]);
+    sRed[0][j][k0] = m;
+    __syncthreads();
+    m = -INFINITY;
+    for (int k = 0; k < ML; ++k) m = fmaxf(m, sRed[0][j][k]);
+    const float base = m == -INFINITY ? 0.f : m;
+    if (j < rows)
+      for (int k = k0; k < n; k += ML) {
+        // a part without weight adds nothing, also where it has met NaN
+        const float lk = part(k)[at_l], w = __builtin_amdgcn_exp2f(part(k)[at_m] - base);
+        sW[k * RJ + j] = lk == 0.f ? 0.f : w;
+        sum += w * lk;
+      }
+    sRed[1][j][k0] = sum;
+    __syncthreads();
+  }
+  const int group = tid / CL, col = tid % CL * 4;
+  for (int j0 = 0; j0 < RJ; j0 += GROUPS / SHARE) {
+    const int j = j0 + group / SHARE, share = group % SHARE;
+    if (j0 >= rows) break;
+    float4v v = {0, 0, 0, 0};
+    if (j < rows && col < p.D) {
+      constexpr int U = 4;
+      for (int k0 = share; k0 < n; k0 += U * SHARE) {
+        float4v x[U];
+        float w[U];
 #pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) mm = fmaxf(mm, __shfl_xor(mm, off, kWave));
-  if (lane == 0) sMax[wave] = mm;
-  __syncthreads();
+        for (int u = 0; u < U; ++u) {
+          const int k = k0 + u * SHARE;
+          x[u] = *reinterpret_cast<const float4v*>(part(k < n ? k : n - 1) + (int64_t)(in0 + j) * p.D + col);
+          w[u] = k < n ? sW[k * RJ + j] : 0.f;
+        }
 #pragma unroll
-  for (int w = 0; w < kTreeWaves; ++w) mm = fmaxf(mm, sMax[w]);
-  const float base = mm == -INFINITY ? 0.f : mm;
-  float sum = 0.f;
-  float4v v = {0, 0, 0, 0};
-  for (int k = wave; k < n; k += kTreeWaves) {
-    const float* o = part(k);
-    const float f = __builtin_amdgcn_exp2f(o[at_m] - base), lk = o[at_l];
-    sum += f * lk;
-    if (lane * 4 < p.D) {
-      const float4v x = *reinterpret_cast<const float4v*>(o + (int64_t)blockIdx.y * p.D + lane * 4);
-      if (lk != 0.f) v += f * x;
+        for (int u = 0; u < U; ++u)
+          if (w[u] != 0.f) v += w[u] * x[u];
+      }
+    }
+    if constexpr (SHARE > 1) {
+      *reinterpret_cast<float4v*>(sV + tid * 4) = v;
+      __syncthreads();
+      v = float4v{0, 0, 0, 0};
+      for (int i = 0; i < SHARE; ++i)
+        v += *reinterpret_cast<const float4v*>(sV + ((group / SHARE * SHARE + i) * CL) * 4 + col);
+      __syncthreads();
+    }
+    if (share == 0 && j < rows && col < p.D) {
+      float m = -INFINITY, total = 0.f;
+      for (int k = 0; k < ML; ++k) {
+        m = fmaxf(m, sRed[0][j][k]);
+        total += sRed[1][j][k];
+      }
+      const int row = row0 + j, i = div_page(p.group, row), g = row - i * p.G;
+      store_row<BF>(p, ((int64_t)b * p.T + i) * p.Hq + h * p.G + g, col, m, total,
+                    total == 0.f ? 0.f : 1.f / total, v);
     }
   }
-  *reinterpret_cast<float4v*>(&sAcc[wave][lane * 4]) = v;
-  if (lane == 0) sSum[wave] = sum;
-  __syncthreads();
-  if (wave != 0 || lane * 4 >= p.D) return;
-  float total = 0.f;
-  float4v t = {0, 0, 0, 0};
-#pragma unroll
-  for (int w = 0; w < kTreeWaves; ++w) {
-    total += sSum[w];
-    t += *reinterpret_cast<const float4v*>(&sAcc[w][lane * 4]);
-  }
-  const int i = div_page(p.group, row), g = row - i * p.G;
-  store_row<BF>(p, ((int64_t)b * p.T + i) * p.Hq + h * p.G + g, lane * 4, mm, total,
-                total == 0.f ? 0.f : 1.f / total, t);
 }
 
 // The path from the root to every node: bit j of word w of node i is set where node
@@ -759,25 +890,24 @@ __global__ __launch_bounds__(kTreeThreads) void tree_mask_kernel(const int32_t* 
   if (depth) depth[tree * T + i] = n - 1;
 }
 
-constexpr int64_t kMostTreeBlocks = 1024;
-
 struct TreeGrid {
-  int64_t blocks;
+  int64_t grid;
   bool direct, wide;
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Workgroups per CU, for which the registers are laid out.
+constexpr int tree_per_cu(int64_t D) { return D > 128 ? 1 : 2; }
+
 TreeGrid tree_grid(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity) {
   const int64_t rows = T * (Hq / Hkv);
   const bool wide = rows > kTeamRows;
-  const int64_t block_rows = wide ? 4 * kTeamRows : kTeamRows, unit = wide ? 64 : 128;
-  const int64_t blocks = B * Hkv * ceil_div(rows, block_rows);
-  const int64_t tiles = ceil_div(capacity, unit);
-  if (tiles <= 4) return {blocks, true, wide};
-  int64_t grid = device_cus() * (D > 128 ? 1 : 2);
-  if (grid > kMostTreeBlocks) grid = kMostTreeBlocks;
-  return {blocks * tiles < grid ? blocks * tiles : grid, false, wide};
+  const int64_t blocks = B * Hkv * ceil_div(rows, wide ? 4 * kTeamRows : kTeamRows);
+  const int64_t tiles = ceil_div(capacity, wide ? 64 : 128) + 1;  // a window may begin inside one
+  const int64_t at_once = device_cus() * tree_per_cu(D);
+  if (tiles <= 5 || blocks >= 4 * at_once) return {blocks, true, wide};
+  return {blocks * tiles < at_once ? blocks * tiles : at_once, false, wide};
 }
 
 template <bool BF, int DP, int TEAM>
@@ -792,8 +922,9 @@ hipError_t launch_tree(const TreeParams& p, int64_t grid, hipStream_t s) {
   hipLaunchKernelGGL(fn, dim3((uint32_t)grid), dim3(kTreeThreads), Sh::LDS, s, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.direct) return e;
-  hipLaunchKernelGGL((tree_join_kernel<BF, Sh::ROWS>), dim3((uint32_t)grid, Sh::ROWS),
-                     dim3(kTreeThreads), 0, s, p);
+  constexpr int RJ = TEAM == 4 ? 16 : 2;
+  hipLaunchKernelGGL((tree_join_kernel<BF, DP, Sh::ROWS, RJ>), dim3((uint32_t)grid, Sh::ROWS / RJ),
+                     dim3(kTreeThreads), (int)grid * RJ * 4, s, p);
   return hipGetLastError();
 }
 
@@ -813,7 +944,7 @@ int64_t tree_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int6
   const TreeGrid g = tree_grid(B, T, Hq, Hkv, D, capacity);
   if (g.direct) return 0;
   const int rows = g.wide ? 4 * kTeamRows : kTeamRows;
-  return g.blocks * (2 * part_floats(rows, (int)D) * (int64_t)sizeof(float) + (int64_t)sizeof(int2));
+  return g.grid * (2 * part_floats(rows, (int)D) * (int64_t)sizeof(float) + (int64_t)sizeof(int2));
 }
 
 hipError_t launch_tree_attention(int dtype, const TreeArgs& a, hipStream_t stream) {
@@ -847,21 +978,22 @@ hipError_t launch_tree_attention(int dtype, const TreeArgs& a, hipStream_t strea
   p.D = (int32_t)a.D;
   p.G = (int32_t)(a.Hq / a.Hkv);
   p.window = (int32_t)a.window;
-  p.flip = a.scale_log2 < 0;
+  p.flip = a.scale_log2 < 0 ? 0x80008000u : 0u;
+  p.runs = a.page_size % 16 == 0;
   // a scale of zero as the least normal number: the exponents of finite scores round to
   // zero all the same, and a masked score stays -inf
-  const float scale = p.flip ? -a.scale_log2 : a.scale_log2;
+  const float scale = fabsf(a.scale_log2);
   p.scale = scale < 0x1p-126f ? 0x1p-126f : scale;
   const TreeGrid g = tree_grid(a.B, a.T, a.Hq, a.Hkv, a.D, a.width * a.page_size);
   p.direct = g.direct;
   p.owner = reinterpret_cast<int2*>(
-      p.partial + 2 * g.blocks * part_floats(g.wide ? 4 * kTeamRows : kTeamRows, p.D));
+      p.partial + 2 * g.grid * part_floats(g.wide ? 4 * kTeamRows : kTeamRows, p.D));
   const bool bf = dtype == TQ_BF16;
   if (g.wide)
-    return bf ? launch_tree_d<true, 4>(p, g.blocks, stream)
-              : launch_tree_d<false, 4>(p, g.blocks, stream);
-  return bf ? launch_tree_d<true, 1>(p, g.blocks, stream)
-            : launch_tree_d<false, 1>(p, g.blocks, stream);
+    return bf ? launch_tree_d<true, 4>(p, g.grid, stream)
+              : launch_tree_d<false, 4>(p, g.grid, stream);
+  return bf ? launch_tree_d<true, 1>(p, g.grid, stream)
+            : launch_tree_d<false, 1>(p, g.grid, stream);
 }
 
 hipError_t launch_tree_mask(const int32_t* parents, int64_t B, int64_t T, void* mask,
