@@ -79,6 +79,26 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((float2v{x, y}), half2));
 }
 
+// A value that the compiler takes for a new one: what follows from it is computed where it
+// stands, instead of being kept in registers through the whole loop.
+__device__ __forceinline__ int anew(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+__device__ __forceinline__ int anew_uniform(int v) {
+  asm volatile("" : "+s"(v));
+  return v;
+}
+
+// f of the values that the lanes l and l ^ 32 hold.
+template <class F>
+__device__ __forceinline__ float over_halves(float x, F f) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto both = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const uint32_t low = both[0], high = both[1];
+  return f(__builtin_bit_cast(float, low), __builtin_bit_cast(float, high));
+}
+
 __device__ __forceinline__ int64_t shfl64(int64_t v, int src) {
   const int lo = __shfl((int)v, src, kWave), hi = __shfl((int)(v >> 32), src, kWave);
   return ((int64_t)hi << 32) | (uint32_t)lo;
@@ -106,17 +126,6 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, int off, unsigne
   const uint32_t to = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)dst;
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :: "s"(to), "v"(off), "s"(r) : "memory", "m0");
-}
-
-// A value that the compiler takes for a new one: what follows from it is computed where it
-// stands, instead of being kept in registers through the whole loop.
-__device__ __forceinline__ int anew(int v) {
-  asm volatile("" : "+v"(v));
-  return v;
-}
-__device__ __forceinline__ int anew_uniform(int v) {
-  asm volatile("" : "+s"(v));
-  return v;
 }
 
 // The low n bits, n of any value.
@@ -165,9 +174,13 @@ struct Unit {
   Seq s;
 };
 
-// Weights are 2^(x - m + kShift): in fp16 the smaller ones then keep all their bits.
+// Weights are 2^(x - m + kShift): in fp16 the smaller ones then keep all their bits.  m follows
+// the row's maximum only where that has risen by more than kSlack, so weights may reach
+// 2^(kShift + kSlack) (fp16: 2^15): with many rows some maximum rises in most tiles, and
+// every change multiplies all sums.
 template <bool BF>
-constexpr float kShift = BF ? 0.f : 14.f;
+constexpr float kShift = BF ? 0.f : 9.f;
+constexpr float kSlack = 6.f;
 
 // Divides by the sum and writes numbers d .. d + 3 of one query, and its lse.
 template <bool BF>
@@ -240,11 +253,15 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
   const int run16 = TEAM == 4 ? wave : 0;  // the first run of 16 tokens that this wave loads
   unsigned char* const sTeam = sTiles + team * 2 * S::TILE * S::BUFFERS;
 
-  // This workgroup's run of units: of the list (row block, sequence, head, tile), one of
-  // gridDim.x equal ones.
+  // This workgroup's run of units: every row block has a list (sequence, head, tile) of the
+  // sequences that reach it, and workgroups by its length, which cut it into equal
+  // runs.  Of equal lists workgroups i of all blocks then read the same tokens at the
+  // same time on the same XCD (their number mostly being a multiple of 8), and all but
+  // the first find them in its L2.
   Unit cur{};
   uint32_t left = 0, run_end = 0;
   Cut cut(0, 1);
+  int part = 0;  // of the runs of its list
   if (p.direct) {
     const int rows = p.B * p.Hkv, rest = blockIdx.x % rows;
     cur.r = blockIdx.x / rows;
@@ -260,28 +277,42 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
       return in && b < p.B && s.blocks > r ? s.t1 - s.t0 : 0;
     };
     uint32_t all = 0;  // tiles x blocks
+    int most = 0;      // blocks
     for (int i = 0; i < per; ++i) {
       const int b = lane * per + i;
       const Seq s = read_seq<UT, ROWS>(p, b < p.B ? b : p.B - 1);
-      if (b < p.B) all += (uint32_t)(s.t1 - s.t0) * s.blocks;
+      if (b < p.B) {
+        all += (uint32_t)(s.t1 - s.t0) * s.blocks;
+        most = s.blocks > most ? s.blocks : most;
+      }
     }
     all = uni((int)__shfl(scan_wave(all, lane), 63, kWave));
-    cut = Cut(all * p.Hkv, gridDim.x);
-    if (blockIdx.x < cut.parts) {
-      uint32_t at = cut.start(blockIdx.x);
-      run_end = cut.start(blockIdx.x + 1);
-      left = run_end - at;
-      // the row block, the lane that looks after the sequence, the sequence
-      uint32_t mine = 0, inc = 0;
-      for (;; ++cur.r) {
-        mine = 0;
-        for (int i = 0; i < per; ++i) mine += tiles_of(lane * per + i, true, cur.r);
-        inc = scan_wave(mine, lane);
-        const uint32_t total = uni((int)__shfl(inc, 63, kWave)) * (uint32_t)p.Hkv;
-        // (the bounds here hold whatever happens to the lengths meanwhile)
-        if (at < total || cur.r >= p.T * p.G / ROWS) break;
-        at -= total;
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) {
+      const int o = __shfl_xor(most, off, kWave);
+      most = o > most ? o : most;
+    }
+    // one workgroup for each block, and of the others its share
+    const uint32_t spare = gridDim.x - uni(most);
+    uint32_t mine = 0, inc = 0, first = 0;
+    for (; cur.r < uni(most); ++cur.r) {
+      mine = 0;
+      for (int i = 0; i < per; ++i) mine += tiles_of(lane * per + i, true, cur.r);
+      inc = scan_wave(mine, lane);
+      const uint32_t total = uni((int)__shfl(inc, 63, kWave));
+      const uint32_t share = 1 + (uint32_t)((uint64_t)total * spare / (all ? all : 1));
+      if (blockIdx.x < first + share) {
+        cut = Cut(total * p.Hkv, share);
+        part = blockIdx.x - first;
+        break;
       }
+      first += share;
+    }
+    if ((uint32_t)part < cut.parts) {
+      uint32_t at = cut.start(part);
+      run_end = cut.start(part + 1);
+      left = run_end - at;
+      // the lane that looks after the sequence, the sequence
       const uint64_t has = __ballot(at < inc * p.Hkv);
       const int src = has ? __builtin_ctzll(has) : 0;
       at -= (uint32_t)__builtin_amdgcn_readlane((int)(inc - mine), src) * p.Hkv;
@@ -298,6 +329,7 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
         }
         at -= (uint32_t)__builtin_amdgcn_readlane((int)run, kWave - 1) * p.Hkv;
       }
+      // (the bounds hold whatever happens to the lengths meanwhile)
       if (cur.b >= p.B) cur.b = p.B - 1;
       cur.s = read_seq<UT, ROWS>(p, cur.b);
       const uint32_t n = cur.s.t1 > cur.s.t0 ? cur.s.t1 - cur.s.t0 : 1;
@@ -306,21 +338,17 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
       if (cur.h >= p.Hkv) cur.h = p.Hkv - 1;
     }
   }
-  // The first unit after c's row (of a row block, sequence and head).
+  // The first unit after c's row (of a sequence and head).
   auto next_row = [&](Unit& c) {
     if (++c.h == p.Hkv) {
       c.h = 0;
-      while (true) {
-        if (++c.b == p.B) {
-          c.b = 0;
-          if (++c.r > p.T * p.G / ROWS) {  // past the end (the lengths have changed)
-            left = 0;
-            return;
-          }
+      do {
+        if (++c.b >= p.B) {  // past the end (the lengths have changed)
+          left = 0;
+          return;
         }
         c.s = read_seq<UT, ROWS>(p, c.b);
-        if (c.s.t1 > c.s.t0 && c.s.blocks > c.r) break;
-      }
+      } while (c.s.t1 <= c.s.t0 || c.s.blocks <= c.r);
     }
     c.tile = c.s.t0;
   };
@@ -385,7 +413,7 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
         const auto rk = rsrc_at(p.K + at), rv = rsrc_at(p.V + at);
 #pragma unroll
         for (int u = 0; u < PH; ++u) {
-          const int x = u * kWave + ln, row = x / PC, place = x - row * PC;
+          const int x = u * kWave + (TEAM == 4 ? lane : ln), row = x / PC, place = x - row * PC;
           if constexpr (TEAM == 4) {
             unsigned char* to = buf + (run16 * 16 * PC + u * kWave) * 16;
             const int kp = S::k_at(row, place), vp = S::v_at(row, place);
@@ -535,7 +563,7 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
     const bool whole = begins && ends;
     float* const part = p.direct ? nullptr : part_of(begins ? 1 : 0);
     const int rows = c.s.m * p.G;
-    const float sum = l + __shfl_xor(l, 32, kWave);
+    const float sum = over_halves(l, [](float x, float y) { return x + y; });
     if constexpr (TEAM == 4) {
       const int row = row0 + col;
       if (row < rows) {
@@ -653,8 +681,8 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
     for (int x = 0; x < SUB; ++x)
 #pragma unroll
       for (int r = 0; r < 16; ++r) top = fmaxf(top, s[x][r]);
-    top = fmaxf(top, __shfl_xor(top, 32, kWave));
-    if (!__all(top <= m)) {
+    top = over_halves(top, [](float x, float y) { return fmaxf(x, y); });
+    if (!__all(top <= m || (top - m) * p.scale <= kSlack)) {
       const float mn = fmaxf(m, top);
       const float alpha = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - mn) * p.scale);
       m = mn;
@@ -733,7 +761,7 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
       close_row(cur, first, begins, ends);
       if (begins && !ends) {  // goes on in the following workgroups
         owned = (cur.r * p.B + cur.b) * p.Hkv + cur.h;
-        last = (int)cut.part_of(row_end - 1);
+        last = (int)blockIdx.x - part + (int)cut.part_of(row_end - 1);
       }
       if (left == 0) break;
       cur = next;
@@ -906,7 +934,8 @@ TreeGrid tree_grid(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int
   const int64_t blocks = B * Hkv * ceil_div(rows, wide ? 4 * kTeamRows : kTeamRows);
   const int64_t tiles = ceil_div(capacity, wide ? 64 : 128) + 1;  // a window may begin inside one
   const int64_t at_once = device_cus() * tree_per_cu(D);
-  if (tiles <= 5 || blocks >= 4 * at_once) return {blocks, true, wide};
+  if (tiles <= 5 || blocks >= 4 * at_once || 4 * blocks >= at_once * B * Hkv)
+    return {blocks, true, wide};
   return {blocks * tiles < at_once ? blocks * tiles : at_once, false, wide};
 }
 
