@@ -32,12 +32,13 @@ struct SelectParams {
   int32_t* counts;
   float* sums;
   int32_t S, B, H, budget, recent, sinks;
+  int32_t sorted;  // rows are taken longest first
 };
 
 constexpr int kDigits = 3;
-__device__ constexpr int kDigitShift[kDigits] = {21, 10, 0};
-__device__ constexpr int kDigitBits[kDigits] = {11, 11, 10};
 constexpr int kBins = 2048;
+__device__ __forceinline__ constexpr int digit_shift(int d) { return d == 0 ? 21 : d == 1 ? 10 : 0; }
+__device__ __forceinline__ constexpr int digit_bits(int d) { return d == 2 ? 10 : 11; }
 
 // A weight as a whole number of the same order: -0 as 0, NaN as the least.
 __device__ __forceinline__ uint32_t order_of(float x) {
@@ -46,82 +47,202 @@ __device__ __forceinline__ uint32_t order_of(float x) {
   return u >> 31 ? ~u : u | 0x80000000u;
 }
 
+template <int WAVES>
+struct SelectShared {
+  int count[kBins];
+  int sum[WAVES];
+  int2 part[WAVES];
+  uint32_t digit;
+  int rest, same;
+};
+
+// The tokens of one row as whole numbers of the order in which they stay: kAlways for the
+// first and the last ones, 0 past the end, no weight being either.  A workgroup of WAVES
+// waves reads them, each wave a run of `steps` times 64.  KPT > 0: they stay in
+// registers (steps <= KPT), otherwise every pass reads them again.
+constexpr uint32_t kAlways = 0xffffffffu;
+template <int WAVES, int KPT>
+struct Tokens {
+  const float* x;
+  int n, lo, hi, first, steps;
+  uint32_t held[KPT > 0 ? KPT : 1];
+  __device__ __forceinline__ uint32_t key(int i, float v) const {
+    return i >= n ? 0u : i < lo || i >= hi ? kAlways : order_of(v);
+  }
+  __device__ __forceinline__ Tokens(const SelectParams& p, const float* scores, int tokens) {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    x = scores;
+    n = tokens;
+    lo = p.sinks;
+    hi = n - p.recent;
+    steps = (int)(((uint32_t)n + WAVES * kWave - 1) / (WAVES * kWave));
+    first = wave * steps * kWave + lane;  // (up to 2^30 tokens: the last index stays below 2^31)
+    if constexpr (KPT > 0) {
+      float v[KPT];
+#pragma unroll
+      for (int j = 0; j < KPT; ++j) {
+        const int i = first + j * kWave;
+        v[j] = j < steps && i < n ? x[(uint32_t)i] : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < KPT; ++j) held[j] = key(first + j * kWave, v[j]);
+    }
+  }
+  // f(index, key) for this lane's tokens, in steps that the whole wave takes.
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+    if constexpr (KPT > 0) {
+#pragma unroll
+      for (int j = 0; j < KPT; ++j)
+        if (j < steps) f(first + j * kWave, held[j]);
+    } else {
+      for (int j0 = 0; j0 < steps; j0 += 4) {
+        float v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = first + (j0 + u) * kWave;
+          v[u] = j0 + u < steps && i < n ? x[i] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (j0 + u < steps) f(first + (j0 + u) * kWave, key(first + (j0 + u) * kWave, v[u]));
+      }
+    }
+  }
+};
+
+// Chooses among the n > budget tokens of a row.
+template <int WAVES, int KPT>
+__device__ __forceinline__ void choose(const SelectParams& p, SelectShared<WAVES>& sh, const float* x,
+                                       int n, int32_t* keep, float* sums) {
+  constexpr int THREADS = WAVES * kWave;
+  constexpr int BINS = kBins / THREADS;  // of a thread
+  const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
+  const Tokens<WAVES, KPT> row(p, x, n);
+  int want = p.budget - p.sinks - p.recent;  // of the tokens between
+  // Those above `most` stay, and of those from `least` on the first `want`.
+  uint32_t least = kAlways, most = kAlways - 1;
+  if (want > 0) {
+    least = 0;
+    for (int d = 0; d < kDigits; ++d) {
+      const int shift = digit_shift(d), bits = digit_bits(d), above = shift + bits;
+#pragma unroll
+      for (int k = 0; k < BINS; ++k) sh.count[k * THREADS + t] = 0;
+      __syncthreads();
+      row.each([&](int, uint32_t u) {
+        if (d == 0 ? u - 1 < kAlways - 1 : u >> above == least >> above)
+          atomicAdd(&sh.count[u >> shift & ((1u << bits) - 1)], 1);
+      });
+      __syncthreads();
+      // from the heaviest bin down, BINS a thread
+      int c[BINS], mine = 0;
+#pragma unroll
+      for (int k = 0; k < BINS; ++k) mine += c[k] = sh.count[kBins - 1 - (t * BINS + k)];
+      int inc = mine;
+#pragma unroll
+      for (int off = 1; off < kWave; off <<= 1) {
+        const int o = __shfl_up(inc, off, kWave);
+        inc += lane >= off ? o : 0;
+      }
+      if (lane == 63) sh.sum[wave] = inc;
+      __syncthreads();
+      int before = inc - mine;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) before += w < wave ? sh.sum[w] : 0;
+#pragma unroll
+      for (int k = 0; k < BINS; ++k) {
+        if (before < want && want <= before + c[k]) {
+          sh.digit = kBins - 1 - (t * BINS + k);
+          sh.rest = want - before;
+          sh.same = c[k];
+        }
+        before += c[k];
+      }
+      __syncthreads();
+      least |= sh.digit << shift;
+      most = least | ((1u << shift) - 1);
+      want = sh.rest;
+      if (want == sh.same) break;  // all of this bin stay, whatever their further digits
+    }
+  } else {
+    want = 0;
+  }
+  int more_before = 0, tie_before = 0;  // of this wave, then of those before it
+  row.each([&](int, uint32_t u) {
+    more_before += __popcll(__ballot(u > most));
+    tie_before += __popcll(__ballot(u >= least));
+  });
+  if (lane == 0) sh.part[wave] = make_int2(more_before, tie_before - more_before);
+  __syncthreads();
+  more_before = tie_before = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    const int2 o = sh.part[w];
+    more_before += w < wave ? o.x : 0;
+    tie_before += w < wave ? o.y : 0;
+  }
+  auto rank = [](uint64_t mask) {  // lanes of it before this one
+    return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                          __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+  };
+  row.each([&](int i, uint32_t u) {
+    const uint64_t m = __ballot(u > most), e = __ballot(u >= least) & ~m;
+    if (!(m | e)) return;
+    const int ties = tie_before + rank(e);
+    const int at = more_before + rank(m) + (ties < want ? ties : want);
+    if (u > most || (u >= least && ties < want)) {
+      keep[at] = i;
+      if (sums) sums[at] = x[i];
+    }
+    more_before += __popcll(m);
+    tie_before += __popcll(e);
+  });
+}
+
 // One workgroup per (sequence, head).
-__global__ __launch_bounds__(kScanThreads) void cache_select_kernel(SelectParams p) {
-  __shared__ int sCount[kBins];
-  __shared__ int red[kScanThreads / kWave];
-  __shared__ uint32_t sDigit;
-  __shared__ int sRest;
+template <int WAVES>
+__global__ __launch_bounds__(WAVES * kWave, 4) void cache_select_kernel(SelectParams p) {
+  constexpr int THREADS = WAVES * kWave;
+  __shared__ SelectShared<WAVES> sh;
   const int t = threadIdx.x;
-  const int b = blockIdx.x / p.H, h = blockIdx.x - b * p.H;
+  int b = blockIdx.x / p.H;
+  const int h = blockIdx.x - b * p.H;
+  if (p.sorted) {
+    // the longest sequences first: workgroup b of a head takes the one of rank b
+    if (t < kWave) {
+      const int mine = t < p.B ? p.lens[t] : INT32_MIN;
+      int rank = 0;
+      for (int i = 0; i < p.B; ++i) {
+        const int other = __builtin_amdgcn_readlane(mine, i);
+        rank += other > mine || (other == mine && i < t);
+      }
+      if (t < p.B && rank == b) sh.rest = t;
+    }
+    __syncthreads();
+    b = sh.rest;
+    __syncthreads();
+  }
+  const int row = b * p.H + h;
   const int len = p.lens[b];
   const int n = len < 0 ? 0 : len < p.S ? len : p.S;
   const float* x = p.scores + b * p.s_seq + h * p.s_head;
-  int32_t* keep = p.keep + (int64_t)blockIdx.x * p.budget;
-  float* sums = p.sums ? p.sums + (int64_t)blockIdx.x * p.budget : nullptr;
+  int32_t* keep = p.keep + (int64_t)row * p.budget;
+  float* sums = p.sums ? p.sums + (int64_t)row * p.budget : nullptr;
   if (h == 0 && t == 0) p.counts[b] = n < p.budget ? n : p.budget;
   if (n <= p.budget) {
-    for (int i = t; i < p.budget; i += kScanThreads) {
+    for (int i = t; i < p.budget; i += THREADS) {
       keep[i] = i < n ? i : -1;
       if (sums) sums[i] = i < n ? x[i] : 0.f;
     }
     return;
   }
-  const int lo = p.sinks, hi = n - p.recent;  // the tokens to choose from
-  int want = p.budget - p.sinks - p.recent;   // fewer than hi - lo of them
-  uint32_t least = 0;  // digits found so far: of the want-th heaviest
-  if (want > 0) {
-    for (int d = 0; d < kDigits; ++d) {
-      const int shift = kDigitShift[d], bits = kDigitBits[d], above = shift + bits;
-      for (int i = t; i < kBins; i += kScanThreads) sCount[i] = 0;
-      __syncthreads();
-      for (int i = lo + t; i < hi; i += kScanThreads) {
-        const uint32_t u = order_of(x[i]);
-        if (d == 0 || u >> above == least >> above)
-          atomicAdd(&sCount[u >> shift & ((1u << bits) - 1)], 1);
-      }
-      __syncthreads();
-      // from the heaviest bin down: two bins a thread
-      const int b1 = kBins - 1 - 2 * t, c1 = sCount[b1], c0 = sCount[b1 - 1];
-      int total;
-      const int before = scan_block(c1 + c0, red, total);
-      if (before < want && want <= before + c1) {
-        sDigit = b1;
-        sRest = want - before;
-      } else if (before + c1 < want && want <= before + c1 + c0) {
-        sDigit = b1 - 1;
-        sRest = want - before - c1;
-      }
-      __syncthreads();
-      least |= sDigit << shift;
-      want = sRest;
-      __syncthreads();
-    }
-  }
-  // `want` of the tokens of just the least weight stay, the first ones
-  int kept = 0, ties = 0;
-  const bool any = p.budget > p.sinks + p.recent;
-  for (int i0 = 0; i0 < n; i0 += kScanThreads) {
-    const int i = i0 + t;
-    bool stays = false, tie = false;
-    float v = 0.f;
-    if (i < n) {
-      v = x[i];
-      const uint32_t u = order_of(v);
-      const bool choose = i >= lo && i < hi;
-      stays = !choose || (any && u > least);
-      tie = choose && any && u == least;
-    }
-    int total;
-    const int tie_rank = ties + scan_block((int)tie, red, total);
-    ties += total;
-    stays |= tie && tie_rank < want;
-    const int at = kept + scan_block((int)stays, red, total);
-    kept += total;
-    if (stays && at < p.budget) {
-      keep[at] = i;
-      if (sums) sums[at] = v;
-    }
+  if constexpr (WAVES == 4) {
+    if (n <= 4 * THREADS) choose<WAVES, 4>(p, sh, x, n, keep, sums);
+    else choose<WAVES, 16>(p, sh, x, n, keep, sums);
+  } else {
+    if (n <= 8 * THREADS) choose<WAVES, 8>(p, sh, x, n, keep, sums);
+    else if (n <= 32 * THREADS) choose<WAVES, 32>(p, sh, x, n, keep, sums);
+    else choose<WAVES, 0>(p, sh, x, n, keep, sums);
   }
 }
 
@@ -378,8 +499,14 @@ hipError_t launch_cache_select(const SelectArgs& a, hipStream_t stream) {
   p.budget = (int32_t)a.budget;
   p.recent = (int32_t)a.recent;
   p.sinks = (int32_t)a.sinks;
-  hipLaunchKernelGGL(cache_select_kernel, dim3((uint32_t)(a.B * a.H)), dim3(kScanThreads), 0,
-                     stream, p);
+  const dim3 grid((uint32_t)(a.B * a.H));
+  // More rows than are at work at once, long ones among them: the longest first, so that none
+  // of those begins last.
+  p.sorted = a.S > 4096 && a.B > 1 && a.B <= kWave && a.B * a.H > device_cus();
+  if (a.S <= 4096)
+    hipLaunchKernelGGL(cache_select_kernel<4>, grid, dim3(4 * kWave), 0, stream, p);
+  else
+    hipLaunchKernelGGL(cache_select_kernel<16>, grid, dim3(16 * kWave), 0, stream, p);
   return hipGetLastError();
 }
 
