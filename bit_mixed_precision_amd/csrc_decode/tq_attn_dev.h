@@ -71,6 +71,17 @@ __device__ __forceinline__ uint32_t div_page(const FastDiv& f, uint32_t t) {
 // A value that every lane holds, as the scalar it is.
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
+// A value that the compiler takes for a new one: what follows from it is computed where it
+// stands, instead of being kept in registers through the whole loop.
+__device__ __forceinline__ int anew(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+__device__ __forceinline__ int anew_uniform(int v) {
+  asm volatile("" : "+s"(v));
+  return v;
+}
+
 // Reads of what no kernel of a call writes, through the scalar cache where the
 // index is uniform.
 typedef const __attribute__((address_space(4))) int32_t* const_i32;

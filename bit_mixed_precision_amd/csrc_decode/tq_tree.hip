@@ -79,17 +79,6 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((float2v{x, y}), half2));
 }
 
-// A value that the compiler takes for a new one: what follows from it is computed where it
-// stands, instead of being kept in registers through the whole loop.
-__device__ __forceinline__ int anew(int v) {
-  asm volatile("" : "+v"(v));
-  return v;
-}
-__device__ __forceinline__ int anew_uniform(int v) {
-  asm volatile("" : "+s"(v));
-  return v;
-}
-
 // f of the values that the lanes l and l ^ 32 hold.
 template <class F>
 __device__ __forceinline__ float over_halves(float x, F f) {

@@ -26,6 +26,8 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kMaskWords = 4;
 constexpr int kMaxNodes = 64 * kMaskWords;
+constexpr int kQueryBytes = 48 * 1024;  // of LDS for queries
+constexpr int kMostRows = 8192;         // (nodes times heads of a group)
 
 struct WeightsParams {
   const unsigned char* Q;
@@ -43,6 +45,7 @@ struct WeightsParams {
   FastDiv page, group;
   int32_t n_pages, width, B, T, words, Hq, Hkv, D, G, window, S;
   int32_t tiles;  // not 0: of the longest sequence; every tile has a workgroup
+  int32_t chunk;  // rows whose queries lie in LDS at once, a multiple of 16
   float scale, decay;
 };
 
@@ -78,9 +81,14 @@ __device__ __forceinline__ Seq read_seq(const WeightsParams& p, int b) {
 
 // DV: 64, 128 or 256, the head dimension rounded up.  NT: 16-token tiles of a wave.
 template <bool BF, int DV, int NT>
-__global__ __launch_bounds__(kThreads) void cache_weights_kernel(WeightsParams p) {
-  constexpr int KS = DV / 32, UT = 16 * NT * kWaves;
-  extern __shared__ float sLse[];  // [rows], times log2 e; +inf: the row adds nothing
+__global__ __launch_bounds__(kThreads, DV > 128 ? 2 : 3) void cache_weights_kernel(WeightsParams p) {
+  constexpr int KS = DV / 32, UT = 16 * NT * kWaves, PC = DV / 8;
+  // queries of `chunk` rows, a row's 16-byte pieces turned so that 16 rows' reads of one piece
+  // spread over the banks; then lse of all rows, times log2 e, +inf: the row adds nothing
+  extern __shared__ __attribute__((aligned(16))) unsigned char sQ[];
+  const int chunk = p.chunk;
+  float* const sLse = reinterpret_cast<float*>(sQ + chunk * DV * 2);
+  __shared__ int sOut;  // some row adds nothing
   __shared__ uint64_t sBits[kMaxNodes][kMaskWords];
   __shared__ int sLow[kMaxNodes];
 
@@ -134,16 +142,90 @@ __global__ __launch_bounds__(kThreads) void cache_weights_kernel(WeightsParams p
     tile = s.t0 + at % n;
   }
 
+  // Rows r0 .. of the queries to LDS, zeros past the last one and past a head's end.
+  auto stage = [&](int r0, int rows) {
+    const int n = (rows - r0 < chunk ? rows - r0 : chunk) + 15 & ~15;
+    for (int x = anew(threadIdx.x); x < n * PC; x += kThreads) {
+      const int r = x / PC, piece = x - r * PC, row = r0 + r;
+      u32x4 v = {0, 0, 0, 0};
+      if (row < rows && piece * 8 < p.D) {
+        const int i = div_page(p.group, row);
+        v = *reinterpret_cast<const u32x4*>(p.Q + b * p.q_seq + i * p.q_tok +
+                                            (int64_t)(h * p.G + (row - i * p.G)) * p.q_head +
+                                            piece * 16);
+      }
+      *reinterpret_cast<u32x4*>(sQ + (r * PC + (piece ^ (r & (PC < 16 ? PC - 1 : 15)))) * 16) = v;
+    }
+  };
+
+  // Keys of a unit as the B operand, lane li holding token t0 + 16 n + li, and whether that
+  // token is there.  They are under way while the unit before is computed, and the pages
+  // of the unit after them, if it is of the same row, are looked up meanwhile.
+  u32x4 k[NT][KS], k_next[NT][KS];
+  bool there[NT], there_next[NT];
+  int ids[NT];
+  auto look_up = [&](int bb, int tt, const Seq& q) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int t = tt * UT + wave * 16 * NT + 16 * n + li;
+      const bool in = t >= q.lo && t < q.hi;
+      ids[n] = in ? p.table[(int64_t)bb * p.width + div_page(p.page, t)] : -1;
+    }
+  };
+  auto load = [&](int bb, int hh, int tt, const Seq& q) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int t = tt * UT + wave * 16 * NT + 16 * n + li;
+      there_next[n] = (uint32_t)ids[n] < (uint32_t)p.n_pages;
+      const int slot = t - (int)(div_page(p.page, there_next[n] ? t : 0) * p.page.d);
+      const unsigned char* kp =
+          p.K + ids[n] * p.page_stride + slot * p.row_stride + hh * p.head_stride;
+#pragma unroll
+      for (int x = 0; x < KS; ++x) {
+        const int d = 32 * x + 8 * g;
+        k_next[n][x] = u32x4{0, 0, 0, 0};
+        if (there_next[n] && d < p.D) k_next[n][x] = *reinterpret_cast<const u32x4*>(kp + d * 2);
+      }
+    }
+  };
+  look_up(b, tile, s);
+  load(b, h, tile, s);
+  if (left > 1 && tile + 1 < s.t1) look_up(b, tile + 1, s);
+
+  int q_at[KS];  // where this lane's pieces of a row tile lie
+#pragma unroll
+  for (int x = 0; x < KS; ++x)
+    q_at[x] = (li * PC + ((4 * x + g) ^ (li & (PC < 16 ? PC - 1 : 15)))) * 16;
   bool fresh = true;
-  for (; left > 0; --left) {
+  while (true) {
     const int rows = s.m * p.G;
+    // the unit that follows
+    int next_b = b, next_h = h, next_tile = tile + 1;
+    Seq next_s = s;
+    if (left > 1 && next_tile >= s.t1) {
+      if (++next_h == p.Hkv) {
+        next_h = 0;
+        while (next_b + 1 < p.B) {
+          next_s = read_seq<UT>(p, ++next_b);
+          if (next_s.t1 > next_s.t0) break;
+        }
+      }
+      next_tile = next_s.t0;
+    }
     if (fresh) {
+      const int tid = anew(threadIdx.x);
       __syncthreads();  // what the rows before needed has been read
+      if (tid == 0) sOut = 0;
+      if (rows <= chunk) stage(0, rows);
+      __syncthreads();
       for (int r = tid; r < rows; r += kThreads) {
         const int i = div_page(p.group, r);
         const float l = p.lse[((int64_t)b * p.T + i) * p.Hq + h * p.G + (r - i * p.G)];
-        sLse[r] = fabsf(l) < INFINITY ? l * kLog2e : INFINITY;
+        const bool adds = fabsf(l) < INFINITY;
+        sLse[r] = adds ? l * kLog2e : INFINITY;
+        if (!adds) sOut = 1;  // every writer writes 1
       }
+      for (int r = rows + tid; r < (rows + 15 & ~15); r += kThreads) sLse[r] = INFINITY;
       for (int i = tid; i < s.m; i += kThreads) {
         int seen = 0;
         for (int w = 0; w < kMaskWords; ++w) {
@@ -160,67 +242,88 @@ __global__ __launch_bounds__(kThreads) void cache_weights_kernel(WeightsParams p
       __syncthreads();
     }
     const int t0 = tile * UT + wave * 16 * NT;
-    // Keys as the B operand: lane li holds token t0 + 16 n + li
-    u32x4 k[NT][KS];
-    bool there[NT];
+    // the sums so far, for lane group g of the tiles g, g + 4, ..
+    float old[(NT + 3) / 4];
+#pragma unroll
+    for (int n0 = 0; n0 < NT; n0 += 4) {
+      const int t = t0 + 16 * (n0 + g) + li;
+      old[n0 / 4] = n0 + g < NT && t < s.n && t < p.S
+                        ? p.scores[b * p.s_seq + h * p.s_head + t] : 0.f;
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int t = t0 + 16 * n + li;
-      const bool in = t >= s.lo && t < s.hi;
-      const int pg = div_page(p.page, in ? t : 0);
-      const int id = in ? p.table[(int64_t)b * p.width + pg] : -1;
-      there[n] = (uint32_t)id < (uint32_t)p.n_pages;
-      const unsigned char* kp = p.K + id * p.page_stride +
-                                (t - pg * (int)p.page.d) * p.row_stride + h * p.head_stride;
+      there[n] = there_next[n];
 #pragma unroll
-      for (int x = 0; x < KS; ++x) {
-        const int d = 32 * x + 8 * g;
-        k[n][x] = u32x4{0, 0, 0, 0};
-        if (there[n] && d < p.D) k[n][x] = *reinterpret_cast<const u32x4*>(kp + d * 2);
-      }
+      for (int x = 0; x < KS; ++x) k[n][x] = k_next[n][x];
+    }
+    if (left > 1) {
+      if (next_b != b || next_h != h) look_up(next_b, next_tile, next_s);
+      load(next_b, next_h, next_tile, next_s);
+      if (left > 2 && next_tile + 1 < next_s.t1) look_up(next_b, next_tile + 1, next_s);
     }
     float sum[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) sum[n] = 0.f;
-    const bool edge = t0 + 16 * NT > s.n || (p.window > 0 && t0 < s.n + s.m - p.window);
-    for (int r0 = 0; r0 < rows; r0 += 16) {
-      // queries as the A operand: lane li holds row r0 + li
-      const int row = r0 + li;
-      const int i = div_page(p.group, row < rows ? row : 0);
-      const unsigned char* qp = p.Q + b * p.q_seq + i * p.q_tok +
-                                (int64_t)(h * p.G + ((row < rows ? row : 0) - i * p.G)) * p.q_head;
-      u32x4 q[KS];
-#pragma unroll
-      for (int x = 0; x < KS; ++x) {
-        const int d = 32 * x + 8 * g;
-        q[x] = u32x4{0, 0, 0, 0};
-        if (row < rows && d < p.D) q[x] = *reinterpret_cast<const u32x4*>(qp + d * 2);
+    const bool edge = t0 + 16 * NT > s.n || (p.window > 0 && t0 < s.n + s.m - p.window) || sOut;
+    for (int c0 = 0; c0 < rows; c0 += chunk) {
+      const int n_rows = rows - c0 < chunk ? rows - c0 : chunk;
+      if (rows > chunk) {
+        __syncthreads();
+        stage(c0, rows);
+        __syncthreads();
       }
-      float ls[4];
+      // queries as the A operand: lane li holds row r + li of the chunk
+      auto query = [&](int r, u32x4* q) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int rj = r0 + 4 * g + j;
-        ls[j] = rj < rows ? sLse[rj] : INFINITY;
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
+        for (int x = 0; x < KS; ++x)
+          q[x] = *reinterpret_cast<const u32x4*>(sQ + r * PC * 16 + q_at[x]);
+        return *reinterpret_cast<const float4v*>(sLse + c0 + r + 4 * g);
+      };
+      auto score = [&](const u32x4* q, int n) {
         float4v c = {0, 0, 0, 0};
 #pragma unroll
         for (int x = 0; x < KS; ++x) c = mma16<BF>(q[x], k[n][x], c);
-        const int t = t0 + 16 * n + li;
+        return c;
+      };
+      if (!edge) {
+        for (int r = 0; r < n_rows; r += 16) {
+          u32x4 q[KS];
+          const float4v ls = query(r, q);
+          float4v c[NT];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          bool ok = ls[j] < INFINITY && there[n];
-          if (edge && ok) {
-            const int node = div_page(p.group, r0 + 4 * g + j), at = t - s.n;
-            ok = at < 0 ? t >= sLow[node]
-                        : at < kMaxNodes && (sBits[node][at >> 6] >> (at & 63) & 1);
+          for (int n = 0; n < NT; ++n) c[n] = score(q, n);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              sum[n] += __builtin_amdgcn_exp2f(fmaf(c[n][j], p.scale, -ls[j]));
+        }
+      } else {
+        const int li = anew(lane & 15), g = anew(lane >> 4);
+        for (int r = 0; r < n_rows; r += 16) {
+          u32x4 q[KS];
+          const float4v ls = query(r, q);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const float4v c = score(q, n);
+            const int t = t0 + 16 * n + li, at = t - s.n;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              bool ok = ls[j] < INFINITY;
+              if (ok) {
+                const int node = div_page(p.group, c0 + r + 4 * g + j);
+                ok = at < 0 ? t >= sLow[node]
+                            : at < kMaxNodes && (sBits[node][at >> 6] >> (at & 63) & 1);
+              }
+              const float w = __builtin_amdgcn_exp2f(fmaf(c[j], p.scale, -ls[j]));
+              sum[n] += ok ? w : 0.f;
+            }
           }
-          const float w = __builtin_amdgcn_exp2f(fmaf(c[j], p.scale, -ls[j]));
-          sum[n] += ok ? w : 0.f;
         }
       }
     }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) sum[n] = there[n] ? sum[n] : 0.f;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       sum[n] += __shfl_xor(sum[n], 16, kWave);
@@ -235,22 +338,15 @@ __global__ __launch_bounds__(kThreads) void cache_weights_kernel(WeightsParams p
         if (n0 + n < NT) w = g == n ? sum[n0 + n] : w;
       const int t = t0 + 16 * (n0 + g) + li;
       if (n0 + g < NT && t < s.hi && t < p.S) {
-        float* to = p.scores + b * p.s_seq + h * p.s_head + t;
-        *to = t < s.n ? fmaf(p.decay, *to, w) : w;
+        p.scores[b * p.s_seq + h * p.s_head + t] = t < s.n ? fmaf(p.decay, old[n0 / 4], w) : w;
       }
     }
-    fresh = false;
-    if (++tile >= s.t1 && left > 1) {
-      fresh = true;
-      if (++h == p.Hkv) {
-        h = 0;
-        while (b + 1 < p.B) {
-          s = read_seq<UT>(p, ++b);
-          if (s.t1 > s.t0) break;
-        }
-      }
-      tile = s.t0;
-    }
+    if (--left == 0) break;
+    fresh = next_b != b || next_h != h;
+    b = next_b;
+    h = next_h;
+    tile = next_tile;
+    s = next_s;
   }
 }
 
@@ -260,10 +356,19 @@ hipError_t launch_nt(WeightsParams p, hipStream_t s) {
   int64_t cap = (int64_t)p.width * p.page.d;
   if (cap > p.S) cap = p.S;
   const int64_t tiles = (cap + UT - 1) / UT, all = (int64_t)p.B * p.Hkv * tiles;
-  const int64_t most = 4 * (int64_t)device_cus();
+  const int64_t most = (DV > 128 ? 2 : 3) * (int64_t)device_cus();  // what the registers allow at once
   if (all == 0) return hipSuccess;
   p.tiles = all <= 2 * most ? (int32_t)tiles : 0;
-  const int lds = p.T * p.G * 4;
+  const int rows = (p.T * p.G + 15) / 16 * 16, most_rows = kQueryBytes / (DV * 2);
+  p.chunk = rows < most_rows ? rows : most_rows;
+  const int lds = p.chunk * DV * 2 + rows * 4;
+  if (lds > 48 * 1024) {
+    static std::atomic<uint64_t> done{0};
+    const hipError_t e =
+        lds_limit_once(reinterpret_cast<const void*>(cache_weights_kernel<BF, DV, NT>),
+                       kQueryBytes + kMostRows * 4, done);
+    if (e != hipSuccess) return e;
+  }
   hipLaunchKernelGGL((cache_weights_kernel<BF, DV, NT>),
                      dim3((uint32_t)(p.tiles || all < most ? all : most)), dim3(kThreads), lds, s, p);
   return hipGetLastError();
