@@ -12,6 +12,7 @@
 // that other rows hold too is not written; the row gets a free page in its place.
 
 #include "tq.h"
+#include "tq_attn_dev.h"
 #include "tq_common.h"
 #include "tq_decode.h"
 #include "tq_kernels.h"
@@ -19,8 +20,6 @@
 
 namespace tq {
 namespace {
-
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // ------------------------------------------------------------------ the choice
 
@@ -253,6 +252,7 @@ struct KeepParams {
   int64_t planes, page_bytes, n_pages;
   int64_t row_bytes, head_bytes;  // of a token, of one of its `heads` parts
   int32_t page_size, rows, width, groups, heads, n;
+  FastDiv page;
   const int32_t* table;
   const int32_t* lens;
   const int32_t* keep;
@@ -323,40 +323,53 @@ __device__ __forceinline__ void mark_row(const KeepParams& p, int r, int thread,
   }
 }
 
-// The entries of a row that need a page of their own, by a workgroup; returns their number.
-__device__ __forceinline__ int mark_fresh(const KeepParams& p, int r, int* sNeed) {
+// The entries of a row that need a page of their own, by a wave: shared ones with a slot that
+// gets another token.  Returns their number.
+__device__ __forceinline__ int mark_fresh(const KeepParams& p, int r, int lane) {
   const Row x = row_of(p, r);
-  if (threadIdx.x == 0) *sNeed = 0;
-  __syncthreads();
   const int64_t lists = (int64_t)p.groups * p.heads;
-  for (int e = x.first / p.page_size; e < entries(p, x.total); ++e) {
-    const int32_t id = p.table[(int64_t)r * p.width + e];
-    if (!names_page(p, id) || !(p.shared[id >> 5] >> (id & 31) & 1)) continue;
-    const int from = e * p.page_size > x.first ? e * p.page_size : x.first;
-    const int64_t end = (int64_t)(e + 1) * p.page_size;
-    const int slots = (end < x.total ? (int)end : x.total) - from;
-    bool acts = false;
-    for (int64_t k = threadIdx.x; k < lists * slots && !acts; k += blockDim.x) {
-      const int list = (int)(k / slots), i = from + (int)(k - (int64_t)list * slots);
-      const int t = source_of(p, x, list / p.heads, r, list % p.heads, i);
-      acts = t >= 0 && t != i;
-    }
-    if (__syncthreads_or(acts) && threadIdx.x == 0) {
-      p.fresh[(int64_t)r * ((p.width + 31) / 32) + e / 32] |= 1u << (e & 31);
-      ++*sNeed;
+  const int held = entries(p, x.total);
+  int need = 0;
+  for (int e0 = x.first / p.page_size; e0 < held; e0 += kWave) {
+    const int mine = e0 + lane;
+    const int32_t id = mine < held ? p.table[(int64_t)r * p.width + mine] : -1;
+    const bool shares = names_page(p, id) && p.shared[id >> 5] >> (id & 31) & 1;
+    for (uint64_t todo = __ballot(shares); todo; todo &= todo - 1) {
+      const int e = e0 + __builtin_ctzll(todo);
+      const int64_t begin = (int64_t)e * p.page_size, end = begin + p.page_size;
+      const int from = begin > x.first ? (int)begin : x.first;
+      const int slots = (end < x.total ? (int)end : x.total) - from;
+      // four of the lists' entries a lane at once, until one is found
+      bool acts = false;
+      for (int64_t k0 = lane; k0 - lane < lists * slots && !__any(acts); k0 += 4 * kWave) {
+        int t[4], i[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int64_t k = k0 + u * kWave;
+          const int list = (int)(k / slots);
+          i[u] = from + (int)(k - (int64_t)list * slots);
+          t[u] = k < lists * slots ? source_of(p, x, list / p.heads, r, list % p.heads, i[u]) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) acts |= t[u] >= 0 && t[u] != i[u];
+      }
+      if (__any(acts)) {
+        if (lane == 0) p.fresh[(int64_t)r * ((p.width + 31) / 32) + e / 32] |= 1u << (e & 31);
+        ++need;
+      }
     }
   }
-  __syncthreads();
-  return *sNeed;
+  return need;
 }
 
 __global__ __launch_bounds__(kKeepThreads) void keep_mark_kernel(KeepParams p) {
   mark_row(p, blockIdx.x, threadIdx.x, kKeepThreads);
 }
 __global__ __launch_bounds__(kKeepThreads) void keep_need_kernel(KeepParams p) {
-  __shared__ int sNeed;
-  const int n = mark_fresh(p, blockIdx.x, &sNeed);
-  if (threadIdx.x == 0) p.need[blockIdx.x] = n;
+  const int r = (int)((blockIdx.x * kKeepThreads + threadIdx.x) / kWave);
+  if (r >= p.rows) return;
+  const int n = mark_fresh(p, r, threadIdx.x & 63);
+  if ((threadIdx.x & 63) == 0) p.need[r] = n;
 }
 
 // Ranks the free pages and deals them out to the rows in order; the new state.
@@ -369,13 +382,23 @@ __device__ __forceinline__ void deal_pages(const KeepParams& p, int* red) {
     const int64_t left = p.n_pages - (int64_t)w * 32;
     return ~p.held[w] & (left >= 32 ? 0xffffffffu : (1u << left) - 1);
   };
-  int mine = 0, free_pages;
-  for (int w = w0; w < w1; ++w) mine += __popc(open(w));
-  int rank = scan_block(mine, red, free_pages);
-  for (int w = w0; w < w1; ++w)
-    for (uint32_t f = open(w); f; f &= f - 1) p.spare[rank++] = w * 32 + __ffs(f) - 1;
-  __syncthreads();
   __shared__ int64_t red64[kScanThreads / kWave];  // wishes may add up past 32 bits
+  int64_t wanted = 0;
+  for (int r0 = 0; r0 < p.rows; r0 += kScanThreads) {
+    int64_t total;
+    (void)scan_block(r0 + t < p.rows ? (int64_t)p.need[r0 + t] : 0, red64, total);
+    wanted += total;
+  }
+  int free_pages = 0;
+  if (wanted > 0) {  // as many of the free pages as are wanted
+    int mine = 0;
+    for (int w = w0; w < w1; ++w) mine += __popc(open(w));
+    int rank = scan_block(mine, red, free_pages);
+    for (int w = w0; w < w1 && rank < wanted; ++w)
+      for (uint32_t f = open(w); f && rank < wanted; f &= f - 1)
+        p.spare[rank++] = w * 32 + __ffs(f) - 1;
+  }
+  __syncthreads();
   int64_t base = 0;
   int refused = 0;
   for (int r0 = 0; r0 < p.rows; r0 += kScanThreads) {
@@ -407,9 +430,10 @@ __global__ __launch_bounds__(kScanThreads) void keep_deal_kernel(KeepParams p) {
 __device__ __forceinline__ void write_table(const KeepParams& p, int r, int thread, int threads) {
   const int held = entries(p, p.lens_out[r]);
   const uint32_t* fresh = p.fresh + (int64_t)r * ((p.width + 31) / 32);
+  const bool moved = p.moved[r] >= 0;
   for (int e = thread; e < p.width; e += threads) {
     int32_t id = e < held ? p.table[(int64_t)r * p.width + e] : -1;
-    if (e < held && p.moved[r] >= 0 && fresh[e / 32] >> (e & 31) & 1) {
+    if (e < held && moved && fresh[e / 32] >> (e & 31) & 1) {
       int k = p.need[r] + __popc(fresh[e / 32] & ((1u << (e & 31)) - 1));
       for (int w = 0; w < e / 32; ++w) k += __popc(fresh[w]);
       id = p.spare[k];
@@ -419,6 +443,30 @@ __device__ __forceinline__ void write_table(const KeepParams& p, int r, int thre
 }
 __global__ __launch_bounds__(kKeepThreads) void keep_table_kernel(KeepParams p) {
   write_table(p, blockIdx.x, threadIdx.x, kKeepThreads);
+}
+
+// All of the bookkeeping by one workgroup, the bitmaps in LDS: one launch instead of five.
+constexpr int kOnePages = 64 * 1024;
+__global__ __launch_bounds__(kScanThreads) void keep_one_kernel(KeepParams p) {
+  __shared__ int red[kScanThreads / kWave];
+  __shared__ uint32_t sHeld[kOnePages / 32], sShared[kOnePages / 32];
+  const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
+  constexpr int kWaves = kScanThreads / kWave;
+  p.held = sHeld;
+  p.shared = sShared;
+  for (int i = t; i < (p.n_pages + 31) / 32; i += kScanThreads) sHeld[i] = sShared[i] = 0;
+  for (int64_t i = t; i < (int64_t)p.rows * ((p.width + 31) / 32); i += kScanThreads) p.fresh[i] = 0;
+  __syncthreads();
+  for (int r = wave; r < p.rows; r += kWaves) mark_row(p, r, lane, kWave);
+  __syncthreads();
+  for (int r = wave; r < p.rows; r += kWaves) {
+    const int n = mark_fresh(p, r, lane);
+    if (lane == 0) p.need[r] = n;
+  }
+  __syncthreads();
+  deal_pages(p, red);
+  __syncthreads();
+  for (int r = wave; r < p.rows; r += kWaves) write_table(p, r, lane, kWave);
 }
 
 // Bytes of a token's part that a workgroup moves: a column of the row's slots.
@@ -439,32 +487,62 @@ __device__ __forceinline__ void move_column(const KeepParams& p, int r, int h, i
   const int32_t* const from = p.table + (int64_t)r * p.width;
   const int32_t* const to = p.table_out + (int64_t)r * p.width;
   const uint32_t* const fresh = p.fresh + (int64_t)r * ((p.width + 31) / 32);
-  // tokens before the first list entry move only with their whole page
-  int64_t i0 = x.first / p.page_size * p.page_size;
-  for (; i0 < x.total; i0 += slots * kDepth) {
+  // One part: kDepth slots a thread.  src, dst: bytes from `pool`, -1 where nothing moves.
+  struct Part {
+    int64_t src[kDepth], dst[kDepth];
     u32x4 v[kDepth];
-    int64_t dst[kDepth];
+  };
+  auto locate = [&](int64_t i0, Part& w) {
+    int t[kDepth];
 #pragma unroll
     for (int k = 0; k < kDepth; ++k) {
-      const int64_t slot = i0 + k * slots + sub;
-      dst[k] = -1;
-      if (sub >= slots || slot >= x.total) continue;
-      const int i = (int)slot, e = i / p.page_size;
-      const int t = source_of(p, x, g, r, h, i);
-      if (t < 0 || (t == i && !(fresh[e / 32] >> (e & 31) & 1))) continue;
-      const int es = t / p.page_size;
+      const int64_t i = i0 + k * slots + sub;
+      t[k] = sub < slots && i < x.total ? source_of(p, x, g, r, h, (int)i) : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kDepth; ++k) {
+      w.src[k] = w.dst[k] = -1;
+      const int i = (int)(i0 + k * slots + sub);
+      if (t[k] < 0) continue;
+      const int e = (int)div_page(p.page, i), es = (int)div_page(p.page, t[k]);
+      if (t[k] == i && !(fresh[e / 32] >> (e & 31) & 1)) continue;
       const int32_t sp = from[es], dp = to[e];
       if (!names_page(p, sp) || !names_page(p, dp)) continue;
-      v[k] = *reinterpret_cast<const u32x4*>(pool + sp * p.page_bytes +
-                                             (t - es * p.page_size) * p.row_bytes);
-      dst[k] = dp * p.page_bytes + (i - e * p.page_size) * p.row_bytes;
+      w.src[k] = sp * p.page_bytes + (t[k] - es * p.page_size) * p.row_bytes;
+      w.dst[k] = dp * p.page_bytes + (i - e * p.page_size) * p.row_bytes;
     }
-    // every read of this part has returned before any of its writes
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  };
+  auto read = [&](Part& w) {
+#pragma unroll
+    for (int k = 0; k < kDepth; ++k)
+      if (w.src[k] >= 0)
+        w.v[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(pool + w.src[k]));
+  };
+  auto write = [&](Part& w) {
+    // every thread's reads of this part have returned before any of its writes; those of
+    // the next part, which are under way, lie behind all that this one writes
+#pragma unroll
+    for (int k = 0; k < kDepth; ++k) asm volatile("" : "+v"(w.v[k])::"memory");
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kDepth; ++k)
-      if (dst[k] >= 0) *reinterpret_cast<u32x4*>(pool + dst[k]) = v[k];
+      if (w.dst[k] >= 0)
+        __builtin_nontemporal_store(w.v[k], reinterpret_cast<u32x4*>(pool + w.dst[k]));
+  };
+  // tokens before the first list entry move only with their whole page
+  const int64_t step = (int64_t)slots * kDepth;
+  int64_t i0 = x.first / p.page_size * p.page_size;
+  Part a, b;
+  locate(i0, a);
+  read(a);
+  for (; i0 < x.total; i0 += 2 * step) {
+    locate(i0 + step, b);
+    read(b);
+    write(a);
+    if (i0 + step >= x.total) break;
+    locate(i0 + 2 * step, a);
+    read(a);
+    write(b);
   }
 }
 
@@ -510,6 +588,9 @@ hipError_t launch_cache_select(const SelectArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Rows and table entries up to which one workgroup does the bookkeeping.
+constexpr int64_t kOneRows = 256, kOneEntries = 48 * 1024;
+
 int64_t keep_workspace_bytes(int64_t rows, int64_t width, int64_t n_pages) {
   return 2 * up16(4 * ((n_pages + 31) / 32)) + up16(4 * rows * ((width + 31) / 32)) +
          2 * up16(4 * rows) + up16(4 * n_pages);
@@ -522,6 +603,7 @@ hipError_t launch_pages_keep(const KeepArgs& a, hipStream_t s) {
   p.page_bytes = a.pages.page_bytes;
   p.n_pages = a.pages.n_pages;
   p.page_size = (int32_t)a.pages.page_size;
+  p.page = fast_div(a.pages.page_size);
   p.row_bytes = a.pages.page_bytes / a.pages.page_size;
   p.head_bytes = p.row_bytes / a.heads;
   p.rows = (int32_t)a.pages.rows;
@@ -549,17 +631,20 @@ hipError_t launch_pages_keep(const KeepArgs& a, hipStream_t s) {
   p.need = reinterpret_cast<int32_t*>(take(p.rows));
   p.moved = reinterpret_cast<int32_t*>(take(p.rows));
   p.spare = reinterpret_cast<int32_t*>(take(p.n_pages));
-  const int64_t words = (p.n_pages + 31) / 32 + (int64_t)p.rows * ((p.width + 31) / 32);
-  const int64_t blocks = (words + kKeepThreads - 1) / kKeepThreads;
-  hipLaunchKernelGGL(keep_clear_kernel, dim3((uint32_t)(blocks < 1024 ? blocks : 1024)),
-                     dim3(kKeepThreads), 0, s, p);
-  if (p.rows > 0) {
+  if (p.rows <= kOneRows && (int64_t)p.rows * p.width <= kOneEntries && p.n_pages <= kOnePages) {
+    hipLaunchKernelGGL(keep_one_kernel, dim3(1), dim3(kScanThreads), 0, s, p);
+  } else {
+    const int64_t words = (p.n_pages + 31) / 32 + (int64_t)p.rows * ((p.width + 31) / 32);
+    const int64_t blocks = (words + kKeepThreads - 1) / kKeepThreads;
+    hipLaunchKernelGGL(keep_clear_kernel, dim3((uint32_t)(blocks < 1024 ? blocks : 1024)),
+                       dim3(kKeepThreads), 0, s, p);
     hipLaunchKernelGGL(keep_mark_kernel, dim3(p.rows), dim3(kKeepThreads), 0, s, p);
-    hipLaunchKernelGGL(keep_need_kernel, dim3(p.rows), dim3(kKeepThreads), 0, s, p);
-  }
-  hipLaunchKernelGGL(keep_deal_kernel, dim3(1), dim3(kScanThreads), 0, s, p);
-  if (p.rows > 0) {
+    hipLaunchKernelGGL(keep_need_kernel, dim3((p.rows + kKeepThreads / kWave - 1) / (kKeepThreads / kWave)),
+                       dim3(kKeepThreads), 0, s, p);
+    hipLaunchKernelGGL(keep_deal_kernel, dim3(1), dim3(kScanThreads), 0, s, p);
     hipLaunchKernelGGL(keep_table_kernel, dim3(p.rows), dim3(kKeepThreads), 0, s, p);
+  }
+  if (p.rows > 0) {
     const int columns = (int)((p.head_bytes + kColumn - 1) / kColumn);
     const int64_t items = (int64_t)p.rows * p.heads * columns * p.planes;
     if (items > 0)
