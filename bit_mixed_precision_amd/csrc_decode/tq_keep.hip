@@ -247,6 +247,7 @@ __global__ __launch_bounds__(WAVES * kWave, 4) void cache_select_kernel(SelectPa
 
 // ------------------------------------------------------------------ the move
 
+struct Row;
 struct KeepParams {
   unsigned char* pool;
   int64_t planes, page_bytes, n_pages;
@@ -267,7 +268,7 @@ struct KeepParams {
   uint32_t* fresh;   // [rows][ceil(width / 32)]: entries that get a free page
   int32_t* need;     // [rows] how many
   int32_t* spare;    // [n_pages] free pages in ascending order
-  int32_t* moved;    // [rows] tokens after the move, -1: the row stays as it is
+  Row* row;          // [rows] what becomes of it
 };
 
 __device__ __forceinline__ bool names_page(const KeepParams& p, int32_t id) {
@@ -282,8 +283,9 @@ __device__ __forceinline__ int tokens_of(const KeepParams& p, int row) {
   return n < 0 ? 0 : n < cap ? n : (int)cap;
 }
 // The tokens [0, first) of a row stay where they are; it has `total` after the move.
-struct Row {
+struct alignas(16) Row {
   int tokens, first, total;
+  int moves;  // 0: refused, the row stays as it is
 };
 __device__ __forceinline__ Row row_of(const KeepParams& p, int r) {
   Row x;
@@ -293,6 +295,7 @@ __device__ __forceinline__ Row row_of(const KeepParams& p, int r) {
   int c = p.counts[r];
   c = c < 0 ? 0 : c < p.n ? c : p.n;
   x.total = c < x.tokens - x.first ? x.first + c : x.tokens;
+  x.moves = 1;
   return x;
 }
 // The token that goes to slot i, -1 if the list names none from i on.
@@ -313,20 +316,25 @@ __global__ __launch_bounds__(kKeepThreads) void keep_clear_kernel(KeepParams p) 
 }
 
 // Marks the pages of a row.
-__device__ __forceinline__ void mark_row(const KeepParams& p, int r, int thread, int threads) {
-  const int held = entries(p, tokens_of(p, r));
+__device__ __forceinline__ bool mark_row(const KeepParams& p, int r, int tokens, int thread,
+                                         int threads) {
+  const int held = entries(p, tokens);
+  bool any = false;  // page that another entry has marked before
   for (int e = thread; e < held; e += threads) {
     const int32_t id = p.table[(int64_t)r * p.width + e];
     if (!names_page(p, id)) continue;
     const uint32_t bit = 1u << (id & 31);
-    if (atomicOr(&p.held[id >> 5], bit) & bit) atomicOr(&p.shared[id >> 5], bit);
+    if (atomicOr(&p.held[id >> 5], bit) & bit) {
+      atomicOr(&p.shared[id >> 5], bit);
+      any = true;
+    }
   }
+  return any;
 }
 
 // The entries of a row that need a page of their own, by a wave: shared ones with a slot that
 // gets another token.  Returns their number.
-__device__ __forceinline__ int mark_fresh(const KeepParams& p, int r, int lane) {
-  const Row x = row_of(p, r);
+__device__ __forceinline__ int mark_fresh(const KeepParams& p, int r, const Row& x, int lane) {
   const int64_t lists = (int64_t)p.groups * p.heads;
   const int held = entries(p, x.total);
   int need = 0;
@@ -363,12 +371,14 @@ __device__ __forceinline__ int mark_fresh(const KeepParams& p, int r, int lane) 
 }
 
 __global__ __launch_bounds__(kKeepThreads) void keep_mark_kernel(KeepParams p) {
-  mark_row(p, blockIdx.x, threadIdx.x, kKeepThreads);
+  (void)mark_row(p, blockIdx.x, tokens_of(p, blockIdx.x), threadIdx.x, kKeepThreads);
 }
 __global__ __launch_bounds__(kKeepThreads) void keep_need_kernel(KeepParams p) {
   const int r = (int)((blockIdx.x * kKeepThreads + threadIdx.x) / kWave);
   if (r >= p.rows) return;
-  const int n = mark_fresh(p, r, threadIdx.x & 63);
+  const Row x = row_of(p, r);
+  const int n = mark_fresh(p, r, x, threadIdx.x & 63);
+  if ((threadIdx.x & 63) == 0) p.row[r] = x;
   if ((threadIdx.x & 63) == 0) p.need[r] = n;
 }
 
@@ -409,9 +419,7 @@ __device__ __forceinline__ void deal_pages(const KeepParams& p, int* red) {
     base += total;
     if (r < p.rows) {
       const bool ok = need == 0 || before + need <= free_pages;
-      const Row x = row_of(p, r);
-      p.lens_out[r] = ok ? x.total : x.tokens;
-      p.moved[r] = ok ? x.total : -1;
+      p.row[r].moves = ok;
       p.need[r] = (int)(ok ? before : 0);  // from here on: its first free page
       refused += !ok;
     }
@@ -426,14 +434,15 @@ __global__ __launch_bounds__(kScanThreads) void keep_deal_kernel(KeepParams p) {
   deal_pages(p, red);
 }
 
-// A row of the new table, by the threads of a wave or more.
-__device__ __forceinline__ void write_table(const KeepParams& p, int r, int thread, int threads) {
-  const int held = entries(p, p.lens_out[r]);
+// A row's length and its part of the new table, by the threads of a wave or more.
+__device__ __forceinline__ void write_row(const KeepParams& p, int r, int thread, int threads) {
+  const Row x = p.row[r];
+  const int tokens = x.moves ? x.total : x.tokens, held = entries(p, tokens);
   const uint32_t* fresh = p.fresh + (int64_t)r * ((p.width + 31) / 32);
-  const bool moved = p.moved[r] >= 0;
+  if (thread == 0) p.lens_out[r] = tokens;
   for (int e = thread; e < p.width; e += threads) {
     int32_t id = e < held ? p.table[(int64_t)r * p.width + e] : -1;
-    if (e < held && moved && fresh[e / 32] >> (e & 31) & 1) {
+    if (e < held && x.moves && fresh[e / 32] >> (e & 31) & 1) {
       int k = p.need[r] + __popc(fresh[e / 32] & ((1u << (e & 31)) - 1));
       for (int w = 0; w < e / 32; ++w) k += __popc(fresh[w]);
       id = p.spare[k];
@@ -442,46 +451,67 @@ __device__ __forceinline__ void write_table(const KeepParams& p, int r, int thre
   }
 }
 __global__ __launch_bounds__(kKeepThreads) void keep_table_kernel(KeepParams p) {
-  write_table(p, blockIdx.x, threadIdx.x, kKeepThreads);
+  write_row(p, blockIdx.x, threadIdx.x, kKeepThreads);
 }
 
-// All of the bookkeeping by one workgroup, the bitmaps in LDS: one launch instead of five.
-constexpr int kOnePages = 64 * 1024;
+// All of the bookkeeping by one workgroup, the bitmaps and rows in LDS: one launch instead
+// of five.
+constexpr int kOnePages = 64 * 1024, kOneRows = 256, kOneEntries = 48 * 1024;
+constexpr int kOneMarks = kOneEntries / 32 + kOneRows;
 __global__ __launch_bounds__(kScanThreads) void keep_one_kernel(KeepParams p) {
   __shared__ int red[kScanThreads / kWave];
-  __shared__ uint32_t sHeld[kOnePages / 32], sShared[kOnePages / 32];
+  __shared__ uint32_t sHeld[kOnePages / 32], sShared[kOnePages / 32], sFresh[kOneMarks];
+  __shared__ Row sRow[kOneRows];
+  __shared__ int sNeed[kOneRows];
   const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
   constexpr int kWaves = kScanThreads / kWave;
+  uint32_t* const fresh = p.fresh;
+  Row* const row = p.row;
   p.held = sHeld;
   p.shared = sShared;
-  for (int i = t; i < (p.n_pages + 31) / 32; i += kScanThreads) sHeld[i] = sShared[i] = 0;
-  for (int64_t i = t; i < (int64_t)p.rows * ((p.width + 31) / 32); i += kScanThreads) p.fresh[i] = 0;
-  __syncthreads();
-  for (int r = wave; r < p.rows; r += kWaves) mark_row(p, r, lane, kWave);
-  __syncthreads();
-  for (int r = wave; r < p.rows; r += kWaves) {
-    const int n = mark_fresh(p, r, lane);
-    if (lane == 0) p.need[r] = n;
+  p.fresh = sFresh;
+  p.row = sRow;
+  p.need = sNeed;
+  const int marks = p.rows * ((p.width + 31) / 32);
+  if (t < p.rows) {
+    sRow[t] = row_of(p, t);
+    sNeed[t] = 0;
   }
+  for (int i = t; i < (p.n_pages + 31) / 32; i += kScanThreads) sHeld[i] = sShared[i] = 0;
+  for (int i = t; i < marks; i += kScanThreads) sFresh[i] = 0;
   __syncthreads();
-  deal_pages(p, red);
-  __syncthreads();
-  for (int r = wave; r < p.rows; r += kWaves) write_table(p, r, lane, kWave);
+  bool any = false;
+  for (int r = wave; r < p.rows; r += kWaves) any |= mark_row(p, r, sRow[r].tokens, lane, kWave);
+  if (__syncthreads_or(any)) {  // a page is shared
+    for (int r = wave; r < p.rows; r += kWaves) {
+      const int n = mark_fresh(p, r, sRow[r], lane);
+      if (lane == 0) sNeed[r] = n;
+    }
+    __syncthreads();
+    deal_pages(p, red);
+    __syncthreads();
+  } else if (t == 0) {
+    *p.result = 0;
+  }
+  for (int r = wave; r < p.rows; r += kWaves) write_row(p, r, lane, kWave);
+  for (int i = t; i < marks; i += kScanThreads) fresh[i] = sFresh[i];
+  if (t < p.rows) row[t] = sRow[t];
 }
 
-// Bytes of a token's part that a workgroup moves: a column of the row's slots.
-constexpr int kColumn = 256;
+// Bytes of a token's part that a workgroup moves, a column of the row's slots: the least and
+// the most.
+constexpr int64_t kColumn = 256, kMostColumn = 16 * kKeepThreads;
 constexpr int kDepth = 4;  // loads of a thread under way
 constexpr int64_t kMostBlocks = 1 << 20;  // of a launch
 
 // A workgroup takes a column of a part of a row's tokens in one plane, slots in
 // ascending order.
-__device__ __forceinline__ void move_column(const KeepParams& p, int r, int h, int column, int plane) {
-  const Row x = row_of(p, r);
+__device__ __forceinline__ void move_column(const KeepParams& p, const Row& x, int r, int h, int column,
+                                            int plane, int64_t width) {
   const int g = plane / (int)(p.planes / p.groups);
-  const int64_t at = (int64_t)h * p.head_bytes + (int64_t)column * kColumn;
-  const int64_t rest = p.head_bytes - (int64_t)column * kColumn;
-  const int lanes = (int)(rest < kColumn ? rest : kColumn) / 16, slots = kKeepThreads / lanes;
+  const int64_t at = (int64_t)h * p.head_bytes + column * width;
+  const int64_t rest = p.head_bytes - column * width;
+  const int lanes = (int)(rest < width ? rest : width) / 16, slots = kKeepThreads / lanes;
   const int sub = threadIdx.x / lanes, lane = threadIdx.x - sub * lanes;
   unsigned char* const pool = p.pool + (int64_t)plane * p.n_pages * p.page_bytes + at + lane * 16;
   const int32_t* const from = p.table + (int64_t)r * p.width;
@@ -546,13 +576,15 @@ __device__ __forceinline__ void move_column(const KeepParams& p, int r, int h, i
   }
 }
 
-__global__ __launch_bounds__(kKeepThreads) void keep_move_kernel(KeepParams p, int columns,
+__global__ __launch_bounds__(kKeepThreads) void keep_move_kernel(KeepParams p, int64_t width,
                                                                  int64_t items) {
+  const int64_t columns = (p.head_bytes + width - 1) / width;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int plane = (int)(item % p.planes), column = (int)(item / p.planes % columns);
     const int64_t part = item / p.planes / columns;
     const int h = (int)(part % p.heads), r = (int)(part / p.heads);
-    if (p.moved[r] >= 0) move_column(p, r, h, column, plane);
+    const Row x = p.row[r];
+    if (x.moves) move_column(p, x, r, h, column, plane, width);
   }
 }
 
@@ -588,12 +620,9 @@ hipError_t launch_cache_select(const SelectArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Rows and table entries up to which one workgroup does the bookkeeping.
-constexpr int64_t kOneRows = 256, kOneEntries = 48 * 1024;
-
 int64_t keep_workspace_bytes(int64_t rows, int64_t width, int64_t n_pages) {
   return 2 * up16(4 * ((n_pages + 31) / 32)) + up16(4 * rows * ((width + 31) / 32)) +
-         2 * up16(4 * rows) + up16(4 * n_pages);
+         up16(4 * rows) + 16 * rows + up16(4 * n_pages);
 }
 
 hipError_t launch_pages_keep(const KeepArgs& a, hipStream_t s) {
@@ -629,7 +658,7 @@ hipError_t launch_pages_keep(const KeepArgs& a, hipStream_t s) {
   p.shared = reinterpret_cast<uint32_t*>(take((p.n_pages + 31) / 32));
   p.fresh = reinterpret_cast<uint32_t*>(take((int64_t)p.rows * ((p.width + 31) / 32)));
   p.need = reinterpret_cast<int32_t*>(take(p.rows));
-  p.moved = reinterpret_cast<int32_t*>(take(p.rows));
+  p.row = reinterpret_cast<Row*>(take(4 * (int64_t)p.rows));
   p.spare = reinterpret_cast<int32_t*>(take(p.n_pages));
   if (p.rows <= kOneRows && (int64_t)p.rows * p.width <= kOneEntries && p.n_pages <= kOnePages) {
     hipLaunchKernelGGL(keep_one_kernel, dim3(1), dim3(kScanThreads), 0, s, p);
@@ -645,11 +674,16 @@ hipError_t launch_pages_keep(const KeepArgs& a, hipStream_t s) {
     hipLaunchKernelGGL(keep_table_kernel, dim3(p.rows), dim3(kKeepThreads), 0, s, p);
   }
   if (p.rows > 0) {
-    const int columns = (int)((p.head_bytes + kColumn - 1) / kColumn);
-    const int64_t items = (int64_t)p.rows * p.heads * columns * p.planes;
+    // Columns as wide as leaves two workgroups for a CU: with few tokens to move each
+    // costs its chain of look-ups.  Measured (us on the GPU): 8 rows of up to 24 tokens of 2 KB
+    // in 32 planes, columns of 256 bytes 12.5, of 1024 6.7.
+    const int64_t parts = (int64_t)p.rows * p.heads * p.planes;
+    int64_t width = kMostColumn, items;
+    while (width > kColumn && (p.head_bytes + width - 1) / width * parts < 2 * device_cus()) width /= 2;
+    items = (p.head_bytes + width - 1) / width * parts;
     if (items > 0)
       hipLaunchKernelGGL(keep_move_kernel, dim3((uint32_t)(items < kMostBlocks ? items : kMostBlocks)),
-                         dim3(kKeepThreads), 0, s, p, columns, items);
+                         dim3(kKeepThreads), 0, s, p, width, items);
   }
   return hipGetLastError();
 }
