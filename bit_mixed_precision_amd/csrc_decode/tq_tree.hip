@@ -182,6 +182,9 @@ __device__ __forceinline__ void store_row(const TreeParams& p, int64_t at, int d
   if (p.lse && d == 0) p.lse[at] = (m + __builtin_amdgcn_logf(sum) - kShift<BF>) / kLog2e;
 }
 
+// Workgroups per CU, for which the registers are laid out.
+constexpr int tree_per_cu(int64_t D) { return D > 128 ? 1 : D > 64 ? 2 : 3; }
+
 // DP: the head dimension rounded up to what the kernel is built for.
 // TEAM: waves that share a tile of tokens, each with 32 rows of its own; a workgroup
 // has 4 / TEAM teams, which take turns at the tokens of the same rows.
@@ -224,7 +227,7 @@ struct Shape {
 };
 
 template <bool BF, int DP, int TEAM>
-__global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention_kernel(
+__global__ __launch_bounds__(kTreeThreads, tree_per_cu(DP)) void tree_attention_kernel(
     TreeParams p) {
   using S = Shape<DP, TEAM>;
   constexpr int KS = S::KS, NE = S::NE, PC = S::PC, TT = S::TT, SUB = S::SUB, UT = S::UT;
@@ -265,9 +268,12 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
       const Seq s = read_seq<UT, ROWS>(p, b < p.B ? b : p.B - 1);
       return in && b < p.B && s.blocks > r ? s.t1 - s.t0 : 0;
     };
-    uint32_t all = 0;  // tiles x blocks
-    int most = 0;      // blocks
-    for (int i = 0; i < per; ++i) {
+    // the first sequence that this lane looks after: mostly its only one
+    const Seq own = read_seq<UT, ROWS>(p, lane * per < p.B ? lane * per : p.B - 1);
+    const bool has_own = lane * per < p.B;
+    uint32_t all = has_own ? (uint32_t)(own.t1 - own.t0) * own.blocks : 0;  // tiles x blocks
+    int most = has_own ? own.blocks : 0;
+    for (int i = 1; i < per; ++i) {
       const int b = lane * per + i;
       const Seq s = read_seq<UT, ROWS>(p, b < p.B ? b : p.B - 1);
       if (b < p.B) {
@@ -285,8 +291,8 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
     const uint32_t spare = gridDim.x - uni(most);
     uint32_t mine = 0, inc = 0, first = 0;
     for (; cur.r < uni(most); ++cur.r) {
-      mine = 0;
-      for (int i = 0; i < per; ++i) mine += tiles_of(lane * per + i, true, cur.r);
+      mine = has_own && own.blocks > cur.r ? own.t1 - own.t0 : 0;
+      for (int i = 1; i < per; ++i) mine += tiles_of(lane * per + i, true, cur.r);
       inc = scan_wave(mine, lane);
       const uint32_t total = uni((int)__shfl(inc, 63, kWave));
       const uint32_t share = 1 + (uint32_t)((uint64_t)total * spare / (all ? all : 1));
@@ -448,9 +454,12 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
       const int d = k * 16 + half * 8;
       q[k] = u32x4{0, 0, 0, 0};
       if (real && d < p.D) q[k] = *reinterpret_cast<const u32x4*>(qp + d * 2);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) q[k][i] ^= p.flip;
     }
+    if (p.flip)  // (without, nothing here waits for the queries)
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[k][i] ^= p.flip;
     int seen = 0;
     for (int w = 0; w < kMaskWords; ++w) {
       const int valid = c.s.m - w * 64;  // nodes of this word
@@ -716,8 +725,9 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
   if (left > 0) {
     unsigned char* buf = sTeam;
     int id = page_id(cur, cur.tile);
+    open_row(cur);
     fetch(cur, cur.tile, id, buf);
-    while (true) {
+    for (bool opened = true;; opened = false) {
       // the tiles [first, end) of one row
       const int first = cur.tile;
       const int end = (uint32_t)(cur.s.t1 - first) < left ? cur.s.t1 : first + (int)left;
@@ -727,7 +737,7 @@ __global__ __launch_bounds__(kTreeThreads, DP > 128 ? 1 : 2) void tree_attention
       Unit next = cur;
       if (left > 0) next_row(next);
       id = end - first > 1 ? page_id(cur, first + 1) : left > 0 ? page_id(next, next.tile) : 0;
-      open_row(cur);
+      if (!opened) open_row(cur);
       for (int tile = first; tile < end; ++tile) {
         const uint64_t there = present;
         if (TEAM == 4) {
@@ -914,9 +924,6 @@ struct TreeGrid {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Workgroups per CU, for which the registers are laid out.
-constexpr int tree_per_cu(int64_t D) { return D > 128 ? 1 : 2; }
-
 TreeGrid tree_grid(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity) {
   const int64_t rows = T * (Hq / Hkv);
   const bool wide = rows > kTeamRows;
@@ -941,7 +948,9 @@ hipError_t launch_tree(const TreeParams& p, int64_t grid, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.direct) return e;
   constexpr int RJ = TEAM == 4 ? 16 : 2;
-  hipLaunchKernelGGL((tree_join_kernel<BF, DP, Sh::ROWS, RJ>), dim3((uint32_t)grid, Sh::ROWS / RJ),
+  const int rows = p.T * p.G < Sh::ROWS ? p.T * p.G : Sh::ROWS;
+  hipLaunchKernelGGL((tree_join_kernel<BF, DP, Sh::ROWS, RJ>),
+                     dim3((uint32_t)grid, (rows + RJ - 1) / RJ),
                      dim3(kTreeThreads), (int)grid * RJ * 4, s, p);
   return hipGetLastError();
 }
