@@ -53,6 +53,7 @@ struct TreeParams {
   int32_t n_pages, width, B, T, words, Hq, Hkv, D, G, window;
   int32_t direct;  // one workgroup per row block: nothing is split
   int32_t runs;    // 16 tokens lie in one page
+  int32_t lines;   // tokens are whole 128-byte lines
   float scale;     // not negative
   uint32_t flip;   // sign bits of two numbers where the caller's scale is negative: of the queries
 };
@@ -95,6 +96,7 @@ __device__ __forceinline__ int64_t shfl64(int64_t v, int src) {
 
 constexpr uint32_t kOut = 0x80000000u;   // a lane offset past every buffer
 constexpr uint32_t kSpan = 0x7ffffffcu;  // bytes a buffer resource covers
+constexpr int kNonTemporal = 2;          // for lines that one wave reads once
 constexpr int kNoLoads = 0x0f70;         // s_waitcnt: until no vector load is under way
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_at(const unsigned char* p) {
@@ -104,8 +106,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_at(const unsigned char* p
   return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(((uint64_t)hi << 32) | lo),
                                            (short)0, (int)kSpan, kBufferWord3);
 }
+template <int AUX>
 __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, AUX));
 }
 // 16 bytes at the resource's base + off to LDS: lane l writes the bytes dst + 16 l.  In
 // assembly, because the compiler would otherwise wait for these copies before every
@@ -416,8 +419,13 @@ __global__ __launch_bounds__(kTreeThreads, tree_per_cu(DP)) void tree_attention_
             if (vp * 8 < D) dma16(rv, row * (int)p.row_stride + vp * 16, to + S::TILE);
           } else {
             const uint32_t off = place * 8 < D ? row * (uint32_t)p.row_stride + place * 16 : kOut;
-            kreg[r * PH + u] = load16(rk, off);
-            vreg[r * PH + u] = load16(rv, off);
+            if (p.lines) {
+              kreg[r * PH + u] = load16<kNonTemporal>(rk, off);
+              vreg[r * PH + u] = load16<kNonTemporal>(rv, off);
+            } else {
+              kreg[r * PH + u] = load16<0>(rk, off);
+              vreg[r * PH + u] = load16<0>(rv, off);
+            }
           }
         }
       }
@@ -653,10 +661,12 @@ __global__ __launch_bounds__(kTreeThreads, tree_per_cu(DP)) void tree_attention_
     for (int x = 0; x < SUB; ++x)
 #pragma unroll
       for (int r = 0; r < 16; ++r) s[x][r] = 0.f;
+    if (TEAM == 4) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int i = 0; i < KS; ++i)
 #pragma unroll
       for (int x = 0; x < SUB; ++x) s[x] = mma32<BF>(k[i][x], q[i], s[x]);
+    if (TEAM == 4) __builtin_amdgcn_s_setprio(0);
     u32x4 v[NE][SUB * 2];
     auto read_v = [&](int e) {
 #pragma unroll
@@ -703,6 +713,7 @@ __global__ __launch_bounds__(kTreeThreads, tree_per_cu(DP)) void tree_attention_
         hi[x][r / 8][r % 8 / 2] = h2;
         lo[x][r / 8][r % 8 / 2] = l2;
       }
+    if (TEAM == 4) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int e = 0; e < NE; ++e) {
       __builtin_amdgcn_sched_barrier(0);
@@ -714,6 +725,7 @@ __global__ __launch_bounds__(kTreeThreads, tree_per_cu(DP)) void tree_attention_
         if constexpr (S::SPLIT) acc[e] = mma32<BF>(v[e][y], lo[y / 2][y % 2], acc[e]);
       }
     }
+    if (TEAM == 4) __builtin_amdgcn_s_setprio(0);
   };
 
   int owned = -1, last = 0;
@@ -1007,6 +1019,9 @@ hipError_t launch_tree_attention(int dtype, const TreeArgs& a, hipStream_t strea
   p.window = (int32_t)a.window;
   p.flip = a.scale_log2 < 0 ? 0x80008000u : 0u;
   p.runs = a.page_size % 16 == 0;
+  const uint64_t places = reinterpret_cast<uint64_t>(p.K) | reinterpret_cast<uint64_t>(p.V) |
+                          (uint64_t)(p.page_stride | p.row_stride | p.head_stride) | (uint64_t)p.D * 2;
+  p.lines = places % 128 == 0;
   // a scale of zero as the least normal number: the exponents of finite scores round to
   // zero all the same, and a masked score stays -inf
   const float scale = fabsf(a.scale_log2);
