@@ -936,13 +936,27 @@ struct TreeGrid {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Two forms.  Wide: four waves share the tokens, each with 32 rows of its own, so that one
+// reading of a tile serves 128 rows.  Thin: 32 rows, and the waves share the tokens: for
+// up to 32 rows, and for short caches where the GPU has a CU for every 32 rows, because
+// four waves then walk through a row's tiles at once.  Measured (us, thin / wide), one tree
+// of 24 nodes, 8 key heads of 128 and 8 query heads each, up to 32, 128, 256, 512 tokens:
+// 10.8 / 10.4, 11.2 / 11.8, 13.2 / 15.5, 16.9 / 23.0; eight trees (384 thin workgroups)
+// 13.8 / 11.1, 14.5 / 12.5, 17.2 / 16.2; four of 64 nodes, 4 heads each of 64 8.0 / 9.7,
+// 10.1 / 10.9, 11.3 / 15.1, 12.3 / 22.9.
+constexpr int64_t kShort = 512;
+
 TreeGrid tree_grid(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity) {
-  const int64_t rows = T * (Hq / Hkv);
-  const bool wide = rows > kTeamRows;
-  const int64_t blocks = B * Hkv * ceil_div(rows, wide ? 4 * kTeamRows : kTeamRows);
+  const int64_t rows = T * (Hq / Hkv), thin = B * Hkv * ceil_div(rows, kTeamRows);
+  const bool wide = rows > kTeamRows && !(capacity <= kShort && thin <= device_cus());
+  const int64_t blocks = wide ? B * Hkv * ceil_div(rows, 4 * kTeamRows) : thin;
   const int64_t tiles = ceil_div(capacity, wide ? 64 : 128) + 1;  // a window may begin inside one
   const int64_t at_once = device_cus() * tree_per_cu(D);
-  if (tiles <= 5 || blocks >= 4 * at_once || 4 * blocks >= at_once * B * Hkv)
+  // Nothing is split where a row has few tiles (splitting and joining cost some 10 us with
+  // 32 rows, 20 with 128), or where there are enough rows, or more blocks of rows of a
+  // sequence than the split could tell apart.
+  const int64_t few = wide ? 12 : blocks < device_cus() ? 5 : 9;
+  if (tiles <= few || blocks >= 4 * at_once || 4 * blocks >= at_once * B * Hkv)
     return {blocks, true, wide};
   return {blocks * tiles < at_once ? blocks * tiles : at_once, false, wide};
 }
