@@ -191,7 +191,7 @@ constexpr int tree_per_cu(int64_t D) { return D > 128 ? 1 : D > 64 ? 2 : 3; }
 // DP: the head dimension rounded up to what the kernel is built for.
 // TEAM: waves that share a tile of tokens, each with 32 rows of its own; a workgroup
 // has 4 / TEAM teams, which take turns at the tokens of the same rows.
-template <int DP, int TEAM>
+template <int DP, int TEAM, bool TWO>
 struct Shape {
   static constexpr int KS = DP / 16;               // steps of a score
   static constexpr int NE = DP / 32;               // blocks of 32 numbers of the output
@@ -213,7 +213,7 @@ struct Shape {
   // A weight as two 16-bit numbers where memory sets the pace, as one with many rows,
   // where each costs a matrix product: rounding it to nearest then adds as much
   // error to the output as the output's own rounding.
-  static constexpr bool SPLIT = TEAM == 1;
+  static constexpr bool SPLIT = TWO;
   // Where piece c of row t lies in its row: rows whose pieces would share banks are
   // turned against each other, for the reads of K (16 rows, one piece) and of V (4
   // rows, 4 pieces).
@@ -229,10 +229,10 @@ struct Shape {
   }
 };
 
-template <bool BF, int DP, int TEAM>
+template <bool BF, int DP, int TEAM, bool TWO>
 __global__ __launch_bounds__(kTreeThreads, tree_per_cu(DP)) void tree_attention_kernel(
     TreeParams p) {
-  using S = Shape<DP, TEAM>;
+  using S = Shape<DP, TEAM, TWO>;
   constexpr int KS = S::KS, NE = S::NE, PC = S::PC, TT = S::TT, SUB = S::SUB, UT = S::UT;
   constexpr int ROWS = S::ROWS, PER = S::PER, PH = S::PH;
   extern __shared__ __attribute__((aligned(16))) unsigned char sTiles[];
@@ -647,26 +647,33 @@ __global__ __launch_bounds__(kTreeThreads, tree_per_cu(DP)) void tree_attention_
     const int a0 = first_token(tile);
     // Reads of LDS are issued well ahead of their use and kept there: a read that
     // is waited for takes longer than a matrix instruction.
-    u32x4 k[KS][SUB];
-#pragma unroll
-    for (int i = 0; i < KS; ++i)
-#pragma unroll
-      for (int x = 0; x < SUB; ++x) {
-        const int t = 32 * x + col;
-        k[i][x] = *reinterpret_cast<const u32x4*>(sK + (t * PC + S::k_at(t, 2 * i + half)) * 16);
-      }
-    __builtin_amdgcn_sched_barrier(0);
+    // (Of long heads half the keys at a time: more registers there are not.)
+    constexpr int KH = KS <= 8 ? KS : KS / 2;
     f32x16 s[SUB];
 #pragma unroll
     for (int x = 0; x < SUB; ++x)
 #pragma unroll
       for (int r = 0; r < 16; ++r) s[x][r] = 0.f;
-    if (TEAM == 4) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int i = 0; i < KS; ++i)
+    for (int i0 = 0; i0 < KS; i0 += KH) {
+      u32x4 k[KH][SUB];
 #pragma unroll
-      for (int x = 0; x < SUB; ++x) s[x] = mma32<BF>(k[i][x], q[i], s[x]);
-    if (TEAM == 4) __builtin_amdgcn_s_setprio(0);
+      for (int i = 0; i < KH; ++i)
+#pragma unroll
+        for (int x = 0; x < SUB; ++x) {
+          const int t = 32 * x + col;
+          k[i][x] = *reinterpret_cast<const u32x4*>(
+              sK + (t * PC + S::k_at(t, 2 * (i0 + i) + half)) * 16);
+        }
+      __builtin_amdgcn_sched_barrier(0);
+      if (TEAM == 4) __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int i = 0; i < KH; ++i)
+#pragma unroll
+        for (int x = 0; x < SUB; ++x) s[x] = mma32<BF>(k[i][x], q[i0 + i], s[x]);
+      if (TEAM == 4) __builtin_amdgcn_s_setprio(0);
+      if (i0 + KH < KS) __builtin_amdgcn_sched_barrier(0);
+    }
     u32x4 v[NE][SUB * 2];
     auto read_v = [&](int e) {
 #pragma unroll
@@ -936,7 +943,7 @@ struct TreeGrid {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Two forms.  Wide: four waves share the tokens, each with 32 rows of its own, so that one
+// Two forms.  Wide (heads of more than 128 numbers: always): four waves share the tokens, each with 32 rows of its own, so that one
 // reading of a tile serves 128 rows.  Thin: 32 rows, and the waves share the tokens: for
 // up to 32 rows, and for short caches where the GPU has a CU for every 32 rows, because
 // four waves then walk through a row's tiles at once.  Measured (us, thin / wide), one tree
@@ -948,7 +955,7 @@ constexpr int64_t kShort = 512;
 
 TreeGrid tree_grid(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity) {
   const int64_t rows = T * (Hq / Hkv), thin = B * Hkv * ceil_div(rows, kTeamRows);
-  const bool wide = rows > kTeamRows && !(capacity <= kShort && thin <= device_cus());
+  const bool wide = D > 128 || (rows > kTeamRows && !(capacity <= kShort && thin <= device_cus()));
   const int64_t blocks = wide ? B * Hkv * ceil_div(rows, 4 * kTeamRows) : thin;
   const int64_t tiles = ceil_div(capacity, wide ? 64 : 128) + 1;  // a window may begin inside one
   const int64_t at_once = device_cus() * tree_per_cu(D);
@@ -961,10 +968,10 @@ TreeGrid tree_grid(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int
   return {blocks * tiles < at_once ? blocks * tiles : at_once, false, wide};
 }
 
-template <bool BF, int DP, int TEAM>
+template <bool BF, int DP, int TEAM, bool TWO>
 hipError_t launch_tree(const TreeParams& p, int64_t grid, hipStream_t s) {
-  using Sh = Shape<DP, TEAM>;
-  const auto fn = tree_attention_kernel<BF, DP, TEAM>;
+  using Sh = Shape<DP, TEAM, TWO>;
+  const auto fn = tree_attention_kernel<BF, DP, TEAM, TWO>;
   if (Sh::LDS > 48 * 1024) {
     static std::atomic<uint64_t> done{0};
     const hipError_t e = lds_limit_once(reinterpret_cast<const void*>(fn), Sh::LDS, done);
@@ -981,13 +988,20 @@ hipError_t launch_tree(const TreeParams& p, int64_t grid, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool BF, int TEAM>
-hipError_t launch_tree_d(const TreeParams& p, int64_t grid, hipStream_t s) {
-  return p.D <= 64    ? launch_tree<BF, 64, TEAM>(p, grid, s)
-         : p.D <= 96  ? launch_tree<BF, 96, TEAM>(p, grid, s)
-         : p.D <= 128 ? launch_tree<BF, 128, TEAM>(p, grid, s)
-         : p.D <= 192 ? launch_tree<BF, 192, TEAM>(p, grid, s)
-                      : launch_tree<BF, 256, TEAM>(p, grid, s);
+template <bool BF>
+hipError_t launch_tree_d(const TreeParams& p, const TreeGrid& g, hipStream_t s) {
+  if (!g.wide)
+    return p.D <= 64   ? launch_tree<BF, 64, 1, true>(p, g.grid, s)
+           : p.D <= 96 ? launch_tree<BF, 96, 1, true>(p, g.grid, s)
+                       : launch_tree<BF, 128, 1, true>(p, g.grid, s);
+  const bool two = p.T * p.G <= kTeamRows;  // of long heads
+  return p.D <= 64    ? launch_tree<BF, 64, 4, false>(p, g.grid, s)
+         : p.D <= 96  ? launch_tree<BF, 96, 4, false>(p, g.grid, s)
+         : p.D <= 128 ? launch_tree<BF, 128, 4, false>(p, g.grid, s)
+         : p.D <= 192 ? two ? launch_tree<BF, 192, 4, true>(p, g.grid, s)
+                            : launch_tree<BF, 192, 4, false>(p, g.grid, s)
+         : two        ? launch_tree<BF, 256, 4, true>(p, g.grid, s)
+                      : launch_tree<BF, 256, 4, false>(p, g.grid, s);
 }
 
 }  // namespace
@@ -1045,11 +1059,7 @@ hipError_t launch_tree_attention(int dtype, const TreeArgs& a, hipStream_t strea
   p.owner = reinterpret_cast<int2*>(
       p.partial + 2 * g.grid * part_floats(g.wide ? 4 * kTeamRows : kTeamRows, p.D));
   const bool bf = dtype == TQ_BF16;
-  if (g.wide)
-    return bf ? launch_tree_d<true, 4>(p, g.grid, stream)
-              : launch_tree_d<false, 4>(p, g.grid, stream);
-  return bf ? launch_tree_d<true, 1>(p, g.grid, stream)
-            : launch_tree_d<false, 1>(p, g.grid, stream);
+  return bf ? launch_tree_d<true>(p, g, stream) : launch_tree_d<false>(p, g, stream);
 }
 
 hipError_t launch_tree_mask(const int32_t* parents, int64_t B, int64_t T, void* mask,
