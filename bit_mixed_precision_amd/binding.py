@@ -99,8 +99,7 @@ SIGNATURES = {
                               _P, _P, _P, _I64, _P, _I64, _I64, _I64, _I64, _I64, _D, _I64, _D, _P,
                               _I64, _I64, _I64, _P]),
     "tq_cache_select": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I64, _P, _P, _P,
-                             _P, _I64, _P]),
-    "tq_cache_select_workspace": (_I64, [_I64, _I64, _I64]),
+                             _P]),
     "tq_pages_keep": (_I, [_P, _I64, _I64, _I64, _P, _P, _I64, _I64, _I64, _P, _I64, _I64, _I64,
                            _P, _P, _P, _P, _P, _P, _I64, _P]),
     "tq_pages_keep_workspace": (_I64, [_I64, _I64, _I64]),
@@ -1065,19 +1064,6 @@ def _sums(scores, B, H, where):
     return shape[2], strides[0], strides[1]
 
 
-def tq_cache_select_workspace(B: int, H: int, S: int) -> int:
-    """Workspace bytes of tq_cache_select on the current GPU."""
-    n = int(lib.tq_cache_select_workspace(B, H, S))
-    _check(min(n, 0), "tq_cache_select_workspace")
-    return n
-
-
-@functools.lru_cache(maxsize=256)
-def _select_workspace(dev, *shape):
-    with _torch.cuda.device(dev):
-        return lib.tq_cache_select_workspace(*shape)
-
-
 def tq_cache_select(scores, lens, budget: int, recent: int = 0, sinks: int = 0, stream=None):
     """Which of the lens[b] tokens of every sequence and head stay within `budget`: the first
     `sinks`, the last `recent`, and of the others those of the largest scores float32
@@ -1094,16 +1080,13 @@ def tq_cache_select(scores, lens, budget: int, recent: int = 0, sinks: int = 0, 
     _int32(lens, "lens", (B,), where)
     dev = scores.get_device()
     _all_on(where, dev, ("scores", scores), ("lens", lens))
-    n = _select_workspace(dev, B, H, S)
-    _check(min(n, 0), where)
     if budget < 0 or budget > 1 << 30:
         raise TQError(TQ_ERR_SHAPE, f"{where}: a budget of {budget}")
-    workspace = _empty(scores, (n,), _torch.uint8, stream) if n else None
     keep, counts = _empty(scores, (B, H, budget), _I32T, stream), _empty(scores, (B,), _I32T, stream)
     sums = _empty(scores, (B, H, budget), _torch.float32, stream)
     _launch(where, dev, lib.tq_cache_select, scores.data_ptr(), s_seq, s_head, S, lens.data_ptr(),
             B, H, budget, recent, sinks, keep.data_ptr(), counts.data_ptr(), sums.data_ptr(),
-            _address(workspace), n, _raw_stream(stream, dev))
+            _raw_stream(stream, dev))
     return keep, counts, sums
 
 

@@ -95,9 +95,7 @@ struct SelectArgs {
   int32_t* keep;    // [B][H][budget]
   int32_t* counts;  // [B]
   float* sums;      // [B][H][budget] or nullptr
-  void* workspace;
 };
-int64_t select_workspace_bytes(int64_t B, int64_t H, int64_t S);
 hipError_t launch_cache_select(const SelectArgs& a, hipStream_t stream);
 
 // Page bookkeeping.  A sequence of `len` tokens holds the first

@@ -527,15 +527,19 @@ __device__ __forceinline__ void move_column(const KeepParams& p, const Row& x, i
 #pragma unroll
     for (int k = 0; k < kDepth; ++k) {
       const int64_t i = i0 + k * slots + sub;
-      t[k] = sub < slots && i < x.total ? source_of(p, x, g, r, h, (int)i) : -1;
+      t[k] = sub < slots && i < x.total ? source_of(p, x, g, r, h, (int)i) : INT32_MIN;
     }
 #pragma unroll
     for (int k = 0; k < kDepth; ++k) {
       w.src[k] = w.dst[k] = -1;
       const int i = (int)(i0 + k * slots + sub);
-      if (t[k] < 0) continue;
-      const int e = (int)div_page(p.page, i), es = (int)div_page(p.page, t[k]);
-      if (t[k] == i && !(fresh[e / 32] >> (e & 31) & 1)) continue;
+      if (t[k] == INT32_MIN) continue;
+      const int e = (int)div_page(p.page, i);
+      if (t[k] < 0 || t[k] == i) {  // the slot keeps its token
+        if (!(fresh[e / 32] >> (e & 31) & 1)) continue;
+        t[k] = i;
+      }
+      const int es = (int)div_page(p.page, t[k]);
       const int32_t sp = from[es], dp = to[e];
       if (!names_page(p, sp) || !names_page(p, dp)) continue;
       w.src[k] = sp * p.page_bytes + (t[k] - es * p.page_size) * p.row_bytes;
@@ -591,8 +595,6 @@ __global__ __launch_bounds__(kKeepThreads) void keep_move_kernel(KeepParams p, i
 int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
 
 }  // namespace
-
-int64_t select_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
 
 hipError_t launch_cache_select(const SelectArgs& a, hipStream_t stream) {
   SelectParams p{};
@@ -667,11 +669,15 @@ hipError_t launch_pages_keep(const KeepArgs& a, hipStream_t s) {
     const int64_t blocks = (words + kKeepThreads - 1) / kKeepThreads;
     hipLaunchKernelGGL(keep_clear_kernel, dim3((uint32_t)(blocks < 1024 ? blocks : 1024)),
                        dim3(kKeepThreads), 0, s, p);
-    hipLaunchKernelGGL(keep_mark_kernel, dim3(p.rows), dim3(kKeepThreads), 0, s, p);
-    hipLaunchKernelGGL(keep_need_kernel, dim3((p.rows + kKeepThreads / kWave - 1) / (kKeepThreads / kWave)),
-                       dim3(kKeepThreads), 0, s, p);
+    constexpr int kRowWaves = kKeepThreads / kWave;
+    if (p.rows > 0) {
+      hipLaunchKernelGGL(keep_mark_kernel, dim3(p.rows), dim3(kKeepThreads), 0, s, p);
+      hipLaunchKernelGGL(keep_need_kernel, dim3((p.rows + kRowWaves - 1) / kRowWaves),
+                         dim3(kKeepThreads), 0, s, p);
+    }
     hipLaunchKernelGGL(keep_deal_kernel, dim3(1), dim3(kScanThreads), 0, s, p);
-    hipLaunchKernelGGL(keep_table_kernel, dim3(p.rows), dim3(kKeepThreads), 0, s, p);
+    if (p.rows > 0)
+      hipLaunchKernelGGL(keep_table_kernel, dim3(p.rows), dim3(kKeepThreads), 0, s, p);
   }
   if (p.rows > 0) {
     // Columns as wide as leaves two workgroups for a CU: with few tokens to move each

@@ -40,7 +40,6 @@ struct Entries {
   decltype(&tq_pages_compact) pages_compact;
   decltype(&tq_cache_weights) cache_weights;
   decltype(&tq_cache_select) cache_select;
-  decltype(&tq_cache_select_workspace) cache_select_workspace;
   decltype(&tq_pages_keep) pages_keep;
   decltype(&tq_pages_keep_workspace) pages_keep_workspace;
 };
@@ -490,20 +489,16 @@ PyObject* cache_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
                     sinks = PyLong_AsLongLong(a[4]);
     if (PyErr_Occurred()) return nullptr;
     const int64_t B = scores.size(0), H = scores.size(1), S = scores.size(2);
-    const int64_t bytes = c.cache_select_workspace(B, H, S);
-    if (bytes < 0) return PyLong_FromLong((long)bytes);
     if (budget < 0 || budget > int64_t(1) << 30) return none();
     bool ok;
     void* s = stream_of(d, &ok);
     if (!ok) return nullptr;
     at::Tensor keep = at::empty({B, H, budget}, lens.options()),
                counts = at::empty({B}, lens.options()),
-               sums = at::empty({B, H, budget}, scores.options()), ws;
-    if (bytes > 0) ws = at::empty({bytes}, lens.options().dtype(at::kByte));
+               sums = at::empty({B, H, budget}, scores.options());
     const int st = c.cache_select(ptr<float>(scores), scores.stride(0), scores.stride(1), S,
                                   ptr<int32_t>(lens), B, H, budget, recent, sinks,
-                                  ptr<int32_t>(keep), ptr<int32_t>(counts), ptr<float>(sums),
-                                  bytes > 0 ? ws.data_ptr() : nullptr, bytes, s);
+                                  ptr<int32_t>(keep), ptr<int32_t>(counts), ptr<float>(sums), s);
     return st == TQ_OK ? tuple({keep, counts, sums}) : PyLong_FromLong(st);
   });
 }
@@ -571,7 +566,6 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !take("tq_pages_workspace", &e.pages_workspace) || !take("tq_pages_fork", &e.pages_fork) ||
       !take("tq_pages_grow", &e.pages_grow) || !take("tq_pages_compact", &e.pages_compact) ||
       !take("tq_cache_weights", &e.cache_weights) || !take("tq_cache_select", &e.cache_select) ||
-      !take("tq_cache_select_workspace", &e.cache_select_workspace) ||
       !take("tq_pages_keep", &e.pages_keep) ||
       !take("tq_pages_keep_workspace", &e.pages_keep_workspace))
     return nullptr;

@@ -21,9 +21,11 @@ int tree_shapes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_
   if (T < 1 || T > kMaxNodes) return TQ_ERR_SHAPE;
   const int st = attn_shapes(B, Hq, Hkv, D, page_size, width);
   if (st != TQ_OK) return st;
-  // the kernels count all tiles (64 tokens of 32 rows at least) in 32 bits
+  // the kernels count all tiles (64 tokens of 32 rows at least) in 32 bits, and a launch holds
+  // fewer than 2^24 workgroups of 256 threads
   const int64_t blocks = B * Hkv * ((T * (Hq / Hkv) + 31) / 32);
-  if (blocks > INT32_MAX || blocks * (width * page_size / 64 + 2) > INT32_MAX) return TQ_ERR_SHAPE;
+  if (blocks >= int64_t(1) << 24 || blocks * (width * page_size / 64 + 2) > INT32_MAX)
+    return TQ_ERR_SHAPE;
   return TQ_OK;
 }
 
@@ -37,7 +39,7 @@ bool tree_strides(const tq::TreeArgs& a) {
          a.row_stride % 8 == 0 && a.head_stride % 8 == 0;
 }
 
-constexpr int64_t kMaxSelectRows = int64_t(1) << 22;  // of 1024 threads: fewer than 2^32 in a launch
+constexpr int64_t kMaxSelectRows = (int64_t(1) << 22) - 1;  // of 1024 threads: fewer than 2^32
 constexpr int64_t kMostWeightRows = 8192;  // their sums lie in LDS
 
 }  // namespace
@@ -181,30 +183,20 @@ int tq_cache_weights(int dtype, const void* Q, int64_t q_seq, int64_t q_tok, int
   return finish(tq::launch_cache_weights(dtype, w, static_cast<hipStream_t>(stream)));
 }
 
-int64_t tq_cache_select_workspace(int64_t B, int64_t H, int64_t S) {
-  if (B < 0 || H < 0 || S < 0 || B > kMaxAttnBatch || H > kMaxAttnHeads || S > kMaxTokens ||
-      B * H > kMaxSelectRows)
-    return TQ_ERR_SHAPE;
-  return tq::select_workspace_bytes(B, H, S);
-}
-
 int tq_cache_select(const float* scores, int64_t s_seq, int64_t s_head, int64_t S,
                     const int32_t* lens, int64_t B, int64_t H, int64_t budget, int64_t recent,
-                    int64_t sinks, int32_t* keep, int32_t* counts, float* sums, void* workspace,
-                    int64_t workspace_bytes, void* stream) {
+                    int64_t sinks, int32_t* keep, int32_t* counts, float* sums, void* stream) {
   if (B < 0 || H < 0 || S < 0 || budget < 0 || recent < 0 || sinks < 0) return TQ_ERR_SHAPE;
   if (B == 0 || H == 0) return TQ_OK;
   if ((S > 0 && !scores) || !lens || (budget > 0 && !keep) || !counts) return TQ_ERR_NULL;
-  const int64_t wants = tq_cache_select_workspace(B, H, S);
-  if (wants < 0 || budget > kMaxTokens || recent > budget || sinks > budget - recent)
+  if (B > kMaxAttnBatch || H > kMaxAttnHeads || S > kMaxTokens || B * H > kMaxSelectRows ||
+      budget > kMaxTokens || recent > budget || sinks > budget - recent)
     return TQ_ERR_SHAPE;
   s_seq = step(B, s_seq);
   s_head = step(H, s_head);
-  if (!stride_ok(B, s_seq) || !stride_ok(H, s_head) || workspace_bytes < wants)
-    return TQ_ERR_SHAPE;
-  if (wants > 0 && !workspace) return TQ_ERR_NULL;
+  if (!stride_ok(B, s_seq) || !stride_ok(H, s_head)) return TQ_ERR_SHAPE;
   if (!aligned(scores, 4) || !aligned(lens, 4) || !aligned(keep, 4) || !aligned(counts, 4) ||
-      !aligned(sums, 4) || !aligned(workspace, 16))
+      !aligned(sums, 4))
     return TQ_ERR_ALIGN;
   const int st = device_ready();
   if (st != TQ_OK) return st;
@@ -222,7 +214,6 @@ int tq_cache_select(const float* scores, int64_t s_seq, int64_t s_head, int64_t 
   a.keep = keep;
   a.counts = counts;
   a.sums = sums;
-  a.workspace = workspace;
   return finish(tq::launch_cache_select(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -142,13 +142,15 @@ __global__ __launch_bounds__(kThreads, DV > 128 ? 2 : 3) void cache_weights_kern
     tile = s.t0 + at % n;
   }
 
-  // Rows r0 .. of the queries to LDS, zeros past the last one and past a head's end.
+  // Rows r0 .. of the queries to LDS, zeros past a head's end.  What stands behind the last row
+  // is multiplied and gets a weight of 2^(-inf): the last row again, since zeros times
+  // an infinite key would make NaN of that.
   auto stage = [&](int r0, int rows) {
     const int n = (rows - r0 < chunk ? rows - r0 : chunk) + 15 & ~15;
     for (int x = anew(threadIdx.x); x < n * PC; x += kThreads) {
-      const int r = x / PC, piece = x - r * PC, row = r0 + r;
+      const int r = x / PC, piece = x - r * PC, row = r0 + r < rows ? r0 + r : rows - 1;
       u32x4 v = {0, 0, 0, 0};
-      if (row < rows && piece * 8 < p.D) {
+      if (piece * 8 < p.D) {
         const int i = div_page(p.group, row);
         v = *reinterpret_cast<const u32x4*>(p.Q + b * p.q_seq + i * p.q_tok +
                                             (int64_t)(h * p.G + (row - i * p.G)) * p.q_head +

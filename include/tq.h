@@ -508,13 +508,15 @@ int tq_tree_mask(const int32_t* parents, int64_t B, int64_t T, int64_t* mask, in
  * lse = -inf.  Q: number d of head h of node i of sequence b at q_seq b + q_tok i +
  * q_head h + d; Out [B][T][Hq][D]; lse fp32 [B][T][Hq] or NULL.
  * fp16 or bfloat16 in and out, fp32 scores, weights and sums.  Up to 32 rows (T G <= 32) a
- * weight enters the product with v as two 16-bit numbers, as in tq_paged_attention; with
- * more rows as one, rounded to nearest (2^-11 of itself in fp16, 2^-8 in bfloat16, and
- * in fp16 within 2^-38 of the row's largest).  A token that a node does not see has no
+ * weight enters the product with v as two 16-bit numbers, rounded to within 2^-22 (fp16;
+ * 2^-16 bfloat16) of itself; with more rows as two or as one, rounded to nearest (2^-11 of
+ * itself in fp16, 2^-8 in bfloat16).  In fp16 a weight may also be off by 2^-34 of the row's
+ * largest, and one below that may add nothing.  An infinite value gives an infinite
+ * result, or NaN where its weight is zero or, in fp16, may add nothing.  A token that a node does not see has no
  * influence on it, whatever its key and value hold.  The same bits on every run.
  * Outputs and workspace must not overlap the inputs.
- * Limits as tq_paged_attention's, and T <= 256; B * Hkv * ceil(T G / 32) * (width *
- * page_size / 64 + 2) < 2^31.  workspace: tq_tree_attention_workspace(...) bytes,
+ * Limits as tq_paged_attention's, and T <= 256; B * Hkv * ceil(T G / 32) < 2^24, and times
+ * (width * page_size / 64 + 2) < 2^31.  workspace: tq_tree_attention_workspace(...) bytes,
  * 16-byte aligned, contents irrelevant; calls that overlap on one workspace race.
  * Errors: as tq_paged_attention's; TQ_ERR_SHAPE for a window below T.  B = 0 or T = 0
  * is a no-op. */
@@ -561,17 +563,12 @@ int tq_cache_weights(int dtype, const void* Q, int64_t q_seq, int64_t q_tok, int
  * sequence b at s_seq b + s_head h + t, t < S.
  * keep int32 [B][H][budget]: their indexes, ascending, then -1; counts int32 [B]:
  * min(n, budget); sums fp32 [B][H][budget] or NULL: their scores, then 0.
- * All device pointers.  sinks + recent <= budget <= 2^30, S <= 2^30, B H <= 2^22.
- * workspace: tq_cache_select_workspace(...) bytes, 16-byte aligned; outputs and
- * workspace must not overlap the inputs.  Errors: TQ_ERR_NULL, TQ_ERR_SHAPE,
+ * All device pointers.  sinks + recent <= budget <= 2^30, S <= 2^30, B <= 2^20, H <= 2^12,
+ * B H < 2^22.  Outputs must not overlap the inputs.  Errors: TQ_ERR_NULL, TQ_ERR_SHAPE,
  * TQ_ERR_ALIGN, TQ_ERR_DEVICE.  B = 0 or H = 0 is a no-op. */
 int tq_cache_select(const float* scores, int64_t s_seq, int64_t s_head, int64_t S,
                     const int32_t* lens, int64_t B, int64_t H, int64_t budget, int64_t recent,
-                    int64_t sinks, int32_t* keep, int32_t* counts, float* sums, void* workspace,
-                    int64_t workspace_bytes, void* stream);
-
-/* Workspace bytes of tq_cache_select; TQ_ERR_SHAPE for shapes it refuses. */
-int64_t tq_cache_select_workspace(int64_t B, int64_t H, int64_t S);
+                    int64_t sinks, int32_t* keep, int32_t* counts, float* sums, void* stream);
 
 /* The pages of a cache.  The page table and the lengths are the whole state: a
  * page is free when no row holds it, and a page held by several rows is shared.
@@ -638,8 +635,8 @@ int tq_pages_copy(void* pool, int64_t planes, int64_t n_pages, int64_t page_byte
  * A token is `heads` parts of page_bytes / page_size / heads bytes, each with a list of
  * its own, and every run of planes / groups planes likewise: keep int32
  * [groups][rows][heads][n].  Slot base[r] + i gets token keep[..][i].  Lists ascend, so
- * that entry i is base[r] + i at least; an entry below that, or past the row's length,
- * leaves its slot as it is.  Slots past the last token, and those of pages that a row
+ * that entry i is base[r] + i at least; for an entry below that, or past the row's length,
+ * the slot keeps its token.  Slots past the last token, and those of pages that a row
  * releases, stay as they are.
  * A page that is held by more than one table entry is not written: where a token in it
  * would change, the row gets a free page in its place, with its kept tokens.  A row that

@@ -189,8 +189,8 @@ def pages_keep_ref(page_table, lens, keep, counts, base, n_pages, size):
         for g in range(groups):
             for h in range(heads):
                 for i in range(total):
-                    t = source(g, h, i)
-                    if t < 0 or (t == i and i // size not in fresh):
+                    t = source(g, h, i) if acts(g, h, i) else i
+                    if t == i and i // size not in fresh:
                         continue
                     sp, dp = page_table[r, t // size], table[r, i // size]
                     if names(sp) and names(dp):

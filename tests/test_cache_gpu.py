@@ -115,6 +115,31 @@ def test_weights_rows_left_out():
     assert torch.equal(got, again)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("T,Hq", [(1, 2), (3, 14), (9, 4)])
+def test_weights_of_infinite_keys(dtype, T, Hq):
+    """A score of -inf is a weight of zero for every row, also where the rows do not fill a
+    tile of the matrix instruction."""
+    q, k, v, pt, lens, nodes = tree(9, dtype, [300, 40], [T, T], T, Hq, 2, 64, 16)
+    q[..., 0] = -q[..., 0].abs() - 1
+    chain = np.tril(np.ones((2, T, T), bool))
+    hit = [(0, 70), (0, 130), (1, 3)]
+    for b, t in hit:
+        k[pt[b, t // 16].long(), t % 16, :, 0] = float("inf")
+    out, lse = tq.tq_tree_attention(q, k, v, pt, lens, nodes=nodes, return_lse=True)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    scores = torch.zeros(2, 2, 330, device="cuda")
+    tq.tq_cache_weights(q, k, pt, lens, lse, scores, nodes=nodes)
+    for b, t in hit:  # the same without these tokens, whose keys are then finite
+        k[pt[b, t // 16].long(), t % 16, :, 0] = 0
+        assert torch.equal(scores[b, :, t], torch.zeros(2, device="cuda"))
+    want = torch.zeros_like(scores)
+    tq.tq_cache_weights(q, k, pt, lens, lse, want, nodes=nodes)
+    for b, t in hit:
+        want[b, :, t] = 0
+    assert torch.equal(scores, want)
+
+
 def test_weights_add_up_and_repeat():
     """One token's weights over a whole cache add up to the heads of a group."""
     q, k, v, pt, lens, nodes = tree(5, "bf16", [4000, 77], [1, 1], 1, 16, 4, 128, 16)
@@ -300,6 +325,27 @@ def test_keep_odd_arguments():
     assert torch.equal(pool[:, same.cuda()], before[:, same.cuda()])
 
 
+def test_keep_entries_that_name_no_token_of_a_shared_page():
+    """A slot whose list entry names no token keeps its token, also where the row gets another
+    page for it."""
+    size = 8
+    pt, ln, P = dealt(9, [20, 20], size, 3, width=4)
+    pt[1, :2] = pt[0, :2]
+    keep = np.array([[-1, 3, 2 ** 31 - 1, 9, 2, 11, 12, 13, 14, -5], list(range(10))], np.int32)
+    pool = pool_of(8, 2, P, size, 2, 16)
+    table, lens, short = check_keep(pool, pt, ln, i32(keep), i32([10, 10]), None, size)
+    assert short.tolist() == [0] and table[1].tolist() == pt[1, :2].tolist() + [-1, -1]
+    mine, old = pool[:, table[0, 0].long()], pool[:, pt[0, 0].long()]
+    assert torch.equal(mine[:, [0, 1, 2, 4]], old[:, [0, 3, 2, 4]])
+
+
+def test_keep_no_rows_of_many_pages():
+    pool = torch.zeros(1, 70000, 1, 8, dtype=torch.float16, device="cuda")
+    none = torch.zeros(0, 4, dtype=torch.int32, device="cuda")
+    table, lens, short = tq.tq_pages_keep(pool, none, none[:, 0].contiguous(), none, none[:, 0].contiguous(), 1)
+    assert table.shape == (0, 4) and short.tolist() == [0]
+
+
 def test_keep_empty_calls():
     pt, ln, P = dealt(6, [30, 20], 4, 1)
     pool = pool_of(5, 2, P, 4, 2, 16)
@@ -397,3 +443,27 @@ def test_captured_steps():
             results.append([x.clone() for x in (r or got)] + [pool.clone(), scores.clone()])
         for x, y in zip(*results):
             assert torch.equal(x, y), i
+
+
+def test_other_streams():
+    """Calls on a stream of their own, handed over or current, give what the first stream does."""
+    q, k, v, pt, lens, nodes = tree(6, "f16", [500, 90], [3, 2], 3, 8, 2, 64, 16, poison=False)
+    _, lse = tq.tq_tree_attention(q, k, v, pt, lens, nodes=nodes, return_lse=True)
+    pool = torch.stack([k, v])
+
+    def run(**kw):
+        s, p = torch.zeros(2, 2, 520, device="cuda"), pool.clone()
+        torch.cuda.synchronize()
+        tq.tq_cache_weights(q, k, pt, lens, lse, s, nodes=nodes, **kw)
+        keep, counts, sums = tq.tq_cache_select(s, lens, 64, 8, 2, **kw)
+        got = tq.tq_pages_keep(p, pt, lens, keep, counts, 16, **kw)
+        torch.cuda.synchronize()
+        return [s, p, keep, counts, sums, *got]
+
+    want = run()
+    stream = torch.cuda.Stream()
+    given = run(stream=stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        current = run()
+    for x, y, z in zip(want, given, current):
+        assert torch.equal(x, y) and torch.equal(x, z)
