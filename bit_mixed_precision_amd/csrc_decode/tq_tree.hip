@@ -48,7 +48,7 @@ struct TreeParams {
   unsigned char* Out;
   float* lse;
   float* partial;  // [workgroups][2][part_floats]
-  int2* owner;     // [workgroups]: the row block it began and left unfinished (or -1), its last workgroup
+  int2* owner;     // [row blocks]: its first workgroup (-1 where that finished it), its last one
   FastDiv page, group;
   int32_t n_pages, width, B, T, words, Hq, Hkv, D, G, window;
   int32_t direct;  // one workgroup per row block: nothing is split
@@ -735,7 +735,6 @@ __global__ __launch_bounds__(kTreeThreads, tree_per_cu(DP)) void tree_attention_
     if (TEAM == 4) __builtin_amdgcn_s_setprio(0);
   };
 
-  int owned = -1, last = 0;
   if (tid < S::TEAMS) sOdd[tid] = 0;
   if (S::BUFFERS == 2 && p.D < DP)  // direct copies leave the numbers past a head's end out
     for (int i = tid; i < S::TILES / 16; i += kTreeThreads)
@@ -777,15 +776,14 @@ __global__ __launch_bounds__(kTreeThreads, tree_per_cu(DP)) void tree_attention_
       }
       cur.tile = end - 1;
       close_row(cur, first, begins, ends);
-      if (begins && !ends) {  // goes on in the following workgroups
-        owned = (cur.r * p.B + cur.b) * p.Hkv + cur.h;
-        last = (int)blockIdx.x - part + (int)cut.part_of(row_end - 1);
-      }
+      if (begins && !p.direct && tid == 0)  // (where it does not end here, the following ones go on)
+        p.owner[(cur.r * p.B + cur.b) * p.Hkv + cur.h] =
+            make_int2(ends ? -1 : (int)blockIdx.x,
+                      (int)blockIdx.x - part + (int)cut.part_of(row_end - 1));
       if (left == 0) break;
       cur = next;
     }
   }
-  if (!p.direct && tid == 0) p.owner[blockIdx.x] = make_int2(owned, last);
 
   // rows of nodes that are not there: zeros and -inf; looked for 64 at a time
   const int64_t all = (int64_t)p.B * p.T;
@@ -803,95 +801,85 @@ __global__ __launch_bounds__(kTreeThreads, tree_per_cu(DP)) void tree_attention_
   }
 }
 
-// Joins the partial results of the row blocks that span workgroups: one workgroup for RJ
-// rows of the block that workgroup blockIdx.x began and left unfinished.  A group of lanes,
-// a power of two that holds D / 4, takes a row's numbers; where there are more groups than
-// rows, they share a row's parts.
+// Joins the partial results of the row blocks that span workgroups.  A group of lanes, a power
+// of two that holds D / 4, takes a row: each lane looks up the maximum and sum of one part, then
+// all of them its numbers, part by part.  `share` groups, where rows are few and their
+// parts many, take a row's parts in turns.
 template <int DP>
 constexpr int join_lanes() {
   return DP <= 64 ? 16 : DP <= 128 ? 32 : 64;
 }
-template <bool BF, int DP, int ROWS, int RJ>
-__global__ __launch_bounds__(kTreeThreads) void tree_join_kernel(TreeParams p) {
-  constexpr int CL = join_lanes<DP>(), GROUPS = kTreeThreads / CL;
-  constexpr int SHARE = GROUPS > RJ ? GROUPS / RJ : 1;  // groups that share a row
-  constexpr int ML = kTreeThreads / RJ;                 // threads that look for a row's maximum
-  extern __shared__ float sW[];                         // [parts][RJ]: weights of the parts
-  __shared__ float sRed[2][RJ][ML];
-  __shared__ __attribute__((aligned(16))) float sV[SHARE > 1 ? GROUPS * CL * 4 : 4];
-  const int2 own = p.owner[blockIdx.x];
-  if (own.x < 0) return;
-  const int h = own.x % p.Hkv, rest = own.x / p.Hkv, b = rest % p.B, r = rest / p.B;
-  const int nodes = p.nodes ? p.nodes[b] : p.T;
-  const int in0 = blockIdx.y * RJ, row0 = r * ROWS + in0;
-  const int rows = (nodes < p.T ? nodes : p.T) * p.G - row0;
-  if (rows <= 0) return;
-  const int tid = threadIdx.x;
+template <bool BF, int DP, int ROWS>
+__global__ __launch_bounds__(kTreeThreads) void tree_join_kernel(TreeParams p, int blocks, int share) {
+  constexpr int CL = join_lanes<DP>(), GROUPS = kTreeThreads / CL, U = 8;
+  __shared__ __attribute__((aligned(16))) float sV[kTreeThreads * 4];
+  const int tid = threadIdx.x, lane = tid % CL, col = lane * 4;
+  const int turn = tid / CL % share, mine = tid / CL / share, step = GROUPS / share;
+  const int base_lane = (tid & (kWave - 1)) - lane;
   const int64_t size = part_floats(ROWS, p.D);
-  const int n = own.y - (int)blockIdx.x + 1;
-  // part 0 is this workgroup's second slot, the others the first slots that follow
-  auto part = [&](int k) {
-    return p.partial + (2 * ((int64_t)blockIdx.x + k) + (k == 0 ? 1 : 0)) * size;
-  };
-  {
-    const int j = tid % RJ, k0 = tid / RJ;
-    const int at_m = ROWS * p.D + in0 + j, at_l = at_m + ROWS;
-    float m = -INFINITY, sum = 0.f;
-    if (j < rows)
-      for (int k = k0; k < n; k += ML) m = fmaxf(m, part(k)[at_m]);
-    sRed[0][j][k0] = m;
-    __syncthreads();
-    m = -INFINITY;
-    for (int k = 0; k < ML; ++k) m = fmaxf(m, sRed[0][j][k]);
-    const float base = m == -INFINITY ? 0.f : m;
-    if (j < rows)
-      for (int k = k0; k < n; k += ML) {
-        // a part without weight adds nothing, also where it has met NaN
-        const float lk = part(k)[at_l], w = __builtin_amdgcn_exp2f(part(k)[at_m] - base);
-        sW[k * RJ + j] = lk == 0.f ? 0.f : w;
-        sum += w * lk;
-      }
-    sRed[1][j][k0] = sum;
-    __syncthreads();
-  }
-  const int group = tid / CL, col = tid % CL * 4;
-  for (int j0 = 0; j0 < RJ; j0 += GROUPS / SHARE) {
-    const int j = j0 + group / SHARE, share = group % SHARE;
-    if (j0 >= rows) break;
-    float4v v = {0, 0, 0, 0};
-    if (j < rows && col < p.D) {
-      constexpr int U = 4;
-      for (int k0 = share; k0 < n; k0 += U * SHARE) {
-        float4v x[U];
-        float w[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int k = k0 + u * SHARE;
-          x[u] = *reinterpret_cast<const float4v*>(part(k < n ? k : n - 1) + (int64_t)(in0 + j) * p.D + col);
-          w[u] = k < n ? sW[k * RJ + j] : 0.f;
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (w[u] != 0.f) v += w[u] * x[u];
-      }
-    }
-    if constexpr (SHARE > 1) {
-      *reinterpret_cast<float4v*>(sV + tid * 4) = v;
-      __syncthreads();
-      v = float4v{0, 0, 0, 0};
-      for (int i = 0; i < SHARE; ++i)
-        v += *reinterpret_cast<const float4v*>(sV + ((group / SHARE * SHARE + i) * CL) * 4 + col);
-      __syncthreads();
-    }
-    if (share == 0 && j < rows && col < p.D) {
+  for (int block = blockIdx.x; block < blocks; block += gridDim.x) {
+    const int2 own = p.owner[block];
+    const int h = block % p.Hkv, rest = block / p.Hkv, b = rest % p.B, r = rest / p.B;
+    const int nodes = p.nodes ? p.nodes[b] : p.T;
+    int rows = (nodes < p.T ? nodes : p.T) * p.G - r * ROWS;
+    if (rows <= 0 || own.x < 0) continue;  // (a block without rows has no owner)
+    rows = rows < ROWS ? rows : ROWS;
+    const int n = own.y - own.x + 1;
+    // part 0 is the second slot of the workgroup that began the block, the others the first
+    // slots of those that follow
+    auto part = [&](int k) {
+      return p.partial + (2 * ((int64_t)own.x + k) + (k == 0 ? 1 : 0)) * size;
+    };
+    for (int j0 = blockIdx.y * step; j0 < rows; j0 += gridDim.y * step) {
+      const int j = j0 + mine;
+      const bool real = j < rows;
+      const int at_m = ROWS * p.D + (real ? j : 0), at_l = at_m + ROWS;
       float m = -INFINITY, total = 0.f;
-      for (int k = 0; k < ML; ++k) {
-        m = fmaxf(m, sRed[0][j][k]);
-        total += sRed[1][j][k];
+      for (int k = lane; k < n; k += CL) m = fmaxf(m, part(k)[at_m]);
+#pragma unroll
+      for (int off = 1; off < CL; off <<= 1) m = fmaxf(m, __shfl_xor(m, off, kWave));
+      const float base = m == -INFINITY ? 0.f : m;
+      float4v v = {0, 0, 0, 0};
+      for (int k0 = 0; k0 < n; k0 += CL) {
+        const int k = k0 + lane < n ? k0 + lane : n - 1;
+        float w = __builtin_amdgcn_exp2f(part(k)[at_m] - base);
+        const float l = part(k)[at_l];
+        // a part without weight adds nothing, also where it has met NaN
+        if (k0 + lane >= n || l == 0.f) w = 0.f;
+        if (w != 0.f) total += w * l;
+        const int most = n - k0 < CL ? n - k0 : CL;
+        for (int x0 = turn; x0 < most; x0 += U * share) {
+          float4v x[U];
+          float wx[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int i = x0 + u * share < most ? x0 + u * share : most - 1;
+            wx[u] = __shfl(w, base_lane + i, kWave);
+            if (x0 + u * share >= most) wx[u] = 0.f;
+            x[u] = float4v{0, 0, 0, 0};
+            if (wx[u] != 0.f && real && col < p.D)
+              x[u] = *reinterpret_cast<const float4v*>(part(k0 + i) + (int64_t)j * p.D + col);
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (wx[u] != 0.f) v += wx[u] * x[u];
+        }
       }
-      const int row = row0 + j, i = div_page(p.group, row), g = row - i * p.G;
-      store_row<BF>(p, ((int64_t)b * p.T + i) * p.Hq + h * p.G + g, col, m, total,
-                    total == 0.f ? 0.f : 1.f / total, v);
+#pragma unroll
+      for (int off = 1; off < CL; off <<= 1) total += __shfl_xor(total, off, kWave);
+      if (share > 1) {
+        *reinterpret_cast<float4v*>(sV + tid * 4) = v;
+        __syncthreads();
+        if (turn == 0)
+          for (int i = 1; i < share; ++i)
+            v += *reinterpret_cast<const float4v*>(sV + (tid + i * CL) * 4);
+        __syncthreads();
+      }
+      if (turn == 0 && real && col < p.D) {
+        const int row = r * ROWS + j, i = div_page(p.group, row), g = row - i * p.G;
+        store_row<BF>(p, ((int64_t)b * p.T + i) * p.Hq + h * p.G + g, col, m, total,
+                      total == 0.f ? 0.f : 1.f / total, v);
+      }
     }
   }
 }
@@ -937,7 +925,7 @@ __global__ __launch_bounds__(kTreeThreads) void tree_mask_kernel(const int32_t* 
 }
 
 struct TreeGrid {
-  int64_t grid;
+  int64_t grid, blocks;
   bool direct, wide;
 };
 
@@ -964,12 +952,18 @@ TreeGrid tree_grid(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int
   // sequence than the split could tell apart.
   const int64_t few = wide ? 12 : blocks < device_cus() ? 5 : 9;
   if (tiles <= few || blocks >= 4 * at_once || 4 * blocks >= at_once * B * Hkv)
-    return {blocks, true, wide};
-  return {blocks * tiles < at_once ? blocks * tiles : at_once, false, wide};
+    return {blocks, blocks, true, wide};
+  return {blocks * tiles < at_once ? blocks * tiles : at_once, blocks, false, wide};
 }
 
+// Workgroups of a join: with one row of 16 lanes and more at a time, as many as keep every CU busy.
+// Measured on the GPU (us): 32 blocks of 128 rows in 16 parts each 15.1 (a workgroup for each
+// that began a block, most of them idle: 45), 384 blocks in some two parts 18.2, with 8192
+// workgroups 14.2 and 20.5.
+constexpr int64_t kJoin = 2048;
+
 template <bool BF, int DP, int TEAM, bool TWO>
-hipError_t launch_tree(const TreeParams& p, int64_t grid, hipStream_t s) {
+hipError_t launch_tree(const TreeParams& p, const TreeGrid& g, hipStream_t s) {
   using Sh = Shape<DP, TEAM, TWO>;
   const auto fn = tree_attention_kernel<BF, DP, TEAM, TWO>;
   if (Sh::LDS > 48 * 1024) {
@@ -977,31 +971,37 @@ hipError_t launch_tree(const TreeParams& p, int64_t grid, hipStream_t s) {
     const hipError_t e = lds_limit_once(reinterpret_cast<const void*>(fn), Sh::LDS, done);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(fn, dim3((uint32_t)grid), dim3(kTreeThreads), Sh::LDS, s, p);
+  hipLaunchKernelGGL(fn, dim3((uint32_t)g.grid), dim3(kTreeThreads), Sh::LDS, s, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.direct) return e;
-  constexpr int RJ = TEAM == 4 ? 16 : 2;
+  constexpr int GROUPS = kTreeThreads / join_lanes<DP>();
+  // groups share a row as long as each then has four parts or more, and a block's rows are
+  // spread over workgroups as long as those are kJoin or fewer
+  int share = 1;
+  while (share < GROUPS && 8 * share * g.blocks <= g.grid) share *= 2;
   const int rows = p.T * p.G < Sh::ROWS ? p.T * p.G : Sh::ROWS;
-  hipLaunchKernelGGL((tree_join_kernel<BF, DP, Sh::ROWS, RJ>),
-                     dim3((uint32_t)grid, (rows + RJ - 1) / RJ),
-                     dim3(kTreeThreads), (int)grid * RJ * 4, s, p);
+  const int64_t across = g.blocks < kJoin ? g.blocks : kJoin;
+  const int64_t slices = ceil_div((int64_t)rows * share, GROUPS), most = kJoin / across;
+  hipLaunchKernelGGL((tree_join_kernel<BF, DP, Sh::ROWS>),
+                     dim3((uint32_t)across, (uint32_t)(slices < most ? slices : most)),
+                     dim3(kTreeThreads), 0, s, p, (int)g.blocks, share);
   return hipGetLastError();
 }
 
 template <bool BF>
 hipError_t launch_tree_d(const TreeParams& p, const TreeGrid& g, hipStream_t s) {
   if (!g.wide)
-    return p.D <= 64   ? launch_tree<BF, 64, 1, true>(p, g.grid, s)
-           : p.D <= 96 ? launch_tree<BF, 96, 1, true>(p, g.grid, s)
-                       : launch_tree<BF, 128, 1, true>(p, g.grid, s);
+    return p.D <= 64   ? launch_tree<BF, 64, 1, true>(p, g, s)
+           : p.D <= 96 ? launch_tree<BF, 96, 1, true>(p, g, s)
+                       : launch_tree<BF, 128, 1, true>(p, g, s);
   const bool two = p.T * p.G <= kTeamRows;  // of long heads
-  return p.D <= 64    ? launch_tree<BF, 64, 4, false>(p, g.grid, s)
-         : p.D <= 96  ? launch_tree<BF, 96, 4, false>(p, g.grid, s)
-         : p.D <= 128 ? launch_tree<BF, 128, 4, false>(p, g.grid, s)
-         : p.D <= 192 ? two ? launch_tree<BF, 192, 4, true>(p, g.grid, s)
-                            : launch_tree<BF, 192, 4, false>(p, g.grid, s)
-         : two        ? launch_tree<BF, 256, 4, true>(p, g.grid, s)
-                      : launch_tree<BF, 256, 4, false>(p, g.grid, s);
+  return p.D <= 64    ? launch_tree<BF, 64, 4, false>(p, g, s)
+         : p.D <= 96  ? launch_tree<BF, 96, 4, false>(p, g, s)
+         : p.D <= 128 ? launch_tree<BF, 128, 4, false>(p, g, s)
+         : p.D <= 192 ? two ? launch_tree<BF, 192, 4, true>(p, g, s)
+                            : launch_tree<BF, 192, 4, false>(p, g, s)
+         : two        ? launch_tree<BF, 256, 4, true>(p, g, s)
+                      : launch_tree<BF, 256, 4, false>(p, g, s);
 }
 
 }  // namespace
@@ -1011,7 +1011,8 @@ int64_t tree_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int6
   const TreeGrid g = tree_grid(B, T, Hq, Hkv, D, capacity);
   if (g.direct) return 0;
   const int rows = g.wide ? 4 * kTeamRows : kTeamRows;
-  return g.grid * (2 * part_floats(rows, (int)D) * (int64_t)sizeof(float) + (int64_t)sizeof(int2));
+  return g.grid * 2 * part_floats(rows, (int)D) * (int64_t)sizeof(float) +
+         g.blocks * (int64_t)sizeof(int2);
 }
 
 hipError_t launch_tree_attention(int dtype, const TreeArgs& a, hipStream_t stream) {
