@@ -75,8 +75,6 @@ namespace {
 constexpr int kAttnThreads = kAttnWaves * kWave;
 constexpr int kTileTokens = 32;
 constexpr int kHeads = 16;                // query heads per workgroup
-constexpr uint32_t kOut = 0x80000000u;    // a lane offset past every buffer
-constexpr uint32_t kSpan = 0x7ffffffcu;   // bytes a buffer resource covers
 struct AttnParams {
   const unsigned char* Q;
   const unsigned char* K;
@@ -112,13 +110,6 @@ __device__ __forceinline__ float4v mma(u32x4 a, u32x4 b, float4v c) {
                                                   __builtin_bit_cast(half8, b), c, 0, 0, 0);
 }
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_at(const unsigned char* p) {
-  const uint64_t a = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
-  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(((uint64_t)hi << 32) | lo),
-                                           (short)0, (int)kSpan, kBufferWord3);
-}
 
 // NT: non-temporal, for lines that one wave reads once.  Measured (us, with /
 // without): 96 sequences of 2048 .. 8192 tokens, 8 key heads of 128: 286 / 323;

@@ -123,4 +123,15 @@ inline FastDiv fast_div(int64_t d) {
   return {(uint32_t)d, (uint32_t)m, 30 + s};
 }
 
+constexpr uint32_t kOut = 0x80000000u;   // a lane offset past every buffer
+constexpr uint32_t kSpan = 0x7ffffffcu;  // bytes a buffer resource covers
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_at(const unsigned char* p) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(((uint64_t)hi << 32) | lo),
+                                           (short)0, (int)kSpan, kBufferWord3);
+}
+
 }  // namespace tq

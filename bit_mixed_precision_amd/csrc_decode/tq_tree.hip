@@ -94,18 +94,9 @@ __device__ __forceinline__ int64_t shfl64(int64_t v, int src) {
   return ((int64_t)hi << 32) | (uint32_t)lo;
 }
 
-constexpr uint32_t kOut = 0x80000000u;   // a lane offset past every buffer
-constexpr uint32_t kSpan = 0x7ffffffcu;  // bytes a buffer resource covers
 constexpr int kNonTemporal = 2;          // for lines that one wave reads once
 constexpr int kNoLoads = 0x0f70;         // s_waitcnt: until no vector load is under way
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_at(const unsigned char* p) {
-  const uint64_t a = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
-  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(((uint64_t)hi << 32) | lo),
-                                           (short)0, (int)kSpan, kBufferWord3);
-}
 template <int AUX>
 __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, AUX));

@@ -79,8 +79,10 @@ __device__ __forceinline__ Seq read_seq(const WeightsParams& p, int b) {
   return s;
 }
 
-// DV: 64, 128 or 256, the head dimension rounded up.  NT: 16-token tiles of a wave.
-template <bool BF, int DV, int NT>
+// DV: 64, 128 or 256, the head dimension rounded up.  NT: 16-token tiles of a wave.  RUNS: 16
+// tokens lie in one page, so that a wave finds them by scalar arithmetic; otherwise each lane
+// finds its own.
+template <bool BF, int DV, int NT, bool RUNS>
 __global__ __launch_bounds__(kThreads, DV > 128 ? 2 : 3) void cache_weights_kernel(WeightsParams p) {
   constexpr int KS = DV / 32, UT = 16 * NT * kWaves, PC = DV / 8;
   // queries of `chunk` rows, a row's 16-byte pieces turned so that 16 rows' reads of one piece
@@ -166,9 +168,20 @@ __global__ __launch_bounds__(kThreads, DV > 128 ? 2 : 3) void cache_weights_kern
   u32x4 k[NT][KS], k_next[NT][KS];
   bool there[NT], there_next[NT];
   int ids[NT];
+  uint32_t k_off[KS];
+#pragma unroll
+  for (int x = 0; x < KS; ++x)
+    k_off[x] = 32 * x + 8 * g < p.D ? li * (uint32_t)p.row_stride + 64 * x + 16 * g : kOut;
   auto look_up = [&](int bb, int tt, const Seq& q) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      if constexpr (RUNS) {
+        const int a = uni(tt * UT + wave * 16 * NT + 16 * n);
+        const int t = a < q.lo ? q.lo : a;  // (a sequence of no tokens has no table entry to read)
+        ids[n] = a + 16 > q.lo && a < q.hi
+                     ? read_const(p.table, (int64_t)bb * p.width + uni(div_page(p.page, t))) : -1;
+        continue;
+      }
       const int t = tt * UT + wave * 16 * NT + 16 * n + li;
       const bool in = t >= q.lo && t < q.hi;
       ids[n] = in ? p.table[(int64_t)bb * p.width + div_page(p.page, t)] : -1;
@@ -177,6 +190,19 @@ __global__ __launch_bounds__(kThreads, DV > 128 ? 2 : 3) void cache_weights_kern
   auto load = [&](int bb, int hh, int tt, const Seq& q) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      if constexpr (RUNS) {
+        const int a = uni(tt * UT + wave * 16 * NT + 16 * n);
+        const bool page = (uint32_t)ids[n] < (uint32_t)p.n_pages;
+        there_next[n] = page && a + li >= q.lo && a + li < q.hi;
+        const int slot = a - (int)(uni(div_page(p.page, page ? a : 0)) * p.page.d);
+        const auto r = rsrc_at(p.K + (page ? ids[n] * p.page_stride + slot * p.row_stride +
+                                                 hh * p.head_stride : 0));
+#pragma unroll
+        for (int x = 0; x < KS; ++x)
+          k_next[n][x] = __builtin_bit_cast(
+              u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, there_next[n] ? k_off[x] : kOut, 0, 0));
+        continue;
+      }
       const int t = tt * UT + wave * 16 * NT + 16 * n + li;
       there_next[n] = (uint32_t)ids[n] < (uint32_t)p.n_pages;
       const int slot = t - (int)(div_page(p.page, there_next[n] ? t : 0) * p.page.d);
@@ -352,7 +378,7 @@ __global__ __launch_bounds__(kThreads, DV > 128 ? 2 : 3) void cache_weights_kern
   }
 }
 
-template <bool BF, int DV, int NT>
+template <bool BF, int DV, int NT, bool RUNS>
 hipError_t launch_nt(WeightsParams p, hipStream_t s) {
   constexpr int64_t UT = 16 * NT * kWaves;
   int64_t cap = (int64_t)p.width * p.page.d;
@@ -367,20 +393,20 @@ hipError_t launch_nt(WeightsParams p, hipStream_t s) {
   if (lds > 48 * 1024) {
     static std::atomic<uint64_t> done{0};
     const hipError_t e =
-        lds_limit_once(reinterpret_cast<const void*>(cache_weights_kernel<BF, DV, NT>),
+        lds_limit_once(reinterpret_cast<const void*>(cache_weights_kernel<BF, DV, NT, RUNS>),
                        kQueryBytes + kMostRows * 4, done);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((cache_weights_kernel<BF, DV, NT>),
+  hipLaunchKernelGGL((cache_weights_kernel<BF, DV, NT, RUNS>),
                      dim3((uint32_t)(p.tiles || all < most ? all : most)), dim3(kThreads), lds, s, p);
   return hipGetLastError();
 }
 
-template <bool BF>
+template <bool BF, bool RUNS>
 hipError_t launch_weights(const WeightsParams& p, hipStream_t s) {
-  return p.D <= 64    ? launch_nt<BF, 64, 2>(p, s)
-         : p.D <= 128 ? launch_nt<BF, 128, 2>(p, s)
-                      : launch_nt<BF, 256, 2>(p, s);
+  return p.D <= 64    ? launch_nt<BF, 64, 2, RUNS>(p, s)
+         : p.D <= 128 ? launch_nt<BF, 128, 2, RUNS>(p, s)
+                      : launch_nt<BF, 256, 2, RUNS>(p, s);
 }
 
 }  // namespace
@@ -420,7 +446,10 @@ hipError_t launch_cache_weights(int dtype, const WeightsArgs& a, hipStream_t str
   p.S = (int32_t)a.S;
   p.scale = t.scale_log2;
   p.decay = a.decay;
-  return dtype == TQ_BF16 ? launch_weights<true>(p, stream) : launch_weights<false>(p, stream);
+  const bool bf = dtype == TQ_BF16;
+  if (t.page_size % 16 == 0)
+    return bf ? launch_weights<true, true>(p, stream) : launch_weights<false, true>(p, stream);
+  return bf ? launch_weights<true, false>(p, stream) : launch_weights<false, false>(p, stream);
 }
 
 }  // namespace tq
