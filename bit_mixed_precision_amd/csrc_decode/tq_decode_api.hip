@@ -81,7 +81,8 @@ int tq_rope_append_at(int dtype, const void* QKV, int64_t qkv_tok, const float* 
       !distinct_cache(n_pages, page_stride, page_size, row_stride, Hkv, head_stride, D))
     return TQ_ERR_SHAPE;
   if (!aligned(QKV, 2) || !aligned(Q, 2) || !aligned(k_pages, 2) || !aligned(v_pages, 2) ||
-      !aligned(table, 8) || !aligned(pos, 4) || !aligned(seqs, 4) || !aligned(slots, 4) || !aligned(page_table, 4))
+      !aligned(table, 8) || !aligned(pos, 4) || !aligned(seqs, 4) || !aligned(slots, 4) ||
+      !aligned(page_table, 4))
     return TQ_ERR_ALIGN;
   if ((dtype != TQ_F16 && dtype != TQ_BF16) || (interleaved & ~1)) return TQ_ERR_VALUE;
   st = device_ready();

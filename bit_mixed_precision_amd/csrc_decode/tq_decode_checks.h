@@ -30,7 +30,9 @@ inline bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintpt
 inline int64_t step(int64_t n, int64_t s) { return n == 1 ? 0 : s; }
 
 // Stride s of a dimension of n >= 1 entries.
-inline bool stride_ok(int64_t n, int64_t s) { return s >= 0 && s <= kMaxStride && s <= kMaxReach / n; }
+inline bool stride_ok(int64_t n, int64_t s) {
+  return s >= 0 && s <= kMaxStride && s <= kMaxReach / n;
+}
 
 inline int device_ready() {
   int dev = -1;
@@ -63,8 +65,8 @@ inline bool distinct(int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t len
 
 // The same for the heads of the slots of the pages of a cache, whose strides are
 // nested in some order.
-inline bool distinct_cache(int64_t n_pages, int64_t page, int64_t page_size, int64_t row, int64_t heads,
-                    int64_t head, int64_t len) {
+inline bool distinct_cache(int64_t n_pages, int64_t page, int64_t page_size, int64_t row,
+                           int64_t heads, int64_t head, int64_t len) {
   struct Level {
     int64_t n, stride;
   } l[3] = {{n_pages, page}, {page_size, row}, {heads, head}};
@@ -104,7 +106,8 @@ inline int pool_shapes(int64_t planes, int64_t page_bytes) {
              : TQ_OK;
 }
 
-inline int attn_shapes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size, int64_t width) {
+inline int attn_shapes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size,
+                       int64_t width) {
   if (B < 0 || B > kMaxAttnBatch || Hkv < 1 || Hq < 1 || Hq > kMaxAttnHeads || Hq % Hkv || D < 8 ||
       D > 256 || D % 8 || page_size < 1 || width < 1 || page_size > kMaxTokens ||
       width > kMaxTokens || width * page_size > kMaxTokens)

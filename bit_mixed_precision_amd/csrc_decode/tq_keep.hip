@@ -5,11 +5,18 @@
 // those between as many of the heaviest as the budget leaves, equal ones in order.
 // The least weight that stays is found digit by digit, from counts of the tokens by
 // 11, 11 and 10 bits of their weight (as a whole number of the same order); then the
-// tokens are walked through in order.
+// tokens are walked through in order.  Up to 32768 tokens stay in registers, so they are read
+// once.  What bounds it is the chain of barriers: a digit costs clearing, counting and
+// ranking 2048 bins, some 1.5 us each.  8 rows of 1009 tokens: 6.5 us with a launch; 384 rows of
+// up to 32768 tokens, 17 MB: 25 us (counted from memory at every digit 40; rows
+// in order of their place instead of the longest first 31).
 //
 // The move.  Slot i of a row gets token keep[i] >= i of the same row, so a row can be
 // moved forward in place, part by part: what a part writes no later part reads.  A page
-// that other rows hold too is not written; the row gets a free page in its place.
+// that other rows hold too is not written; the row gets a free page in its place.  A row's
+// parts follow each other, rows, heads and planes run side by side.  16 rows that keep
+// 1024 of up to 2048 tokens of 2 KB in 32 planes, 1.08 GB read and written: 240 us, 4.5 TB/s, a
+// plain copy's 4.9 less the parts that are as short as a head.
 
 #include "tq.h"
 #include "tq_attn_dev.h"
@@ -198,7 +205,8 @@ __device__ __forceinline__ void choose(const SelectParams& p, SelectShared<WAVES
   });
 }
 
-// One workgroup per (sequence, head).
+// One workgroup per (sequence, head).  Four waves a SIMD: with eight the 32 tokens a lane do not
+// fit its registers (66 us against 31 for 384 long rows).
 template <int WAVES>
 __global__ __launch_bounds__(WAVES * kWave, 4) void cache_select_kernel(SelectParams p) {
   constexpr int THREADS = WAVES * kWave;
@@ -615,6 +623,7 @@ hipError_t launch_cache_select(const SelectArgs& a, hipStream_t stream) {
   // More rows than are at work at once, long ones among them: the longest first, so that none
   // of those begins last.
   p.sorted = a.S > 4096 && a.B > 1 && a.B <= kWave && a.B * a.H > device_cus();
+  // (four waves hold 4096 tokens in registers, and their barriers are shorter)
   if (a.S <= 4096)
     hipLaunchKernelGGL(cache_select_kernel<4>, grid, dim3(4 * kWave), 0, stream, p);
   else

@@ -235,7 +235,8 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int st = c.rope_append(
         kd, x.data_ptr(), x.stride(0), ptr<float>(table), table.size(0), 2 * table.size(1),
         ptr<int32_t>(pos), slots ? ptr<int32_t>(*slots) : nullptr,
-        seqs ? ptr<int32_t>(*seqs) : nullptr, ptr<int32_t>(pages), pages.size(0), pages.size(1), k.data_ptr(), v.data_ptr(), k.size(0), k.size(1),
+        seqs ? ptr<int32_t>(*seqs) : nullptr, ptr<int32_t>(pages), pages.size(0), pages.size(1),
+        k.data_ptr(), v.data_ptr(), k.size(0), k.size(1),
         k.stride(0), k.stride(1), k.stride(2), q.data_ptr(), T, Hq, Hkv, D, inter, s);
     return st == TQ_OK ? THPVariable_Wrap(q) : PyLong_FromLong(st);
   });

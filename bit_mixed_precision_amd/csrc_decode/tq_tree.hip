@@ -9,7 +9,28 @@
 // carries log2 e).
 //
 // The m * G queries that share a key-value head are the rows of one matrix product
-// each with K and V; a row block of them and a run of tokens are a unit of work.
+// each with K and V; a row block of them and a tile of tokens are a unit of work.
+//
+// What bounds it.  A token is 4 D bytes of a key-value head and 4 m G D operations: memory
+// below some 200 rows, the matrix cores above.  Both forms compute S^T = K Q^T with the
+// 32 x 32 x 16 instruction, so that a lane holds 16 scores of one row: the row's maximum and sum
+// need one exchange between two lanes, and the weights are the second product's
+// operand (O^T += V^T P^T) where they lie.  V is turned by the transposing read of LDS.
+//   wide, for many rows: four waves of 32 rows each share tiles of 64 tokens, copied to LDS
+//   past the registers, two tiles in turn.  131072 tokens, 64 nodes, 8 heads of 128 with 8
+//   query heads each: 275 GFLOP in 375 us, 730 TFLOP/s (a plain product of 8192^3 reaches
+//   1330).  Matrix and other vector instructions take turns more than they overlap: 39% and
+//   42% of a SIMD's time, and waves wait a quarter of theirs; two waves a SIMD are what
+//   the registers allow.  Four blocks of rows read the same tokens, and the L2s
+//   catch half of that: 1.2 GB from memory of 0.54.  Mixing one tile's scores
+//   with the product of the tile before inside a wave brought nothing (414 against 394).
+//   thin, for up to 32 rows and short caches: the four waves share 128 tokens of the same
+//   rows, each tile through registers to LDS that only its wave reads, and their sums meet
+//   at the end.  37 ragged sequences of up to 4096 tokens, 24 heads of 64, 13 nodes: 122 MB in
+//   37 us, 3.3 TB/s; half a tile's time goes to its chain page -> keys -> LDS -> scores, for
+//   which three workgroups a CU do not make up.
+// Row blocks are cut into equal runs over all workgroups; what spans several is joined by
+// a second kernel in a fixed order (no atomics, the same bits on every run).
 
 #include <math.h>
 
@@ -756,11 +777,13 @@ __global__ __launch_bounds__(kTreeThreads, tree_per_cu(DP)) void tree_attention_
           stage(edge(cur.s, tile), buf);
           __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         }
-        unsigned char* const to = S::BUFFERS == 1 ? buf : buf == sTeam ? sTeam + 2 * S::TILE : sTeam;
+        unsigned char* const other = buf == sTeam ? sTeam + 2 * S::TILE : sTeam;
+        unsigned char* const to = S::BUFFERS == 1 ? buf : other;
         const bool here = tile + 1 < end;  // the tile that follows is this row's
         if (here || left > 0) {
           fetch(here ? cur : next, here ? tile + 1 : next.tile, id, to);
-          if (here) id = tile + 2 < end ? page_id(cur, tile + 2) : left > 0 ? page_id(next, next.tile) : 0;
+          if (here)
+            id = tile + 2 < end ? page_id(cur, tile + 2) : left > 0 ? page_id(next, next.tile) : 0;
         }
         compute(cur, tile, there, buf);
         buf = to;
@@ -801,7 +824,8 @@ constexpr int join_lanes() {
   return DP <= 64 ? 16 : DP <= 128 ? 32 : 64;
 }
 template <bool BF, int DP, int ROWS>
-__global__ __launch_bounds__(kTreeThreads) void tree_join_kernel(TreeParams p, int blocks, int share) {
+__global__ __launch_bounds__(kTreeThreads) void tree_join_kernel(TreeParams p, int blocks,
+                                                                 int share) {
   constexpr int CL = join_lanes<DP>(), GROUPS = kTreeThreads / CL, U = 8;
   __shared__ __attribute__((aligned(16))) float sV[kTreeThreads * 4];
   const int tid = threadIdx.x, lane = tid % CL, col = lane * 4;
@@ -922,8 +946,9 @@ struct TreeGrid {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Two forms.  Wide (heads of more than 128 numbers: always): four waves share the tokens, each with 32 rows of its own, so that one
-// reading of a tile serves 128 rows.  Thin: 32 rows, and the waves share the tokens: for
+// Two forms.  Wide (heads of more than 128 numbers: always, the thin form's registers do not hold
+// them): four waves share the tokens, each with 32 rows of its own, so that one reading of a
+// tile serves 128 rows.  Thin: 32 rows, and the waves share the tokens: for
 // up to 32 rows, and for short caches where the GPU has a CU for every 32 rows, because
 // four waves then walk through a row's tiles at once.  Measured (us, thin / wide), one tree
 // of 24 nodes, 8 key heads of 128 and 8 query heads each, up to 32, 128, 256, 512 tokens:

@@ -8,7 +8,15 @@
 //
 // The normalizing sums are known (the attention before returned them), so tokens do not
 // depend on each other and nothing is split or joined: a wave holds some tokens' keys in
-// registers and walks through the rows (node, head of the group).
+// registers and walks through the rows (node, head of the group), whose queries lie in LDS.
+//
+// What bounds it: a token is 2 D bytes of a key-value head, and with R rows R exponentials at a
+// quarter of the vector rate beside 2 R D operations.  16 sequences of up to 16384 tokens, 8 heads
+// of 128, 128 rows each: 307 MB in 86 us (94 with each lane finding its own tokens), 3.6 TB/s;
+// exponentials and the additions around them take 25 us, the matrix product 25, reading 44, and
+// a unit of 128 tokens is too short to hide one behind the other.  Two tiles of 16 tokens a wave:
+// four need twice the registers, two workgroups a CU instead of three: 91 against 86, and one
+// sequence of 2000 tokens 7.3 against 5.5.
 
 #include <atomic>
 

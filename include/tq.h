@@ -512,9 +512,9 @@ int tq_tree_mask(const int32_t* parents, int64_t B, int64_t T, int64_t* mask, in
  * 2^-16 bfloat16) of itself; with more rows as two or as one, rounded to nearest (2^-11 of
  * itself in fp16, 2^-8 in bfloat16).  In fp16 a weight may also be off by 2^-34 of the row's
  * largest, and one below that may add nothing.  An infinite value gives an infinite
- * result, or NaN where its weight is zero or, in fp16, may add nothing.  A token that a node does not see has no
- * influence on it, whatever its key and value hold.  The same bits on every run.
- * Outputs and workspace must not overlap the inputs.
+ * result, or NaN where its weight is zero or, in fp16, may add nothing.  A token that a
+ * node does not see has no influence on it, whatever its key and value hold.  The same
+ * bits on every run.  Outputs and workspace must not overlap the inputs.
  * Limits as tq_paged_attention's, and T <= 256; B * Hkv * ceil(T G / 32) < 2^24, and times
  * (width * page_size / 64 + 2) < 2^31.  workspace: tq_tree_attention_workspace(...) bytes,
  * 16-byte aligned, contents irrelevant; calls that overlap on one workspace race.
