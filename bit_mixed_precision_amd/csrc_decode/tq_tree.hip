@@ -185,6 +185,7 @@ struct Unit {
 template <bool BF>
 constexpr float kShift = BF ? 0.f : 9.f;
 constexpr float kSlack = 6.f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 // Divides by the sum and writes numbers d .. d + 3 of one query, and its lse.
 template <bool BF>
@@ -194,7 +195,7 @@ __device__ __forceinline__ void store_row(const TreeParams& p, int64_t at, int d
   u[0] = pack2<BF>(v[0] * inv, v[1] * inv);
   u[1] = pack2<BF>(v[2] * inv, v[3] * inv);
   *reinterpret_cast<u32x2*>(p.Out + (at * p.D + d) * 2) = u;
-  if (p.lse && d == 0) p.lse[at] = (m + __builtin_amdgcn_logf(sum) - kShift<BF>) / kLog2e;
+  if (p.lse && d == 0) p.lse[at] = (m + __builtin_amdgcn_logf(sum) - kShift<BF>) * kLn2;
 }
 
 // Workgroups per CU, for which the registers are laid out.
@@ -402,7 +403,9 @@ __global__ __launch_bounds__(kTreeThreads, tree_per_cu(DP)) void tree_attention_
   // Fetches a tile.  A wave takes runs of 16 tokens, lane x their pieces x, x + 64, ..  Teams
   // of four copy straight to LDS where every token is there, none is at an edge and a
   // run lies in one page: where a piece lies in LDS is turned, so a lane fetches what
-  // belongs to its place.  Other tiles, and those of single waves, go through registers.
+  // belongs to its place.  Other tiles, and those of single waves, go through registers,
+  // where a run lies in one page by offsets that tokens that are not there send past
+  // the buffer's end.
   uint64_t present = 0;  // tokens that are there, of the tile last fetched
   constexpr uint64_t kFull = TT == 64 ? ~0ull : 0xffffffffull;
   auto fetch = [&](const Unit& c, int tile, int id, unsigned char* buf) {
@@ -413,13 +416,21 @@ __global__ __launch_bounds__(kTreeThreads, tree_per_cu(DP)) void tree_attention_
     present = __ballot(ok) & kFull;
     const int64_t head = c.h * p.head_stride;
     const int D = anew_uniform(p.D), ln = anew(lane);
-    if (p.runs && present == kFull && !at_edge) {
+    if (p.runs && (TEAM == 1 || (present == kFull && !at_edge))) {
 #pragma unroll
       for (int r = 0; r < S::HALVES; ++r) {
         const int first = a + 16 * (run16 + r);
         const int slot = first - (int)(div_page(p.page, first) * p.page.d);
-        const int64_t at = __builtin_amdgcn_readlane(id, 16 * (run16 + r)) * p.page_stride +
-                           slot * p.row_stride + head;
+        // tokens [begin, begin + count) of the run are there
+        int begin = 0, count = 16, page = __builtin_amdgcn_readlane(id, 16 * (run16 + r));
+        if constexpr (TEAM == 1) {
+          const uint32_t have = (uint32_t)(present >> (16 * r)) & 0xffff;  // no gaps: one page
+          begin = have ? __builtin_ctz(have) : 0;
+          count = __builtin_popcount(have);
+          page = __builtin_amdgcn_readlane(id, 16 * r + begin);
+          page = have ? page : 0;
+        }
+        const int64_t at = page * p.page_stride + slot * p.row_stride + head;
         const auto rk = rsrc_at(p.K + at), rv = rsrc_at(p.V + at);
 #pragma unroll
         for (int u = 0; u < PH; ++u) {
@@ -430,7 +441,8 @@ __global__ __launch_bounds__(kTreeThreads, tree_per_cu(DP)) void tree_attention_
             if (kp * 8 < D) dma16(rk, row * (int)p.row_stride + kp * 16, to);
             if (vp * 8 < D) dma16(rv, row * (int)p.row_stride + vp * 16, to + S::TILE);
           } else {
-            const uint32_t off = place * 8 < D ? row * (uint32_t)p.row_stride + place * 16 : kOut;
+            const bool in = (uint32_t)(row - begin) < (uint32_t)count && place * 8 < D;
+            const uint32_t off = in ? row * (uint32_t)p.row_stride + place * 16 : kOut;
             if (p.lines) {
               kreg[r * PH + u] = load16<kNonTemporal>(rk, off);
               vreg[r * PH + u] = load16<kNonTemporal>(rv, off);
@@ -481,6 +493,7 @@ __global__ __launch_bounds__(kTreeThreads, tree_per_cu(DP)) void tree_attention_
 #pragma unroll
         for (int i = 0; i < 4; ++i) q[k][i] ^= p.flip;
     int seen = 0;
+#pragma unroll 1
     for (int w = 0; w < kMaskWords; ++w) {
       const int valid = c.s.m - w * 64;  // nodes of this word
       const uint64_t some = valid >= 64 ? ~0ull : valid <= 0 ? 0ull : (1ull << valid) - 1;
@@ -622,22 +635,32 @@ __global__ __launch_bounds__(kTreeThreads, tree_per_cu(DP)) void tree_attention_
       }
       __syncthreads();
       const int first = c.r * ROWS, n = rows - first < ROWS ? rows - first : ROWS;
-      const int units = p.D / 4;
-      for (int j = tid; j < n * units; j += kTreeThreads) {
-        const int r = j / units, d = (j - r * units) * 4;
-        float mm = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kTreeWaves; ++w) mm = fmaxf(mm, sM[w][r]);
-        const float base = mm == -INFINITY ? 0.f : mm;
-        float total = 0.f;
-        float4v v = {0, 0, 0, 0};
+      // a thread has four numbers of rows r, r + EACH, ..
+      constexpr int EACH = kTreeThreads / (DP / 4);
+      const int r0 = tid / (DP / 4), d = (tid - r0 * (DP / 4)) * 4;
+#pragma unroll 2
+      for (int k = 0; k < (kTeamRows + EACH - 1) / EACH; ++k) {
+        const int r = r0 + k * EACH;
+        if (r0 >= EACH || r >= n || d >= p.D) continue;
+        // (all of LDS is read before anything waits for it)
+        float mw[kTreeWaves], lw[kTreeWaves], mm = -INFINITY, total = 0.f;
+        float4v x[kTreeWaves], v = {0, 0, 0, 0};
 #pragma unroll
         for (int w = 0; w < kTreeWaves; ++w) {
-          const float f = __builtin_amdgcn_exp2f(sM[w][r] - base);
-          total += f * sL[w][r];
-          const float4v x = *reinterpret_cast<const float4v*>(sO + (w * kTeamRows + r) * S::PAD + d);
+          mw[w] = sM[w][r];
+          lw[w] = sL[w][r];
+          x[w] = *reinterpret_cast<const float4v*>(sO + (w * kTeamRows + r) * S::PAD + d);
+        }
+#pragma unroll
+        for (int w = 0; w < kTreeWaves; ++w) mm = fmaxf(mm, mw[w]);
+        const float base = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+        for (int w = 0; w < kTreeWaves; ++w) {
+          const float f = __builtin_amdgcn_exp2f(mw[w] - base);
+          total += f * lw[w];
           // a wave without weight adds nothing, also where it has met NaN
-          if (sL[w][r] != 0.f) v += f * x;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] += lw[w] != 0.f ? f * x[w][i] : 0.f;
         }
         if (whole) {
           store_row<BF>(p, query_of(c, first + r), d, mm, total, total == 0.f ? 0.f : 1.f / total, v);
@@ -755,8 +778,9 @@ __global__ __launch_bounds__(kTreeThreads, tree_per_cu(DP)) void tree_attention_
   if (left > 0) {
     unsigned char* buf = sTeam;
     int id = page_id(cur, cur.tile);
-    open_row(cur);
+    if (TEAM == 4) open_row(cur);
     fetch(cur, cur.tile, id, buf);
+    if (TEAM == 1) open_row(cur);  // its loads are waited for together with the tile's
     for (bool opened = true;; opened = false) {
       // the tiles [first, end) of one row
       const int first = cur.tile;
