@@ -381,16 +381,28 @@ __global__ __launch_bounds__(kTreeThreads, tree_per_cu(DP)) void tree_attention_
   u32x4 kreg[PER], vreg[PER];
   auto stage = [&](bool at_edge, unsigned char* buf) {
     if (at_edge) {
-      bool odd = false;
+      // (single waves look first whether there are any: a number's exponent is all ones where
+      // one more carries into its sign)
+      constexpr uint32_t exps = BF ? 0x7f807f80u : 0x7c007c00u, one = BF ? 0x00800080u : 0x04000400u;
+      uint32_t odd = TEAM == 4;
+      if constexpr (TEAM == 1) {
 #pragma unroll
-      for (int u = 0; u < PER; ++u)
+        for (int u = 0; u < PER; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t f = finite_of<BF>(vreg[u][i]);
-          odd |= f != vreg[u][i];
-          vreg[u][i] = f;
-        }
-      if (odd) sOdd[team] = 1;  // every writer writes 1
+          for (int i = 0; i < 4; ++i) odd |= (vreg[u][i] & exps) + one & 0x80008000u;
+      }
+      if (odd) {
+        odd = 0;
+#pragma unroll
+        for (int u = 0; u < PER; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t f = finite_of<BF>(vreg[u][i]);
+            odd |= f ^ vreg[u][i];
+            vreg[u][i] = f;
+          }
+        if (odd) sOdd[team] = 1;  // every writer writes 1
+      }
     }
     const int ln = TEAM == 1 ? lane : anew(lane);
 #pragma unroll
