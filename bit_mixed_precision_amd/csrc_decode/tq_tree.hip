@@ -985,17 +985,19 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Two forms.  Wide (heads of more than 128 numbers: always, the thin form's registers do not hold
 // them): four waves share the tokens, each with 32 rows of its own, so that one reading of a
 // tile serves 128 rows.  Thin: 32 rows, and the waves share the tokens: for
-// up to 32 rows, and for short caches where the GPU has a CU for every 32 rows, because
-// four waves then walk through a row's tiles at once.  Measured (us, thin / wide), one tree
-// of 24 nodes, 8 key heads of 128 and 8 query heads each, up to 32, 128, 256, 512 tokens:
-// 10.8 / 10.4, 11.2 / 11.8, 13.2 / 15.5, 16.9 / 23.0; eight trees (384 thin workgroups)
-// 13.8 / 11.1, 14.5 / 12.5, 17.2 / 16.2; four of 64 nodes, 4 heads each of 64 8.0 / 9.7,
-// 10.1 / 10.9, 11.3 / 15.1, 12.3 / 22.9.
+// up to 32 rows, and for short caches where the GPU has a CU for every 32 rows (heads of up to 64:
+// for every 64), because four waves then walk through a row's tiles at once.  Measured (us,
+// thin / wide), one tree of 24 nodes, 8 key heads of 128 and 8 query heads each, up to
+// 32, 128, 256, 512 tokens: 9.6 / 10.2, 9.6 / 11.5, 11.7 / 14.9, 15.8 / 21.3; eight trees (384 thin
+// workgroups) 12.8 / 10.8, 12.9 / 12.3, 16.1 / 15.7, 21.5 / 22.2; four of 64 nodes, 4 heads each of
+// 64 7.2 / 8.7, 8.4 / 11.1, 10.9 / 16.0; ten of 100 nodes, 8 heads of 64 (320 thin workgroups), up to
+// 204, 500 tokens 10.3 / 13.1, 13.6 / 17.4.
 constexpr int64_t kShort = 512;
 
 TreeGrid tree_grid(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity) {
   const int64_t rows = T * (Hq / Hkv), thin = B * Hkv * ceil_div(rows, kTeamRows);
-  const bool wide = D > 128 || (rows > kTeamRows && !(capacity <= kShort && thin <= device_cus()));
+  const int64_t room = device_cus() * (D > 64 ? 1 : 2);
+  const bool wide = D > 128 || (rows > kTeamRows && !(capacity <= kShort && thin <= room));
   const int64_t blocks = wide ? B * Hkv * ceil_div(rows, 4 * kTeamRows) : thin;
   const int64_t tiles = ceil_div(capacity, wide ? 64 : 128) + 1;  // a window may begin inside one
   const int64_t at_once = device_cus() * tree_per_cu(D);
