@@ -72,7 +72,7 @@ def _log(rng, lo, hi):
 def draw(rng):
     op = rng.choice(["tree", "tree", "tree", "weights", "weights", "select", "keep", "keep", "mask"])
     if op == "mask":
-        return dict(op=op, B=_log(rng, 1, 96), T=_log(rng, 8, 256), deep=rng.choice([1, 2, 4, 8]))
+        return dict(op=op, B=_log(rng, 1, 96), T=_log(rng, 1, 256), deep=rng.choice([0, 1, 2, 4, 8]))
     if op == "select":
         H = rng.choice([1, 2, 8, 8, 24])
         B = _log(rng, 1, 384 // H)
@@ -174,7 +174,7 @@ def _bits(parents):
 def _cached(c, gen, rng, lens, tokens, both):
     """A page table for `tokens` cached tokens per sequence, in shuffled pages."""
     need = -(-tokens // c["page"])
-    width, total = -(-(c["hi"] + c["T"]) // c["page"]), int(need.sum())
+    width, total = max(1, int(need.max())), int(need.sum())
     pages = total + 3
     table = np.full((c["B"], width), -1, np.int32)
     table[np.arange(width)[None, :] < need[:, None]] = rng.permutation(pages)[:total]
@@ -201,7 +201,8 @@ def _prepare_attn(c, gen, rng):
         # what the attention before returned, and the sums of the steps so far
         s["lse"] = torch.stack([_scores64(s, b)[0].logsumexp(-1).float() for b in range(c["B"])])
         L = s["pages"].shape[1] * c["page"]
-        s["scores"] = torch.rand(c["B"], c["Hkv"], L, generator=gen, device="cuda") ** 4
+        old = torch.rand(c["B"], c["Hkv"], L, generator=gen, device="cuda") ** 4
+        s["scores"] = old * (torch.arange(L, device="cuda") < s["lens"][:, None, None])
     return s
 
 
@@ -228,7 +229,7 @@ def _prepare_keep(c, gen, rng):
     pairs[pairs] = np.minimum(lens[1::2], lens[:B // 2 * 2:2]) >= c["shared"] * page
     own_from = np.where(pairs, c["shared"], 0)
     mine = (np.arange(width) >= own_from[:, None]) & (np.arange(width) < need[:, None])
-    pages = int(need.sum()) + B * (c["shared"] + 1)
+    pages = int(mine.sum()) + B * (c["shared"] + 1)
     table[mine] = rng.permutation(pages)[:int(mine.sum())]
     follow = np.nonzero(pairs)[0]
     table[follow, :c["shared"]] = table[follow - 1, :c["shared"]]
@@ -357,7 +358,7 @@ def _plain_weights(s):
     w = torch.exp(x - lse).masked_fill(~torch.isfinite(lse), 0.0).sum(2)
     at, lens, nodes = torch.arange(L, device="cuda"), s["lens"][:, None, None], s["nodes"][:, None, None]
     w = torch.where(at < lens, s["scores"] * c["decay"] + w, w)
-    return {"scores": s["scores"].copy_(torch.where(at < lens + nodes, w, s["scores"]))}
+    return {"scores": w.masked_fill(at >= lens + nodes, 0.0)}
 
 
 def _plain_select(s):
@@ -376,9 +377,9 @@ def _plain_select(s):
     best = torch.where(held, best, x.shape[-1]).sort(-1).values
     keep = torch.full((c["B"], c["H"], c["budget"]), -1, dtype=torch.int32, device="cuda")
     keep[..., :width] = torch.where(held, best, -1).int()
-    sums = torch.zeros(keep.shape, device="cuda")
-    sums[..., :width] = x.gather(2, best.clamp(max=x.shape[-1] - 1)).masked_fill(~held, 0.0)
-    return {"keep": keep, "counts": count.view(-1).int(), "sums": sums}
+    out = torch.zeros_like(x)
+    out[..., :width] = x.gather(2, best.clamp(max=x.shape[-1] - 1)).masked_fill(~held, 0.0)
+    return {"keep": keep, "counts": count.view(-1).int(), "scores": out}
 
 
 def _plain_keep(s):
@@ -437,13 +438,13 @@ def _own(s):
                                         nodes=s["nodes"], window=c["window"], return_lse=True)
         return {"out": out, "lse": lse}
     if c["op"] == "weights":
-        tq.tq_cache_weights(s["q"], s["k"], s["pages"], s["lens"], s["lse"], s["scores"], mask=s["mask"],
-                            nodes=s["nodes"], window=c["window"], decay=c["decay"])
-        return {"scores": s["scores"]}
+        return {"scores": tq.tq_cache_weights(s["q"], s["k"], s["pages"], s["lens"], s["lse"], s["scores"],
+                                              mask=s["mask"], nodes=s["nodes"], window=c["window"],
+                                              decay=c["decay"])}
     if c["op"] == "select":
-        keep, counts, sums = tq.tq_cache_select(s["scores"], s["lens"], c["budget"], recent=c["recent"],
-                                                sinks=c["sinks"])
-        return {"keep": keep, "counts": counts, "sums": sums}
+        keep, counts, scores = tq.tq_cache_select(s["scores"], s["lens"], c["budget"], recent=c["recent"],
+                                                  sinks=c["sinks"])
+        return {"keep": keep, "counts": counts, "scores": scores}
     pages, lens, short = tq.tq_pages_keep(s["pool"], s["pages"], s["lens"], s["keep"], s["counts"], c["page"],
                                           base=s["base"])
     return {"pages": pages, "lens": lens, "short": short, "pool": s["pool"]}
@@ -488,18 +489,18 @@ def exact(case, seed):
     s = prepare(c, seed)
     B, T, G, Hkv = c["B"], c["T"], c["Hq"] // c["Hkv"], c["Hkv"]
     if c["op"] == "weights":
-        got = s["scores"].double()
+        L = s["pages"].shape[1] * c["page"]
+        got = torch.zeros(B, Hkv, L, dtype=torch.float64, device="cuda")
         for b in range(B):
             n, m = int(s["lens"][b]), int(s["nodes"][b])
-            got[b, :, :n] *= c["decay"]
             if m == 0:
+                got[b, :, :n] = s["scores"][b, :, :n].double() * c["decay"]
                 continue
             x, _ = _scores64(s, b)
             lse = s["lse"][b].double()[..., None]
             w = torch.where(torch.isfinite(lse), torch.exp(x - lse), 0.0)
-            w = w.view(T, Hkv, G, -1).sum((0, 2))
-            got[b, :, :n] += w[:, :n]
-            got[b, :, n:n + m] = w[:, n:n + m]
+            got[b, :, :n + m] = w.view(T, Hkv, G, -1).sum((0, 2))
+            got[b, :, :n] += s["scores"][b, :, :n].double() * c["decay"]
         return {"scores": got}
     out = torch.zeros(B, T, c["Hq"], c["D"], dtype=torch.float64, device="cuda")
     lse = torch.full((B, T, c["Hq"]), -math.inf, dtype=torch.float64, device="cuda")
