@@ -438,12 +438,17 @@ def _own(s):
                                         nodes=s["nodes"], window=c["window"], return_lse=True)
         return {"out": out, "lse": lse}
     if c["op"] == "weights":
-        return {"scores": tq.tq_cache_weights(s["q"], s["k"], s["pages"], s["lens"], s["lse"], s["scores"],
-                                              mask=s["mask"], nodes=s["nodes"], window=c["window"],
-                                              decay=c["decay"])}
+        # the library adds in place: to a copy, since the sums so far are an input
+        return {"scores": tq.tq_cache_weights(s["q"], s["k"], s["pages"], s["lens"], s["lse"],
+                                              s["scores"].clone(), mask=s["mask"], nodes=s["nodes"],
+                                              window=c["window"], decay=c["decay"])}
     if c["op"] == "select":
-        keep, counts, scores = tq.tq_cache_select(s["scores"], s["lens"], c["budget"], recent=c["recent"],
-                                                  sinks=c["sinks"])
+        keep, counts, sums = tq.tq_cache_select(s["scores"], s["lens"], c["budget"], recent=c["recent"],
+                                                sinks=c["sinks"])
+        # the library's sums are as long as the budget: at the front of new rows
+        width = min(c["budget"], s["scores"].shape[-1])
+        scores = torch.zeros_like(s["scores"])
+        scores[..., :width] = sums[..., :width]
         return {"keep": keep, "counts": counts, "scores": scores}
     pages, lens, short = tq.tq_pages_keep(s["pool"], s["pages"], s["lens"], s["keep"], s["counts"], c["page"],
                                           base=s["base"])
