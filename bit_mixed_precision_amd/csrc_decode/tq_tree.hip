@@ -744,9 +744,11 @@ __global__ __launch_bounds__(kTreeThreads, tree_per_cu(DP)) void tree_attention_
 #pragma unroll
       for (int r = 0; r < 16; ++r) top = fmaxf(top, s[x][r]);
     top = over_halves(top, [](float x, float y) { return fmaxf(x, y); });
-    if (!__all(top <= m || (top - m) * p.scale <= kSlack)) {
-      const float mn = fmaxf(m, top);
-      const float alpha = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - mn) * p.scale);
+    const bool stays = top <= m || (top - m) * p.scale <= kSlack;
+    if (!__all(stays)) {
+      // (every row by what it sees itself: a row beside it that rises changes none of its bits)
+      const float mn = stays ? m : fmaxf(m, top);
+      const float alpha = stays ? 1.f : __builtin_amdgcn_exp2f((m - mn) * p.scale);
       m = mn;
       l *= alpha;
 #pragma unroll
