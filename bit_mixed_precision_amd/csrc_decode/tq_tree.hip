@@ -897,8 +897,10 @@ __global__ __launch_bounds__(kTreeThreads) void tree_join_kernel(TreeParams p, i
         const int k = k0 + lane < n ? k0 + lane : n - 1;
         float w = __builtin_amdgcn_exp2f(part(k)[at_m] - base);
         const float l = part(k)[at_l];
-        // a part without weight adds nothing, also where it has met NaN
+        // a part without weight adds nothing, also where it has met NaN; one whose sum is NaN
+        // has a weight of NaN, also where all its scores are, so that its maximum is -inf
         if (k0 + lane >= n || l == 0.f) w = 0.f;
+        else if (l != l) w = l;
         if (w != 0.f) total += w * l;
         const int most = n - k0 < CL ? n - k0 : CL;
         for (int x0 = turn; x0 < most; x0 += U * share) {

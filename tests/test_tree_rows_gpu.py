@@ -1,4 +1,5 @@
-"""Rows of tree attention next to each other: what one node sees reaches no other node's bits."""
+"""Rows of tree attention: what one node sees reaches no other node's
+bits, and what is no number reaches every row that sees it, however the row is cut."""
 
 import pytest
 
@@ -9,6 +10,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 tq = pytest.importorskip("bit_mixed_precision_amd.binding")
 
+from test_decode_gpu import NAN  # noqa: E402
 from test_tree_gpu import parents_of, tree, words  # noqa: E402
 
 
@@ -39,3 +41,35 @@ def test_a_large_key_of_a_sibling_changes_no_bits(dtype, T, Hq, Hkv, D, lens):
     assert not torch.equal(got[1][~clean], want[1][~clean])
     for x, y in zip(got, want):
         assert torch.equal(x[clean], y[clean])
+
+
+LONG = [(4, 8, 2, 64, [9000]), (2, 4, 1, 128, [5000, 0, 12000]), (20, 8, 2, 128, [9000, 100]), (3, 4, 2, 256, [8000])]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("T,Hq,Hkv,D,lens", LONG)
+def test_undefined_queries_of_long_rows(dtype, T, Hq, Hkv, D, lens):
+    """A query of NaN: its output and log-sum-exp are NaN, and nothing else is."""
+    q, k, v, pt, ln, nodes = tree(T, dtype, lens, [T] * len(lens), T, Hq, Hkv, D, 16, poison=False)
+    want = tq.tq_tree_attention(q, k, v, pt, ln, return_lse=True)
+    q[0, 1, Hq - 1] = NAN
+    got = tq.tq_tree_attention(q, k, v, pt, ln, return_lse=True)
+    assert torch.isnan(got[0][0, 1, Hq - 1]).all() and torch.isnan(got[1][0, 1, Hq - 1])
+    rest = torch.ones(q.shape[:3], dtype=torch.bool, device="cuda")
+    rest[0, 1, Hq - 1] = False
+    for x, y in zip(got, want):
+        assert torch.equal(x[rest], y[rest])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("T,Hq,Hkv,D,lens", LONG)
+def test_undefined_keys_in_the_midst_of_long_rows(dtype, T, Hq, Hkv, D, lens):
+    """Keys of NaN in a thousand neighbouring tokens, whole parts of a row that is cut: every
+    row that sees them is NaN."""
+    q, k, v, pt, ln, nodes = tree(T, dtype, lens, [T] * len(lens), T, Hq, Hkv, D, 16, poison=False)
+    want = tq.tq_tree_attention(q, k, v, pt, ln, return_lse=True)
+    k[pt[0, 128:192].long()] = NAN  # tokens 2048 .. 3071
+    got = tq.tq_tree_attention(q, k, v, pt, ln, return_lse=True)
+    for x, y in zip(got, want):
+        assert torch.isnan(x[0]).all() and torch.isfinite(y).all()
+        assert torch.equal(x[1:], y[1:])
