@@ -897,11 +897,12 @@ __global__ __launch_bounds__(kTreeThreads) void tree_join_kernel(TreeParams p, i
         const int k = k0 + lane < n ? k0 + lane : n - 1;
         float w = __builtin_amdgcn_exp2f(part(k)[at_m] - base);
         const float l = part(k)[at_l];
-        // a part without weight adds nothing, also where it has met NaN; one whose sum is NaN
-        // has a weight of NaN, also where all its scores are, so that its maximum is -inf
-        if (k0 + lane >= n || l == 0.f) w = 0.f;
+        // a part without weight adds nothing (-1), also where it has met NaN; one whose sum is NaN
+        // has a weight of NaN, also where all its scores are, so that its maximum is -inf; and
+        // one whose weight rounds to zero counts: an infinite value in it makes NaN
+        if (k0 + lane >= n || l == 0.f) w = -1.f;
         else if (l != l) w = l;
-        if (w != 0.f) total += w * l;
+        if (!(w < 0.f)) total += w * l;
         const int most = n - k0 < CL ? n - k0 : CL;
         for (int x0 = turn; x0 < most; x0 += U * share) {
           float4v x[U];
@@ -910,14 +911,14 @@ __global__ __launch_bounds__(kTreeThreads) void tree_join_kernel(TreeParams p, i
           for (int u = 0; u < U; ++u) {
             const int i = x0 + u * share < most ? x0 + u * share : most - 1;
             wx[u] = __shfl(w, base_lane + i, kWave);
-            if (x0 + u * share >= most) wx[u] = 0.f;
+            if (x0 + u * share >= most) wx[u] = -1.f;
             x[u] = float4v{0, 0, 0, 0};
-            if (wx[u] != 0.f && real && col < p.D)
+            if (!(wx[u] < 0.f) && real && col < p.D)
               x[u] = *reinterpret_cast<const float4v*>(part(k0 + i) + (int64_t)j * p.D + col);
           }
 #pragma unroll
           for (int u = 0; u < U; ++u)
-            if (wx[u] != 0.f) v += wx[u] * x[u];
+            if (!(wx[u] < 0.f)) v += wx[u] * x[u];
         }
       }
 #pragma unroll

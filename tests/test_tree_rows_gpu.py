@@ -73,3 +73,20 @@ def test_undefined_keys_in_the_midst_of_long_rows(dtype, T, Hq, Hkv, D, lens):
     for x, y in zip(got, want):
         assert torch.isnan(x[0]).all() and torch.isfinite(y).all()
         assert torch.equal(x[1:], y[1:])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("T,Hq,Hkv,D,lens", LONG)
+def test_infinite_values_of_parts_that_weigh_nothing(dtype, T, Hq, Hkv, D, lens):
+    """An infinite value of a token whose weight rounds to zero makes NaN (or stays infinite), and
+    does so too where its whole part of a long row weighs nothing beside the others."""
+    q, k, v, pt, ln, nodes = tree(T, dtype, lens, [T] * len(lens), T, Hq, Hkv, D, 16, poison=False)
+    want = tq.tq_tree_attention(q, k, v, pt, ln, scale=30.0, return_lse=True)
+    page = pt[0, 130].long()  # a part of a row whose keys are short: scores near zero
+    k[pt[0, 128:192].long()] *= 2.0 ** -10
+    v[page, 5, :, 3], v[page, 5, :, 7] = float("inf"), -float("inf")
+    out, lse = tq.tq_tree_attention(q, k, v, pt, ln, scale=30.0, return_lse=True)
+    other = [d for d in range(D) if d not in (3, 7)]
+    assert not torch.isfinite(out[0][..., [3, 7]]).any()
+    assert torch.isfinite(out[0][..., other]).all() and torch.isfinite(lse[0]).all()
+    assert torch.equal(out[1:], want[0][1:])
