@@ -253,6 +253,15 @@ __global__ __launch_bounds__(WAVES * kWave, 4) void cache_select_kernel(SelectPa
   }
 }
 
+// How many tokens stay of each sequence, where there are no heads to choose for.
+constexpr int kCountThreads = 256;
+__global__ __launch_bounds__(kCountThreads) void cache_counts_kernel(SelectParams p) {
+  const int b = blockIdx.x * kCountThreads + threadIdx.x;
+  if (b >= p.B) return;
+  const int most = p.S < p.budget ? p.S : p.budget, len = p.lens[b];
+  p.counts[b] = len < 0 ? 0 : len < most ? len : most;
+}
+
 // ------------------------------------------------------------------ the move
 
 struct Row;
@@ -619,6 +628,11 @@ hipError_t launch_cache_select(const SelectArgs& a, hipStream_t stream) {
   p.budget = (int32_t)a.budget;
   p.recent = (int32_t)a.recent;
   p.sinks = (int32_t)a.sinks;
+  if (a.H == 0) {
+    hipLaunchKernelGGL(cache_counts_kernel, dim3((uint32_t)((a.B + kCountThreads - 1) / kCountThreads)),
+                       dim3(kCountThreads), 0, stream, p);
+    return hipGetLastError();
+  }
   const dim3 grid((uint32_t)(a.B * a.H));
   // More rows than are at work at once, long ones among them: the longest first, so that none
   // of those begins last.

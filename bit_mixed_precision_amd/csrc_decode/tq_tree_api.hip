@@ -187,14 +187,15 @@ int tq_cache_select(const float* scores, int64_t s_seq, int64_t s_head, int64_t 
                     const int32_t* lens, int64_t B, int64_t H, int64_t budget, int64_t recent,
                     int64_t sinks, int32_t* keep, int32_t* counts, float* sums, void* stream) {
   if (B < 0 || H < 0 || S < 0 || budget < 0 || recent < 0 || sinks < 0) return TQ_ERR_SHAPE;
-  if (B == 0 || H == 0) return TQ_OK;
-  if ((S > 0 && !scores) || !lens || (budget > 0 && !keep) || !counts) return TQ_ERR_NULL;
+  if (B == 0 || (H == 0 && !counts)) return TQ_OK;  // (without heads only counts are written)
+  if ((S > 0 && H > 0 && !scores) || !lens || (budget > 0 && H > 0 && !keep) || !counts)
+    return TQ_ERR_NULL;
   if (B > kMaxAttnBatch || H > kMaxAttnHeads || S > kMaxTokens || B * H > kMaxSelectRows ||
       budget > kMaxTokens || recent > budget || sinks > budget - recent)
     return TQ_ERR_SHAPE;
   s_seq = step(B, s_seq);
   s_head = step(H, s_head);
-  if (!stride_ok(B, s_seq) || !stride_ok(H, s_head)) return TQ_ERR_SHAPE;
+  if (H > 0 && (!stride_ok(B, s_seq) || !stride_ok(H, s_head))) return TQ_ERR_SHAPE;
   if (!aligned(scores, 4) || !aligned(lens, 4) || !aligned(keep, 4) || !aligned(counts, 4) ||
       !aligned(sums, 4))
     return TQ_ERR_ALIGN;

@@ -565,7 +565,7 @@ int tq_cache_weights(int dtype, const void* Q, int64_t q_seq, int64_t q_tok, int
  * min(n, budget); sums fp32 [B][H][budget] or NULL: their scores, then 0.
  * All device pointers.  sinks + recent <= budget <= 2^30, S <= 2^30, B <= 2^20, H <= 2^12,
  * B H < 2^22.  Outputs must not overlap the inputs.  Errors: TQ_ERR_NULL, TQ_ERR_SHAPE,
- * TQ_ERR_ALIGN, TQ_ERR_DEVICE.  B = 0 or H = 0 is a no-op. */
+ * TQ_ERR_ALIGN, TQ_ERR_DEVICE.  B = 0 is a no-op; H = 0 writes counts alone, unless that is NULL. */
 int tq_cache_select(const float* scores, int64_t s_seq, int64_t s_head, int64_t S,
                     const int32_t* lens, int64_t B, int64_t H, int64_t budget, int64_t recent,
                     int64_t sinks, int32_t* keep, int32_t* counts, float* sums, void* stream);

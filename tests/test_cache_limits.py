@@ -1,0 +1,18 @@
+"""Argument checks of calls on kept caches at the ends of their ranges.  As in
+test_tree_limits.py every call is refused, so that none reaches a device."""
+
+import pytest
+
+torch = pytest.importorskip("torch")
+tq = pytest.importorskip("bit_mixed_precision_amd.binding")
+
+from test_tree_limits import A, G, N, S, refuses, select  # noqa: E402
+
+
+def test_choice_without_heads():
+    """Counts are wanted all the same; nothing else is looked at."""
+    none = dict(H=0, scores=None, keep=None, sums=None)
+    refuses(select, N, dict(none, lens=None))
+    refuses(select, G, dict(none, counts=A + 2), dict(none, lens=A + 2), dict(none, ss=-1, sh=-1, counts=A + 1))
+    refuses(select, S, dict(none, B=(1 << 20) + 1), dict(none, recent=65), dict(none, S=(1 << 30) + 1))
+    refuses(select, tq.TQ_OK, dict(none, counts=None), dict(none, B=0))
