@@ -643,7 +643,8 @@ int tq_pages_copy(void* pool, int64_t planes, int64_t n_pages, int64_t page_byte
  * needs more pages, together with those before it, than are free keeps its tokens, length
  * and pages, and short_out int32 [1] counts such rows.  lens_out int32 [rows]: base +
  * counts.  page_bytes a multiple of page_size * heads * 16, planes one of groups; heads
- * <= 2^16.  workspace: tq_pages_keep_workspace(rows, width, n_pages) bytes. */
+ * <= 2^16, groups * heads < 2^31.  workspace: tq_pages_keep_workspace(rows, width, n_pages)
+ * bytes. */
 int tq_pages_keep(void* pool, int64_t planes, int64_t n_pages, int64_t page_bytes,
                   const int32_t* table, const int32_t* lens, int64_t rows, int64_t width,
                   int64_t page_size, const int32_t* keep, int64_t groups, int64_t heads, int64_t n,

@@ -6,7 +6,7 @@ import pytest
 torch = pytest.importorskip("torch")
 tq = pytest.importorskip("bit_mixed_precision_amd.binding")
 
-from test_tree_limits import A, G, N, S, refuses, select  # noqa: E402
+from test_tree_limits import A, G, N, S, keep, refuses, select  # noqa: E402
 
 
 def test_choice_without_heads():
@@ -16,3 +16,11 @@ def test_choice_without_heads():
     refuses(select, G, dict(none, counts=A + 2), dict(none, lens=A + 2), dict(none, ss=-1, sh=-1, counts=A + 1))
     refuses(select, S, dict(none, B=(1 << 20) + 1), dict(none, recent=65), dict(none, S=(1 << 30) + 1))
     refuses(select, tq.TQ_OK, dict(none, counts=None), dict(none, B=0))
+
+
+def test_lists_of_a_row_are_counted_in_32_bits():
+    """2^31 lists and more (groups times heads) are refused, one less passes on to the last check."""
+    refuses(keep, S, *(dict(groups=g, planes=g, heads=h, size=1, pb=16 * h)
+                       for g, h in ((1 << 15, 1 << 16), (1 << 16, 1 << 15), (1 << 16, 1 << 16))))
+    refuses(keep, G, *(dict(groups=g, planes=g, heads=h, size=1, pb=16 * h)
+                       for g, h in (((1 << 15) - 1, 1 << 16), (1 << 16, (1 << 15) - 1))))
