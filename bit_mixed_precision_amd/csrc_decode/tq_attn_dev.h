@@ -31,8 +31,9 @@ struct FastDiv {
 // no less than `least` wherever x is not: an infinite value times them then stays
 // infinite instead of becoming NaN.  Below that x has one number only, or none: a
 // token without weight adds nothing, however large its value.  `least`: 2^-126 in
-// bf16 (the least weight there is); in fp16 the type's own 2^-24, of weights scaled by
-// 2^14.
+// bf16 (the least weight there is); in fp16 the type's own 2^-24, so that a weight that one
+// number holds is off by as much: of a row's largest, which its caller scales to 2^14 (or to
+// 2^9 at least), 2^-38 (2^-33).
 template <bool BF>
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
   constexpr float least = BF ? 0x1p-126f : 0x1p-24f;
