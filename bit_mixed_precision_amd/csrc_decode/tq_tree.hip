@@ -125,10 +125,12 @@ __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) 
 // 16 bytes at the resource's base + off to LDS: lane l writes the bytes dst + 16 l.  In
 // assembly, because the compiler would otherwise wait for these copies before every
 // transposing read of LDS, of whatever buffer; waited for by kNoLoads.  (Nothing is
-// returned to a register.  A copy needs one state between the write of m0 and itself.)
+// returned to a register.  A copy needs one state between the write of m0 and itself, and
+// five after a vector instruction's write of its resource, which may be the one before: the
+// compiler counts no states into assembly.)
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, int off, unsigned char* dst) {
   const uint32_t to = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)dst;
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :: "s"(to), "v"(off), "s"(r) : "memory", "m0");
 }
 
