@@ -1009,10 +1009,23 @@ TreeGrid tree_grid(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int
   const int64_t tiles = ceil_div(capacity, wide ? 64 : 128) + 1;  // a window may begin inside one
   const int64_t at_once = device_cus() * tree_per_cu(D);
   // Nothing is split where a row has few tiles (splitting and joining cost some 10 us with
-  // 32 rows, 20 with 128), or where there are enough rows, or more blocks of rows of a
-  // sequence than the split could tell apart.
-  const int64_t few = wide ? 12 : blocks < device_cus() ? 5 : 9;
-  if (tiles <= few || blocks >= 4 * at_once || 4 * blocks >= at_once * B * Hkv)
+  // 32 rows, 20 with 128), or where there are so many rows that others are at work while a
+  // workgroup takes a long one: four rounds, and no more than eight tiles of the longest row a
+  // round, as the table has room for; or where there are more blocks of rows of a sequence
+  // than the split could tell apart.
+  // Measured (us, whole / split).  Few tiles, all rows equally long, heads of 128: thin, 8 blocks of
+  // 512, 1024 tokens 16.6 / 15.3, 24.5 / 16.1; 128 blocks of 512, 1024, 1536 19.5 / 26.8, 29.6 / 31.6,
+  // 40.4 / 36.7; 320 blocks of 1024, 2048 47.7 / 56.8, 83.0 / 86.8.  Wide, 16 blocks of 704
+  // 27.7 / 22.4; 128 of 704, 1024, 1536 29.6 / 42.3, 37.9 / 38.2, 51.6 / 44.2; 384 of 704, 2048
+  // 40.2 / 67.6, 92.1 / 110.9.  Equal rows would stay whole for longer where blocks are many; the
+  // split is for those that are not equal.
+  // Many rows, one of as many tokens as the table holds and the others of 400: 2048 thin blocks (four
+  // rounds), 2048, 4096, 32768 tokens 143 / 123, 180 / 126, 709 / 158, without the long one 115 / 115;
+  // 2048 wide ones 185 / 232, 236 / 199, 971 / 267, without 148 / 150; 4096 thin ones of heads of 64
+  // (4096 sequences, whose lengths every workgroup reads) 115 / 156, 135 / 157, 418 / 159, without
+  // 102 / 157.
+  const int64_t few = wide ? 12 : blocks < device_cus() ? 5 : 9, rounds = blocks / at_once;
+  if (tiles <= few || (rounds >= 4 && tiles <= 8 * rounds) || 4 * blocks >= at_once * B * Hkv)
     return {blocks, blocks, true, wide};
   return {blocks * tiles < at_once ? blocks * tiles : at_once, blocks, false, wide};
 }

@@ -24,3 +24,13 @@ def test_lists_of_a_row_are_counted_in_32_bits():
                        for g, h in ((1 << 15, 1 << 16), (1 << 16, 1 << 15), (1 << 16, 1 << 16))))
     refuses(keep, G, *(dict(groups=g, planes=g, heads=h, size=1, pb=16 * h)
                        for g, h in (((1 << 15) - 1, 1 << 16), (1 << 16, (1 << 15) - 1))))
+
+
+def test_large_batches_are_cut_where_their_tables_hold_long_rows():
+    """Tree attention gives a workgroup a whole row only where the longest that the table
+    holds does not outlast the others: the workspace is what a cut needs."""
+    ws = tq.tq_tree_attention_workspace
+    for T in (4, 16):  # either form
+        for B in (255, 256, 300, 1000):
+            assert ws(B, T, 64, 8, 128, 16, 8192) > 0, (T, B)
+        assert ws(256, T, 64, 8, 128, 16, 100) == ws(1000, T, 64, 8, 128, 16, 400) == 0
