@@ -36,6 +36,9 @@ constexpr int kMaskWords = 4;
 constexpr int kMaxNodes = 64 * kMaskWords;
 constexpr int kQueryBytes = 48 * 1024;  // of LDS for queries
 constexpr int kMostRows = 8192;         // (nodes times heads of a group)
+constexpr int kCuLds = 160 * 1024;
+// What the kernel declares itself: every node's bits and first token (and a flag).
+constexpr int kFixedLds = kMaxNodes * (kMaskWords * 8 + 4) + 16;
 
 struct WeightsParams {
   const unsigned char* Q;
@@ -392,12 +395,17 @@ hipError_t launch_nt(WeightsParams p, hipStream_t s) {
   int64_t cap = (int64_t)p.width * p.page.d;
   if (cap > p.S) cap = p.S;
   const int64_t tiles = (cap + UT - 1) / UT, all = (int64_t)p.B * p.Hkv * tiles;
-  const int64_t most = (DV > 128 ? 2 : 3) * (int64_t)device_cus();  // what the registers allow at once
   if (all == 0) return hipSuccess;
-  p.tiles = all <= 2 * most ? (int32_t)tiles : 0;
   const int rows = (p.T * p.G + 15) / 16 * 16, most_rows = kQueryBytes / (DV * 2);
   p.chunk = rows < most_rows ? rows : most_rows;
   const int lds = p.chunk * DV * 2 + rows * 4;
+  // What registers and LDS allow at once: with more, equal runs would be a full round and part
+  // of another.  Measured (us, by registers alone / so), 16 sequences of 4096 .. 16384 tokens, 8 heads,
+  // 176 rows, heads of 128 (two a CU instead of three) 159 / 130, 256 rows 333 / 287; 512 rows of heads
+  // of 64 382 / 329.
+  const int64_t by_lds = kCuLds / (lds + kFixedLds), by_registers = DV > 128 ? 2 : 3;
+  const int64_t most = (by_lds < by_registers ? by_lds : by_registers) * device_cus();
+  p.tiles = all <= 2 * most ? (int32_t)tiles : 0;
   if (lds > 48 * 1024) {
     static std::atomic<uint64_t> done{0};
     const hipError_t e =
