@@ -642,8 +642,8 @@ int tq_pages_copy(void* pool, int64_t planes, int64_t n_pages, int64_t page_byte
  * releases, stay as they are.
  * A page that is held by more than one table entry is not written: where a token in it
  * would change, the row gets a free page in its place, with its kept tokens.  A row that
- * needs more pages, together with those before it, than are free keeps its tokens, length
- * and pages, and short_out int32 [1] counts such rows.  lens_out int32 [rows]: base +
+ * needs pages, and together with those before it more than are free, keeps its tokens, length
+ * and pages, and short_out int32 [1] counts such rows; one that needs none never does.  lens_out int32 [rows]: base +
  * counts.  page_bytes a multiple of page_size * heads * 16, planes one of groups; heads
  * <= 2^16, groups * heads < 2^31.  workspace: tq_pages_keep_workspace(rows, width, n_pages)
  * bytes. */

@@ -176,7 +176,7 @@ def pages_keep_ref(page_table, lens, keep, counts, base, n_pages, size):
                     for i in range(max(first, e * size), min(total, (e + 1) * size))):
                 fresh.append(e)
         asked += len(fresh)
-        if asked > len(free):
+        if fresh and asked > len(free):
             short += 1
             out[r] = length[r]
             held = _held(lens, r, width, size)

@@ -1,7 +1,10 @@
 """Argument checks of calls on kept caches at the ends of their ranges.  As in
 test_tree_limits.py every call is refused, so that none reaches a device."""
 
+import numpy as np
 import pytest
+
+from oracle import pages_keep_ref
 
 torch = pytest.importorskip("torch")
 tq = pytest.importorskip("bit_mixed_precision_amd.binding")
@@ -34,3 +37,13 @@ def test_large_batches_are_cut_where_their_tables_hold_long_rows():
         for B in (255, 256, 300, 1000):
             assert ws(B, T, 64, 8, 128, 16, 8192) > 0, (T, B)
         assert ws(256, T, 64, 8, 128, 16, 100) == ws(1000, T, 64, 8, 128, 16, 400) == 0
+
+
+def test_keep_oracle_where_pages_are_short():
+    """Rows that need pages are refused once those are used up; one that needs none is not."""
+    table = np.array([[0, 1], [0, 2], [0, 3], [4, 5]])
+    lists = np.array([[[[1, 2]], [[1, 3]], [[0, 1]], [[1, 3]]]])
+    got, lens, short, moves = pages_keep_ref(table, [4, 4, 4, 4], lists, [2, 2, 2, 2], None, 7, 2)
+    assert got.tolist() == [[6, -1], [0, 2], [0, -1], [4, -1]]
+    assert lens.tolist() == [2, 4, 2, 2] and short == 1
+    assert {m[4] for m in moves} == {6, 4}
