@@ -9,13 +9,14 @@
 // once.  What bounds it is the chain of barriers: a digit costs clearing, counting and
 // ranking 2048 bins, some 1.5 us each.  8 rows of 1009 tokens: 6.5 us with a launch; 384 rows of
 // up to 32768 tokens, 17 MB: 25 us (counted from memory at every digit 40; rows
-// in order of their place instead of the longest first 31).
+// in order of their place instead of the longest first 31).  Longer rows are read from memory at
+// every digit and twice more, still by one workgroup each: 8 rows of 131072 tokens 110 us.
 //
 // The move.  Slot i of a row gets token keep[i] >= i of the same row, so a row can be
 // moved forward in place, part by part: what a part writes no later part reads.  A page
 // that other rows hold too is not written; the row gets a free page in its place.  A row's
 // parts follow each other, rows, heads and planes run side by side.  16 rows that keep
-// 1024 of up to 2048 tokens of 2 KB in 32 planes, 1.08 GB read and written: 240 us, 4.5 TB/s, a
+// 1024 of up to 2048 tokens of 2 KB in 16 planes, 1.07 GB read and written: 240 us, 4.5 TB/s, a
 // plain copy's 4.9 less the parts that are as short as a head.
 
 #include "tq.h"

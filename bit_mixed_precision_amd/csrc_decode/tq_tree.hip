@@ -18,11 +18,12 @@
 // operand (O^T += V^T P^T) where they lie.  V is turned by the transposing read of LDS.
 //   wide, for many rows: four waves of 32 rows each share tiles of 64 tokens, copied to LDS
 //   past the registers, two tiles in turn.  131072 tokens, 64 nodes, 8 heads of 128 with 8
-//   query heads each: 275 GFLOP in 375 us, 730 TFLOP/s (a plain product of 8192^3 reaches
-//   1330).  Matrix and other vector instructions take turns more than they overlap: 39% and
-//   42% of a SIMD's time, and waves wait a quarter of theirs; two waves a SIMD are what
-//   the registers allow.  Four blocks of rows read the same tokens, and the L2s
-//   catch half of that: 1.2 GB from memory of 0.54.  Mixing one tile's scores
+//   query heads each: 275 GFLOP in 370 us, 740 TFLOP/s, and 15 for the join (a plain product
+//   of 8192^3 reaches 1330).  (Once the GPU has taken up the load: the calls 4 .. 40 after a
+//   pause take up to 500.)  Matrix and other vector instructions take turns more than they
+//   overlap: 39% and 42% of a SIMD's time, and waves wait a quarter of theirs; two waves a SIMD
+//   are what the registers allow.  Four blocks of rows read the same tokens, and the L2s
+//   catch half of that: 1.1 GB from memory of 0.54.  Mixing one tile's scores
 //   with the product of the tile before inside a wave brought nothing (414 against 394).
 //   thin, for up to 32 rows and short caches: the four waves share 128 tokens of the same
 //   rows, each tile through registers to LDS that only its wave reads, and their sums meet
@@ -998,7 +999,10 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // 32, 128, 256, 512 tokens: 9.6 / 10.2, 9.6 / 11.5, 11.7 / 14.9, 15.8 / 21.3; eight trees (384 thin
 // workgroups) 12.8 / 10.8, 12.9 / 12.3, 16.1 / 15.7, 21.5 / 22.2; four of 64 nodes, 4 heads each of
 // 64 7.2 / 8.7, 8.4 / 11.1, 10.9 / 16.0; ten of 100 nodes, 8 heads of 64 (320 thin workgroups), up to
-// 204, 500 tokens 10.3 / 13.1, 13.6 / 17.4.
+// 204, 500 tokens 10.3 / 13.1, 13.6 / 17.4.  Either side of the limit, 192 and 512 tokens: heads of 64,
+// 512 thin workgroups 11.8 / 11.2 and 15.8 / 18.3 (32 nodes, 8 / 1 heads), 12.7 / 12.1 and 16.9 / 19.4
+// (100 nodes), 640 of them 14.7 / 11.2 and 19.5 / 18.4, 14.9 / 12.7 and 20.6 / 19.5; heads of 128, 256
+// 13.8 / 14.4 and 19.2 / 23.3, 384 17.2 / 15.0 and 24.7 / 24.3.
 constexpr int64_t kShort = 512;
 
 TreeGrid tree_grid(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity) {
@@ -1033,7 +1037,9 @@ TreeGrid tree_grid(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int
 // Workgroups of a join: with one row of 16 lanes and more at a time, as many as keep every CU busy.
 // Measured on the GPU (us): 32 blocks of 128 rows in 16 parts each 15.1 (a workgroup for each
 // that began a block, most of them idle: 45), 384 blocks in some two parts 18.2, with 8192
-// workgroups 14.2 and 20.5.
+// workgroups 14.2 and 20.5.  Whole calls of six shapes (1 .. 37 sequences of 2048 .. 32768 tokens,
+// heads of 64 .. 256) differ by 3% at most between 1024, 2048 and 8192; with 512 24 sequences of
+// 4096 tokens take 206 against 192.
 constexpr int64_t kJoin = 2048;
 
 template <bool BF, int DP, int TEAM, bool TWO>

@@ -12,11 +12,14 @@
 //
 // What bounds it: a token is 2 D bytes of a key-value head, and with R rows R exponentials at a
 // quarter of the vector rate beside 2 R D operations.  16 sequences of up to 16384 tokens, 8 heads
-// of 128, 128 rows each: 307 MB in 86 us (94 with each lane finding its own tokens), 3.6 TB/s;
-// exponentials and the additions around them take 25 us, the matrix product 25, reading 44, and
-// a unit of 128 tokens is too short to hide one behind the other.  Two tiles of 16 tokens a wave:
-// four need twice the registers, two workgroups a CU instead of three: 91 against 86, and one
-// sequence of 2000 tokens 7.3 against 5.5.
+// of 128, 128 rows each: 303 MB in 86 - 90 us (in turn 94 against 86 with each lane finding its own
+// tokens), 3.4 TB/s; exponentials and the additions around them take 25 us, the matrix product
+// 25, reading 44, and a unit of 128 tokens is too short to hide one behind the other.  Vector
+// units are busy 56% of the time, twice what those exponentials and additions need; what
+// the other half is has not been looked into.  Of one row each, 64 sequences of
+// 1000 .. 8000 tokens: 458 MB in 105 us, 4.4 TB/s, waves waiting half their time.
+// Two tiles of 16 tokens a wave: four need twice the registers, two workgroups a CU instead of
+// three: 91 against 86, and one sequence of 2000 tokens 7.3 against 5.5.
 
 #include <atomic>
 

@@ -511,8 +511,8 @@ int tq_tree_mask(const int32_t* parents, int64_t B, int64_t T, int64_t* mask, in
  * weight enters the product with v as two 16-bit numbers, rounded to within 2^-22 (fp16;
  * 2^-16 bfloat16) of itself; with more rows as two or as one, rounded to nearest (2^-11 of
  * itself in fp16, 2^-8 in bfloat16).  Which it is goes by all sizes of the call, the batch and
- * the table's width among them, as does the order of the sums: a sequence may have other last
- * bits in a call of other sizes.  In fp16 a weight may also be off by 2^-33 of the row's
+ * the table's width among them, and the order of the sums by these and all lengths: a sequence
+ * may have other last bits beside other sequences.  In fp16 a weight may also be off by 2^-33 of the row's
  * largest, and one below 2^-34 of it may add nothing.  An infinite value gives an infinite
  * result, or NaN where its weight is zero or, in fp16, may add nothing.  A token that a
  * node does not see has no influence on it, whatever its key and value hold.  The same
