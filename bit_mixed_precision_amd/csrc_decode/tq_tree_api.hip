@@ -237,7 +237,8 @@ int tq_pages_keep(void* pool, int64_t planes, int64_t n_pages, int64_t page_byte
   if (st != TQ_OK || (st = pool_shapes(planes, page_bytes)) != TQ_OK) return st;
   // (a row's lists are counted in 32 bits)
   if (groups < 1 || groups > kMaxPlanes || planes % groups || heads < 1 || heads > kMaxHeads ||
-      groups * heads > INT32_MAX || page_bytes % (page_size * heads) || page_bytes / (page_size * heads) % 16 || n > kMaxTokens ||
+      groups * heads > INT32_MAX || page_bytes % (page_size * heads) ||
+      page_bytes / (page_size * heads) % 16 || n > kMaxTokens ||
       workspace_bytes < tq::keep_workspace_bytes(rows, width, n_pages))
     return TQ_ERR_SHAPE;
   if (!aligned(pool, 16) || !aligned(workspace, 16) || !aligned(table, 4) || !aligned(lens, 4) ||
